@@ -70,6 +70,7 @@ typedef enum {
 #define ZL_DEVERR_BAD_SEQ_LEN 2u /* seq_len < 0 or > block_table_stride * page_size */
 #define ZL_DEVERR_TIMEOUT 4u     /* a pipeline wait gave up after ~2 s */
 #define ZL_DEVERR_BAD_PREFIX 8u  /* shared_prefix_pages does not hold for some sequence */
+#define ZL_DEVERR_BAD_PATH 16u   /* zl_kv_commit: accepted count or path index out of range */
 
 typedef struct {
   size_t struct_size; /* sizeof(zl_decode_attn_params), for ABI checks */
@@ -310,6 +311,153 @@ typedef struct {
 } zl_kv_append_params;
 
 zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
+
+/*
+ * Modified scores: zl_decode_attn with, for query token i at position pos(i)
+ * and cached token t at position pos(t) (s = scale * q . k_t),
+ *   softcap c > 0     s <- c * tanh(s / c)
+ *   alibi_slopes      s <- s - slope[h] * (pos(i) - pos(t))
+ *   window w > 0      token t is seen only if pos(i) - pos(t) < w
+ *   tree_mask         the q_len query tokens are a drafted tree (below)
+ * in that order, and lse = ln sum exp over the modified scores. Positions: a
+ * token t before the last q_len ones is at t; the drafted ones, without a
+ * mask, are a chain (token i at seq_lens[b] - q_len + i, causal).
+ *
+ * tree_mask, uint32 [B, q_len, ceil(q_len / 32)]: bit j % 32 of word [b, i,
+ * j / 32] set = query token i sees drafted token j (an ancestor of i, or i
+ * itself; any other set is taken as it is). Every query token sees the tokens
+ * before the drafted ones. Token i is then at position seq_lens[b] - q_len +
+ * (its set bits - 1, at least 0). A row that sees no token gives out = 0 and
+ * lse = -inf. Bits at q_len and above must be 0.
+ *
+ * weights, fp32: element (b, kh, t) at b * weights_seq_stride + kh *
+ * weights_head_stride + t, t < weights_tokens. The call also updates
+ *   weights[b, kh, t] <- weights_decay * weights[b, kh, t]
+ *                        + sum over query tokens i and the heads of kv head kh
+ *                          of the softmax weight of token t
+ * for t < seq_lens[b] (elements at and after it stay as they are; with
+ * weights_decay 0 the old values are not read). Rows zeroed for a bad page add
+ * nothing. A sequence longer than weights_tokens counts as a bad length
+ * (ZL_DEVERR_BAD_SEQ_LEN: zeros, weights untouched). Rows of different
+ * sequences and heads must not overlap.
+ *
+ * Everything else is as for zl_decode_attn, fused append included, with two
+ * limits: flags must be 0 and shared_prefix_pages 0 (ZL_ERR_UNSUPPORTED). A
+ * softcap outside [1e-6, 1e6] is ZL_ERR_UNSUPPORTED. Results depend only on
+ * logical content, and repeated calls are bit-identical. K and V rows of
+ * tokens that no query token's window reaches are never used and pages that
+ * hold only such tokens need not be mapped; rows that some query sees and
+ * others do not must be finite.
+ */
+typedef struct {
+  size_t struct_size;        /* sizeof(zl_score_params) */
+  float softcap;             /* 0 = none */
+  int32_t window;            /* 0 = none */
+  const float* alibi_slopes; /* fp32 [Hq], or NULL */
+  const uint32_t* tree_mask; /* or NULL */
+  float* weights;            /* or NULL */
+  int64_t weights_seq_stride, weights_head_stride;
+  int32_t weights_tokens;
+  float weights_decay;
+} zl_score_params;
+
+zl_status zl_decode_attn_ex(const zl_decode_attn_params* params, const zl_score_params* scores,
+                            zl_stream_t stream);
+
+/* Workspace bytes zl_decode_attn_ex needs; of the score params the pointers
+   only as present or absent. With weights it holds the scores of every query
+   row: B * q_len * Hq * weights_tokens * 4 bytes more. */
+zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
+                                           const zl_score_params* scores, size_t* bytes);
+
+/*
+ * Eviction by accumulated weights: hold every (sequence, kv head) to `budget`
+ * cached tokens. A sequence of L = seq_lens[b] > budget tokens keeps, in each
+ * kv head, its first `sink` tokens, its last `recent` ones and, of those
+ * between, the budget - sink - recent with the largest weights (equal weights:
+ * the earlier token; NaN counts as below every number). The kept rows move, in
+ * order, to positions 0 .. budget - 1: K, V and weights. Each kv head chooses
+ * for itself. A sequence of at most budget tokens keeps everything.
+ *   - new_lens[b] = min(L, budget). kept, int32 [B, Hkv, budget] contiguous:
+ *     the kept positions, ascending, then -1. Both are written.
+ *   - dst_block_table NULL: in place (no page of these sequences may be mapped
+ *     by another one, or twice). Otherwise the rows are copied to the pages
+ *     that dst_block_table maps, which must be no page that block_table maps
+ *     in this call: the pages of a shared prefix stay whole for their other
+ *     users. Pages past the new length are the caller's to free.
+ *   - weights_out NULL: in place; otherwise element (b, kh, j) at
+ *     b * weights_out_seq_stride + kh * weights_out_head_stride + j, and it
+ *     must not overlap weights. Only j < new_lens[b] is written.
+ *   - Pools, strides, row widths, block table and v_pool = NULL as for
+ *     zl_kv_append. budget >= 1, sink + recent <= budget.
+ *   - Device data errors: seq_lens[b] < 0, above the block table's reach or
+ *     above weights_tokens, or a new length above the destination table's
+ *     reach: nothing of the sequence moves, its kept entries are -1 and
+ *     new_lens[b] = seq_lens[b] (ZL_DEVERR_BAD_SEQ_LEN). A row whose source or
+ *     destination page id is outside [0, num_pages) does not move
+ *     (ZL_DEVERR_BAD_PAGE).
+ *   - Rows are copies: bit-exact. new_lens must not overlap seq_lens.
+ */
+typedef struct {
+  size_t struct_size; /* sizeof(zl_kv_evict_params) */
+  void* k_pool;
+  void* v_pool;
+  int64_t page_stride, token_stride, head_stride;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* dst_block_table; /* or NULL */
+  int64_t dst_block_table_stride;
+  const int32_t* seq_lens;
+  int32_t* new_lens;
+  int32_t* kept;
+  float* weights;
+  int64_t weights_seq_stride, weights_head_stride;
+  float* weights_out; /* or NULL */
+  int64_t weights_out_seq_stride, weights_out_head_stride;
+  int32_t weights_tokens;
+  int32_t B, Hkv, D_k, D_v, page_size, num_pages;
+  int32_t budget, sink, recent;
+  uint32_t* err_flags; /* optional */
+} zl_kv_evict_params;
+
+zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream);
+
+/*
+ * Commit of a drafted tree's accepted path: the last q_len of sequence b's
+ * seq_lens[b] cached tokens are the drafted tree; its accepted[b] tokens
+ * path[b, 0 .. accepted[b]) (indices into the q_len drafted ones, in any
+ * order, repeats allowed) become the tokens at positions seq_lens[b] - q_len +
+ * 0, 1, ...: their K and V rows move there, in place, and new_lens[b] =
+ * seq_lens[b] - q_len + accepted[b].
+ *   - path int32, row b of path_len entries at b * path_stride; accepted int32
+ *     [B]; 0 <= accepted[b] <= min(q_len, path_len), q_len <= 128. Entries past accepted[b] are not read.
+ *   - Pools, strides, row widths, block table and v_pool = NULL as for
+ *     zl_kv_append; no page of these sequences may be mapped by another one.
+ *   - Device data errors: seq_lens[b] < q_len or above the block table's reach
+ *     (ZL_DEVERR_BAD_SEQ_LEN), accepted[b] or a path entry out of range
+ *     (ZL_DEVERR_BAD_PATH): nothing of the sequence moves and new_lens[b] =
+ *     seq_lens[b]. A row whose source or destination page id is outside [0,
+ *     num_pages) does not move (ZL_DEVERR_BAD_PAGE).
+ *   - Rows are copies: bit-exact. new_lens must not overlap seq_lens.
+ */
+typedef struct {
+  size_t struct_size; /* sizeof(zl_kv_commit_params) */
+  void* k_pool;
+  void* v_pool;
+  int64_t page_stride, token_stride, head_stride;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* accepted;
+  int32_t* new_lens;
+  int32_t path_len; /* entries of a path row */
+  int32_t B, q_len, Hkv, D_k, D_v, page_size, num_pages;
+  uint32_t* err_flags; /* optional */
+} zl_kv_commit_params;
+
+zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t stream);
 
 /* Static description of a status code. */
 const char* zl_status_string(zl_status status);

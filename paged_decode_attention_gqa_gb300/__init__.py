@@ -14,6 +14,7 @@ Tensors are torch CUDA tensors (PyTorch provides device memory and streams).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -24,9 +25,12 @@ import torch
 from ._build import LIB_PATH, build  # noqa: F401  (build() is the public build step)
 
 __all__ = [
-    "ZlError", "Params", "AppendParams", "lib", "decode_attn", "decode_attn_mla", "kv_append",
-    "workspace_size", "workspace_size_mla", "call", "call_noalloc", "build", "LIB_PATH",
-    "DEVERR_BAD_PAGE", "DEVERR_BAD_SEQ_LEN", "DEVERR_TIMEOUT", "HEADER", "declared_symbols",
+    "ZlError", "Params", "AppendParams", "ScoreParams", "EvictParams", "CommitParams", "lib",
+    "decode_attn", "decode_attn_mla", "kv_append", "kv_evict", "kv_commit", "tree_mask",
+    "workspace_size", "workspace_size_mla", "workspace_size_ex", "call", "call_ex",
+    "call_noalloc", "build", "LIB_PATH",
+    "DEVERR_BAD_PAGE", "DEVERR_BAD_SEQ_LEN", "DEVERR_TIMEOUT", "DEVERR_BAD_PATH", "HEADER",
+    "declared_symbols",
 ]
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
@@ -36,6 +40,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA = range(5)
 SINGLE_LAUNCH = 1  # ZL_DECODE_SINGLE_LAUNCH
 TEST_STALL = 0x80000000  # ZL_DECODE_TEST_STALL (failure-detection test hook)
 DEVERR_BAD_PAGE, DEVERR_BAD_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_BAD_PREFIX = 1, 2, 4, 8
+DEVERR_BAD_PATH = 16
 NOALLOC_WORKSPACE_BYTES = 8 << 20  # ZL_NOALLOC_WORKSPACE_BYTES
 
 
@@ -108,6 +113,86 @@ class AppendParams(ctypes.Structure):
     ]
 
 
+class ScoreParams(ctypes.Structure):
+    """Mirror of zl_score_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("tree_mask", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("weights_seq_stride", ctypes.c_int64),
+        ("weights_head_stride", ctypes.c_int64),
+        ("weights_tokens", ctypes.c_int32),
+        ("weights_decay", ctypes.c_float),
+    ]
+
+
+class EvictParams(ctypes.Structure):
+    """Mirror of zl_kv_evict_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("dst_block_table", ctypes.c_void_p),
+        ("dst_block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p),
+        ("kept", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("weights_seq_stride", ctypes.c_int64),
+        ("weights_head_stride", ctypes.c_int64),
+        ("weights_out", ctypes.c_void_p),
+        ("weights_out_seq_stride", ctypes.c_int64),
+        ("weights_out_head_stride", ctypes.c_int64),
+        ("weights_tokens", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D_k", ctypes.c_int32),
+        ("D_v", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("budget", ctypes.c_int32),
+        ("sink", ctypes.c_int32),
+        ("recent", ctypes.c_int32),
+        ("err_flags", ctypes.c_void_p),
+    ]
+
+
+class CommitParams(ctypes.Structure):
+    """Mirror of zl_kv_commit_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("path", ctypes.c_void_p),
+        ("path_stride", ctypes.c_int64),
+        ("accepted", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p),
+        ("path_len", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D_k", ctypes.c_int32),
+        ("D_v", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("err_flags", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -135,6 +220,16 @@ def lib():
             handle.zl_decode_attn_launches.argtypes = [P, ctypes.POINTER(ctypes.c_int32)]
             handle.zl_kv_append.restype = ctypes.c_int
             handle.zl_kv_append.argtypes = [ctypes.POINTER(AppendParams), ctypes.c_void_p]
+            S = ctypes.POINTER(ScoreParams)
+            handle.zl_decode_attn_ex.restype = ctypes.c_int
+            handle.zl_decode_attn_ex.argtypes = [P, S, ctypes.c_void_p]
+            handle.zl_decode_attn_ex_workspace_size.restype = ctypes.c_int
+            handle.zl_decode_attn_ex_workspace_size.argtypes = [P, S,
+                                                                ctypes.POINTER(ctypes.c_size_t)]
+            handle.zl_kv_evict.restype = ctypes.c_int
+            handle.zl_kv_evict.argtypes = [ctypes.POINTER(EvictParams), ctypes.c_void_p]
+            handle.zl_kv_commit.restype = ctypes.c_int
+            handle.zl_kv_commit.argtypes = [ctypes.POINTER(CommitParams), ctypes.c_void_p]
             handle.zl_status_string.restype = ctypes.c_char_p
             handle.zl_status_string.argtypes = [ctypes.c_int]
             _lib = handle
@@ -228,6 +323,14 @@ def workspace_size_mla(params: Params) -> int:
     return n.value
 
 
+def workspace_size_ex(params: Params, scores: ScoreParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().zl_decode_attn_ex_workspace_size(ctypes.byref(params), ctypes.byref(scores),
+                                                  ctypes.byref(n)),
+           "zl_decode_attn_ex_workspace_size")
+    return n.value
+
+
 _ws_cache: dict = {}
 
 
@@ -275,6 +378,144 @@ def call(params: Params, *, mla: bool, stream=None):
            "zl_decode_attn_mla" if mla else "zl_decode_attn")
 
 
+def call_ex(params: Params, scores: ScoreParams, stream=None):
+    """zl_decode_attn_ex on ``stream`` (default: torch's current stream)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    _check(lib().zl_decode_attn_ex(ctypes.byref(params), ctypes.byref(scores),
+                                   ctypes.c_void_p(stream.cuda_stream)), "zl_decode_attn_ex")
+
+
+def _expect(t, name, dtype, shape, device, contiguous=True):
+    """Check a tensor argument of the entry points below (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pools on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags,
+                  same_width=True):
+    """The checks every call over a paged cache shares; returns (B, Hkv)."""
+    dev = k_pool.device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"the pools are on {dev}, which is not the current device")
+    if k_pool.dim() != 4 or (v_pool is not None and v_pool.dim() != 4):
+        raise ValueError("pools are 4-D: [pages, slot, head, dim] (NHD) or "
+                         "[pages, head, slot, dim] (HND)")
+    if v_pool is not None:
+        shape = k_pool.shape if same_width else k_pool.shape[:3] + v_pool.shape[3:]
+        _expect(v_pool, "v_pool", torch.bfloat16, shape, dev, contiguous=False)
+        if v_pool.stride(3) != 1:
+            raise ValueError("pool rows must be contiguous")
+    _expect(k_pool, "k_pool", torch.bfloat16, k_pool.shape, dev, contiguous=False)
+    slots, Hkv = (k_pool.shape[1], k_pool.shape[2]) if layout == "NHD" else (
+        k_pool.shape[2], k_pool.shape[1])
+    if slots != page_size:
+        raise ValueError(f"the pools hold {slots} slots per page, page_size is {page_size}")
+    B = seq_lens.shape[0]
+    _expect(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D")
+    _expect(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev,
+            contiguous=False)
+    if block_table.stride(1) != 1 or (B > 1 and block_table.stride(0) < block_table.shape[1]):
+        raise ValueError("block_table rows must be contiguous and distinct")
+    if err_flags is not None:
+        if err_flags.dtype not in (torch.int32, torch.uint32) or err_flags.numel() < 1:
+            raise ValueError("err_flags must be a 32-bit integer tensor")
+        if err_flags.device != dev:
+            raise ValueError(f"err_flags is on {err_flags.device}, the pools on {dev}")
+    return B, Hkv
+
+
+def _token_rows(t, name, B, Hkv, device):
+    """fp32 [B, Hkv, tokens] with contiguous token rows that do not overlap."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B, Hkv, tokens]")
+    _expect(t, name, torch.float32, (B, Hkv, t.shape[2]), device, contiguous=False)
+    if t.shape[2] < 1 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} needs contiguous rows of at least one token")
+
+
+def _table_stride(block_table):
+    """A row's reach: the stride, or the width where a row is all there is."""
+    return block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+
+
+def _on(stream):
+    """The stream a call goes to, and the context its scratch is allocated in:
+    memory from torch's allocator is reused in the order of that stream."""
+    cur = torch.cuda.current_stream()
+    if stream is None or stream == cur:
+        return cur, contextlib.nullcontext()
+    return stream, torch.cuda.stream(stream)
+
+
+def make_score_params(q, Hkv, *, softcap=0.0, alibi_slopes=None, window=0, tree_mask=None,
+                      weights=None, weights_decay=1.0) -> ScoreParams:
+    """The score modifications of one decode_attn call (see there)."""
+    B, q_len, Hq, _ = q.shape
+    _expect(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), q.device)
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.int32, torch.uint32):
+            raise ValueError("tree_mask must be 32-bit words")
+        _expect(tree_mask, "tree_mask", tree_mask.dtype, (B, q_len, (q_len + 31) // 32), q.device)
+    m = ScoreParams()
+    m.struct_size = ctypes.sizeof(ScoreParams)
+    m.softcap, m.window = float(softcap), int(window)
+    m.alibi_slopes, m.tree_mask = _ptr(alibi_slopes), _ptr(tree_mask)
+    m.weights_decay = float(weights_decay)
+    if weights is not None:
+        _token_rows(weights, "weights", B, Hkv, q.device)
+        m.weights = weights.data_ptr()
+        m.weights_seq_stride, m.weights_head_stride = weights.stride(0), weights.stride(1)
+        m.weights_tokens = weights.shape[2]
+    m.tensors = (alibi_slopes, tree_mask, weights)
+    return m
+
+
+def _run_ex(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, Hkv, out, lse,
+            workspace, err_flags, num_ctas, max_seq_len, layout, stream, events, k_new, v_new,
+            mods):
+    """decode_attn with modified scores (zl_decode_attn_ex)."""
+    if q.dim() != 4 or v_pool is None:
+        raise ValueError("q must be [B, q_len, Hq, D], with K and V pools")
+    _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    B, q_len, Hq, D = q.shape
+    dev = k_pool.device
+    _expect(q, "q", torch.bfloat16, (seq_lens.shape[0], q_len, Hq, k_pool.shape[3]), dev)
+    _expect(out, "out", torch.bfloat16, (B, q_len, Hq, D), dev)
+    _expect(lse, "lse", torch.float32, (B, q_len, Hq), dev)
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _expect(t, name, torch.bfloat16, (B, q_len, Hkv, D), dev)
+    m = make_score_params(q, Hkv, **mods)
+    on, scratch = _on(stream)
+    with scratch:
+        if out is None:
+            out = torch.empty((B, q_len, Hq, D), dtype=torch.bfloat16, device=dev)
+        p = make_params(q, k_pool, v_pool, block_table, seq_lens, out, page_size=page_size,
+                        scale=scale, Hkv=Hkv, D_v=D, lse=lse, err_flags=err_flags,
+                        num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout, events=events,
+                        k_new=k_new, v_new=v_new)
+        p.block_table_stride = _table_stride(block_table)
+        if workspace is None:
+            # a call's own: stream order alone separates it from other calls,
+            # and a captured graph keeps it
+            workspace = torch.empty(max(workspace_size_ex(p, m), 256), dtype=torch.uint8,
+                                    device=dev)
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.numel() * workspace.element_size()
+        call_ex(p, m, on)
+    return out
+
+
 def _run(q, k_pool, v_pool, block_table, seq_lens, *, mla, page_size, scale, Hkv, D_v, out, lse,
          workspace, err_flags, num_ctas, max_seq_len, layout, stream, events, single_launch=False,
          shared_prefix_pages=0, k_new=None, v_new=None):
@@ -299,7 +540,8 @@ def _run(q, k_pool, v_pool, block_table, seq_lens, *, mla, page_size, scale, Hkv
 def decode_attn(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, out=None, lse=None,
                 workspace=None, err_flags=None, num_ctas=0, max_seq_len=0, layout="NHD",
                 stream=None, events=None, single_launch=False, shared_prefix_pages=0,
-                k_new=None, v_new=None):
+                k_new=None, v_new=None, softcap=0.0, alibi_slopes=None, window=0, tree_mask=None,
+                weights=None, weights_decay=1.0):
     """GQA/MHA/MQA paged decode attention (zl_decode_attn).
 
     q [B, q_len, Hq, 128] bf16; k_pool, v_pool [pages, page_size, Hkv, 128]
@@ -313,8 +555,28 @@ def decode_attn(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, o
     k_new, v_new: the q_len new tokens' K and V rows [B, q_len, Hkv, 128] bf16;
     the call stores them in their page slots (as kv_append does) and then
     attends, in the same launch.
+
+    Modified scores (zl_decode_attn_ex; not with single_launch or
+    shared_prefix_pages), for query position pos and token position t:
+    softcap: s -> softcap * tanh(s / softcap). alibi_slopes [Hq] fp32: s ->
+    s - slope * (pos - t). window: tokens with pos - t < window are seen.
+    tree_mask int32 [B, q_len, ceil(q_len / 32)]: the q_len query tokens are a
+    drafted tree, bit j of row i set where token i sees drafted token j (see
+    tree_mask()). weights fp32 [B, Hkv, tokens]: each cached token's softmax
+    weight, summed over the query tokens and the heads of its kv head, is added
+    to weights_decay times what it holds.
     """
     Hkv = k_pool.shape[2] if layout == "NHD" else k_pool.shape[1]
+    if softcap or window or any(t is not None for t in (alibi_slopes, tree_mask, weights)):
+        if single_launch or shared_prefix_pages:
+            raise ZlError(ERR_UNSUPPORTED, "modified scores with single_launch or a shared prefix")
+        return _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size=page_size, scale=scale,
+                       Hkv=Hkv, out=out, lse=lse, workspace=workspace, err_flags=err_flags,
+                       num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout, stream=stream,
+                       events=events, k_new=k_new, v_new=v_new,
+                       mods=dict(softcap=softcap, alibi_slopes=alibi_slopes, window=window,
+                                 tree_mask=tree_mask, weights=weights,
+                                 weights_decay=weights_decay))
     return _run(q, k_pool, v_pool, block_table, seq_lens, mla=False, page_size=page_size,
                 scale=scale, Hkv=Hkv, D_v=q.shape[3], out=out, lse=lse, workspace=workspace,
                 err_flags=err_flags, num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout,
@@ -381,3 +643,131 @@ def kv_append(k_new, v_new, k_pool, v_pool, block_table, seq_lens, *, page_size,
         stream = torch.cuda.current_stream()
     _check(lib().zl_kv_append(ctypes.byref(p), ctypes.c_void_p(stream.cuda_stream)),
            "zl_kv_append")
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """The ancestor bits decode_attn's tree_mask takes, from drafted trees.
+
+    parents: int [B, q_len] on the host (list, array or CPU tensor): the index
+    of each drafted token's parent, smaller than its own, or -1 for a child of
+    the context's last token. Host-side planning, as for a block table; returns
+    int32 [B, q_len, ceil(q_len / 32)] on the CPU.
+    """
+    par = torch.as_tensor(parents)
+    if par.dim() != 2 or par.is_floating_point() or par.is_cuda:
+        raise ValueError("parents must be int [B, q_len] on the host")
+    par = par.to(torch.int64)
+    B, q_len = par.shape
+    if ((par < -1) | (par >= torch.arange(q_len))).any():
+        raise ValueError("a parent's index is -1 or smaller than its child's")
+    words = torch.zeros(B, q_len, (q_len + 31) // 32, dtype=torch.int64)
+    rows = torch.arange(B)
+    for i in range(q_len):
+        p = par[:, i]
+        words[:, i] = torch.where(p[:, None] >= 0, words[rows, p.clamp(min=0)], 0)
+        words[:, i, i // 32] |= 1 << (i % 32)
+    return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+
+
+def _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, *, page_size, layout,
+                 err_flags):
+    # (new_lens and other outputs left out are allocated once the checks have passed)
+    """The fields zl_kv_evict_params and zl_kv_commit_params share."""
+    B, Hkv = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags,
+                           same_width=False)
+    _expect(new_lens, "new_lens", torch.int32, (B,), k_pool.device)
+    ps, ts, hs = _pool_strides(k_pool, layout)
+    if v_pool is not None and _pool_strides(v_pool, layout) != (ps, ts, hs):
+        raise ValueError("K and V pools must share strides")
+    if k_pool.stride(3) != 1:
+        raise ValueError("pool rows must be contiguous")
+    p.struct_size = ctypes.sizeof(type(p))
+    p.k_pool, p.v_pool = _ptr(k_pool), _ptr(v_pool)
+    p.page_stride, p.token_stride, p.head_stride = ps, ts, hs
+    p.block_table, p.block_table_stride = _ptr(block_table), _table_stride(block_table)
+    p.seq_lens = _ptr(seq_lens)
+    p.B, p.Hkv, p.D_k = B, Hkv, k_pool.shape[3]
+    p.D_v = 0 if v_pool is None else v_pool.shape[3]
+    p.page_size, p.num_pages = page_size, k_pool.shape[0]
+    p.err_flags = _ptr(err_flags)
+    return B, Hkv
+
+
+def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budget, sink=0,
+             recent=0, new_lens=None, kept=None, weights_out=None, dst_block_table=None,
+             layout="NHD", err_flags=None, stream=None):
+    """Hold every (sequence, kv head) to ``budget`` cached tokens (zl_kv_evict).
+
+    weights [B, Hkv, tokens] fp32, as decode_attn accumulates them: a sequence
+    of more than budget tokens keeps its first ``sink``, its last ``recent``
+    and the ones between with the largest weights, in order; their K, V and
+    weights move to the front. In place, or to the pages of dst_block_table
+    (weights to weights_out when given). v_pool None: a latent-only pool.
+    Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]: the kept
+    positions, then -1).
+    """
+    if weights is None or seq_lens.dim() != 1:
+        raise ValueError("weights is required, and seq_lens is 1-D")
+    p = EvictParams()
+    B, Hkv = _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, page_size=page_size,
+                          layout=layout, err_flags=err_flags)
+    _token_rows(weights, "weights", B, Hkv, k_pool.device)
+    _expect(kept, "kept", torch.int32, (B, Hkv, budget), k_pool.device)
+    p.weights, p.weights_tokens = weights.data_ptr(), weights.shape[2]
+    p.weights_seq_stride, p.weights_head_stride = weights.stride(0), weights.stride(1)
+    if weights_out is not None:
+        _token_rows(weights_out, "weights_out", B, Hkv, k_pool.device)
+        if weights_out.shape[2] < min(budget, weights.shape[2]):
+            raise ValueError("weights_out is shorter than what the budget may leave")
+        p.weights_out = weights_out.data_ptr()
+        p.weights_out_seq_stride = weights_out.stride(0)
+        p.weights_out_head_stride = weights_out.stride(1)
+    if dst_block_table is not None:
+        _expect(dst_block_table, "dst_block_table", torch.int32, (B, dst_block_table.shape[1]),
+                k_pool.device, contiguous=False)
+        if dst_block_table.stride(1) != 1:
+            raise ValueError("block_table rows must be contiguous")
+        p.dst_block_table = dst_block_table.data_ptr()
+        p.dst_block_table_stride = _table_stride(dst_block_table)
+    p.budget, p.sink, p.recent = int(budget), int(sink), int(recent)
+    on, scratch = _on(stream)
+    with scratch:
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=k_pool.device)
+        if kept is None:
+            kept = torch.empty(B, Hkv, max(int(budget), 1), dtype=torch.int32,
+                               device=k_pool.device)
+    p.new_lens, p.kept = new_lens.data_ptr(), kept.data_ptr()
+    _check(lib().zl_kv_evict(ctypes.byref(p), ctypes.c_void_p(on.cuda_stream)), "zl_kv_evict")
+    return new_lens, kept
+
+
+def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_size, q_len,
+              new_lens=None, layout="NHD", err_flags=None, stream=None):
+    """Move the accepted path of a drafted tree behind the context (zl_kv_commit).
+
+    The last q_len of each sequence's seq_lens[b] tokens are the drafted tree;
+    its tokens path[b, :accepted[b]] (path int32 [B, n], accepted int32 [B])
+    become the tokens after the context, in place. v_pool None: a latent-only
+    pool. Returns new_lens int32 [B] (context plus accepted).
+    """
+    if seq_lens.dim() != 1 or path.dim() != 2:
+        raise ValueError("seq_lens is 1-D and path 2-D")
+    p = CommitParams()
+    B, _ = _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, page_size=page_size,
+                        layout=layout, err_flags=err_flags)
+    _expect(path, "path", torch.int32, (B, path.shape[1]), k_pool.device, contiguous=False)
+    _expect(accepted, "accepted", torch.int32, (B,), k_pool.device)
+    if path.shape[1] > 1 and path.stride(1) != 1:
+        raise ValueError("path rows must be contiguous")
+    p.path, p.path_len = path.data_ptr(), path.shape[1]
+    p.path_stride = path.stride(0) if B > 1 else path.shape[1]
+    p.accepted = accepted.data_ptr()
+    p.q_len = int(q_len)
+    on, scratch = _on(stream)
+    with scratch:
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=k_pool.device)
+    p.new_lens = new_lens.data_ptr()
+    _check(lib().zl_kv_commit(ctypes.byref(p), ctypes.c_void_p(on.cuda_stream)), "zl_kv_commit")
+    return new_lens

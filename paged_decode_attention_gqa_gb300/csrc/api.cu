@@ -91,6 +91,9 @@ struct GqaPlan {
   bool unit_cut = false;  // one CTA per (sequence, head group): no cut unit, no merge
   size_t off_lse = 0, off_o = 0, off_pre_lse = 0, off_pre_o = 0;
   size_t off_suf_lse = 0, off_suf_o = 0, bytes = 0;
+  // modified scores with weights: each row's base and 1 / sum, then its scores
+  size_t off_stat = 0, off_scores = 0;
+  int64_t score_stride = 0;
 };
 
 // Query tokens per sequence one call takes, and query heads per kv head (the
@@ -130,9 +133,32 @@ zl_status gqa_validate_shape(const zl_decode_attn_params* a) {
   return ZL_OK;
 }
 
-zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan) {
+// Score modifications (zl_decode_attn_ex): what does not depend on the call's pointers.
+zl_status mods_validate(const zl_decode_attn_params* a, const zl_score_params* m) {
+  if (!m || m->struct_size != sizeof(zl_score_params)) return ZL_ERR_INVALID_ARG;
+  if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap) || m->window < 0)
+    return ZL_ERR_INVALID_ARG;
+  // scale / c and c * log2(e) must be normal numbers
+  if (m->softcap > 0.f && (m->softcap < 1e-6f || m->softcap > 1e6f)) return ZL_ERR_UNSUPPORTED;
+  if (!aligned(m->alibi_slopes, 4) || !aligned(m->tree_mask, 4) || !aligned(m->weights, 4))
+    return ZL_ERR_INVALID_ARG;
+  if (m->weights) {
+    if (m->weights_tokens < 1 || !std::isfinite(m->weights_decay) || m->weights_decay < 0.f)
+      return ZL_ERR_INVALID_ARG;
+    // rows of different sequences and heads must not overlap
+    if ((a->B > 1 && m->weights_seq_stride < m->weights_tokens) ||
+        (a->Hkv > 1 && m->weights_head_stride < m->weights_tokens))
+      return ZL_ERR_INVALID_ARG;
+  }
+  if (a->flags || a->shared_prefix_pages != 0) return ZL_ERR_UNSUPPORTED;
+  return ZL_OK;
+}
+
+zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
+                   const zl_score_params* mods = nullptr) {
   zl_status st = gqa_validate_shape(a);
   if (st != ZL_OK) return st;
+  if (mods && (st = mods_validate(a, mods)) != ZL_OK) return st;
   DeviceInfo dev;
   if ((st = current_device(&dev)) != ZL_OK) return st;
   plan->g = a->Hq / a->Hkv;
@@ -171,7 +197,8 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan) {
     // sequences) plus the total; the launch takes the same layout
     const bool small = (plan->prefix_tiles > 0 ? plan->ng : 0) + a->B + 1 <= zl::kSmallTable;
     const int per_sm =
-        plan->prefix_tiles > 0
+        mods ? zl::gqa_mod_ctas_per_sm(plan->hpc, rps > 8, plan->tg, small, dev.device)
+        : plan->prefix_tiles > 0
             ? zl::gqa_shared_ctas_per_sm(plan->hpc, rows_per_warp > 8, a->q_len > 1, small,
                                          dev.device)
             : zl::gqa_ctas_per_sm(plan->hpc, rps > 8, a->q_len > 1, plan->fused, plan->tg, small,
@@ -179,7 +206,12 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan) {
     if (per_sm < 1) return ZL_ERR_CUDA;
     grid = dev.sms * per_sm;
     if (a->max_seq_len > 0 && plan->prefix_tiles == 0) {
-      const int64_t max_tiles = (int64_t(a->max_seq_len) + zl::kGqaTile - 1) / zl::kGqaTile;
+      // a window bounds what a sequence reads: the tiles from its oldest
+      // token on (which may start inside a tile)
+      int64_t max_len = a->max_seq_len;
+      if (mods && mods->window > 0)
+        max_len = std::min(max_len, int64_t(mods->window) + a->q_len + zl::kGqaTile);
+      const int64_t max_tiles = (max_len + zl::kGqaTile - 1) / zl::kGqaTile;
       const int64_t units = int64_t(a->B) * plan->nhg;
       if (units <= grid && max_tiles <= zl::kGqaUnitCutTiles) {
         // Short contexts: one CTA per whole unit. Streaming the longest unit
@@ -210,6 +242,13 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan) {
       plan->off_pre_o + round_up(store_rows * zl::kGqaHeadDim * sizeof(float), 256);
   plan->off_suf_o = plan->off_suf_lse + round_up(store_rows * sizeof(float), 256);
   plan->bytes = plan->off_suf_o + store_rows * zl::kGqaHeadDim * sizeof(float);
+  if (mods && mods->weights) {
+    const size_t qrows = size_t(a->B) * a->q_len * a->Hq;
+    plan->score_stride = int64_t(round_up(size_t(mods->weights_tokens), zl::kGqaTile));
+    plan->off_stat = round_up(plan->bytes, 256);
+    plan->off_scores = plan->off_stat + round_up(qrows * sizeof(float2), 256);
+    plan->bytes = plan->off_scores + qrows * size_t(plan->score_stride) * sizeof(float);
+  }
   return ZL_OK;
 }
 
@@ -340,44 +379,69 @@ zl_status validate_pointers(const zl_decode_attn_params* a, bool need_v) {
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-const char* zl_status_string(zl_status s) {
-  switch (s) {
-    case ZL_OK: return "ok";
-    case ZL_ERR_INVALID_ARG: return "invalid argument";
-    case ZL_ERR_UNSUPPORTED: return "unsupported shape or layout";
-    case ZL_ERR_WORKSPACE: return "workspace missing or too small";
-    case ZL_ERR_CUDA: return "CUDA error";
+// The modified-score launches: every row group in one attention launch, its
+// merge, and the weights kernel when the call accumulates weights.
+zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, const GqaPlan& plan,
+                   GqaParams& p, char* ws, cudaStream_t s) {
+  if (m.softcap > 0.f) {
+    p.cap_in = float(double(a->scale) / m.softcap);
+    p.cap_out = float(double(m.softcap) * kLog2e);
   }
-  return "unknown status";
+  p.slopes = m.alibi_slopes;
+  p.window = m.window;
+  p.tree = m.tree_mask;
+  p.tree_words = (a->q_len + 31) / 32;
+  p.len_cap = a->block_table_stride * int64_t(a->page_size);
+  if (m.weights) {
+    p.len_cap = std::min(p.len_cap, int64_t(m.weights_tokens));
+    p.row_stat = reinterpret_cast<float2*>(ws + plan.off_stat);
+    p.scores = reinterpret_cast<float*>(ws + plan.off_scores);
+    p.score_stride = plan.score_stride;
+  }
+  // one row group, two that share every CTA, or more side by side (see gqa_run)
+  p.q_tok0 = 0;
+  p.q_len = plan.q_group;
+  p.ngroups = plan.ngroups;
+  p.tg = plan.tg;
+  p.group_ctas = plan.unit_cut || plan.tg == 2 ? plan.grid : std::max(1, plan.grid / plan.ngroups);
+  const int grid = plan.tg == 2 ? plan.grid : p.group_ctas * plan.ngroups;
+  cudaError_t e = zl::gqa_mod_launch(p, grid, s, reinterpret_cast<cudaEvent_t>(a->attn_begin),
+                                     reinterpret_cast<cudaEvent_t>(a->attn_end));
+  if (e == cudaSuccess && m.weights) {
+    zl::WeightsParams w;
+    std::memset(&w, 0, sizeof(w));
+    w.scores = p.scores;
+    w.score_stride = p.score_stride;
+    w.row_stat = p.row_stat;
+    w.seq_lens = a->seq_lens;
+    w.weights = m.weights;
+    w.seq_stride = m.weights_seq_stride;
+    w.head_stride = m.weights_head_stride;
+    w.decay = m.weights_decay;
+    w.B = a->B;
+    w.q_total = a->q_len;
+    w.Hq = a->Hq;
+    w.Hkv = a->Hkv;
+    w.g = plan.g;
+    w.window = m.window;
+    w.len_cap = p.len_cap;
+    w.max_tokens = m.weights_tokens;
+    e = zl::weights_launch(w, s);
+  }
+  return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
-zl_status zl_decode_attn_workspace_size(const zl_decode_attn_params* a, size_t* bytes) {
-  if (!bytes) return ZL_ERR_INVALID_ARG;
-  GqaPlan plan;
-  const zl_status st = gqa_plan(a, &plan);
-  if (st != ZL_OK) return st;
-  *bytes = plan.bytes;
-  return ZL_OK;
-}
-
-zl_status zl_decode_attn_launches(const zl_decode_attn_params* a, int32_t* launches) {
-  if (!launches) return ZL_ERR_INVALID_ARG;
-  GqaPlan plan;
-  const zl_status st = gqa_plan(a, &plan);
-  if (st != ZL_OK) return st;
-  const int per_launch = (plan.fused || plan.unit_cut) ? 1 : 2;
-  *launches = groups_together(plan) ? per_launch : plan.ngroups * per_launch;
-  return ZL_OK;
-}
-
-zl_status zl_decode_attn(const zl_decode_attn_params* a, zl_stream_t stream) {
+// zl_decode_attn (mods = nullptr) and zl_decode_attn_ex.
+zl_status gqa_run(const zl_decode_attn_params* a, const zl_score_params* mods,
+                  zl_stream_t stream) {
   zl_status st = gqa_validate_shape(a);
   if (st != ZL_OK) return st;
+  if (mods && (st = mods_validate(a, mods)) != ZL_OK) return st;
   if ((st = validate_pointers(a, true)) != ZL_OK) return st;
   GqaPlan plan;
-  if ((st = gqa_plan(a, &plan)) != ZL_OK) return st;
+  if ((st = gqa_plan(a, &plan, mods)) != ZL_OK) return st;
   if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < plan.bytes)
     return ZL_ERR_WORKSPACE;
 
@@ -431,6 +495,7 @@ zl_status zl_decode_attn(const zl_decode_attn_params* a, zl_stream_t stream) {
   }
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (mods) return mods_run(a, *mods, plan, p, ws, s);
   const int ngroups = plan.ngroups;
   if (groups_together(plan)) {
     // Every row group (q_group query tokens, gh heads of each kv head) in one
@@ -477,6 +542,60 @@ zl_status zl_decode_attn(const zl_decode_attn_params* a, zl_stream_t stream) {
     if (e != cudaSuccess) return ZL_ERR_CUDA;
   }
   return ZL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* zl_status_string(zl_status s) {
+  switch (s) {
+    case ZL_OK: return "ok";
+    case ZL_ERR_INVALID_ARG: return "invalid argument";
+    case ZL_ERR_UNSUPPORTED: return "unsupported shape or layout";
+    case ZL_ERR_WORKSPACE: return "workspace missing or too small";
+    case ZL_ERR_CUDA: return "CUDA error";
+  }
+  return "unknown status";
+}
+
+zl_status zl_decode_attn_workspace_size(const zl_decode_attn_params* a, size_t* bytes) {
+  if (!bytes) return ZL_ERR_INVALID_ARG;
+  GqaPlan plan;
+  const zl_status st = gqa_plan(a, &plan);
+  if (st != ZL_OK) return st;
+  *bytes = plan.bytes;
+  return ZL_OK;
+}
+
+zl_status zl_decode_attn_launches(const zl_decode_attn_params* a, int32_t* launches) {
+  if (!launches) return ZL_ERR_INVALID_ARG;
+  GqaPlan plan;
+  const zl_status st = gqa_plan(a, &plan);
+  if (st != ZL_OK) return st;
+  const int per_launch = (plan.fused || plan.unit_cut) ? 1 : 2;
+  *launches = groups_together(plan) ? per_launch : plan.ngroups * per_launch;
+  return ZL_OK;
+}
+
+zl_status zl_decode_attn(const zl_decode_attn_params* a, zl_stream_t stream) {
+  return gqa_run(a, nullptr, stream);
+}
+
+zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* a,
+                                           const zl_score_params* mods, size_t* bytes) {
+  if (!bytes || !mods) return ZL_ERR_INVALID_ARG;
+  GqaPlan plan;
+  const zl_status st = gqa_plan(a, &plan, mods);
+  if (st != ZL_OK) return st;
+  *bytes = plan.bytes;
+  return ZL_OK;
+}
+
+zl_status zl_decode_attn_ex(const zl_decode_attn_params* a, const zl_score_params* mods,
+                            zl_stream_t stream) {
+  if (!mods) return ZL_ERR_INVALID_ARG;
+  return gqa_run(a, mods, stream);
 }
 
 zl_status zl_decode_attn_mla_workspace_size(const zl_decode_attn_params* a, size_t* bytes) {

@@ -33,6 +33,7 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "score_mods.cuh"
 
 #include <math_constants.h>
 
@@ -53,6 +54,10 @@ constexpr int kModePlain = 0;   // every sequence over all of its own pages
 // the prefix, on one tile line; whole units leave fp32 results in the prefix
 // and suffix stores, and the merge kernel combines both parts of every row.
 constexpr int kModeShared = 1;
+// Modified scores: plain units with a tanh cap, a distance bias, a window, an
+// ancestor mask over the drafted tokens, and optionally the scores stored for
+// the weights kernel (see gqa_mod.cu).
+constexpr int kModeMod = 2;
 constexpr uint64_t kTestStallNs = 50ull * 1000 * 1000;  // bound of the test-hook wait
 // A row's softmax base moves only when a tile's scores exceed it by more than
 // this (base 2): P stays at most 2^8 in between.
@@ -303,7 +308,7 @@ __device__ __forceinline__ void merge_add_store(MergeAcc<NR>& m, const GqaParams
 // Writes the merged rows of sequence b (row r: token tok0 + r / gh, head
 // head0 + r % gh) as bf16 out and natural-log lse; a bad source or a row with
 // no weight gives zeros and lse = -inf.
-template <int NR>
+template <int MODE, int NR>
 __device__ __forceinline__ void merge_write_out(const MergeAcc<NR>& m, const GqaParams& p, int b,
                                                 int tok0, int head0, int gh, int r0, int nrows,
                                                 int lane) {
@@ -323,6 +328,8 @@ __device__ __forceinline__ void merge_write_out(const MergeAcc<NR>& m, const Gqa
       if (p.lse && lane == 0)
         p.lse[orow] = none ? -CUDART_INF_F
                            : __fmul_rn(__fadd_rn(m.mx[k], log2f(m.den[k])), 0.69314718055994531f);
+      if (MODE == kModeMod && p.scores && lane == 0)
+        p.row_stat[orow] = none ? make_float2(0.f, 0.f) : make_float2(m.mx[k], inv);
     }
   }
 }
@@ -330,7 +337,7 @@ __device__ __forceinline__ void merge_write_out(const MergeAcc<NR>& m, const Gqa
 // A plain unit (sequence b, kv head w of the CTA group, first tile U0) cut
 // between CTAs c_lo..c_hi: merge rows [r_begin, r_end), NR at a time, and
 // write them.
-template <int NR, int P>
+template <int MODE, int NR, int P>
 __device__ __forceinline__ void merge_split_rows(const GqaParams& p, const TileCut& cut, int cta0,
                                                  int64_t U0, int c_lo, int c_hi, int b, int tok0,
                                                  int w, int head0, int gh, int R, int r_begin,
@@ -340,8 +347,21 @@ __device__ __forceinline__ void merge_split_rows(const GqaParams& p, const TileC
     MergeAcc<NR> m;
     m.init();
     merge_add_pieces<NR, P>(m, p, cut, cta0, U0, c_lo, c_hi, w, R, 0, r0, nrows, lane);
-    merge_write_out(m, p, b, tok0, head0, gh, r0, nrows, lane);
+    merge_write_out<MODE>(m, p, b, tok0, head0, gh, r0, nrows, lane);
   }
+}
+
+// Longest valid length of a sequence, and (modified scores) the first tile any
+// query token of a sequence of L tokens sees: the oldest query position is L -
+// q_total.
+template <int MODE>
+__device__ __forceinline__ int64_t length_cap(const GqaParams& p) {
+  return MODE == kModeMod ? p.len_cap : p.bt_stride * int64_t(p.page_size);
+}
+template <int MODE>
+__device__ __forceinline__ int first_tile(const GqaParams& p, int L) {
+  if (MODE != kModeMod || p.window == 0) return 0;
+  return max(L - p.q_total - p.window + 1, 0) / kGqaTile;
 }
 
 // Tiles of sequence b's own unit for this launch (seq_lens[b] = L): they end
@@ -350,10 +370,11 @@ __device__ __forceinline__ void merge_split_rows(const GqaParams& p, const TileC
 // invalid length (negative, or more tokens than the block table maps) has none.
 template <int MODE>
 __device__ __forceinline__ int seq_unit_tiles(const GqaParams& p, int L) {
-  const int64_t cap = p.bt_stride * int64_t(p.page_size);
-  if (!(L >= 0 && int64_t(L) <= cap)) return 0;
-  const int unseen = p.ngroups > 1 ? 0 : p.q_total - p.q_tok0 - p.q_len;
-  const int t = (L - unseen + kGqaTile - 1) / kGqaTile - (MODE == kModeShared ? p.prefix_tiles : 0);
+  if (!(L >= 0 && int64_t(L) <= length_cap<MODE>(p))) return 0;
+  // (a modified-score launch always covers every query token)
+  const int unseen = MODE == kModeMod || p.ngroups > 1 ? 0 : p.q_total - p.q_tok0 - p.q_len;
+  const int t = (L - unseen + kGqaTile - 1) / kGqaTile - first_tile<MODE>(p, L) -
+                (MODE == kModeShared ? p.prefix_tiles : 0);
   return t > 0 ? t : 0;
 }
 
@@ -410,12 +431,76 @@ __device__ __forceinline__ void append_tile_rows(const GqaParams& p, int b, int 
   fence_proxy_async_global();
 }
 
+// A query row under modified scores: its position, the oldest position its
+// window reaches, its head's bias slope in base 2 and its ancestor bits.
+struct ModRow {
+  int ctx;             // cached tokens before the query tokens (may be negative)
+  int pos, lo;
+  float slope2;
+  const uint32_t* bits;  // of the row's query token, or nullptr
+  const uint32_t* seq_bits;  // of the sequence's query token 0
+  bool live;
+  __device__ __forceinline__ void init(const GqaParams& p, int b, int L, int tok0, int head0,
+                                       int gh, int r, bool exists) {
+    live = exists;
+    ctx = L - p.q_total;
+    const int i = exists ? tok0 + r / gh : 0;
+    pos = ctx + i;
+    bits = seq_bits = nullptr;
+    if (p.tree) {
+      seq_bits = p.tree + int64_t(b) * p.q_total * p.tree_words;
+      bits = seq_bits + int64_t(i) * p.tree_words;
+      pos = ctx + tree_depth(bits, p.tree_words);
+    }
+    lo = p.window ? pos - p.window + 1 : -(1 << 30);
+    slope2 = p.slopes && exists ? __ldg(p.slopes + head0 + r % gh) * 1.4426950408889634f : 0.f;
+  }
+};
+
+// One row's scores over this thread's four tokens of a tile (2 t4, 2 t4 + 1, 2
+// t4 + 8, 2 t4 + 9): dot products -> base-2 scores, -inf where the row does
+// not see the token; mx = the row's max over the whole tile. Returns whether
+// the row sees any of the four.
+__device__ __forceinline__ bool mod_row_scores(const GqaParams& p, const ModRow& row,
+                                               const float (&dot)[4], int tok0, int L, int t4,
+                                               float (&x)[4], float& mx) {
+  const bool drafted = row.bits != nullptr && tok0 + kGqaTile > row.ctx;
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = tok0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+    int dist = row.pos - t;  // in positions
+    bool vis = dist >= 0 && t >= row.lo && t < L;
+    if (drafted) {
+      const int j = t - row.ctx;
+      if (j >= 0 && t < L) {
+        vis = (__ldg(row.bits + (j >> 5)) >> (j & 31)) & 1u;
+        if (vis && (p.window || p.slopes)) {
+          dist = row.pos - row.ctx - tree_depth(row.seq_bits + int64_t(j) * p.tree_words,
+                                                p.tree_words);
+          vis = !p.window || dist < p.window;
+        }
+      }
+    }
+    vis = vis && row.live;
+    any |= vis;
+    float v = p.cap_in > 0.f ? cap_tanh(dot[k] * p.cap_in) * p.cap_out : dot[k] * p.scale_log2;
+    v = fmaf(-row.slope2, float(dist), v);
+    x[k] = vis ? v : -CUDART_INF_F;
+  }
+  mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  return any;
+}
+
 template <int HPC, bool ROWS16, bool CAUSAL, bool FUSED, int MODE = kModePlain, int TG = 1>
 __global__ void __launch_bounds__(GqaCfg<HPC, TG>::kThreads, GqaCfg<HPC, TG>::kMinBlocks)
 gqa_decode_kernel(const __grid_constant__ GqaParams p) {
   static_assert(MODE == kModePlain || !FUSED, "the in-kernel merge is for plain launches");
-  static_assert(TG == 1 || (MODE == kModePlain && !FUSED && CAUSAL),
-                "two row groups per CTA: plain launches, causal instances, merge launch");
+  static_assert(TG == 1 || (MODE != kModeShared && !FUSED && CAUSAL),
+                "two row groups per CTA: own pages, causal instances, merge launch");
+  static_assert(MODE != kModeMod || CAUSAL, "modified scores mask every row on its own");
   using Cfg = GqaCfg<HPC, TG>;
   constexpr int NS = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -432,7 +517,7 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.B;
-  const int64_t cap = p.bt_stride * int64_t(p.page_size);
+  const int64_t cap = length_cap<MODE>(p);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -537,7 +622,7 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
   int64_t s_c = c < int(cut.G) ? cut.start(c) : W;
   int64_t e_c = c < int(cut.G) ? cut.start(c + 1) : W;
   const bool unit_cut =
-      MODE == kModePlain &&
+      MODE != kModeShared &&
       (p.unit_cut || (p.auto_cut && short_units(int64_t(V) * nhg, unit_max[0], G)));
   if (unit_cut) {
     // Unit (v, hg) holds tiles [nhg * prefix[v] + hg * n, + n) of the line.
@@ -580,8 +665,10 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
         const int64_t r = idx - int64_t(nhg) * prefix[v];
         hg = int(r / n);
         const bool pre = v < NG;  // a prefix unit
-        const int tok0 = (MODE == kModeShared && !pre ? PT * kGqaTile : 0) + int(r % n) * kGqaTile;
         const int trow = pre ? v * p.sgs : v - NG;  // a block-table row to read
+        const int tile0 = MODE == kModeMod ? first_tile<MODE>(p, p.seq_lens[trow])
+                          : MODE == kModeShared && !pre ? PT : 0;
+        const int tok0 = (tile0 + int(r % n)) * kGqaTile;
         slot = tok0 % p.page_size;
         page = p.block_table[int64_t(trow) * p.bt_stride + tok0 / p.page_size];
         bad = (page < 0 || page >= p.num_pages) ? 1 : 0;
@@ -678,6 +765,8 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
     const int b = pre ? v * p.sgs : v - NG;
     // Tokens the unit's tiles cover end at L (a prefix unit: the whole prefix).
     const int L = pre ? PT * kGqaTile : p.seq_lens[b];
+    const int unit_tile0 = MODE == kModeMod ? first_tile<MODE>(p, L)
+                           : MODE == kModeShared && !pre ? PT : 0;
     const int head0 = (hg * HPC + w) * g + rg.hoff;  // the group's first query head
     // m16 tile rows are (sequence b + r / rps, query token i, head head0 + j)
     // with rps = gh * qlen rows per sequence, r % rps = i * gh + j; R rows per
@@ -718,6 +807,12 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
     float o[16][4];
 #pragma unroll
     for (int nt = 0; nt < 16; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+    // Modified scores: what masks and biases this thread's two rows.
+    ModRow mod_a, mod_b;
+    if constexpr (MODE == kModeMod) {
+      mod_a.init(p, b, L, tok0, head0, gh, ra, ra < R_act);
+      mod_b.init(p, b, L, tok0, head0, gh, rb, ROWS16 && rb < R_act);
+    }
     // Rows (a, b) of this thread whose visible tokens reach a tile over a bad
     // page: those rows, and only those, are written as zeros.
     bool bad_a = false, bad_b = false;
@@ -757,12 +852,23 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
       const float2 f0 = unpack_bf16x2(p_lo), f2 = unpack_bf16x2(p_hi);
       l += (f0.x + f0.y) + (f2.x + f2.y);
     };
+    // The same with the sum taken before the rounding: lse and the weights are
+    // 32-bit outputs of the modified path, and a sum of rounded P would leave
+    // an error of up to 2^-9 in them. (P itself is rounded for the tensor core.)
+    auto row_p_exact = [&](const float (&x)[4], float m, float& l, uint32_t& p_lo, uint32_t& p_hi) {
+      const float base = m == -CUDART_INF_F ? 0.f : m;
+      const float e0 = ex2_approx(x[0] - base), e1 = ex2_approx(x[1] - base);
+      const float e2 = ex2_approx(x[2] - base), e3 = ex2_approx(x[3] - base);
+      p_lo = pack_bf16x2(e0, e1);
+      p_hi = pack_bf16x2(e2, e3);
+      l += (e0 + e1) + (e2 + e3);
+    };
 
     for (int t = 0; t < ntiles; ++t, ++it) {
       const int stage = it % NS;
       const uint32_t phase = (it / NS) & 1;
-      const int tok0 = (MODE == kModeShared && !pre ? PT * kGqaTile : 0) + (j0 + t) * kGqaTile;
-      const int valid = min(kGqaTile, L - tok0);  // tokens in the cache (V rows to keep)
+      const int tok0 = (unit_tile0 + j0 + t) * kGqaTile;
+      int valid = min(kGqaTile, L - tok0);  // tokens in the cache (V rows to keep)
       // every lane leaves together (the mma.sync below is warp-wide)
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag))) {
         if (lane == 0) {
@@ -771,7 +877,8 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
         }
         return;
       }
-      if (stage_bad[stage]) {
+      const bool stage_is_bad = stage_bad[stage] != 0;
+      if (MODE != kModeMod && stage_is_bad) {
         bad_a |= !CAUSAL || tok0 < lim_a;
         bad_b |= !CAUSAL || tok0 < lim_b;
       }
@@ -797,11 +904,38 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
       uint32_t pa[4];
       {
         float xa[4], xb[4];
-        const float mxa = row_scores(s[0][0], s[0][1], s[1][0], s[1][1],
-                                     CAUSAL ? min(valid, lim_a - tok0) : valid, xa);
-        const float mxb = ROWS16 ? row_scores(s[0][2], s[0][3], s[1][2], s[1][3],
-                                              CAUSAL ? min(valid, lim_b - tok0) : valid, xb)
-                                 : -CUDART_INF_F;
+        float mxa, mxb = -CUDART_INF_F;
+        if constexpr (MODE == kModeMod) {
+          const float sa[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
+          bool seen = mod_row_scores(p, mod_a, sa, tok0, L, t4, xa, mxa);
+          bad_a |= stage_is_bad && seen;
+          if (ROWS16) {
+            const float sb[4] = {s[0][2], s[0][3], s[1][2], s[1][3]};
+            seen = mod_row_scores(p, mod_b, sb, tok0, L, t4, xb, mxb);
+            bad_b |= stage_is_bad && seen;
+          }
+          if (p.scores) {
+            // two 32-byte sectors per row and tile; a tile's tokens past the
+            // cache end lie within the row's rounded-up stride
+            const int64_t t_at = tok0 + 2 * t4;
+            if (ra < R_act) {
+              float* dst = p.scores + qrow_index(ra) * p.score_stride + t_at;
+              *reinterpret_cast<float2*>(dst) = make_float2(xa[0], xa[1]);
+              *reinterpret_cast<float2*>(dst + 8) = make_float2(xa[2], xa[3]);
+            }
+            if (ROWS16 && rb < R_act) {
+              float* dst = p.scores + qrow_index(rb) * p.score_stride + t_at;
+              *reinterpret_cast<float2*>(dst) = make_float2(xb[0], xb[1]);
+              *reinterpret_cast<float2*>(dst + 8) = make_float2(xb[2], xb[3]);
+            }
+          }
+        } else {
+          mxa = row_scores(s[0][0], s[0][1], s[1][0], s[1][1],
+                           CAUSAL ? min(valid, lim_a - tok0) : valid, xa);
+          if (ROWS16)
+            mxb = row_scores(s[0][2], s[0][3], s[1][2], s[1][3],
+                             CAUSAL ? min(valid, lim_b - tok0) : valid, xb);
+        }
         if (__any_sync(0xffffffffu, mxa > m0 + kLazyLog2 || mxb > m1 + kLazyLog2)) {
           const float aa = move_base(m0, fmaxf(m0, mxa));
           l0 *= aa;
@@ -820,19 +954,30 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
             }
           }
         }
-        row_p(xa, m0, l0, pa[0], pa[2]);
-        if (ROWS16) {
-          row_p(xb, m1, l1, pa[1], pa[3]);
+        if constexpr (MODE == kModeMod) row_p_exact(xa, m0, l0, pa[0], pa[2]);
+        else row_p(xa, m0, l0, pa[0], pa[2]);
+        if constexpr (ROWS16) {
+          if constexpr (MODE == kModeMod) row_p_exact(xb, m1, l1, pa[1], pa[3]);
+          else row_p(xb, m1, l1, pa[1], pa[3]);
         } else {
           pa[1] = pa[3] = 0u;
         }
       }
 
       // O += P V. Token rows of V past the cache end are zeroed in registers so
-      // that NaN in unused slots cannot reach the output (0 * NaN = NaN).
+      // that NaN in unused slots cannot reach the output (0 * NaN = NaN). With
+      // modified scores so are the rows before the oldest window, and every row
+      // of a stage that was not loaded (rows that do not see it keep P = 0).
+      int vlo = 0;
+      if constexpr (MODE == kModeMod) {
+        if (stage_is_bad) valid = 0;
+        if (p.window) vlo = L - p.q_total - p.window + 1 - tok0;
+      }
       {
-        const bool v00 = 2 * t4 < valid, v01 = 2 * t4 + 1 < valid;
-        const bool v10 = 2 * t4 + 8 < valid, v11 = 2 * t4 + 9 < valid;
+        const bool v00 = 2 * t4 < valid && 2 * t4 >= vlo;
+        const bool v01 = 2 * t4 + 1 < valid && 2 * t4 + 1 >= vlo;
+        const bool v10 = 2 * t4 + 8 < valid && 2 * t4 + 8 >= vlo;
+        const bool v11 = 2 * t4 + 9 < valid && 2 * t4 + 9 >= vlo;
         const uint32_t m01 = (v00 ? 0x0000ffffu : 0u) | (v01 ? 0xffff0000u : 0u);
         const uint32_t m89 = (v10 ? 0x0000ffffu : 0u) | (v11 ? 0xffff0000u : 0u);
         const int tok = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -843,7 +988,7 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
           const uint32_t addr = row + (jj >> 2) * Cfg::kHalfBytes + ((chunk ^ (tok & 7)) << 4);
           uint32_t b0, b1, b2, b3;
           ldsm_x4_trans(addr, b0, b1, b2, b3);
-          if (valid < kGqaTile) {
+          if (valid < kGqaTile || vlo > 0) {
             b0 &= m01;
             b1 &= m89;
             b2 &= m01;
@@ -863,6 +1008,13 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
     if (ROWS16) {
       l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
       l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    }
+    if constexpr (MODE == kModeMod) {
+      // a row's four lanes hold different tokens: one that met a bad page is enough
+      bad_a |= __shfl_xor_sync(0xffffffffu, int(bad_a), 1) != 0;
+      bad_a |= __shfl_xor_sync(0xffffffffu, int(bad_a), 2) != 0;
+      bad_b |= __shfl_xor_sync(0xffffffffu, int(bad_b), 1) != 0;
+      bad_b |= __shfl_xor_sync(0xffffffffu, int(bad_b), 2) != 0;
     }
     if (__any_sync(0xffffffffu, bad_a || bad_b) && lane == 0) raise_error(p.err_flags, kErrBadPage);
 #pragma unroll
@@ -897,6 +1049,10 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
           dst[nt * 4 + t4] =
               none ? 0u : pack_bf16x2(o[nt][2 * half] * inv, o[nt][2 * half + 1] * inv);
         if (p.lse && t4 == 0) p.lse[orow] = lse2 * 0.69314718055994531f;
+        if constexpr (MODE == kModeMod) {
+          if (p.scores && t4 == 0)
+            p.row_stat[orow] = none ? make_float2(0.f, 0.f) : make_float2(m, inv);
+        }
       } else {
         // partial slots are per (token group, CTA) pair: every group has its own
         const int64_t wrow = ((int64_t(vcta) * 2 + slot) * HPC + w) * R + r;
@@ -941,13 +1097,13 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
     const int64_t U0 = int64_t(nhg) * prefix[b] + int64_t(hg) * n;
     int c_lo, c_hi;
     split_cta_span(cut, U0, n, c_lo, c_hi);
-    merge_split_rows<kMergeRows, 4>(p, cut, vcta - c, U0, c_lo, c_hi, b, tok0, w,
+    merge_split_rows<MODE, kMergeRows, 4>(p, cut, vcta - c, U0, c_lo, c_hi, b, tok0, w,
                                     (hg * HPC + w) * g + rg.hoff, gh, p.gh * p.q_len, 0,
                                     gh * qlen, lane);
   }
   }
 
-  if constexpr (MODE == kModePlain) {
+  if constexpr (MODE != kModeShared) {
     // Sequences with no tiles (empty or invalid length): zeros, lse = -inf,
     // for every head of the tokens of the CTA's groups: [ztok0, + zlen).
     const RowGroup zlast = row_group(p, TG - 1);
@@ -963,6 +1119,10 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
       for (int64_t i = tid; i < n16; i += kStride) dst[i] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
         for (int64_t i = tid; i < rows; i += kStride) p.lse[row0 + i] = -CUDART_INF_F;
+      if constexpr (MODE == kModeMod) {
+        if (p.scores)
+          for (int64_t i = tid; i < rows; i += kStride) p.row_stat[row0 + i] = make_float2(0.f, 0.f);
+      }
     }
   }
 }
@@ -1034,14 +1194,14 @@ __global__ void __launch_bounds__(128) gqa_merge_kernel(const __grid_constant__ 
   const TileCut cut(W, G);
   const int64_t U0 = int64_t(p.nhg) * (int64_t(NG) * PT + before) + int64_t(hg) * n;
   const int c_lo = n ? cut.owner(U0) : 0, c_hi = n ? cut.owner(U0 + n - 1) : 0;
-  if constexpr (MODE == kModePlain) {
+  if constexpr (MODE != kModeShared) {
     // a unit-cut launch (chosen on the device, as the attention kernel did)
     // left every unit whole
     if (p.auto_cut && short_units(int64_t(p.B) * p.nhg, nmax, G)) return;
     if (n == 0 || c_lo == c_hi) return;
     // PIECES pieces per round trip to L2 (launch_merge takes the larger batch
     // when the merge grid fits in one wave at the registers that needs).
-    merge_split_rows<NR, PIECES>(p, cut, cta0, U0, c_lo, c_hi, b, tok0, w, head0, gh, rmax, r0,
+    merge_split_rows<MODE, NR, PIECES>(p, cut, cta0, U0, c_lo, c_hi, b, tok0, w, head0, gh, rmax, r0,
                                  r0 + nrows, lane);
   } else {
     const int R = p.sgs * rps;  // rows of a partial slot
@@ -1064,7 +1224,7 @@ __global__ void __launch_bounds__(128) gqa_merge_kernel(const __grid_constant__ 
       else
         merge_add_pieces<NR, PIECES>(m, p, cut, cta0, U0, c_lo, c_hi, w, R, 0, r0, nrows, lane);
     }
-    merge_write_out(m, p, b, tok0, head0, gh, r0, nrows, lane);
+    merge_write_out<MODE>(m, p, b, tok0, head0, gh, r0, nrows, lane);
   }
 }
 

@@ -90,7 +90,36 @@ struct GqaParams {
   uint4* k_pool;
   uint4* v_pool;
   int64_t page_stride16, token_stride16, head_stride16;
+  // Modified scores (the kModeMod instances; zero otherwise; see gqa_mod.cu).
+  float cap_in;            // tanh cap c: scale / c, 0 = no cap
+  float cap_out;           // c * log2(e)
+  const float* slopes;     // distance bias of each query head [Hq], or nullptr
+  int window;              // tokens a query sees back from its position, 0 = all
+  const uint32_t* tree;    // ancestor bits [B, q_total, tree_words], or nullptr (a chain)
+  int tree_words;
+  int64_t len_cap;         // longest valid length (the block table's or the weights' reach)
+  // Accumulated weights (scores = nullptr: none): each (query row, token)'s
+  // base-2 score [B, q_total, Hq][score_stride], -inf where it is not visible,
+  // and each row's softmax base and 1 / sum (0, 0 for a row without weight).
+  float* scores;
+  int64_t score_stride;
+  float2* row_stat;
 };
+
+// The weights kernel that follows a launch with p.scores set.
+struct WeightsParams {
+  const float* scores;
+  int64_t score_stride;
+  const float2* row_stat;
+  const int32_t* seq_lens;
+  float* weights;          // [B][Hkv][tokens], strides in elements
+  int64_t seq_stride, head_stride;
+  float decay;
+  int B, q_total, Hq, Hkv, g, window;
+  int64_t len_cap;
+  int max_tokens;          // tokens the grid covers (weights row length)
+};
+cudaError_t weights_launch(const WeightsParams& p, cudaStream_t stream);
 
 constexpr int kMlaTile = 64;       // tokens per MLA tile (page sizes are multiples of it)
 constexpr int kMlaDqk = 576;       // latent 512 + rope 64
@@ -142,6 +171,12 @@ int gqa_ctas_per_sm(int hpc, bool rows16, bool causal, bool fused, int tg, bool 
 int gqa_shared_ctas_per_sm(int hpc, bool rows16, bool causal, bool small, int device);
 cudaError_t gqa_shared_launch(const GqaParams& p, int grid, cudaStream_t stream,
                               cudaEvent_t attn_begin, cudaEvent_t attn_end);
+// Modified scores (tanh cap, distance bias, window, tree mask, stored scores):
+// CTAs per SM of its attention kernel (tg = 1 or 2 row groups per CTA), and
+// its two launches (attention, merge).
+int gqa_mod_ctas_per_sm(int hpc, bool rows16, int tg, bool small, int device);
+cudaError_t gqa_mod_launch(const GqaParams& p, int grid, cudaStream_t stream,
+                           cudaEvent_t attn_begin, cudaEvent_t attn_end);
 // Launches the attention kernel on `grid` CTAs. fused: split units are merged
 // inside it (one launch); otherwise a merge kernel follows as a programmatic
 // dependent launch.
