@@ -1,6 +1,7 @@
 // C-ABI front end: argument validation, split plan (grid size), TMA tensor
 // maps, workspace layout, launches. Declared in include/zl_decode_attn.h.
 #include "../../include/zl_decode_attn.h"
+#include "gqa_wide.h"
 #include "kernels.h"
 
 #include <cudaTypedefs.h>
@@ -94,7 +95,13 @@ struct GqaPlan {
   // modified scores with weights: each row's base and 1 / sum, then its scores
   size_t off_stat = 0, off_scores = 0;
   int64_t score_stride = 0;
+  // modified scores with many rows: the tcgen05 kernel (gqa_wide.cu)
+  bool wide = false;
+  int mt = 1, nblk = 1;
 };
+
+// Rows per kv head above which a modified-score call runs the tcgen05 kernel.
+constexpr int kWideRows = 32;
 
 // Query tokens per sequence one call takes, and query heads per kv head (the
 // GQA path takes the (token, head) rows of a kv head in groups of at most 16).
@@ -162,6 +169,25 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
   DeviceInfo dev;
   if ((st = current_device(&dev)) != ZL_OK) return st;
   plan->g = a->Hq / a->Hkv;
+  const int rows_per_head = plan->g * a->q_len;
+  if (mods && !mods->weights && rows_per_head > kWideRows) {
+    plan->wide = true;
+    plan->mt = rows_per_head > 128 ? 2 : 1;
+    plan->nblk = (rows_per_head + plan->mt * 128 - 1) / (plan->mt * 128);
+    plan->grid = a->num_ctas > 0 ? a->num_ctas : dev.sms;
+    if (a->num_ctas == 0 && a->max_seq_len > 0) {
+      int64_t len = a->max_seq_len;
+      if (mods->window > 0) len = std::min(len, int64_t(mods->window) + a->q_len + zl::kWideTile);
+      const int64_t tiles = int64_t(a->B) * a->Hkv * plan->nblk *
+                            ((len + zl::kWideTile - 1) / zl::kWideTile);
+      plan->grid = int(std::min(int64_t(plan->grid), std::max<int64_t>(tiles, 1)));
+    }
+    const size_t rows = size_t(plan->grid) * 2 * plan->mt * 128;
+    plan->off_lse = round_up((size_t(a->B) + 1) * sizeof(int32_t), 256);
+    plan->off_o = plan->off_lse + round_up(rows * sizeof(float), 256);
+    plan->bytes = plan->off_o + rows * zl::kGqaHeadDim * sizeof(float);
+    return ZL_OK;
+  }
   plan->fused = (a->flags & ZL_DECODE_SINGLE_LAUNCH) != 0;
   plan->hpc = zl::gqa_heads_per_cta(a->Hkv);
   plan->nhg = a->Hkv / plan->hpc;
@@ -315,11 +341,12 @@ zl_status mla_plan(const zl_decode_attn_params* a, MlaPlan* plan) {
 struct PoolMapKey {
   const void* pool;
   int64_t page_stride, token_stride, head_stride;
-  int32_t D, page_size, Hkv, num_pages, box_heads;
+  int32_t D, page_size, Hkv, num_pages, box_heads, box_tokens;
   bool operator==(const PoolMapKey& o) const {
     return pool == o.pool && page_stride == o.page_stride && token_stride == o.token_stride &&
            head_stride == o.head_stride && D == o.D && page_size == o.page_size &&
-           Hkv == o.Hkv && num_pages == o.num_pages && box_heads == o.box_heads;
+           Hkv == o.Hkv && num_pages == o.num_pages && box_heads == o.box_heads &&
+           box_tokens == o.box_tokens;
   }
 };
 constexpr int kMapCache = 8;
@@ -328,9 +355,9 @@ thread_local CUtensorMap t_maps[kMapCache];
 thread_local int t_map_used = 0, t_map_next = 0;
 
 zl_status encode_pool_map(CUtensorMap* map, const void* pool, const zl_decode_attn_params* a,
-                          int box_heads) {
+                          int box_heads, int box_tokens = zl::kGqaTile) {
   const PoolMapKey key{pool, a->page_stride, a->token_stride, a->head_stride, a->D_qk,
-                       a->page_size, a->Hkv, a->num_pages, box_heads};
+                       a->page_size, a->Hkv, a->num_pages, box_heads, box_tokens};
   for (int i = 0; i < t_map_used; ++i)
     if (t_map_keys[i] == key) {
       *map = t_maps[i];
@@ -342,7 +369,7 @@ zl_status encode_pool_map(CUtensorMap* map, const void* pool, const zl_decode_at
                               cuuint64_t(a->num_pages)};
   const cuuint64_t strides[3] = {cuuint64_t(a->token_stride) * 2, cuuint64_t(a->head_stride) * 2,
                                  cuuint64_t(a->page_stride) * 2};
-  const cuuint32_t box[4] = {64, cuuint32_t(zl::kGqaTile), cuuint32_t(box_heads), 1};
+  const cuuint32_t box[4] = {64, cuuint32_t(box_tokens), cuuint32_t(box_heads), 1};
   const cuuint32_t elem[4] = {1, 1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool),
                             dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -433,6 +460,78 @@ zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
 
+// A modified-score call with many rows per kv head (gqa_wide.cu). A fused
+// append is a launch of its own here.
+zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, const GqaPlan& plan,
+                   cudaStream_t s) {
+  zl::WideParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.box = a->page_size % 128 == 0 ? 128 : a->page_size % 64 == 0 ? 64
+          : a->page_size % 32 == 0 ? 32 : 16;
+  zl_status st;
+  if ((st = encode_pool_map(&p.tmap_k, a->k_pool, a, 1, p.box)) != ZL_OK) return st;
+  if ((st = encode_pool_map(&p.tmap_v, a->v_pool, a, 1, p.box)) != ZL_OK) return st;
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.out = static_cast<__nv_bfloat16*>(a->out);
+  p.lse = a->lse;
+  p.block_table = a->block_table;
+  p.seq_lens = a->seq_lens;
+  p.bt_stride = a->block_table_stride;
+  char* ws = static_cast<char*>(a->workspace);
+  p.ws_prefix = reinterpret_cast<int32_t*>(ws);
+  p.ws_lse = reinterpret_cast<float*>(ws + plan.off_lse);
+  p.ws_o = reinterpret_cast<float*>(ws + plan.off_o);
+  p.err_flags = a->err_flags;
+  p.B = a->B;
+  p.q_total = a->q_len;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.g = plan.g;
+  p.page_size = a->page_size;
+  p.num_pages = a->num_pages;
+  p.mt = plan.mt;
+  p.nblk = plan.nblk;
+  p.len_cap = a->block_table_stride * int64_t(a->page_size);
+  p.scale_log2 = float(double(a->scale) * kLog2e);
+  if (m.softcap > 0.f) {
+    p.cap_in = float(double(a->scale) / m.softcap);
+    p.cap_out = float(double(m.softcap) * kLog2e);
+  }
+  p.slopes = m.alibi_slopes;
+  p.window = m.window;
+  p.tree = m.tree_mask;
+  p.tree_words = (a->q_len + 31) / 32;
+  if (a->k_new) {
+    zl_kv_append_params ap;
+    std::memset(&ap, 0, sizeof(ap));
+    ap.struct_size = sizeof(ap);
+    ap.k_new = a->k_new;
+    ap.v_new = a->v_new;
+    ap.k_pool = const_cast<void*>(a->k_pool);
+    ap.v_pool = const_cast<void*>(a->v_pool);
+    ap.page_stride = a->page_stride;
+    ap.token_stride = a->token_stride;
+    ap.head_stride = a->head_stride;
+    ap.block_table = a->block_table;
+    ap.block_table_stride = a->block_table_stride;
+    ap.seq_lens = a->seq_lens;
+    ap.B = a->B;
+    ap.q_len = a->q_len;
+    ap.Hkv = a->Hkv;
+    ap.D_k = a->D_qk;
+    ap.D_v = a->D_v;
+    ap.page_size = a->page_size;
+    ap.num_pages = a->num_pages;
+    // no err_flags: a bad length or page is the attention's to report (short
+    // sequences are no error for it)
+    if ((st = zl_kv_append(&ap, reinterpret_cast<zl_stream_t>(s))) != ZL_OK) return st;
+  }
+  const cudaError_t e = zl::gqa_wide_launch(p, plan.grid, s,
+                                            reinterpret_cast<cudaEvent_t>(a->attn_begin),
+                                            reinterpret_cast<cudaEvent_t>(a->attn_end));
+  return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+}
+
 // zl_decode_attn (mods = nullptr) and zl_decode_attn_ex.
 zl_status gqa_run(const zl_decode_attn_params* a, const zl_score_params* mods,
                   zl_stream_t stream) {
@@ -444,6 +543,8 @@ zl_status gqa_run(const zl_decode_attn_params* a, const zl_score_params* mods,
   if ((st = gqa_plan(a, &plan, mods)) != ZL_OK) return st;
   if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < plan.bytes)
     return ZL_ERR_WORKSPACE;
+
+  if (plan.wide) return wide_run(a, *mods, plan, reinterpret_cast<cudaStream_t>(stream));
 
   GqaParams p;
   std::memset(&p, 0, sizeof(p));

@@ -1,0 +1,810 @@
+// GQA decode with modified scores for many query rows per kv head (a large
+// drafted tree, or many heads), on tcgen05.
+//
+// With R = g q_len rows, the m16 tiles of gqa_kernel.cuh read every K/V tile R
+// / 16 times from shared memory and L2. Here up to 256 rows share each K/V
+// tile: S = Q K^T (M = 128 rows, N = 128 tokens) and O += P V (N = 128
+// columns) are tcgen05.mma with S, P and O in TMEM, so a tile of 128 tokens
+// (64 KB) is loaded once for all of them and the load is what bounds it: 64 KB
+// at this card's bandwidth are about 2800 cycles per SM, the products of 256
+// rows 2100, their exponentials 2000.
+//
+// Two softmax warpgroups keep the tensor pipe fed, each with its own S and O
+// ("streams"). MT = 2: stream s has rows [128 s, 128 s + 128) of the block and
+// takes every tile. MT = 1 (at most 128 rows): both streams have the same rows
+// and take the tiles in turn, and their two results are joined in TMEM at the
+// end of the piece. Either way one stream's softmax runs under the other
+// one's products.
+//
+// Work is cut as in gqa_kernel.cuh: units (sequence, kv head, row block) of
+// 128-token tiles on one line, cut into equal ranges, one per CTA; cut units
+// leave normalised fp32 partials for the merge kernel.
+//
+// TMEM (512 columns): S of stream 0, 1 (128 each; P, 64 columns of bf16 pairs,
+// replaces S once it is read), O of stream 0, 1 (128 each). MMAs of one CTA
+// execute in the order of their issue, so QK of a stream's next tile may
+// follow the PV that reads its P without a wait; the commit after a QK covers
+// the PV before it, so a softmax thread that sees S of a tile may also rescale
+// O.
+#include "gqa_kernel.cuh"
+#include "gqa_wide.h"
+
+namespace zl {
+
+namespace {
+
+constexpr int kWT = kWideTile;                 // tokens per tile
+constexpr int kHalf = kWT * 128;               // 16 KB: 128 rows x 64 columns
+constexpr int kBuf = 2 * kHalf;                // one K or V tile, or 128 rows of Q
+constexpr int kInfo = 8;                       // tiles whose load info is kept
+constexpr int kSoft = 256;                     // softmax threads
+constexpr int kWideThreads = kSoft + 64;       // + producer warp, MMA warp
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream
+
+template <int MT>
+struct WideCfg {
+  static constexpr int kRing = MT == 2 ? 4 : 5;      // K/V buffers
+  static constexpr int kAhead = MT == 2 ? 1 : 2;     // tiles QK runs ahead of PV
+  static constexpr int kOffRing = MT * kBuf;
+  static constexpr int kOffBar = kOffRing + kRing * kBuf;
+  enum : int {
+    B_Q = 0, B_ML, B_FINAL, B_S0, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_FULL0 = B_O0 + 2,
+    B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing, B_COUNT = B_INFO0 + kInfo
+  };
+  static constexpr int kOffMisc = kOffBar + 8 * B_COUNT;   // TMEM address, abort flag
+  static constexpr int kOffInfo = kOffMisc + 16;           // kInfo words
+  static constexpr int kOffMl = kOffInfo + 4 * kInfo;      // [2][128] (m, l), MT = 1
+  static constexpr int kOffDepth = kOffMl + (MT == 1 ? 2 * 128 * 8 : 0);  // [2][128] bytes
+  static constexpr int kOffPrefix = kOffDepth + 2 * 128;
+  static constexpr size_t smem_bytes(int B) { return 1024 + kOffPrefix + size_t(B + 1) * 4; }
+  static constexpr size_t kSmemMax = smem_bytes(kMaxBatch);
+  static_assert(kSmemMax <= 232448, "shared memory of one CTA");
+};
+
+// Wait on an mbarrier with the whole warp by polling; every lane gets the same
+// answer, false after a timeout or an abort.
+__device__ __forceinline__ bool wide_warp_wait(uint32_t bar, uint32_t parity,
+                                               const volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if ((i & 63u) == 0) {
+      const bool stop = *abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs;
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
+
+// Bits [a, b) of a 32-bit word, both clamped to 0..32.
+__device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 32);
+  if (a >= b) return 0u;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// Drafted bits [j0, j0 + 32) of a row's ancestor mask (words 32-bit words).
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* bits, int words, int j0) {
+  if (j0 <= -32 || j0 >= 32 * words) return 0u;
+  if (j0 < 0) return __ldg(bits) << (-j0);
+  const int w = j0 >> 5, sh = j0 & 31;
+  uint32_t x = __ldg(bits + w) >> sh;
+  if (sh && w + 1 < words) x |= __ldg(bits + w + 1) << (32 - sh);
+  return x;
+}
+
+// Registers that tcgen05.ld fills are valid after tcgen05.wait::ld: nothing
+// computed from them may be scheduled above it.
+__device__ __forceinline__ void hold(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
+}
+
+// One contiguous run of tiles of one unit, as every role walks them.
+struct Piece {
+  int b, kvh, blk, L, n_unit, j0, ntiles, tile0;
+  bool partial;
+  int slot;
+  int64_t next;
+};
+
+__device__ __forceinline__ int wide_first_tile(const WideParams& p, int L) {
+  return p.window ? max(L - p.q_total - p.window + 1, 0) / kWT : 0;
+}
+__device__ __forceinline__ int wide_tiles(const WideParams& p, int L) {
+  if (!(L >= 0 && int64_t(L) <= p.len_cap)) return 0;
+  return (L + kWT - 1) / kWT - wide_first_tile(p, L);
+}
+
+__device__ __forceinline__ Piece piece_at(const WideParams& p, const int* prefix, int64_t idx,
+                                          int64_t s_c, int64_t e_c) {
+  Piece q;
+  const int U = p.Hkv * p.nblk;
+  q.b = locate_seq(prefix, p.B, U, idx);
+  q.n_unit = prefix[q.b + 1] - prefix[q.b];
+  const int64_t unit0 = int64_t(U) * prefix[q.b];
+  const int u = int((idx - unit0) / q.n_unit);
+  q.j0 = int((idx - unit0) % q.n_unit);
+  q.kvh = u / p.nblk;
+  q.blk = u % p.nblk;
+  const int64_t unit_end = unit0 + int64_t(u + 1) * q.n_unit;
+  q.next = min(e_c, unit_end);
+  q.ntiles = int(q.next - idx);
+  q.partial = q.j0 > 0 || q.next < unit_end;
+  q.slot = idx == s_c ? 0 : 1;
+  q.L = p.seq_lens[q.b];
+  q.tile0 = wide_first_tile(p, q.L) + q.j0;
+  return q;
+}
+
+template <int MT>
+__global__ void __launch_bounds__(kWideThreads, 1)
+gqa_wide_kernel(const __grid_constant__ WideParams p) {
+  using Cfg = WideCfg<MT>;
+  constexpr int NB = Cfg::kRing, D = Cfg::kAhead;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  auto bar = [&](int i) -> uint32_t { return sbase + Cfg::kOffBar + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 8);
+  uint32_t* info = reinterpret_cast<uint32_t*>(smem + Cfg::kOffInfo);
+  float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffMl);
+  uint8_t* depth_s = smem + Cfg::kOffDepth;
+  int* prefix = reinterpret_cast<int*>(smem + Cfg::kOffPrefix);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = p.B;
+
+  if (tid == 0) {
+    mbar_init(bar(Cfg::B_Q), kSoft);
+    mbar_init(bar(Cfg::B_ML), kSoft);
+    mbar_init(bar(Cfg::B_FINAL), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(Cfg::B_S0 + s), 1);
+      mbar_init(bar(Cfg::B_P0 + s), 128);
+      mbar_init(bar(Cfg::B_O0 + s), 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(bar(Cfg::B_FULL0 + i), 1);
+      mbar_init(bar(Cfg::B_EMPTY0 + i), 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(bar(Cfg::B_INFO0 + i), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // A programmatic dependent of the kernel before it on the stream: global
+  // memory, and TMEM that kernel may still hold, only after it has finished.
+  griddep_wait();
+  if (warp == 9) {
+    tmem_alloc(sbase + Cfg::kOffMisc, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&p.tmap_k);
+    tma_prefetch_desc(&p.tmap_v);
+  }
+  if (warp == 0) {  // tiles per sequence, exclusive prefix sum
+    const int per = (B + 31) / 32, b0 = lane * per;
+    int local = 0;
+    for (int i = 0; i < per; ++i) {
+      if (b0 + i < B) {
+        const int L = p.seq_lens[b0 + i];
+        if (blockIdx.x == 0 && !(L >= 0 && int64_t(L) <= p.len_cap))
+          raise_error(p.err_flags, kErrBadLen);
+        local += wide_tiles(p, L);
+      }
+    }
+    int incl = local;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    int run = incl - local;
+    for (int i = 0; i < per; ++i) {
+      if (b0 + i < B) {
+        prefix[b0 + i] = run;
+        run += wide_tiles(p, p.seq_lens[b0 + i]);
+      }
+    }
+    if (lane == 31) prefix[B] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();  // the merge kernel waits for this whole grid
+  const uint32_t tmem = *tmem_slot;
+  const int c = blockIdx.x;
+  if (c == 0)
+    for (int b = tid; b <= B; b += kWideThreads) p.ws_prefix[b] = prefix[b];
+  const int64_t W = int64_t(p.Hkv) * p.nblk * prefix[B];
+  const TileCut cut(W, gridDim.x);
+  const int64_t s_c = c < int(cut.G) && W > 0 ? cut.start(c) : 0;
+  const int64_t e_c = c < int(cut.G) && W > 0 ? cut.start(c + 1) : 0;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    // Items (K or V of a tile) in the order the MMA warp uses them: the K of
+    // the first D tiles, then V of tile t and K of tile t + D. Lane i loads
+    // half i & 1 (64 columns) of token block i >> 1 of the tile; blocks wholly
+    // past the cache end or before the oldest window, or on a bad page, are
+    // not loaded.
+    const int nblocks = kWT / p.box;
+    const int blk = lane >> 1, half = lane & 1;
+    uint32_t item = 0, tile_no = 0;
+    bool ok = true;
+    for (int64_t idx = s_c; idx < e_c && ok;) {
+      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      const int32_t* bt = p.block_table + int64_t(pc.b) * p.bt_stride;
+      const int lo = p.window ? pc.L - p.q_total - p.window + 1 : 0;
+      // this lane's block of tile t: page, or -1 (nothing there), -2 (bad page)
+      auto page_of = [&](int t) -> int {
+        const int tok = (pc.tile0 + t) * kWT + blk * p.box;
+        if (blk >= nblocks || t >= pc.ntiles || tok >= pc.L || tok + p.box <= lo) return -1;
+        const int pg = __ldg(bt + tok / p.page_size);
+        return pg < 0 || pg >= p.num_pages ? -2 : pg;
+      };
+      auto load = [&](const CUtensorMap* map, int t, int page) -> bool {
+        const uint32_t s = item % NB, ph = (item / NB) & 1;
+        if (!mbar_wait(bar(Cfg::B_EMPTY0 + s), ph ^ 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        ++item;
+        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t fb = bar(Cfg::B_FULL0 + s);
+        if (lane == 0) {
+          const uint32_t bytes = uint32_t(__popc(there)) * uint32_t(p.box) * 128u;
+          if (bytes) mbar_arrive_expect_tx(fb, bytes);
+          else mbar_arrive(fb);
+        }
+        __syncwarp();
+        if (page >= 0) {
+          const int tok = (pc.tile0 + t) * kWT + blk * p.box;
+          tma_load_4d(sbase + Cfg::kOffRing + s * kBuf + half * kHalf + blk * p.box * 128, map,
+                      fb, half * 64, tok % p.page_size, pc.kvh, page);
+        }
+        return true;
+      };
+      int pages[D + 1];  // of tiles t .. t + D
+#pragma unroll
+      for (int i = 0; i <= D; ++i) pages[i] = page_of(i);
+      // K of tile t, with what the softmax threads need to know of its blocks:
+      // bits 0-7 the 16-token blocks on a bad page, bits 8-15 those not loaded
+      auto load_k = [&](int t, int page) -> bool {
+        const uint32_t n = p.box / 16;
+        const uint32_t mine = half == 0 && blk < nblocks ? ((1u << n) - 1u) << (blk * n) : 0u;
+        const uint32_t word = __reduce_or_sync(
+            0xffffffffu, (page == -2 ? mine : 0u) | (page < 0 ? mine << 8 : 0u));
+        if (!load(&p.tmap_k, t, page)) return false;
+        if (lane == 0) {
+          info[tile_no % kInfo] = word;
+          mbar_arrive(bar(Cfg::B_INFO0 + tile_no % kInfo));
+        }
+        ++tile_no;
+        return true;
+      };
+#pragma unroll
+      for (int t = 0; t < D; ++t)
+        if (t < pc.ntiles && ok) load_k(t, pages[t]);
+      for (int t = 0; t < pc.ntiles && ok; ++t) {
+        const int ahead = page_of(t + D + 1);  // in flight while the loads wait
+        if (!load(&p.tmap_v, t, pages[0])) break;
+        if (t + D < pc.ntiles && !load_k(t + D, pages[D])) break;
+#pragma unroll
+        for (int i = 0; i < D; ++i) pages[i] = pages[i + 1];
+        pages[D] = ahead;
+      }
+      idx = pc.next;
+    }
+    if (!ok && lane == 0) {
+      raise_error(p.err_flags, kErrTimeout);
+      *abort_flag = 1;
+    }
+    // Leave no copy in flight.
+    const volatile int never = 0;
+    for (uint32_t i = item > NB ? item - NB : 0; i < item; ++i)
+      mbar_wait(bar(Cfg::B_FULL0 + i % NB), (i / NB) & 1, &never);
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
+    const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
+    uint32_t item = 0, pieces = 0;
+    uint32_t pn[2] = {0, 0};  // P tiles taken from each stream
+    bool ok = true;
+    auto wait = [&](int i, uint32_t parity) -> bool {
+      ok = ok && wide_warp_wait(bar(i), parity, abort_flag);
+      return ok;
+    };
+    auto wait_item = [&](uint32_t it) { return wait(Cfg::B_FULL0 + it % NB, (it / NB) & 1); };
+    auto buf = [&](uint32_t it) -> uint32_t {
+      return sbase + Cfg::kOffRing + (it % NB) * kBuf;
+    };
+    // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step
+    auto qk = [&](int s, uint32_t it, bool release) {
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t qb = sbase + (MT == 2 ? s * kBuf : 0), kb = buf(it);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
+          umma_bf16(tmem + kTmemS + 128 * s, umma_smem_desc(qb + off, 0, 1024, 2),
+                    umma_smem_desc(kb + off, 0, 1024, 2), idesc_qk, k ? 1u : 0u);
+        }
+        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
+        umma_commit(bar(Cfg::B_S0 + s));
+      }
+      __syncwarp();
+    };
+    // O_s (+)= P_s V, 16 tokens (8 TMEM columns of P) per step
+    auto pv = [&](int s, uint32_t it, bool first, bool release, bool last) {
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t vb = buf(it);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_bf16_tmem_a(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * k,
+                           umma_smem_desc(vb + k * 16 * 128, kHalf, 1024, 2), idesc_pv,
+                           first && k == 0 ? 0u : 1u);
+        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
+        if (last) umma_commit(bar(Cfg::B_O0 + s));
+      }
+      __syncwarp();
+    };
+    for (int64_t idx = s_c; idx < e_c && ok;) {
+      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      const int n = pc.ntiles;
+      if (!wait(Cfg::B_Q, pieces & 1)) break;
+      if (MT == 2) {
+        if (!wait_item(item)) break;
+        qk(0, item, false);
+        qk(1, item, true);
+        ++item;
+        for (int t = 0; t < n && ok; ++t) {
+          const uint32_t iv = item, ik = item + 1;
+          const bool more = t + 1 < n;
+          if (!wait_item(iv) || !wait(Cfg::B_P0, pn[0] & 1)) break;
+          pv(0, iv, t == 0, false, !more);
+          ++pn[0];
+          if (more) {
+            if (!wait_item(ik)) break;
+            qk(0, ik, false);
+          }
+          if (!wait(Cfg::B_P0 + 1, pn[1] & 1)) break;
+          pv(1, iv, t == 0, true, !more);
+          ++pn[1];
+          if (more) qk(1, ik, true);
+          item += more ? 2 : 1;
+        }
+      } else {
+        for (int t = 0; t < 2 && t < n; ++t) {
+          if (!wait_item(item)) break;
+          qk(t, item++, true);
+        }
+        for (int t = 0; t < n && ok; ++t) {
+          const int s = t & 1;
+          if (!wait_item(item) || !wait(Cfg::B_P0 + s, pn[s] & 1)) break;
+          pv(s, item++, t < 2, true, t + 2 >= n);
+          ++pn[s];
+          if (t + 2 < n) {
+            if (!wait_item(item)) break;
+            qk(s, item++, true);
+          }
+        }
+      }
+      ++pieces;
+      idx = pc.next;
+    }
+    if (!ok && lane == 0) {
+      raise_error(p.err_flags, kErrTimeout);
+      *abort_flag = 1;
+    }
+    // Every MMA done before TMEM is released.
+    if (elect_one()) umma_commit(bar(Cfg::B_FINAL));
+    __syncwarp();
+    const volatile int never = 0;
+    mbar_wait(bar(Cfg::B_FINAL), 0, &never);
+  } else {
+    // ------------------------------------------------------ softmax, epilogue
+    const int s = warp >> 2;                          // stream
+    const int row = 32 * (warp & 3) + lane;           // TMEM lane
+    const int wtid = tid & 127;                       // thread of the warpgroup
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t ts = tl + kTmemS + 128 * s, to = tl + kTmemO + 128 * s;
+    const int nrows = p.g * p.q_total;
+    bool ok = true;
+    auto wait_all = [&](int i, uint32_t parity) -> bool {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag));
+      return ok;
+    };
+    uint32_t tile_no = 0, pieces = 0, sn = 0;  // tiles of the CTA, pieces, tiles of this stream
+    uint32_t on[2] = {0, 0};                   // finished O of each stream
+    for (int64_t idx = s_c; idx < e_c && ok; ++pieces) {
+      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      const int n = pc.ntiles, L = pc.L, ctx = L - p.q_total;
+      const int blk0 = pc.blk * MT * 128;
+      const int r = blk0 + (MT == 2 ? s * 128 : 0) + row;
+      const bool exists = r < nrows;
+      const int qi = exists ? r / p.g : 0, head = pc.kvh * p.g + (exists ? r % p.g : 0);
+
+      // Q rows into the swizzled K-major layout: MT = 2, this stream's own; MT
+      // = 1, half of the shared ones. (Every QK of the piece before is done: a
+      // softmax thread has seen its last S, and for MT = 1 both have met.)
+      {
+        constexpr int kPer = MT == 2 ? 16 : 8;
+        const uint32_t qb = sbase + (MT == 2 ? s * kBuf : 0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int ch = i * 128 + wtid, k = ch & 15;
+          const int rr = (ch >> 4) + (MT == 2 ? 0 : s * 64);
+          const int rg = blk0 + (MT == 2 ? s * 128 : 0) + rr;
+          const uint32_t dst = qb + (k >> 3) * kHalf + rr * 128 + (((k & 7) ^ (rr & 7)) << 4);
+          if (rg < nrows) {
+            const int64_t qrow =
+                (int64_t(pc.b) * p.q_total + rg / p.g) * p.Hq + pc.kvh * p.g + rg % p.g;
+            cp_async_16(dst, p.q + qrow * kGqaHeadDim + k * 8);
+          } else {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u)
+                         : "memory");
+          }
+        }
+      }
+      const uint32_t* seq_bits =
+          p.tree ? p.tree + int64_t(pc.b) * p.q_total * p.tree_words : nullptr;
+      const uint32_t* bits = p.tree ? seq_bits + int64_t(qi) * p.tree_words : nullptr;
+      const int pos = ctx + (p.tree ? tree_depth(bits, p.tree_words) : qi);
+      const uint8_t* depth = depth_s + (pieces & 1) * 128;
+      if (p.tree && s == 0 && wtid < p.q_total)
+        depth_s[(pieces & 1) * 128 + wtid] =
+            uint8_t(tree_depth(seq_bits + int64_t(wtid) * p.tree_words, p.tree_words));
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(bar(Cfg::B_Q));
+      if (p.tree && !wait_all(Cfg::B_Q, pieces & 1)) break;  // the depths
+
+      const int lo_unit = p.window ? ctx - p.window + 1 : 0;  // oldest token any row sees
+      const int lo_row = p.window ? pos - p.window + 1 : -(1 << 30);
+      const float slope2 = p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+      float m = -CUDART_INF_F, l = 0.f;
+      bool bad = false;
+      for (int t = MT == 2 ? 0 : s; t < n; t += MT == 2 ? 1 : 2, ++sn) {
+        const uint32_t tn = tile_no + t;
+        const int tok0 = (pc.tile0 + t) * kWT;
+        if (!wait_all(Cfg::B_INFO0 + tn % kInfo, (tn / kInfo) & 1)) break;
+        const uint32_t load_info = info[tn % kInfo];
+        // all of the tile is context that every row sees
+        const bool plain = load_info == 0 && tok0 + kWT <= ctx &&
+                           (!p.window || tok0 >= ctx + p.q_total - p.window);
+        if (!wait_all(Cfg::B_S0 + s, sn & 1)) break;
+        tc_fence_after();
+        float x[kWT];
+        {
+          uint32_t v[4][32];
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) tmem_ld32(ts + 32 * cc, v[cc]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            hold(v[cc]);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[32 * cc + k] = __uint_as_float(v[cc][k]);
+          }
+        }
+        // scores in units of sc (base 2 once multiplied by it; sc > 0)
+        float sc = p.scale_log2;
+        if (p.cap_in > 0.f) {
+#pragma unroll
+          for (int k = 0; k < kWT; ++k) x[k] = cap_tanh(x[k] * p.cap_in);
+          sc = p.cap_out;
+        }
+        if (p.slopes) {
+          const float d0 = float(pos - tok0);
+          if (p.tree && tok0 + kWT > ctx) {
+#pragma unroll
+            for (int k = 0; k < kWT; ++k) {
+              const int j = tok0 + k - ctx;
+              const int dist = j < 0 ? pos - tok0 - k
+                               : j < p.q_total ? pos - ctx - int(depth[j]) : 0;
+              x[k] = fmaf(-slope2, float(dist), x[k] * sc);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kWT; ++k) x[k] = fmaf(slope2, float(k) - d0, x[k] * sc);
+          }
+          sc = 1.f;
+        }
+        if (!plain) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int base = tok0 + 32 * w;
+            uint32_t vis;
+            if (p.tree) {
+              vis = bit_range(max(lo_row, 0) - base, min(ctx, L) - base);
+              uint32_t dr = mask_word(bits, p.tree_words, base - ctx) & bit_range(-base, L - base);
+              if (p.window && p.window < p.q_total)  // only then can it hide a drafted token
+                for (uint32_t todo = dr; todo; todo &= todo - 1) {
+                  const int k = __ffs(todo) - 1;
+                  if (pos - ctx - int(depth[base + k - ctx]) >= p.window) dr &= ~(1u << k);
+                }
+              vis |= dr;
+            } else {
+              vis = bit_range(max(lo_row, 0) - base, min(pos + 1, L) - base);
+            }
+            const uint32_t two = load_info >> (2 * w);
+            bad |= (vis & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u))) != 0;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((vis >> k) & 1u)) x[32 * w + k] = -CUDART_INF_F;
+          }
+          // V rows that were not loaded, lie past the end or before the oldest
+          // window are zeroed (P is 0 there, but 0 * NaN is not)
+          if (MT == 1 || s == 0) {
+            // item numbers of the CTA: two per tile; see the producer's order
+            const uint32_t iv = 2 * tile_no + uint32_t(MT == 2 ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1));
+            if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
+            const int tok = tok0 + row;
+            if (((load_info >> (8 + (row >> 4))) & 1u) || tok >= L || tok < lo_unit) {
+              const uint32_t vr = sbase + Cfg::kOffRing + (iv % NB) * kBuf + row * 128;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 vr + (k >> 3) * kHalf + (k & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float mq[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int k = 4; k < kWT; ++k) mq[k & 3] = fmaxf(mq[k & 3], x[k]);
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
+        // The base moves only past 2^8 (P stays at most 256); one vote per
+        // warp, since the TMEM accesses are warp-wide.
+        if (__any_sync(0xffffffffu, mx > m + kLazyLog2)) {
+          const float mn = fmaxf(m, mx);
+          const float alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn);
+          m = mn;
+          l *= alpha;
+          if (t >= (MT == 2 ? 1 : 2)) {  // O holds earlier tiles
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * cc, o);
+              tmem_wait_ld();
+              hold(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(to + 32 * cc, o);
+            }
+          }
+        }
+        const float base = m == -CUDART_INF_F ? 0.f : m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float a = ex2_approx(fmaf(x[64 * hf + 2 * k], sc, -base));
+            const float e = ex2_approx(fmaf(x[64 * hf + 2 * k + 1], sc, -base));
+            pk[k] = pack_bf16x2(a, e);
+            ls[k & 3] += a + e;
+          }
+          tmem_st32(ts + 32 * hf, pk);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::B_P0 + s));
+      }
+      if (!ok) break;
+
+      // ---- the piece's result: O / l, joined over the streams for MT = 1
+      float mine = 1.f, theirs = 0.f;  // weights of this and the other stream's O
+      bool both = false;
+      if (MT == 1) {
+        ml[s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
+        mbar_arrive(bar(Cfg::B_ML));
+        if (!wait_all(Cfg::B_ML, pieces & 1)) break;
+        const float2 o = ml[(s ^ 1) * 128 + row];
+        bad |= isnan(o.y);
+        both = n > 1;  // stream 1 had a tile
+        const float mn = fmaxf(m, o.x);
+        mine = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn);
+        theirs = o.x == -CUDART_INF_F ? 0.f : ex2_approx(o.x - mn);
+        // the same order of the sum in both streams' threads
+        const float l0 = s ? o.y * theirs : l * mine, l1 = s ? l * mine : o.y * theirs;
+        m = mn;
+        l = l0 + l1;
+      }
+      const bool none = bad || !(l > 0.f);
+      const float inv = none ? 0.f : 1.f / l;
+      const float lse2 = none ? -CUDART_INF_F : m + log2f(l);
+      if (__any_sync(0xffffffffu, bad && exists) && lane == 0) raise_error(p.err_flags, kErrBadPage);
+      const int need = MT == 2 ? (1 << s) : (n > 1 ? 3 : 1);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (need >> q & 1) {
+          if (!wait_all(Cfg::B_O0 + q, on[q] & 1)) break;
+          ++on[q];
+        }
+      if (!ok) break;
+      tc_fence_after();
+      const int64_t orow = (int64_t(pc.b) * p.q_total + qi) * p.Hq + head;
+      const int64_t wrow =
+          (int64_t(c) * 2 + pc.slot) * (MT * 128) + (MT == 2 ? s * 128 : 0) + row;
+      // MT = 1: stream s writes columns [64 s, 64 s + 64) of the joined row
+#pragma unroll 1
+      for (int cc = 0; cc < (MT == 2 ? 4 : 2); ++cc) {
+        const int col = (MT == 2 ? 0 : 64 * s) + 32 * cc;
+        float f[32];
+        uint32_t a[32];
+        if (MT == 2) {
+          tmem_ld32(to + col, a);
+          tmem_wait_ld();
+          hold(a);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[k]) * inv;
+        } else {
+          // O_0 w_0 + O_1 w_1, in that order
+          const float w0 = (s ? theirs : mine) * inv, w1 = (s ? mine : theirs) * inv;
+          tmem_ld32(tl + kTmemO + col, a);
+          tmem_wait_ld();
+          hold(a);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[k]) * w0;
+          if (both) {
+            tmem_ld32(tl + kTmemO + 128 + col, a);
+            tmem_wait_ld();
+            hold(a);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
+          }
+        }
+        if (!exists) continue;
+        if (pc.partial) {
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + wrow * kGqaHeadDim + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                          : make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kGqaHeadDim + col);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = none ? make_uint4(0u, 0u, 0u, 0u)
+                          : make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]),
+                                       pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                                       pack_bf16x2(f[8 * k + 4], f[8 * k + 5]),
+                                       pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+        }
+      }
+      if (exists && (MT == 2 || s == 0)) {
+        if (pc.partial) p.ws_lse[wrow] = bad ? CUDART_NAN_F : lse2;
+        else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
+      }
+      tc_fence_before();
+      tile_no += n;
+      idx = pc.next;
+    }
+    if (!ok) {
+      raise_error(p.err_flags, kErrTimeout);
+      *abort_flag = 1;
+    }
+    // Sequences without tiles: zeros, lse = -inf.
+    for (int b = c; b < B; b += gridDim.x) {
+      if (prefix[b + 1] != prefix[b]) continue;
+      const int64_t rows = int64_t(p.q_total) * p.Hq, row0 = int64_t(b) * rows;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kGqaHeadDim);
+      for (int64_t i = tid; i < rows * kGqaHeadDim / 8; i += kSoft)
+        dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int64_t i = tid; i < rows; i += kSoft) p.lse[row0 + i] = -CUDART_INF_F;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) {
+    __syncwarp();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the partials of the units cut between CTAs, one warp per row. Block
+// (c, y) looks at the boundary between CTAs c - 1 and c: if it is the first
+// one inside a unit, the block merges 8 of the unit's rows over the unit's
+// CTAs, in their order.
+template <int MT>
+__global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ WideParams p,
+                                                      int ctas) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1, U = p.Hkv * p.nblk;
+  const int64_t W = int64_t(U) * p.ws_prefix[p.B];
+  if (W == 0) return;
+  const TileCut cut(W, ctas);
+  if (c >= int(cut.G)) return;
+  const int64_t x = cut.start(c);
+  const int b = locate_seq(p.ws_prefix, p.B, U, x);
+  const int first = p.ws_prefix[b], n = p.ws_prefix[b + 1] - first;
+  const int u = int((x - int64_t(U) * first) / n);
+  const int64_t U0 = int64_t(U) * first + int64_t(u) * n;
+  if (x == U0 || cut.start(c - 1) > U0) {
+    // not cut here, or an earlier boundary cuts it too (a CTA whose range
+    // starts inside the unit)
+    return;
+  }
+  const int c_hi = cut.owner(U0 + n - 1);
+  const int row = blockIdx.y * 8 + warp;
+  const int r = (u % p.nblk) * MT * 128 + row;
+  if (r >= p.g * p.q_total) return;
+  MergeAcc<1> acc;
+  acc.init();
+  for (int cc = c - 1; cc <= c_hi; ++cc) {
+    const int slot = cc == c - 1 && U0 > cut.start(cc) ? 1 : 0;
+    const int64_t wrow = (int64_t(cc) * 2 + slot) * (MT * 128) + row;
+    acc.add(0, __ldcg(p.ws_lse + wrow),
+            __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * kGqaHeadDim) + lane));
+  }
+  const bool none = acc.bad || !(acc.den[0] > 0.f);
+  const float inv = none ? 0.f : 1.f / acc.den[0];
+  const int64_t orow =
+      (int64_t(b) * p.q_total + r / p.g) * p.Hq + (u / p.nblk) * p.g + r % p.g;
+  uint2 o = make_uint2(0u, 0u);
+  if (!none)
+    o = make_uint2(pack_bf16x2(acc.acc[0].x * inv, acc.acc[0].y * inv),
+                   pack_bf16x2(acc.acc[0].z * inv, acc.acc[0].w * inv));
+  reinterpret_cast<uint2*>(p.out + orow * kGqaHeadDim)[lane] = o;
+  if (p.lse && lane == 0)
+    p.lse[orow] = none ? -CUDART_INF_F
+                       : (acc.mx[0] + log2f(acc.den[0])) * 0.69314718055994531f;
+}
+
+template <int MT>
+cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent_t attn_begin,
+                   cudaEvent_t attn_end) {
+  static bool done[kMaxDevices] = {};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!done[device]) {
+    if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  int(WideCfg<MT>::kSmemMax))) != cudaSuccess)
+      return e;
+    done[device] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (attn_begin && (e = cudaEventRecord(attn_begin, stream)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = WideCfg<MT>::smem_bytes(p.B);
+  if ((e = cudaLaunchKernelEx(&cfg, gqa_wide_kernel<MT>, p)) != cudaSuccess) return e;
+  if (attn_end && (e = cudaEventRecord(attn_end, stream)) != cudaSuccess) return e;
+  if (grid < 2) return cudaSuccess;  // nothing is cut
+  cfg.gridDim = dim3(unsigned(grid - 1), unsigned(MT * 128 / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, gqa_wide_merge<MT>, p, grid);
+}
+
+}  // namespace
+
+cudaError_t gqa_wide_launch(const WideParams& p, int grid, cudaStream_t stream,
+                            cudaEvent_t attn_begin, cudaEvent_t attn_end) {
+  return p.mt == 2 ? launch<2>(p, grid, stream, attn_begin, attn_end)
+                   : launch<1>(p, grid, stream, attn_begin, attn_end);
+}
+
+}  // namespace zl

@@ -1,0 +1,39 @@
+// Interface between the C-ABI front end and the many-row kernel (gqa_wide.cu).
+#pragma once
+
+#include "kernels.h"
+
+namespace zl {
+
+constexpr int kWideTile = 128;  // tokens per tile
+
+struct WideParams {
+  CUtensorMap tmap_k;  // 4-D {D, page_size, Hkv, num_pages}, box {64, box, 1, 1}, 128B swizzle
+  CUtensorMap tmap_v;
+  const __nv_bfloat16* q;  // [B, q_total, Hq, 128]
+  __nv_bfloat16* out;
+  float* lse;              // natural log, or nullptr
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int64_t bt_stride;
+  int32_t* ws_prefix;  // [B + 1] tile prefix sums, for the merge
+  float* ws_lse;       // [CTAs][2][mt * 128] base-2 lse of partials (NaN = bad)
+  float* ws_o;         // [..][128] normalised partial outputs
+  uint32_t* err_flags;
+  int B, q_total, Hq, Hkv, g, page_size, num_pages;
+  int box;   // tokens per bulk copy: the largest of 128, 64, 32, 16 dividing page_size
+  int mt;    // 1: at most 128 rows per kv head, 2: blocks of 256 rows
+  int nblk;  // row blocks per kv head
+  int64_t len_cap;
+  float scale_log2, cap_in, cap_out;  // as in GqaParams
+  const float* slopes;
+  int window;
+  const uint32_t* tree;
+  int tree_words;
+};
+
+// The attention kernel on `grid` CTAs, then the merge of the units it cut.
+cudaError_t gqa_wide_launch(const WideParams& p, int grid, cudaStream_t stream,
+                            cudaEvent_t attn_begin, cudaEvent_t attn_end);
+
+}  // namespace zl
