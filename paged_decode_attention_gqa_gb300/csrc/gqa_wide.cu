@@ -38,7 +38,12 @@ constexpr int kHalf = kWT * 128;               // 16 KB: 128 rows x 64 columns
 constexpr int kBuf = 2 * kHalf;                // one K or V tile, or 128 rows of Q
 constexpr int kInfo = 8;                       // tiles whose load info is kept
 constexpr int kSoft = 256;                     // softmax threads
-constexpr int kWideThreads = kSoft + 64;       // + producer warp, MMA warp
+constexpr int kWideThreads = kSoft + 128;      // + producer warp, MMA warp, two idle ones
+// Registers per thread: the launch gives every thread kRegsLaunch (the most
+// that 384 threads can have); the third warpgroup hands kRegsLaunch - kRegsLoad
+// back and the softmax warpgroups, which hold 128 scores each, take them.
+constexpr int kRegsLaunch = 168, kRegsLoad = 88, kRegsSoft = 208;
+static_assert(2 * kRegsSoft + kRegsLoad <= 3 * kRegsLaunch, "registers of the launch");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream
 
@@ -225,6 +230,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   const int64_t s_c = c < int(cut.G) && W > 0 ? cut.start(c) : 0;
   const int64_t e_c = c < int(cut.G) && W > 0 ? cut.start(c + 1) : 0;
 
+  if (warp >= 8) {
+  reg_dealloc<kRegsLoad>();
   if (warp == 8) {
     // ------------------------------------------------------------ producer
     // Items (K or V of a tile) in the order the MMA warp uses them: the K of
@@ -406,8 +413,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     __syncwarp();
     const volatile int never = 0;
     mbar_wait(bar(Cfg::B_FINAL), 0, &never);
+  }
   } else {
     // ------------------------------------------------------ softmax, epilogue
+    reg_alloc<kRegsSoft>();
     const int s = warp >> 2;                          // stream
     const int row = 32 * (warp & 3) + lane;           // TMEM lane
     const int wtid = tid & 127;                       // thread of the warpgroup
@@ -774,6 +783,11 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!done[device]) {
+    // the register split above counts on this many per thread at launch: with
+    // fewer, the softmax warpgroups would wait for registers that never come
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, gqa_wide_kernel<MT>)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(WideCfg<MT>::kSmemMax))) != cudaSuccess)
       return e;

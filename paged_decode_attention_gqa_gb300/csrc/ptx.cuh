@@ -426,3 +426,18 @@ __device__ __forceinline__ void st_global_v8(void* dst, uint32_t a0, uint32_t a1
 }
 
 }  // namespace zl
+
+namespace zl {
+
+// Registers per thread of the executing warpgroup from here on: hand back down
+// to N, or take up to N (waits until they are free).
+template <int N>
+__device__ __forceinline__ void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+}  // namespace zl
