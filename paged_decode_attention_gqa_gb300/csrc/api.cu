@@ -97,7 +97,7 @@ struct GqaPlan {
   int64_t score_stride = 0;
   // modified scores with many rows: the tcgen05 kernel (gqa_wide.cu)
   bool wide = false;
-  int mt = 1, nblk = 1;
+  int tpt = 1, mt = 1, nblk = 1;
 };
 
 // Rows per kv head above which a modified-score call runs the tcgen05 kernel.
@@ -172,8 +172,10 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
   const int rows_per_head = plan->g * a->q_len;
   if (mods && !mods->weights && rows_per_head > kWideRows) {
     plan->wide = true;
-    plan->mt = rows_per_head > 128 ? 2 : 1;
-    plan->nblk = (rows_per_head + plan->mt * 128 - 1) / (plan->mt * 128);
+    plan->tpt = 128 / plan->g;
+    const int row_tiles = (a->q_len + plan->tpt - 1) / plan->tpt;
+    plan->mt = row_tiles > 1 ? 2 : 1;
+    plan->nblk = (row_tiles + plan->mt - 1) / plan->mt;
     plan->grid = a->num_ctas > 0 ? a->num_ctas : dev.sms;
     if (a->num_ctas == 0 && a->max_seq_len > 0) {
       int64_t len = a->max_seq_len;
@@ -383,6 +385,23 @@ zl_status encode_pool_map(CUtensorMap* map, const void* pool, const zl_decode_at
   return ZL_OK;
 }
 
+// Query rows [B, q_len, Hq, 128] in boxes of g heads x tpt tokens.
+zl_status encode_query_map(CUtensorMap* map, const zl_decode_attn_params* a, int g, int tpt) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return ZL_ERR_CUDA;
+  const cuuint64_t row = cuuint64_t(a->D_qk) * 2;
+  const cuuint64_t dims[4] = {cuuint64_t(a->D_qk), cuuint64_t(a->Hq), cuuint64_t(a->q_len),
+                              cuuint64_t(a->B)};
+  const cuuint64_t strides[3] = {row, row * a->Hq, row * a->Hq * a->q_len};
+  const cuuint32_t box[4] = {64, cuuint32_t(g), cuuint32_t(tpt), 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a->q),
+                            dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ZL_OK : ZL_ERR_UNSUPPORTED;
+}
+
 zl_status validate_pointers(const zl_decode_attn_params* a, bool need_v) {
   if (!a->q || !a->k_pool || !a->block_table || !a->seq_lens || !a->out)
     return ZL_ERR_INVALID_ARG;
@@ -471,7 +490,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   zl_status st;
   if ((st = encode_pool_map(&p.tmap_k, a->k_pool, a, 1, p.box)) != ZL_OK) return st;
   if ((st = encode_pool_map(&p.tmap_v, a->v_pool, a, 1, p.box)) != ZL_OK) return st;
-  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  if ((st = encode_query_map(&p.tmap_q, a, plan.g, plan.tpt)) != ZL_OK) return st;
   p.out = static_cast<__nv_bfloat16*>(a->out);
   p.lse = a->lse;
   p.block_table = a->block_table;
@@ -489,6 +508,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.g = plan.g;
   p.page_size = a->page_size;
   p.num_pages = a->num_pages;
+  p.tpt = plan.tpt;
   p.mt = plan.mt;
   p.nblk = plan.nblk;
   p.len_cap = a->block_table_stride * int64_t(a->page_size);

@@ -38,7 +38,7 @@ constexpr int kHalf = kWT * 128;               // 16 KB: 128 rows x 64 columns
 constexpr int kBuf = 2 * kHalf;                // one K or V tile, or 128 rows of Q
 constexpr int kInfo = 8;                       // tiles whose load info is kept
 constexpr int kSoft = 256;                     // softmax threads
-constexpr int kWideThreads = kSoft + 128;      // + producer warp, MMA warp, two idle ones
+constexpr int kWideThreads = kSoft + 128;      // + K, MMA, V and Q warps
 // Registers per thread: the launch gives every thread kRegsLaunch (the most
 // that 384 threads can have); the third warpgroup hands kRegsLaunch - kRegsLoad
 // back and the softmax warpgroups, which hold 128 scores each, take them.
@@ -50,18 +50,28 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream
 template <int MT>
 struct WideCfg {
   static constexpr int kRing = MT == 2 ? 4 : 5;      // K/V buffers
-  static constexpr int kAhead = MT == 2 ? 1 : 2;     // tiles QK runs ahead of PV
   static constexpr int kOffRing = MT * kBuf;
   static constexpr int kOffBar = kOffRing + kRing * kBuf;
+  // (MASK and DONE of piece i are barriers i & 1: the same barrier's next phase
+  // then waits for those that wait for this one)
   enum : int {
-    B_Q = 0, B_ML, B_FINAL, B_S0, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_FULL0 = B_O0 + 2,
+    B_Q = 0, B_QFREE, B_MASK0, B_DONE0 = B_MASK0 + 2, B_ML = B_DONE0 + 2, B_FINAL, B_S0, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_FULL0 = B_O0 + 2,
     B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing, B_COUNT = B_INFO0 + kInfo
   };
   static constexpr int kOffMisc = kOffBar + 8 * B_COUNT;   // TMEM address, abort flag
   static constexpr int kOffInfo = kOffMisc + 16;           // kInfo words
-  static constexpr int kOffMl = kOffInfo + 4 * kInfo;      // [2][128] (m, l), MT = 1
-  static constexpr int kOffDepth = kOffMl + (MT == 1 ? 2 * 128 * 8 : 0);  // [2][128] bytes
+  static constexpr int kOffMl = kOffInfo + 4 * kInfo;      // [2][2][128] (m, l), MT = 1
+  static constexpr int kOffMask = kOffMl + (MT == 1 ? 4 * 128 * 8 : 0);  // [2][512] words
+  static constexpr int kOffDepth = kOffMask + 2 * 512 * 4;               // [2][128] bytes
   static constexpr int kOffPrefix = kOffDepth + 2 * 128;
+  // Ring place of K and V of tile t (of n in its piece, tile_no tiles before it
+  // in the CTA): the order in which the MMA warp uses them.
+  static __device__ __forceinline__ uint32_t k_item(uint32_t tile_no, int t) {
+    return 2 * tile_no + uint32_t(MT == 2 ? 2 * t : t == 0 ? 0 : 2 * t - 1);
+  }
+  static __device__ __forceinline__ uint32_t v_item(uint32_t tile_no, int t, int n) {
+    return 2 * tile_no + uint32_t(MT == 2 ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1));
+  }
   static constexpr size_t smem_bytes(int B) { return 1024 + kOffPrefix + size_t(B + 1) * 4; }
   static constexpr size_t kSmemMax = smem_bytes(kMaxBatch);
   static_assert(kSmemMax <= 232448, "shared memory of one CTA");
@@ -93,10 +103,10 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 // Drafted bits [j0, j0 + 32) of a row's ancestor mask (words 32-bit words).
 __device__ __forceinline__ uint32_t mask_word(const uint32_t* bits, int words, int j0) {
   if (j0 <= -32 || j0 >= 32 * words) return 0u;
-  if (j0 < 0) return __ldg(bits) << (-j0);
+  if (j0 < 0) return bits[0] << (-j0);
   const int w = j0 >> 5, sh = j0 & 31;
-  uint32_t x = __ldg(bits + w) >> sh;
-  if (sh && w + 1 < words) x |= __ldg(bits + w + 1) << (32 - sh);
+  uint32_t x = bits[w] >> sh;
+  if (sh && w + 1 < words) x |= bits[w + 1] << (32 - sh);
   return x;
 }
 
@@ -129,9 +139,9 @@ __device__ __forceinline__ Piece piece_at(const WideParams& p, const int* prefix
   const int U = p.Hkv * p.nblk;
   q.b = locate_seq(prefix, p.B, U, idx);
   q.n_unit = prefix[q.b + 1] - prefix[q.b];
-  const int64_t unit0 = int64_t(U) * prefix[q.b];
-  const int u = int((idx - unit0) / q.n_unit);
-  q.j0 = int((idx - unit0) % q.n_unit);
+  const int64_t unit0 = int64_t(U) * prefix[q.b], off = idx - unit0;
+  const int u = off <= 0x7fffffff ? int(off) / q.n_unit : int(off / q.n_unit);
+  q.j0 = int(off - int64_t(u) * q.n_unit);
   q.kvh = u / p.nblk;
   q.blk = u % p.nblk;
   const int64_t unit_end = unit0 + int64_t(u + 1) * q.n_unit;
@@ -148,7 +158,7 @@ template <int MT>
 __global__ void __launch_bounds__(kWideThreads, 1)
 gqa_wide_kernel(const __grid_constant__ WideParams p) {
   using Cfg = WideCfg<MT>;
-  constexpr int NB = Cfg::kRing, D = Cfg::kAhead;
+  constexpr int NB = Cfg::kRing;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -158,16 +168,20 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 8);
   uint32_t* info = reinterpret_cast<uint32_t*>(smem + Cfg::kOffInfo);
   float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffMl);
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMask);
   uint8_t* depth_s = smem + Cfg::kOffDepth;
   int* prefix = reinterpret_cast<int*>(smem + Cfg::kOffPrefix);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.B;
 
   if (tid == 0) {
-    mbar_init(bar(Cfg::B_Q), kSoft);
+    mbar_init(bar(Cfg::B_Q), 1);
+    mbar_init(bar(Cfg::B_QFREE), 1);
     mbar_init(bar(Cfg::B_ML), kSoft);
     mbar_init(bar(Cfg::B_FINAL), 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(Cfg::B_MASK0 + s), 32);
+      mbar_init(bar(Cfg::B_DONE0 + s), kSoft);
       mbar_init(bar(Cfg::B_S0 + s), 1);
       mbar_init(bar(Cfg::B_P0 + s), 128);
       mbar_init(bar(Cfg::B_O0 + s), 1);
@@ -190,6 +204,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
+    tma_prefetch_desc(&p.tmap_q);
   }
   if (warp == 0) {  // tiles per sequence, exclusive prefix sum
     const int per = (B + 31) / 32, b0 = lane * per;
@@ -231,90 +246,133 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   const int64_t e_c = c < int(cut.G) && W > 0 ? cut.start(c + 1) : 0;
 
   if (warp >= 8) {
-  reg_dealloc<kRegsLoad>();
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
-    // Items (K or V of a tile) in the order the MMA warp uses them: the K of
-    // the first D tiles, then V of tile t and K of tile t + D. Lane i loads
-    // half i & 1 (64 columns) of token block i >> 1 of the tile; blocks wholly
-    // past the cache end or before the oldest window, or on a bad page, are
-    // not loaded.
-    const int nblocks = kWT / p.box;
-    const int blk = lane >> 1, half = lane & 1;
-    uint32_t item = 0, tile_no = 0;
-    bool ok = true;
-    for (int64_t idx = s_c; idx < e_c && ok;) {
-      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
-      const int32_t* bt = p.block_table + int64_t(pc.b) * p.bt_stride;
-      const int lo = p.window ? pc.L - p.q_total - p.window + 1 : 0;
-      // this lane's block of tile t: page, or -1 (nothing there), -2 (bad page)
-      auto page_of = [&](int t) -> int {
-        const int tok = (pc.tile0 + t) * kWT + blk * p.box;
-        if (blk >= nblocks || t >= pc.ntiles || tok >= pc.L || tok + p.box <= lo) return -1;
-        const int pg = __ldg(bt + tok / p.page_size);
-        return pg < 0 || pg >= p.num_pages ? -2 : pg;
-      };
-      auto load = [&](const CUtensorMap* map, int t, int page) -> bool {
-        const uint32_t s = item % NB, ph = (item / NB) & 1;
-        if (!mbar_wait(bar(Cfg::B_EMPTY0 + s), ph ^ 1u, abort_flag)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        ++item;
-        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-        const uint32_t fb = bar(Cfg::B_FULL0 + s);
-        if (lane == 0) {
-          const uint32_t bytes = uint32_t(__popc(there)) * uint32_t(p.box) * 128u;
-          if (bytes) mbar_arrive_expect_tx(fb, bytes);
-          else mbar_arrive(fb);
+    reg_dealloc<kRegsLoad>();
+    if (warp == 8 || warp == 10) {
+      // --------------------------------------------------- K and V producers
+      // Warp 8 loads the K, warp 10 the V of every tile into the ring places
+      // of their turn. Lane i looks up the page of the tile's token block i;
+      // blocks wholly past the cache end or before the oldest window, or on a
+      // bad page, are not loaded. (One warp for both took 1300-1700 cycles to
+      // issue the 16 copies of a tile with 16-token pages, and bounded the
+      // kernel.)
+      const bool is_v = warp == 10;
+      const CUtensorMap* map = is_v ? &p.tmap_v : &p.tmap_k;
+      const int nblocks = kWT / p.box;
+      uint32_t tile_no = 0;
+      bool ok = true;
+      for (int64_t idx = s_c; idx < e_c && ok;) {
+        const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+        const int32_t* bt = p.block_table + int64_t(pc.b) * p.bt_stride;
+        const int lo = p.window ? pc.L - p.q_total - p.window + 1 : 0;
+        // this lane's block of tile t: its page, -1 (nothing there), -2 (bad page)
+        auto page_of = [&](int t) -> int {
+          const int tok = (pc.tile0 + t) * kWT + lane * p.box;
+          if (lane >= nblocks || t >= pc.ntiles || tok >= pc.L || tok + p.box <= lo) return -1;
+          const int pg = __ldg(bt + tok / p.page_size);
+          return pg < 0 || pg >= p.num_pages ? -2 : pg;
+        };
+        int page = page_of(0);
+        for (int t = 0; t < pc.ntiles && ok; ++t) {
+          const int ahead = page_of(t + 1);  // in flight while this tile waits
+          const uint32_t item = is_v ? Cfg::v_item(tile_no, t, pc.ntiles) : Cfg::k_item(tile_no, t);
+          const uint32_t s = item % NB, ph = (item / NB) & 1;
+          const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+          const uint32_t fb = bar(Cfg::B_FULL0 + s);
+          const uint32_t dst = sbase + Cfg::kOffRing + s * kBuf;
+          const int slot0 = (pc.tile0 + t) * kWT % p.page_size;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(Cfg::B_EMPTY0 + s), ph ^ 1u, abort_flag));
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bytes = uint32_t(__popc(there)) * uint32_t(p.box) * 256u;
+            if (bytes) mbar_arrive_expect_tx(fb, bytes);
+            else mbar_arrive(fb);
+          }
+          __syncwarp();
+          int slot = slot0;
+#pragma unroll
+          for (int k = 0; k < kWT / kGqaTile; ++k) {
+            if (k >= nblocks) break;
+            const int pg = __shfl_sync(0xffffffffu, page, k);
+            if (pg >= 0 && elect_one()) {
+              const uint32_t d = dst + uint32_t(k * p.box) * 128u;
+              tma_load_4d(d, map, fb, 0, slot, pc.kvh, pg);
+              tma_load_4d(d + kHalf, map, fb, 64, slot, pc.kvh, pg);
+            }
+            __syncwarp();
+            slot += p.box;
+            if (slot >= p.page_size) slot -= p.page_size;
+          }
+          if (!is_v) {
+            // what the softmax threads need to know of the tile's 16-token
+            // blocks: bits 0-7 on a bad page, bits 8-15 not loaded
+            const int n = p.box / 16;
+            const uint32_t mine = lane < nblocks ? ((1u << n) - 1u) << (lane * n) : 0u;
+            const uint32_t word = __reduce_or_sync(
+                0xffffffffu, (page == -2 ? mine : 0u) | (page < 0 ? mine << 8 : 0u));
+            const uint32_t i = (tile_no + t) % kInfo;
+            if (lane == 0) {
+              info[i] = word;
+              mbar_arrive(bar(Cfg::B_INFO0 + i));
+            }
+          }
+          page = ahead;
+        }
+        tile_no += pc.ntiles;
+        idx = pc.next;
+      }
+      if (!ok && lane == 0) {
+        raise_error(p.err_flags, kErrTimeout);
+        *abort_flag = 1;
+      }
+    } else if (warp == 11) {
+      // ------------------------------------------------------------ Q loader
+      // The piece's Q rows (two bulk copies per row tile: rows (token, head) in
+      // the order of the tensor, tokens past the last one read as zeros) as
+      // soon as the last QK of the piece before is done, and the tree's masks
+      // and depths in a buffer of their own.
+      uint32_t pieces = 0;
+      bool ok = true;
+      for (int64_t idx = s_c; idx < e_c && ok; ++pieces) {
+        const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+        if (p.tree) {
+          const int words = p.q_total * p.tree_words;
+          const uint32_t* src = p.tree + int64_t(pc.b) * words;
+          uint32_t* dst = mask_s + (pieces & 1) * 512;
+          if (pieces >= 2)  // the piece that used this buffer
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(Cfg::B_DONE0 + (pieces & 1)),
+                                                   ((pieces >> 1) - 1) & 1, abort_flag));
+          if (!ok) break;
+          for (int i = lane; i < words; i += 32) dst[i] = __ldg(src + i);
+          __syncwarp();
+          for (int i = lane; i < p.q_total; i += 32) {
+            int n = 0;
+            for (int w = 0; w < p.tree_words; ++w) n += __popc(dst[i * p.tree_words + w]);
+            depth_s[(pieces & 1) * 128 + i] = uint8_t(max(n - 1, 0));
+          }
+          mbar_arrive(bar(Cfg::B_MASK0 + (pieces & 1)));
+        }
+        if (pieces > 0)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(bar(Cfg::B_QFREE), (pieces - 1) & 1, abort_flag));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar(Cfg::B_Q), uint32_t(MT * 2 * 128 * p.g * p.tpt));
+#pragma unroll
+          for (int s = 0; s < MT; ++s) {
+            const int tok = (pc.blk * MT + s) * p.tpt;
+            tma_load_4d(sbase + s * kBuf, &p.tmap_q, bar(Cfg::B_Q), 0, pc.kvh * p.g, tok, pc.b);
+            tma_load_4d(sbase + s * kBuf + kHalf, &p.tmap_q, bar(Cfg::B_Q), 64, pc.kvh * p.g,
+                        tok, pc.b);
+          }
         }
         __syncwarp();
-        if (page >= 0) {
-          const int tok = (pc.tile0 + t) * kWT + blk * p.box;
-          tma_load_4d(sbase + Cfg::kOffRing + s * kBuf + half * kHalf + blk * p.box * 128, map,
-                      fb, half * 64, tok % p.page_size, pc.kvh, page);
-        }
-        return true;
-      };
-      int pages[D + 1];  // of tiles t .. t + D
-#pragma unroll
-      for (int i = 0; i <= D; ++i) pages[i] = page_of(i);
-      // K of tile t, with what the softmax threads need to know of its blocks:
-      // bits 0-7 the 16-token blocks on a bad page, bits 8-15 those not loaded
-      auto load_k = [&](int t, int page) -> bool {
-        const uint32_t n = p.box / 16;
-        const uint32_t mine = half == 0 && blk < nblocks ? ((1u << n) - 1u) << (blk * n) : 0u;
-        const uint32_t word = __reduce_or_sync(
-            0xffffffffu, (page == -2 ? mine : 0u) | (page < 0 ? mine << 8 : 0u));
-        if (!load(&p.tmap_k, t, page)) return false;
-        if (lane == 0) {
-          info[tile_no % kInfo] = word;
-          mbar_arrive(bar(Cfg::B_INFO0 + tile_no % kInfo));
-        }
-        ++tile_no;
-        return true;
-      };
-#pragma unroll
-      for (int t = 0; t < D; ++t)
-        if (t < pc.ntiles && ok) load_k(t, pages[t]);
-      for (int t = 0; t < pc.ntiles && ok; ++t) {
-        const int ahead = page_of(t + D + 1);  // in flight while the loads wait
-        if (!load(&p.tmap_v, t, pages[0])) break;
-        if (t + D < pc.ntiles && !load_k(t + D, pages[D])) break;
-#pragma unroll
-        for (int i = 0; i < D; ++i) pages[i] = pages[i + 1];
-        pages[D] = ahead;
+        idx = pc.next;
       }
-      idx = pc.next;
-    }
-    if (!ok && lane == 0) {
-      raise_error(p.err_flags, kErrTimeout);
-      *abort_flag = 1;
-    }
-    // Leave no copy in flight.
-    const volatile int never = 0;
-    for (uint32_t i = item > NB ? item - NB : 0; i < item; ++i)
-      mbar_wait(bar(Cfg::B_FULL0 + i % NB), (i / NB) & 1, &never);
-  } else if (warp == 9) {
+      if (!ok && lane == 0) {
+        raise_error(p.err_flags, kErrTimeout);
+        *abort_flag = 1;
+      }
+    } else {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
     const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
@@ -330,7 +388,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       return sbase + Cfg::kOffRing + (it % NB) * kBuf;
     };
     // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step
-    auto qk = [&](int s, uint32_t it, bool release) {
+    auto qk = [&](int s, uint32_t it, bool release, bool last) {
       tc_fence_after();
       if (elect_one()) {
         const uint32_t qb = sbase + (MT == 2 ? s * kBuf : 0), kb = buf(it);
@@ -340,8 +398,9 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           umma_bf16(tmem + kTmemS + 128 * s, umma_smem_desc(qb + off, 0, 1024, 2),
                     umma_smem_desc(kb + off, 0, 1024, 2), idesc_qk, k ? 1u : 0u);
         }
-        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
         umma_commit(bar(Cfg::B_S0 + s));
+        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
+        if (last) umma_commit(bar(Cfg::B_QFREE));  // Q is read for the last time
       }
       __syncwarp();
     };
@@ -355,8 +414,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           umma_bf16_tmem_a(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * k,
                            umma_smem_desc(vb + k * 16 * 128, kHalf, 1024, 2), idesc_pv,
                            first && k == 0 ? 0u : 1u);
-        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
         if (last) umma_commit(bar(Cfg::B_O0 + s));
+        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
       }
       __syncwarp();
     };
@@ -366,8 +425,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       if (!wait(Cfg::B_Q, pieces & 1)) break;
       if (MT == 2) {
         if (!wait_item(item)) break;
-        qk(0, item, false);
-        qk(1, item, true);
+        qk(0, item, false, false);
+        qk(1, item, true, n == 1);
         ++item;
         for (int t = 0; t < n && ok; ++t) {
           const uint32_t iv = item, ik = item + 1;
@@ -377,19 +436,21 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           ++pn[0];
           if (more) {
             if (!wait_item(ik)) break;
-            qk(0, ik, false);
+            qk(0, ik, false, false);
           }
           if (!wait(Cfg::B_P0 + 1, pn[1] & 1)) break;
           pv(1, iv, t == 0, true, !more);
           ++pn[1];
-          if (more) qk(1, ik, true);
+          if (more) qk(1, ik, true, t + 2 == n);
           item += more ? 2 : 1;
         }
       } else {
         for (int t = 0; t < 2 && t < n; ++t) {
           if (!wait_item(item)) break;
-          qk(t, item++, true);
+          qk(t, item++, true, t + 1 == n);
         }
+        // the softmax threads of both streams read both O at a piece's end
+        if (pieces > 0 && !wait(Cfg::B_DONE0 + ((pieces - 1) & 1), ((pieces - 1) >> 1) & 1)) break;
         for (int t = 0; t < n && ok; ++t) {
           const int s = t & 1;
           if (!wait_item(item) || !wait(Cfg::B_P0 + s, pn[s] & 1)) break;
@@ -397,7 +458,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           ++pn[s];
           if (t + 2 < n) {
             if (!wait_item(item)) break;
-            qk(s, item++, true);
+            qk(s, item++, true, t + 3 == n);
           }
         }
       }
@@ -419,10 +480,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     reg_alloc<kRegsSoft>();
     const int s = warp >> 2;                          // stream
     const int row = 32 * (warp & 3) + lane;           // TMEM lane
-    const int wtid = tid & 127;                       // thread of the warpgroup
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t ts = tl + kTmemS + 128 * s, to = tl + kTmemO + 128 * s;
-    const int nrows = p.g * p.q_total;
     bool ok = true;
     auto wait_all = [&](int i, uint32_t parity) -> bool {
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag));
@@ -433,46 +492,17 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     for (int64_t idx = s_c; idx < e_c && ok; ++pieces) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
       const int n = pc.ntiles, L = pc.L, ctx = L - p.q_total;
-      const int blk0 = pc.blk * MT * 128;
-      const int r = blk0 + (MT == 2 ? s * 128 : 0) + row;
-      const bool exists = r < nrows;
-      const int qi = exists ? r / p.g : 0, head = pc.kvh * p.g + (exists ? r % p.g : 0);
-
-      // Q rows into the swizzled K-major layout: MT = 2, this stream's own; MT
-      // = 1, half of the shared ones. (Every QK of the piece before is done: a
-      // softmax thread has seen its last S, and for MT = 1 both have met.)
-      {
-        constexpr int kPer = MT == 2 ? 16 : 8;
-        const uint32_t qb = sbase + (MT == 2 ? s * kBuf : 0);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int ch = i * 128 + wtid, k = ch & 15;
-          const int rr = (ch >> 4) + (MT == 2 ? 0 : s * 64);
-          const int rg = blk0 + (MT == 2 ? s * 128 : 0) + rr;
-          const uint32_t dst = qb + (k >> 3) * kHalf + rr * 128 + (((k & 7) ^ (rr & 7)) << 4);
-          if (rg < nrows) {
-            const int64_t qrow =
-                (int64_t(pc.b) * p.q_total + rg / p.g) * p.Hq + pc.kvh * p.g + rg % p.g;
-            cp_async_16(dst, p.q + qrow * kGqaHeadDim + k * 8);
-          } else {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u)
-                         : "memory");
-          }
-        }
-      }
-      const uint32_t* seq_bits =
-          p.tree ? p.tree + int64_t(pc.b) * p.q_total * p.tree_words : nullptr;
-      const uint32_t* bits = p.tree ? seq_bits + int64_t(qi) * p.tree_words : nullptr;
-      const int pos = ctx + (p.tree ? tree_depth(bits, p.tree_words) : qi);
+      // Row `row` of this stream's row tile: token row / g of the tile's tpt,
+      // head row % g (rows past the last token have zeros in Q, rows past g tpt
+      // whatever the buffer holds: both are computed and dropped).
+      const int tile = pc.blk * MT + (MT == 2 ? s : 0);
+      const int qi_all = tile * p.tpt + row / p.g;
+      const bool exists = row < p.g * p.tpt && qi_all < p.q_total;
+      const int qi = exists ? qi_all : 0, head = pc.kvh * p.g + (exists ? row % p.g : 0);
+      const uint32_t* bits = mask_s + (pieces & 1) * 512 + qi * p.tree_words;
       const uint8_t* depth = depth_s + (pieces & 1) * 128;
-      if (p.tree && s == 0 && wtid < p.q_total)
-        depth_s[(pieces & 1) * 128 + wtid] =
-            uint8_t(tree_depth(seq_bits + int64_t(wtid) * p.tree_words, p.tree_words));
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      mbar_arrive(bar(Cfg::B_Q));
-      if (p.tree && !wait_all(Cfg::B_Q, pieces & 1)) break;  // the depths
-
+      if (p.tree && !wait_all(Cfg::B_MASK0 + (pieces & 1), (pieces >> 1) & 1)) break;
+      const int pos = ctx + (p.tree ? int(depth[qi]) : qi);
       const int lo_unit = p.window ? ctx - p.window + 1 : 0;  // oldest token any row sees
       const int lo_row = p.window ? pos - p.window + 1 : -(1 << 30);
       const float slope2 = p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
@@ -550,8 +580,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           // V rows that were not loaded, lie past the end or before the oldest
           // window are zeroed (P is 0 there, but 0 * NaN is not)
           if (MT == 1 || s == 0) {
-            // item numbers of the CTA: two per tile; see the producer's order
-            const uint32_t iv = 2 * tile_no + uint32_t(MT == 2 ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1));
+            const uint32_t iv = Cfg::v_item(tile_no, t, n);
             if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
             const int tok = tok0 + row;
             if (((load_info >> (8 + (row >> 4))) & 1u) || tok >= L || tok < lo_unit) {
@@ -615,10 +644,11 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       float mine = 1.f, theirs = 0.f;  // weights of this and the other stream's O
       bool both = false;
       if (MT == 1) {
-        ml[s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
+        float2* mlp = ml + (pieces & 1) * 256;
+        mlp[s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
         mbar_arrive(bar(Cfg::B_ML));
         if (!wait_all(Cfg::B_ML, pieces & 1)) break;
-        const float2 o = ml[(s ^ 1) * 128 + row];
+        const float2 o = mlp[(s ^ 1) * 128 + row];
         bad |= isnan(o.y);
         both = n > 1;  // stream 1 had a tile
         const float mn = fmaxf(m, o.x);
@@ -696,6 +726,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
       }
       tc_fence_before();
+      mbar_arrive(bar(Cfg::B_DONE0 + (pieces & 1)));
       tile_no += n;
       idx = pc.next;
     }
@@ -717,6 +748,13 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort_flag) {
+    // a role gave up: copies may still be on their way into this CTA's shared
+    // memory (otherwise the MMA warp has waited for every one)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000) {
+    }
+  }
   if (warp == 9) {
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
@@ -750,8 +788,9 @@ __global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ Wi
   }
   const int c_hi = cut.owner(U0 + n - 1);
   const int row = blockIdx.y * 8 + warp;
-  const int r = (u % p.nblk) * MT * 128 + row;
-  if (r >= p.g * p.q_total) return;
+  const int tile = (u % p.nblk) * MT + row / 128, r = row % 128;
+  const int qi = tile * p.tpt + r / p.g;
+  if (r >= p.g * p.tpt || qi >= p.q_total) return;
   MergeAcc<1> acc;
   acc.init();
   for (int cc = c - 1; cc <= c_hi; ++cc) {
@@ -762,8 +801,7 @@ __global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ Wi
   }
   const bool none = acc.bad || !(acc.den[0] > 0.f);
   const float inv = none ? 0.f : 1.f / acc.den[0];
-  const int64_t orow =
-      (int64_t(b) * p.q_total + r / p.g) * p.Hq + (u / p.nblk) * p.g + r % p.g;
+  const int64_t orow = (int64_t(b) * p.q_total + qi) * p.Hq + (u / p.nblk) * p.g + r % p.g;
   uint2 o = make_uint2(0u, 0u);
   if (!none)
     o = make_uint2(pack_bf16x2(acc.acc[0].x * inv, acc.acc[0].y * inv),

@@ -10,7 +10,7 @@ constexpr int kWideTile = 128;  // tokens per tile
 struct WideParams {
   CUtensorMap tmap_k;  // 4-D {D, page_size, Hkv, num_pages}, box {64, box, 1, 1}, 128B swizzle
   CUtensorMap tmap_v;
-  const __nv_bfloat16* q;  // [B, q_total, Hq, 128]
+  CUtensorMap tmap_q;  // 4-D {D, Hq, q_total, B}, box {64, g, tpt, 1}, 128B swizzle
   __nv_bfloat16* out;
   float* lse;              // natural log, or nullptr
   const int32_t* block_table;
@@ -22,7 +22,8 @@ struct WideParams {
   uint32_t* err_flags;
   int B, q_total, Hq, Hkv, g, page_size, num_pages;
   int box;   // tokens per bulk copy: the largest of 128, 64, 32, 16 dividing page_size
-  int mt;    // 1: at most 128 rows per kv head, 2: blocks of 256 rows
+  int tpt;   // query tokens per row tile: 128 / g
+  int mt;    // row tiles per row block: 1 (the call has only one) or 2
   int nblk;  // row blocks per kv head
   int64_t len_cap;
   float scale_log2, cap_in, cap_out;  // as in GqaParams
