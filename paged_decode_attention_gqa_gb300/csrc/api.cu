@@ -169,13 +169,15 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
   DeviceInfo dev;
   if ((st = current_device(&dev)) != ZL_OK) return st;
   plan->g = a->Hq / a->Hkv;
-  const int rows_per_head = plan->g * a->q_len;
-  if (mods && !mods->weights && rows_per_head > kWideRows) {
+  plan->tpt = 128 / plan->g;
+  const int row_tiles = (a->q_len + plan->tpt - 1) / plan->tpt;
+  plan->mt = row_tiles > 1 ? 2 : 1;
+  plan->nblk = (row_tiles + plan->mt - 1) / plan->mt;
+  // (the tcgen05 kernel counts tiles in 32 bits)
+  const double most_tiles = double(a->B) * a->Hkv * plan->nblk *
+                            (double(a->block_table_stride) * a->page_size / zl::kWideTile + 1);
+  if (mods && !mods->weights && plan->g * a->q_len > kWideRows && most_tiles < 2e9) {
     plan->wide = true;
-    plan->tpt = 128 / plan->g;
-    const int row_tiles = (a->q_len + plan->tpt - 1) / plan->tpt;
-    plan->mt = row_tiles > 1 ? 2 : 1;
-    plan->nblk = (row_tiles + plan->mt - 1) / plan->mt;
     plan->grid = a->num_ctas > 0 ? a->num_ctas : dev.sms;
     if (a->num_ctas == 0 && a->max_seq_len > 0) {
       int64_t len = a->max_seq_len;

@@ -38,12 +38,8 @@ constexpr int kHalf = kWT * 128;               // 16 KB: 128 rows x 64 columns
 constexpr int kBuf = 2 * kHalf;                // one K or V tile, or 128 rows of Q
 constexpr int kInfo = 8;                       // tiles whose load info is kept
 constexpr int kSoft = 256;                     // softmax threads
-constexpr int kWideThreads = kSoft + 128;      // + K, MMA, V and Q warps
-// Registers per thread: the launch gives every thread kRegsLaunch (the most
-// that 384 threads can have); the third warpgroup hands kRegsLaunch - kRegsLoad
-// back and the softmax warpgroups, which hold 128 scores each, take them.
-constexpr int kRegsLaunch = 168, kRegsLoad = 88, kRegsSoft = 208;
-static_assert(2 * kRegsSoft + kRegsLoad <= 3 * kRegsLaunch, "registers of the launch");
+constexpr int kWideThreads = kSoft + 256;      // + K, MMA, V, Q warps and the epilogue's four
+constexpr int kStage = 32 * 64;                // bytes of an epilogue warp's staging rows
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream
 
@@ -52,18 +48,21 @@ struct WideCfg {
   static constexpr int kRing = MT == 2 ? 4 : 5;      // K/V buffers
   static constexpr int kOffRing = MT * kBuf;
   static constexpr int kOffBar = kOffRing + kRing * kBuf;
-  // (MASK and DONE of piece i are barriers i & 1: the same barrier's next phase
-  // then waits for those that wait for this one)
+  // (MASK, ML and EPI of piece i are barriers i & 1: the same barrier's next
+  // phase then waits for those that wait for this one)
   enum : int {
-    B_Q = 0, B_QFREE, B_MASK0, B_DONE0 = B_MASK0 + 2, B_ML = B_DONE0 + 2, B_FINAL, B_S0, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_FULL0 = B_O0 + 2,
-    B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing, B_COUNT = B_INFO0 + kInfo
+    B_Q = 0, B_QFREE, B_FINAL, B_MASK0, B_ML0 = B_MASK0 + 2, B_EPI0 = B_ML0 + 2,
+    B_S0 = B_EPI0 + 2, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_OFREE0 = B_O0 + 2,
+    B_FULL0 = B_OFREE0 + 2, B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing,
+    B_COUNT = B_INFO0 + kInfo
   };
   static constexpr int kOffMisc = kOffBar + 8 * B_COUNT;   // TMEM address, abort flag
   static constexpr int kOffInfo = kOffMisc + 16;           // kInfo words
-  static constexpr int kOffMl = kOffInfo + 4 * kInfo;      // [2][2][128] (m, l), MT = 1
-  static constexpr int kOffMask = kOffMl + (MT == 1 ? 4 * 128 * 8 : 0);  // [2][512] words
-  static constexpr int kOffDepth = kOffMask + 2 * 512 * 4;               // [2][128] bytes
-  static constexpr int kOffPrefix = kOffDepth + 2 * 128;
+  static constexpr int kOffMl = kOffInfo + 4 * kInfo;          // [2][2][128] (m, l)
+  static constexpr int kOffMask = kOffMl + 2 * 2 * 128 * 8;    // [2][512] words
+  static constexpr int kOffDepth = kOffMask + 2 * 512 * 4;     // [2][128] bytes
+  static constexpr int kOffStage = (kOffDepth + 2 * 128 + 127) / 128 * 128;  // [4] epilogue rows
+  static constexpr int kOffPrefix = kOffStage + 4 * kStage;
   // Ring place of K and V of tile t (of n in its piece, tile_no tiles before it
   // in the CTA): the order in which the MMA warp uses them.
   static __device__ __forceinline__ uint32_t k_item(uint32_t tile_no, int t) {
@@ -117,12 +116,43 @@ __device__ __forceinline__ void hold(uint32_t (&r)[32]) {
   for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
 }
 
+constexpr int kChunk = 64;  // scores a softmax thread holds at a time
+
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint64_t (&x)[kChunk / 2]) {
+  uint32_t v[2][32];
+  tmem_ld32(taddr, v[0]);
+  tmem_ld32(taddr + 32, v[1]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    hold(v[h]);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      x[16 * h + k] =
+          pack_f32x2(__uint_as_float(v[h][2 * k]), __uint_as_float(v[h][2 * k + 1]));
+  }
+}
+
+__device__ __forceinline__ void store_chunk(uint32_t taddr, const uint64_t (&x)[kChunk / 2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 f = unpack_f32x2(x[16 * h + k]);
+      v[2 * k] = __float_as_uint(f.x);
+      v[2 * k + 1] = __float_as_uint(f.y);
+    }
+    tmem_st32(taddr + 32 * h, v);
+  }
+}
+
 // One contiguous run of tiles of one unit, as every role walks them.
 struct Piece {
-  int b, kvh, blk, L, n_unit, j0, ntiles, tile0;
+  int b, kvh, blk, L, ntiles, tile0;
   bool partial;
   int slot;
-  int64_t next;
+  int next;
 };
 
 __device__ __forceinline__ int wide_first_tile(const WideParams& p, int L) {
@@ -133,28 +163,29 @@ __device__ __forceinline__ int wide_tiles(const WideParams& p, int L) {
   return (L + kWT - 1) / kWT - wide_first_tile(p, L);
 }
 
-__device__ __forceinline__ Piece piece_at(const WideParams& p, const int* prefix, int64_t idx,
-                                          int64_t s_c, int64_t e_c) {
+// (Tile numbers fit 32 bits: the host takes this kernel only when they do.)
+__device__ __forceinline__ Piece piece_at(const WideParams& p, const int* prefix, int idx, int s_c,
+                                          int e_c) {
   Piece q;
   const int U = p.Hkv * p.nblk;
   q.b = locate_seq(prefix, p.B, U, idx);
-  q.n_unit = prefix[q.b + 1] - prefix[q.b];
-  const int64_t unit0 = int64_t(U) * prefix[q.b], off = idx - unit0;
-  const int u = off <= 0x7fffffff ? int(off) / q.n_unit : int(off / q.n_unit);
-  q.j0 = int(off - int64_t(u) * q.n_unit);
+  const int first = prefix[q.b], n_unit = prefix[q.b + 1] - first;
+  const int off = idx - U * first, u = off / n_unit, j0 = off - u * n_unit;
   q.kvh = u / p.nblk;
-  q.blk = u % p.nblk;
-  const int64_t unit_end = unit0 + int64_t(u + 1) * q.n_unit;
+  q.blk = u - q.kvh * p.nblk;
+  const int unit_end = U * first + (u + 1) * n_unit;
   q.next = min(e_c, unit_end);
-  q.ntiles = int(q.next - idx);
-  q.partial = q.j0 > 0 || q.next < unit_end;
+  q.ntiles = q.next - idx;
+  q.partial = j0 > 0 || q.next < unit_end;
   q.slot = idx == s_c ? 0 : 1;
   q.L = p.seq_lens[q.b];
-  q.tile0 = wide_first_tile(p, q.L) + q.j0;
+  q.tile0 = wide_first_tile(p, q.L) + j0;
   return q;
 }
 
-template <int MT>
+// CAP: the scores are capped (instances of their own: the uncapped tile loop
+// then has no registers to spare for the polynomial's constants).
+template <int MT, bool CAP>
 __global__ void __launch_bounds__(kWideThreads, 1)
 gqa_wide_kernel(const __grid_constant__ WideParams p) {
   using Cfg = WideCfg<MT>;
@@ -177,14 +208,15 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   if (tid == 0) {
     mbar_init(bar(Cfg::B_Q), 1);
     mbar_init(bar(Cfg::B_QFREE), 1);
-    mbar_init(bar(Cfg::B_ML), kSoft);
     mbar_init(bar(Cfg::B_FINAL), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(Cfg::B_MASK0 + s), 32);
-      mbar_init(bar(Cfg::B_DONE0 + s), kSoft);
+      mbar_init(bar(Cfg::B_ML0 + s), kSoft);
+      mbar_init(bar(Cfg::B_EPI0 + s), 128);
       mbar_init(bar(Cfg::B_S0 + s), 1);
       mbar_init(bar(Cfg::B_P0 + s), 128);
       mbar_init(bar(Cfg::B_O0 + s), 1);
+      mbar_init(bar(Cfg::B_OFREE0 + s), 128);
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(bar(Cfg::B_FULL0 + i), 1);
@@ -242,11 +274,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     for (int b = tid; b <= B; b += kWideThreads) p.ws_prefix[b] = prefix[b];
   const int64_t W = int64_t(p.Hkv) * p.nblk * prefix[B];
   const TileCut cut(W, gridDim.x);
-  const int64_t s_c = c < int(cut.G) && W > 0 ? cut.start(c) : 0;
-  const int64_t e_c = c < int(cut.G) && W > 0 ? cut.start(c + 1) : 0;
+  const int s_c = c < int(cut.G) && W > 0 ? int(cut.start(c)) : 0;
+  const int e_c = c < int(cut.G) && W > 0 ? int(cut.start(c + 1)) : 0;
 
-  if (warp >= 8) {
-    reg_dealloc<kRegsLoad>();
+  if (warp >= 8 && warp < 12) {
     if (warp == 8 || warp == 10) {
       // --------------------------------------------------- K and V producers
       // Warp 8 loads the K, warp 10 the V of every tile into the ring places
@@ -260,7 +291,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       const int nblocks = kWT / p.box;
       uint32_t tile_no = 0;
       bool ok = true;
-      for (int64_t idx = s_c; idx < e_c && ok;) {
+      for (int idx = s_c; idx < e_c && ok;) {
         const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
         const int32_t* bt = p.block_table + int64_t(pc.b) * p.bt_stride;
         const int lo = p.window ? pc.L - p.q_total - p.window + 1 : 0;
@@ -332,14 +363,14 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       // and depths in a buffer of their own.
       uint32_t pieces = 0;
       bool ok = true;
-      for (int64_t idx = s_c; idx < e_c && ok; ++pieces) {
+      for (int idx = s_c; idx < e_c && ok; ++pieces) {
         const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
         if (p.tree) {
           const int words = p.q_total * p.tree_words;
           const uint32_t* src = p.tree + int64_t(pc.b) * words;
           uint32_t* dst = mask_s + (pieces & 1) * 512;
-          if (pieces >= 2)  // the piece that used this buffer
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(Cfg::B_DONE0 + (pieces & 1)),
+          if (pieces >= 2)  // the softmax threads are past the piece that used this buffer
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(Cfg::B_ML0 + (pieces & 1)),
                                                    ((pieces >> 1) - 1) & 1, abort_flag));
           if (!ok) break;
           for (int i = lane; i < words; i += 32) dst[i] = __ldg(src + i);
@@ -419,10 +450,14 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       }
       __syncwarp();
     };
-    for (int64_t idx = s_c; idx < e_c && ok;) {
+    for (int idx = s_c; idx < e_c && ok;) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
       const int n = pc.ntiles;
       if (!wait(Cfg::B_Q, pieces & 1)) break;
+      // the first PV of a stream overwrites the O that the epilogue reads
+      auto o_free = [&](int s) -> bool {
+        return pieces == 0 || wait(Cfg::B_OFREE0 + s, (pieces - 1) & 1);
+      };
       if (MT == 2) {
         if (!wait_item(item)) break;
         qk(0, item, false, false);
@@ -431,17 +466,17 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         for (int t = 0; t < n && ok; ++t) {
           const uint32_t iv = item, ik = item + 1;
           const bool more = t + 1 < n;
-          if (!wait_item(iv) || !wait(Cfg::B_P0, pn[0] & 1)) break;
-          pv(0, iv, t == 0, false, !more);
-          ++pn[0];
-          if (more) {
-            if (!wait_item(ik)) break;
-            qk(0, ik, false, false);
+          if (!wait_item(iv)) break;
+#pragma unroll 1
+          for (int s = 0; s < 2; ++s) {
+            if (!wait(Cfg::B_P0 + s, pn[0] & 1) || (t == 0 && !o_free(s))) break;
+            pv(s, iv, t == 0, s == 1, !more);
+            if (more) {
+              if (s == 0 && !wait_item(ik)) break;
+              qk(s, ik, s == 1, s == 1 && t + 2 == n);
+            }
           }
-          if (!wait(Cfg::B_P0 + 1, pn[1] & 1)) break;
-          pv(1, iv, t == 0, true, !more);
-          ++pn[1];
-          if (more) qk(1, ik, true, t + 2 == n);
+          ++pn[0];
           item += more ? 2 : 1;
         }
       } else {
@@ -449,11 +484,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           if (!wait_item(item)) break;
           qk(t, item++, true, t + 1 == n);
         }
-        // the softmax threads of both streams read both O at a piece's end
-        if (pieces > 0 && !wait(Cfg::B_DONE0 + ((pieces - 1) & 1), ((pieces - 1) >> 1) & 1)) break;
         for (int t = 0; t < n && ok; ++t) {
           const int s = t & 1;
-          if (!wait_item(item) || !wait(Cfg::B_P0 + s, pn[s] & 1)) break;
+          if (!wait_item(item) || !wait(Cfg::B_P0 + s, pn[s] & 1) || (t < 2 && !o_free(s)))
+            break;
           pv(s, item++, t < 2, true, t + 2 >= n);
           ++pn[s];
           if (t + 2 < n) {
@@ -475,9 +509,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     const volatile int never = 0;
     mbar_wait(bar(Cfg::B_FINAL), 0, &never);
   }
-  } else {
-    // ------------------------------------------------------ softmax, epilogue
-    reg_alloc<kRegsSoft>();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------- softmax
     const int s = warp >> 2;                          // stream
     const int row = 32 * (warp & 3) + lane;           // TMEM lane
     const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -488,24 +521,24 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       return ok;
     };
     uint32_t tile_no = 0, pieces = 0, sn = 0;  // tiles of the CTA, pieces, tiles of this stream
-    uint32_t on[2] = {0, 0};                   // finished O of each stream
-    for (int64_t idx = s_c; idx < e_c && ok; ++pieces) {
+    for (int idx = s_c; idx < e_c && ok; ++pieces) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
       const int n = pc.ntiles, L = pc.L, ctx = L - p.q_total;
       // Row `row` of this stream's row tile: token row / g of the tile's tpt,
       // head row % g (rows past the last token have zeros in Q, rows past g tpt
       // whatever the buffer holds: both are computed and dropped).
-      const int tile = pc.blk * MT + (MT == 2 ? s : 0);
-      const int qi_all = tile * p.tpt + row / p.g;
+      const int qi_all = (pc.blk * MT + (MT == 2 ? s : 0)) * p.tpt + row / p.g;
       const bool exists = row < p.g * p.tpt && qi_all < p.q_total;
-      const int qi = exists ? qi_all : 0, head = pc.kvh * p.g + (exists ? row % p.g : 0);
+      const int qi = exists ? qi_all : 0;
       const uint32_t* bits = mask_s + (pieces & 1) * 512 + qi * p.tree_words;
       const uint8_t* depth = depth_s + (pieces & 1) * 128;
       if (p.tree && !wait_all(Cfg::B_MASK0 + (pieces & 1), (pieces >> 1) & 1)) break;
       const int pos = ctx + (p.tree ? int(depth[qi]) : qi);
       const int lo_unit = p.window ? ctx - p.window + 1 : 0;  // oldest token any row sees
-      const int lo_row = p.window ? pos - p.window + 1 : -(1 << 30);
-      const float slope2 = p.slopes ? __ldg(p.slopes + head) * 1.4426950408889634f : 0.f;
+      const int lo_row = p.window ? max(pos - p.window + 1, 0) : 0;
+      const float slope2 =
+          p.slopes ? __ldg(p.slopes + pc.kvh * p.g + (exists ? row % p.g : 0)) * 1.4426950408889634f
+                   : 0.f;
       float m = -CUDART_INF_F, l = 0.f;
       bool bad = false;
       for (int t = MT == 2 ? 0 : s; t < n; t += MT == 2 ? 1 : 2, ++sn) {
@@ -518,87 +551,115 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
                            (!p.window || tok0 >= ctx + p.q_total - p.window);
         if (!wait_all(Cfg::B_S0 + s, sn & 1)) break;
         tc_fence_after();
-        float x[kWT];
-        {
-          uint32_t v[4][32];
+        // The row's scores in two passes over 64-column chunks, two scores to a
+        // register pair: first modified (written back to TMEM) and their max
+        // taken, then exponentiated. A chunk is read from TMEM twice (about 50
+        // cycles) so that a thread holds 64 scores, not 128: those and the
+        // piece's state do not fit 192 registers without spills.
+        // Scores are in units of sc: base 2 once multiplied by it (sc > 0, so it
+        // also takes the max).
+        const bool change = CAP || !plain || p.slopes != nullptr;
+        const float sc = p.slopes ? 1.f : CAP ? p.cap_out : p.scale_log2;
+        float mx = -CUDART_INF_F;
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          uint64_t x[kChunk / 2];
+          load_chunk(ts + kChunk * ch, x);
+          if (CAP) {
+            float hi = 0.f;
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) tmem_ld32(ts + 32 * cc, v[cc]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            hold(v[cc]);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[32 * cc + k] = __uint_as_float(v[cc][k]);
-          }
-        }
-        // scores in units of sc (base 2 once multiplied by it; sc > 0)
-        float sc = p.scale_log2;
-        if (p.cap_in > 0.f) {
-#pragma unroll
-          for (int k = 0; k < kWT; ++k) x[k] = cap_tanh(x[k] * p.cap_in);
-          sc = p.cap_out;
-        }
-        if (p.slopes) {
-          const float d0 = float(pos - tok0);
-          if (p.tree && tok0 + kWT > ctx) {
-#pragma unroll
-            for (int k = 0; k < kWT; ++k) {
-              const int j = tok0 + k - ctx;
-              const int dist = j < 0 ? pos - tok0 - k
-                               : j < p.q_total ? pos - ctx - int(depth[j]) : 0;
-              x[k] = fmaf(-slope2, float(dist), x[k] * sc);
+            for (int k = 0; k < kChunk / 2; ++k) {
+              const float2 f = unpack_f32x2(x[k]);
+              hi = fmaxf(hi, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-          } else {
+            if (__any_sync(0xffffffffu, !(hi * p.cap_in <= 0.5f))) {
 #pragma unroll
-            for (int k = 0; k < kWT; ++k) x[k] = fmaf(slope2, float(k) - d0, x[k] * sc);
+              for (int k = 0; k < kChunk / 2; ++k) {
+                const float2 f = unpack_f32x2(x[k]);
+                x[k] = pack_f32x2(cap_tanh(f.x * p.cap_in), cap_tanh(f.y * p.cap_in));
+              }
+            } else {  // every |s| <= c / 2: the short polynomial, two scores at a time
+              const uint64_t cin = pack_f32x2(p.cap_in, p.cap_in);
+              const uint64_t c4 = pack_f32x2(kTanhLow4, kTanhLow4);
+              const uint64_t c3 = pack_f32x2(kTanhLow3, kTanhLow3);
+              const uint64_t c2 = pack_f32x2(kTanhLow2, kTanhLow2);
+              const uint64_t c1 = pack_f32x2(kTanhLow1, kTanhLow1);
+              const uint64_t c0 = pack_f32x2(kTanhLow0, kTanhLow0);
+#pragma unroll
+              for (int k = 0; k < kChunk / 2; ++k) {
+                const uint64_t y = mul_f32x2(x[k], cin), z = mul_f32x2(y, y);
+                uint64_t q = fma_f32x2(z, c4, c3);
+                q = fma_f32x2(q, z, c2);
+                q = fma_f32x2(q, z, c1);
+                q = fma_f32x2(q, z, c0);
+                x[k] = mul_f32x2(q, y);
+              }
+            }
           }
-          sc = 1.f;
-        }
-        if (!plain) {
+          const int tok = tok0 + kChunk * ch;
+          if (p.slopes) {
+            const float d0 = float(pos - tok), raw = CAP ? p.cap_out : p.scale_log2;
+            const uint64_t sc2 = pack_f32x2(raw, raw), sl2 = pack_f32x2(slope2, slope2);
+            if (p.tree && tok + kChunk > ctx) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int base = tok0 + 32 * w;
-            uint32_t vis;
-            if (p.tree) {
-              vis = bit_range(max(lo_row, 0) - base, min(ctx, L) - base);
-              uint32_t dr = mask_word(bits, p.tree_words, base - ctx) & bit_range(-base, L - base);
-              if (p.window && p.window < p.q_total)  // only then can it hide a drafted token
-                for (uint32_t todo = dr; todo; todo &= todo - 1) {
-                  const int k = __ffs(todo) - 1;
-                  if (pos - ctx - int(depth[base + k - ctx]) >= p.window) dr &= ~(1u << k);
+              for (int k = 0; k < kChunk / 2; ++k) {
+                float d[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = tok + 2 * k + e - ctx;
+                  d[e] = j < 0 ? float(2 * k + e) - d0
+                         : j < p.q_total ? float(int(depth[j]) + ctx - pos) : 0.f;
                 }
-              vis |= dr;
+                x[k] = fma_f32x2(sl2, pack_f32x2(d[0], d[1]), mul_f32x2(x[k], sc2));
+              }
             } else {
-              vis = bit_range(max(lo_row, 0) - base, min(pos + 1, L) - base);
-            }
-            const uint32_t two = load_info >> (2 * w);
-            bad |= (vis & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u))) != 0;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((vis >> k) & 1u)) x[32 * w + k] = -CUDART_INF_F;
-          }
-          // V rows that were not loaded, lie past the end or before the oldest
-          // window are zeroed (P is 0 there, but 0 * NaN is not)
-          if (MT == 1 || s == 0) {
-            const uint32_t iv = Cfg::v_item(tile_no, t, n);
-            if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
-            const int tok = tok0 + row;
-            if (((load_info >> (8 + (row >> 4))) & 1u) || tok >= L || tok < lo_unit) {
-              const uint32_t vr = sbase + Cfg::kOffRing + (iv % NB) * kBuf + row * 128;
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 vr + (k >> 3) * kHalf + (k & 7) * 16),
-                             "r"(0u)
-                             : "memory");
+              for (int k = 0; k < kChunk / 2; ++k)
+                x[k] = fma_f32x2(sl2, pack_f32x2(float(2 * k) - d0, float(2 * k + 1) - d0),
+                                 mul_f32x2(x[k], sc2));
             }
-            fence_proxy_async_smem();
           }
+          if (!plain) {
+#pragma unroll
+            for (int w = 0; w < kChunk / 32; ++w) {
+              const int base = tok + 32 * w;
+              uint32_t vis;
+              if (p.tree) {
+                vis = bit_range(lo_row - base, min(ctx, L) - base);
+                if (base + 32 > ctx) {
+                  uint32_t dr =
+                      mask_word(bits, p.tree_words, base - ctx) & bit_range(-base, L - base);
+                  if (p.window && p.window < p.q_total)  // only then can it hide a drafted token
+                    for (uint32_t todo = dr; todo; todo &= todo - 1) {
+                      const int k = __ffs(todo) - 1;
+                      if (pos - ctx - int(depth[base + k - ctx]) >= p.window) dr &= ~(1u << k);
+                    }
+                  vis |= dr;
+                }
+              } else {
+                vis = bit_range(lo_row - base, min(pos + 1, L) - base);
+              }
+              const uint32_t two = load_info >> (2 * (kChunk / 32 * ch + w));
+              bad |= (vis & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u))) != 0;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 f = unpack_f32x2(x[16 * w + k]);
+                x[16 * w + k] = pack_f32x2((vis >> (2 * k)) & 1u ? f.x : -CUDART_INF_F,
+                                           (vis >> (2 * k + 1)) & 1u ? f.y : -CUDART_INF_F);
+              }
+            }
+          }
+          float mq[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+          for (int k = 0; k < kChunk / 2; ++k) {
+            const float2 f = unpack_f32x2(x[k]);
+            mq[k & 1] = fmaxf(mq[k & 1], fmaxf(f.x, f.y));
+          }
+          mx = fmaxf(mx, fmaxf(mq[0], mq[1]));
+          if (change) store_chunk(ts + kChunk * ch, x);
         }
-        float mq[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int k = 4; k < kWT; ++k) mq[k & 3] = fmaxf(mq[k & 3], x[k]);
-        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
+        if (change) tmem_wait_st();
+        mx *= sc;
         // The base moves only past 2^8 (P stays at most 256); one vote per
         // warp, since the TMEM accesses are warp-wide.
         if (__any_sync(0xffffffffu, mx > m + kLazyLog2)) {
@@ -608,126 +669,215 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           l *= alpha;
           if (t >= (MT == 2 ? 1 : 2)) {  // O holds earlier tiles
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * cc, o);
+            for (int cc = 0; cc < 8; ++cc) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * cc, o);
               tmem_wait_ld();
-              hold(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(to + 32 * cc, o);
+              for (int k = 0; k < 16; ++k) {
+                asm volatile("" : "+r"(o[k]));
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              }
+              tmem_st16(to + 16 * cc, o);
             }
           }
         }
         const float base = m == -CUDART_INF_F ? 0.f : m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = pack_f32x2(sc, sc), nb2 = pack_f32x2(-base, -base);
+        uint64_t ls[2] = {0ull, 0ull};  // sums of the even and the odd tokens' P, twice
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          uint64_t x[kChunk / 2];
+          load_chunk(ts + kChunk * ch, x);
+          uint32_t pk[kChunk / 2];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float a = ex2_approx(fmaf(x[64 * hf + 2 * k], sc, -base));
-            const float e = ex2_approx(fmaf(x[64 * hf + 2 * k + 1], sc, -base));
+          for (int k = 0; k < kChunk / 2; ++k) {
+            const float2 f = unpack_f32x2(fma_f32x2(x[k], sc2, nb2));
+            const float a = ex2_approx(f.x), e = ex2_approx(f.y);
             pk[k] = pack_bf16x2(a, e);
-            ls[k & 3] += a + e;
+            ls[k & 1] = add_f32x2(ls[k & 1], pack_f32x2(a, e));
           }
-          tmem_st32(ts + 32 * hf, pk);
+          // (the scores in these columns have been read by both passes)
+          tmem_st32(ts + kChunk / 2 * ch, pk);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        {
+          const float2 a = unpack_f32x2(add_f32x2(ls[0], ls[1]));
+          l += a.x + a.y;
+        }
         tmem_wait_st();
+        // V rows that were not loaded, lie past the end or before the oldest
+        // window are zeroed (P is 0 there, but 0 * NaN is not)
+        if (!plain && (MT == 1 || s == 0) &&
+            ((load_info >> 8) != 0 || tok0 + kWT > L || tok0 < lo_unit)) {
+          const uint32_t iv = Cfg::v_item(tile_no, t, n);
+          if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
+          const int tok = tok0 + row;
+          if (((load_info >> (8 + (row >> 4))) & 1u) || tok >= L || tok < lo_unit) {
+            const uint32_t vr = sbase + Cfg::kOffRing + (iv % NB) * kBuf + row * 128;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               vr + (k >> 3) * kHalf + (k & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+          }
+          fence_proxy_async_smem();
+        }
         tc_fence_before();
         mbar_arrive(bar(Cfg::B_P0 + s));
       }
       if (!ok) break;
-
-      // ---- the piece's result: O / l, joined over the streams for MT = 1
-      float mine = 1.f, theirs = 0.f;  // weights of this and the other stream's O
-      bool both = false;
-      if (MT == 1) {
-        float2* mlp = ml + (pieces & 1) * 256;
-        mlp[s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
-        mbar_arrive(bar(Cfg::B_ML));
-        if (!wait_all(Cfg::B_ML, pieces & 1)) break;
-        const float2 o = mlp[(s ^ 1) * 128 + row];
-        bad |= isnan(o.y);
-        both = n > 1;  // stream 1 had a tile
-        const float mn = fmaxf(m, o.x);
-        mine = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn);
-        theirs = o.x == -CUDART_INF_F ? 0.f : ex2_approx(o.x - mn);
-        // the same order of the sum in both streams' threads
-        const float l0 = s ? o.y * theirs : l * mine, l1 = s ? l * mine : o.y * theirs;
-        m = mn;
-        l = l0 + l1;
+      // the row's base and sum for the epilogue (once it has read the ones that
+      // were here; l = NaN: the row saw a bad page)
+      const uint32_t par = pieces & 1;
+      if (pieces >= 2 && !wait_all(Cfg::B_EPI0 + par, ((pieces >> 1) - 1) & 1)) break;
+      ml[par * 256 + s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
+      mbar_arrive(bar(Cfg::B_ML0 + par));
+      tile_no += n;
+      idx = pc.next;
+    }
+    if (!ok) {
+      raise_error(p.err_flags, kErrTimeout);
+      *abort_flag = 1;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // O / l of the finished piece, while the softmax warpgroups are at the
+    // next one; for MT = 1 joined over the streams. Thread `row` holds row
+    // `row`; the values pass through 2 KB of shared memory per warp so that a
+    // store instruction covers 8 rows x 64 bytes (one row per thread would
+    // touch 32 lines with 16 bytes each).
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t stage = sbase + Cfg::kOffStage + (warp & 3) * kStage;
+    bool ok = true;
+    auto wait_all = [&](int i, uint32_t parity) -> bool {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag));
+      return ok;
+    };
+    // this lane's 16-byte chunks of the 64-byte staging rows (chunk c of row r
+    // at c ^ (r / 2 % 4): free of bank conflicts both ways)
+    const uint32_t put = stage + lane * 64, sw = (lane >> 1) & 3;
+    auto flush = [&](char* const (&dst)[4], int64_t off) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        uint4 u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))
+                     : "memory");
+        if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + off) = u;
       }
-      const bool none = bad || !(l > 0.f);
-      const float inv = none ? 0.f : 1.f / l;
-      const float lse2 = none ? -CUDART_INF_F : m + log2f(l);
-      if (__any_sync(0xffffffffu, bad && exists) && lane == 0) raise_error(p.err_flags, kErrBadPage);
-      const int need = MT == 2 ? (1 << s) : (n > 1 ? 3 : 1);
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        if (need >> q & 1) {
-          if (!wait_all(Cfg::B_O0 + q, on[q] & 1)) break;
-          ++on[q];
-        }
-      if (!ok) break;
-      tc_fence_after();
-      const int64_t orow = (int64_t(pc.b) * p.q_total + qi) * p.Hq + head;
-      const int64_t wrow =
-          (int64_t(c) * 2 + pc.slot) * (MT * 128) + (MT == 2 ? s * 128 : 0) + row;
-      // MT = 1: stream s writes columns [64 s, 64 s + 64) of the joined row
+      __syncwarp();
+    };
+    auto stash = [&](int c, uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       put + ((uint32_t(c) ^ sw) << 4)),
+                   "r"(a), "r"(b), "r"(d), "r"(e)
+                   : "memory");
+    };
+    uint32_t pieces = 0, on1 = 0;  // pieces, and those with an O of stream 1 (MT = 1)
+    for (int idx = s_c; idx < e_c && ok; ++pieces) {
+      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      const bool both = MT == 1 && pc.ntiles > 1;  // stream 1 had a tile
+      const uint32_t par = pieces & 1;
+      if (!wait_all(Cfg::B_ML0 + par, (pieces >> 1) & 1)) break;
+      float2 r[2];
+      r[0] = ml[par * 256 + row];
+      r[1] = ml[par * 256 + 128 + row];
+      mbar_arrive(bar(Cfg::B_EPI0 + par));
 #pragma unroll 1
-      for (int cc = 0; cc < (MT == 2 ? 4 : 2); ++cc) {
-        const int col = (MT == 2 ? 0 : 64 * s) + 32 * cc;
-        float f[32];
-        uint32_t a[32];
-        if (MT == 2) {
-          tmem_ld32(to + col, a);
-          tmem_wait_ld();
-          hold(a);
+      for (int s = 0; s < MT && ok; ++s) {
+        const int qi = (pc.blk * MT + s) * p.tpt + row / p.g;
+        const bool exists = row < p.g * p.tpt && qi < p.q_total;
+        const int64_t orow =
+            (int64_t(pc.b) * p.q_total + qi) * p.Hq + pc.kvh * p.g + row % p.g;
+        const int64_t wrow = (int64_t(c) * 2 + pc.slot) * (MT * 128) + s * 128 + row;
+        // m, l and the weights w0, w1 of the streams' O
+        float m = s ? r[1].x : r[0].x, l = s ? r[1].y : r[0].y, w0 = 1.f, w1 = 0.f;
+        if (MT == 1) {
+          m = fmaxf(r[0].x, r[1].x);
+          w0 = r[0].x == -CUDART_INF_F ? 0.f : ex2_approx(r[0].x - m);
+          w1 = r[1].x == -CUDART_INF_F ? 0.f : ex2_approx(r[1].x - m);
+          l = r[0].y * w0 + r[1].y * w1;
+        }
+        const bool bad = isnan(r[0].y) || (MT == 1 && isnan(r[1].y));
+        const bool row_bad = MT == 1 ? bad : isnan(l);
+        const bool none = row_bad || !(l > 0.f);
+        const float inv = none ? 0.f : 1.f / l;
+        const float lse2 = none ? -CUDART_INF_F : m + log2f(l);
+        w0 *= inv;
+        w1 *= inv;
+        if (__any_sync(0xffffffffu, row_bad && exists) && lane == 0)
+          raise_error(p.err_flags, kErrBadPage);
+        // rows 8 i + lane / 4 of the warp, 16-byte chunk lane % 4
+        char* mine = !exists ? nullptr
+                     : pc.partial ? reinterpret_cast<char*>(p.ws_o + wrow * kGqaHeadDim)
+                                  : reinterpret_cast<char*>(p.out + orow * kGqaHeadDim);
+        char* dst[4];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[k]) * inv;
-        } else {
-          // O_0 w_0 + O_1 w_1, in that order
-          const float w0 = (s ? theirs : mine) * inv, w1 = (s ? mine : theirs) * inv;
-          tmem_ld32(tl + kTmemO + col, a);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine),
+                                         8 * i + (lane >> 2));
+          dst[i] = a ? reinterpret_cast<char*>(a) + (lane & 3) * 16 : nullptr;
+        }
+        if (!wait_all(Cfg::B_O0 + s, pieces & 1)) break;
+        if (both && !wait_all(Cfg::B_O0 + 1, on1 & 1)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {  // 16 columns
+          float f[16];
+          uint32_t a[16];
+          tmem_ld16(tl + kTmemO + 128 * s + 16 * cc, a);
           tmem_wait_ld();
-          hold(a);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(a[k]) * w0;
+          for (int k = 0; k < 16; ++k) {
+            asm volatile("" : "+r"(a[k]));
+            f[k] = __uint_as_float(a[k]) * w0;
+          }
           if (both) {
-            tmem_ld32(tl + kTmemO + 128 + col, a);
+            tmem_ld16(tl + kTmemO + 128 + 16 * cc, a);
             tmem_wait_ld();
-            hold(a);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
+            for (int k = 0; k < 16; ++k) {
+              asm volatile("" : "+r"(a[k]));
+              f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
+            }
+          }
+          if (cc == 7) {  // read in full: the next piece may overwrite O
+            tc_fence_before();
+            // (stream 1 first: the MMA warp does not wait for it in every piece)
+            if (MT == 1) mbar_arrive(bar(Cfg::B_OFREE0 + 1));
+            mbar_arrive(bar(Cfg::B_OFREE0 + s));
+          }
+          if (none) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[k] = 0.f;
+          }
+          if (pc.partial) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              stash(q, __float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]),
+                    __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3]));
+            flush(dst, int64_t(cc) * 64);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              stash((cc & 1) * 2 + q, pack_bf16x2(f[8 * q], f[8 * q + 1]),
+                    pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                    pack_bf16x2(f[8 * q + 4], f[8 * q + 5]),
+                    pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+            if (cc & 1) flush(dst, int64_t(cc >> 1) * 64);
           }
         }
-        if (!exists) continue;
-        if (pc.partial) {
-          float4* dst = reinterpret_cast<float4*>(p.ws_o + wrow * kGqaHeadDim + col);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                          : make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kGqaHeadDim + col);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = none ? make_uint4(0u, 0u, 0u, 0u)
-                          : make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]),
-                                       pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                                       pack_bf16x2(f[8 * k + 4], f[8 * k + 5]),
-                                       pack_bf16x2(f[8 * k + 6], f[8 * k + 7]));
+        if (exists) {
+          if (pc.partial) p.ws_lse[wrow] = row_bad ? CUDART_NAN_F : lse2;
+          else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
         }
       }
-      if (exists && (MT == 2 || s == 0)) {
-        if (pc.partial) p.ws_lse[wrow] = bad ? CUDART_NAN_F : lse2;
-        else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
-      }
-      tc_fence_before();
-      mbar_arrive(bar(Cfg::B_DONE0 + (pieces & 1)));
-      tile_no += n;
+      on1 += both ? 1 : 0;
       idx = pc.next;
     }
     if (!ok) {
@@ -739,10 +889,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       if (prefix[b + 1] != prefix[b]) continue;
       const int64_t rows = int64_t(p.q_total) * p.Hq, row0 = int64_t(b) * rows;
       uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kGqaHeadDim);
-      for (int64_t i = tid; i < rows * kGqaHeadDim / 8; i += kSoft)
+      for (int64_t i = row; i < rows * kGqaHeadDim / 8; i += 128)
         dst[i] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
-        for (int64_t i = tid; i < rows; i += kSoft) p.lse[row0 + i] = -CUDART_INF_F;
+        for (int64_t i = row; i < rows; i += 128) p.lse[row0 + i] = -CUDART_INF_F;
     }
   }
   tc_fence_before();
@@ -812,7 +962,7 @@ __global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ Wi
                        : (acc.mx[0] + log2f(acc.den[0])) * 0.69314718055994531f;
 }
 
-template <int MT>
+template <int MT, bool CAP>
 cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent_t attn_begin,
                    cudaEvent_t attn_end) {
   static bool done[kMaxDevices] = {};
@@ -821,12 +971,7 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!done[device]) {
-    // the register split above counts on this many per thread at launch: with
-    // fewer, the softmax warpgroups would wait for registers that never come
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, gqa_wide_kernel<MT>)) != cudaSuccess) return e;
-    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(WideCfg<MT>::kSmemMax))) != cudaSuccess)
       return e;
     done[device] = true;
@@ -842,7 +987,7 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(kWideThreads);
   cfg.dynamicSmemBytes = WideCfg<MT>::smem_bytes(p.B);
-  if ((e = cudaLaunchKernelEx(&cfg, gqa_wide_kernel<MT>, p)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, gqa_wide_kernel<MT, CAP>, p)) != cudaSuccess) return e;
   if (attn_end && (e = cudaEventRecord(attn_end, stream)) != cudaSuccess) return e;
   if (grid < 2) return cudaSuccess;  // nothing is cut
   cfg.gridDim = dim3(unsigned(grid - 1), unsigned(MT * 128 / 8));
@@ -855,8 +1000,12 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
 
 cudaError_t gqa_wide_launch(const WideParams& p, int grid, cudaStream_t stream,
                             cudaEvent_t attn_begin, cudaEvent_t attn_end) {
-  return p.mt == 2 ? launch<2>(p, grid, stream, attn_begin, attn_end)
-                   : launch<1>(p, grid, stream, attn_begin, attn_end);
+  const bool cap = p.cap_in > 0.f;
+  if (p.mt == 2)
+    return cap ? launch<2, true>(p, grid, stream, attn_begin, attn_end)
+               : launch<2, false>(p, grid, stream, attn_begin, attn_end);
+  return cap ? launch<1, true>(p, grid, stream, attn_begin, attn_end)
+             : launch<1, false>(p, grid, stream, attn_begin, attn_end);
 }
 
 }  // namespace zl
