@@ -518,6 +518,20 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   if (m.softcap > 0.f) {
     p.cap_in = float(double(a->scale) / m.softcap);
     p.cap_out = float(double(m.softcap) * kLog2e);
+    // coefficients and bound in the dot product's own units; where they leave
+    // the range of normal 32-bit numbers, every chunk takes the full function
+    const double in = double(a->scale) / m.softcap, poly[4] = ZL_CAP_POLYNOMIAL;
+    bool normal = true;
+    double f = in * m.softcap * kLog2e;
+    for (int i = 0; i < 4; ++i, f *= in * in) {
+      p.cap_f[i] = float(poly[i] * f);
+      normal = normal && std::isnormal(p.cap_f[i]);
+    }
+    p.cap_z = float(0.25 / (in * in));
+    if (!normal || !std::isnormal(p.cap_z)) {
+      std::memset(p.cap_f, 0, sizeof(p.cap_f));
+      p.cap_z = -1.f;
+    }
   }
   p.slopes = m.alibi_slopes;
   p.window = m.window;

@@ -41,7 +41,8 @@ constexpr int kSoft = 256;                     // softmax threads
 constexpr int kWideThreads = kSoft + 256;      // + K, MMA, V, Q warps and the epilogue's four
 constexpr int kStage = 32 * 64;                // bytes of an epilogue warp's staging rows
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream
+constexpr uint32_t kTmemS = 0, kTmemO = 256;   // + 128 * stream (S: + 64 * half tile)
+constexpr int kHT = kWT / 2;                   // tokens of a half tile
 
 template <int MT>
 struct WideCfg {
@@ -52,8 +53,8 @@ struct WideCfg {
   // phase then waits for those that wait for this one)
   enum : int {
     B_Q = 0, B_QFREE, B_FINAL, B_MASK0, B_ML0 = B_MASK0 + 2, B_EPI0 = B_ML0 + 2,
-    B_S0 = B_EPI0 + 2, B_P0 = B_S0 + 2, B_O0 = B_P0 + 2, B_OFREE0 = B_O0 + 2,
-    B_FULL0 = B_OFREE0 + 2, B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing,
+    B_S0 = B_EPI0 + 2, B_P0 = B_S0 + 2, B_PV0 = B_P0 + 4, B_O0 = B_PV0 + 2,
+    B_OFREE0 = B_O0 + 2, B_FULL0 = B_OFREE0 + 2, B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing,
     B_COUNT = B_INFO0 + kInfo
   };
   static constexpr int kOffMisc = kOffBar + 8 * B_COUNT;   // TMEM address, abort flag
@@ -91,6 +92,12 @@ __device__ __forceinline__ bool wide_warp_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Bits [a, b) of a 32-bit word, both clamped to 0..32.
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   a = max(a, 0);
@@ -111,14 +118,14 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* bits, int words, i
 
 // Registers that tcgen05.ld fills are valid after tcgen05.wait::ld: nothing
 // computed from them may be scheduled above it.
-__device__ __forceinline__ void hold(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void hold(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(r[k]));
 }
 
-constexpr int kChunk = 64;  // scores a softmax thread holds at a time
-
-__device__ __forceinline__ void load_chunk(uint32_t taddr, uint64_t (&x)[kChunk / 2]) {
+// The 64 scores of a half tile, two to a register pair.
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint64_t (&x)[kHT / 2]) {
   uint32_t v[2][32];
   tmem_ld32(taddr, v[0]);
   tmem_ld32(taddr + 32, v[1]);
@@ -130,20 +137,6 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, uint64_t (&x)[kChunk 
     for (int k = 0; k < 16; ++k)
       x[16 * h + k] =
           pack_f32x2(__uint_as_float(v[h][2 * k]), __uint_as_float(v[h][2 * k + 1]));
-  }
-}
-
-__device__ __forceinline__ void store_chunk(uint32_t taddr, const uint64_t (&x)[kChunk / 2]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[32];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float2 f = unpack_f32x2(x[16 * h + k]);
-      v[2 * k] = __float_as_uint(f.x);
-      v[2 * k + 1] = __float_as_uint(f.y);
-    }
-    tmem_st32(taddr + 32 * h, v);
   }
 }
 
@@ -214,7 +207,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       mbar_init(bar(Cfg::B_ML0 + s), kSoft);
       mbar_init(bar(Cfg::B_EPI0 + s), 128);
       mbar_init(bar(Cfg::B_S0 + s), 1);
-      mbar_init(bar(Cfg::B_P0 + s), 128);
+      for (int h = 0; h < 2; ++h) mbar_init(bar(Cfg::B_P0 + 2 * s + h), 128);
+      mbar_init(bar(Cfg::B_PV0 + s), 1);
       mbar_init(bar(Cfg::B_O0 + s), 1);
       mbar_init(bar(Cfg::B_OFREE0 + s), 128);
     }
@@ -408,7 +402,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
     const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
     uint32_t item = 0, pieces = 0;
-    uint32_t pn[2] = {0, 0};  // P tiles taken from each stream
+    uint32_t pn[2] = {0, 0};  // tiles whose P was taken from each stream
     bool ok = true;
     auto wait = [&](int i, uint32_t parity) -> bool {
       ok = ok && wide_warp_wait(bar(i), parity, abort_flag);
@@ -418,16 +412,26 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     auto buf = [&](uint32_t it) -> uint32_t {
       return sbase + Cfg::kOffRing + (it % NB) * kBuf;
     };
-    // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step
+    // The low words of the shared-memory descriptors, and the TMEM address,
+    // through a shuffle: the compiler then knows them to be the same in every
+    // lane and keeps them, and what is added per step, in uniform registers.
+    // (From ordinary ones each MMA took about 70 cycles to issue.)
+    auto uni = [](uint32_t v) -> uint32_t { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tm = uni(tmem);
+    constexpr uint32_t kDescHi = desc_hi(1024);
+    constexpr uint32_t kLboV = uint32_t(kHalf >> 4) << 16;  // V's next 64 columns
+    // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step. (All 128
+    // tokens at once: with 64, each MMA still reads 4 KB of Q and takes as long.)
     auto qk = [&](int s, uint32_t it, bool release, bool last) {
+      const uint32_t ad = uni((sbase + (MT == 2 ? s * kBuf : 0)) >> 4);
+      const uint32_t bd = uni(buf(it) >> 4), d = uni(tm + kTmemS + 128 * s);
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t qb = sbase + (MT == 2 ? s * kBuf : 0), kb = buf(it);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-          umma_bf16(tmem + kTmemS + 128 * s, umma_smem_desc(qb + off, 0, 1024, 2),
-                    umma_smem_desc(kb + off, 0, 1024, 2), idesc_qk, k ? 1u : 0u);
+          constexpr uint32_t kNext = kHalf >> 4;
+          const uint32_t off = (k >> 2) * kNext + (k & 3) * 2;
+          umma_ss(d, ad + off, bd + off, kDescHi, idesc_qk, k > 0);
         }
         umma_commit(bar(Cfg::B_S0 + s));
         if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
@@ -435,16 +439,16 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       }
       __syncwarp();
     };
-    // O_s (+)= P_s V, 16 tokens (8 TMEM columns of P) per step
-    auto pv = [&](int s, uint32_t it, bool first, bool release, bool last) {
+    // O_s (+)= P_s[h] V_h, 16 tokens (8 TMEM columns of P) per step
+    auto pv = [&](int s, int h, uint32_t it, bool first, bool release, bool last) {
+      const uint32_t bd = uni(((buf(it) + h * (kHT * 128)) >> 4) | kLboV);
+      const uint32_t d = uni(tm + kTmemO + 128 * s), a = uni(tm + kTmemS + 128 * s + kHT * h);
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t vb = buf(it);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_tmem_a(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * k,
-                           umma_smem_desc(vb + k * 16 * 128, kHalf, 1024, 2), idesc_pv,
-                           first && k == 0 ? 0u : 1u);
+        for (int k = 0; k < 4; ++k)
+          umma_ts(d, a + 8 * k, bd + k * (16 * 128 / 16), kDescHi, idesc_pv, !first || k > 0);
+        umma_commit(bar(Cfg::B_PV0 + s));
         if (last) umma_commit(bar(Cfg::B_O0 + s));
         if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
       }
@@ -467,11 +471,14 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           const uint32_t iv = item, ik = item + 1;
           const bool more = t + 1 < n;
           if (!wait_item(iv)) break;
+          // stream 1 runs about half a tile behind stream 0, so this is the
+          // order in which the P halves come
 #pragma unroll 1
-          for (int s = 0; s < 2; ++s) {
-            if (!wait(Cfg::B_P0 + s, pn[0] & 1) || (t == 0 && !o_free(s))) break;
-            pv(s, iv, t == 0, s == 1, !more);
-            if (more) {
+          for (int k = 0; k < 4; ++k) {
+            const int s = k >> 1, h = k & 1;
+            if (!wait(Cfg::B_P0 + k, pn[0] & 1) || (t == 0 && h == 0 && !o_free(s))) break;
+            pv(s, h, iv, t == 0 && h == 0, k == 3, h == 1 && !more);
+            if (h == 1 && more) {
               if (s == 0 && !wait_item(ik)) break;
               qk(s, ik, s == 1, s == 1 && t + 2 == n);
             }
@@ -486,11 +493,17 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         }
         for (int t = 0; t < n && ok; ++t) {
           const int s = t & 1;
-          if (!wait_item(item) || !wait(Cfg::B_P0 + s, pn[s] & 1) || (t < 2 && !o_free(s)))
-            break;
-          pv(s, item++, t < 2, true, t + 2 >= n);
+          const bool more = t + 2 < n;
+          if (!wait_item(item)) break;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(Cfg::B_P0 + 2 * s + h, pn[s] & 1) || (t < 2 && h == 0 && !o_free(s))) break;
+            pv(s, h, item, t < 2 && h == 0, h == 1, h == 1 && !more);
+          }
+          if (!ok) break;
           ++pn[s];
-          if (t + 2 < n) {
+          ++item;
+          if (more) {
             if (!wait_item(item)) break;
             qk(s, item++, true, t + 3 == n);
           }
@@ -545,64 +558,58 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         const uint32_t tn = tile_no + t;
         const int tok0 = (pc.tile0 + t) * kWT;
         if (!wait_all(Cfg::B_INFO0 + tn % kInfo, (tn / kInfo) & 1)) break;
-        const uint32_t load_info = info[tn % kInfo];
-        // all of the tile is context that every row sees
-        const bool plain = load_info == 0 && tok0 + kWT <= ctx &&
-                           (!p.window || tok0 >= ctx + p.q_total - p.window);
-        if (!wait_all(Cfg::B_S0 + s, sn & 1)) break;
-        tc_fence_after();
-        // The row's scores in two passes over 64-column chunks, two scores to a
-        // register pair: first modified (written back to TMEM) and their max
-        // taken, then exponentiated. A chunk is read from TMEM twice (about 50
-        // cycles) so that a thread holds 64 scores, not 128: those and the
-        // piece's state do not fit 192 registers without spills.
-        // Scores are in units of sc: base 2 once multiplied by it (sc > 0, so it
-        // also takes the max).
-        const bool change = CAP || !plain || p.slopes != nullptr;
-        const float sc = p.slopes ? 1.f : CAP ? p.cap_out : p.scale_log2;
-        float mx = -CUDART_INF_F;
+        const uint32_t tile_info = info[tn % kInfo];
+        // Half tiles of 64 tokens, P in the place of S: the first half's PV runs
+        // while the second half is here.
 #pragma unroll 1
-        for (int ch = 0; ch < 2; ++ch) {
-          uint64_t x[kChunk / 2];
-          load_chunk(ts + kChunk * ch, x);
+        for (int h = 0; h < 2; ++h) {
+          const int tok = tok0 + kHT * h;
+          const uint32_t load_info = (tile_info >> (4 * h)) & 0xf0fu;  // 4 blocks of 16 tokens
+          // all of it is context that every row sees
+          const bool plain = load_info == 0 && tok + kHT <= ctx &&
+                             (!p.window || tok >= ctx + p.q_total - p.window);
+          const uint32_t tsh = ts + kHT * h;
+          if (h == 0) {
+            if (!wait_all(Cfg::B_S0 + s, sn & 1)) break;
+            tc_fence_after();
+          }
+          uint64_t x[kHT / 2];  // the row's scores, two to a register pair
+          load_scores(tsh, x);
+          // Scores are in units of sc: base 2 once multiplied by it (sc > 0, so
+          // it also takes the max).
+          const float sc = CAP || p.slopes ? 1.f : p.scale_log2;
           if (CAP) {
-            float hi = 0.f;
+            // c tanh(s / c) in base 2 as x (f0 + f1 z + f2 z^2 + f3 z^3), z =
+            // x^2, of the raw dot product x, two at a time; right up to |s| = c
+            // / 2, else the scores are read again and take the full function
+            float zq[2] = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < kChunk / 2; ++k) {
-              const float2 f = unpack_f32x2(x[k]);
-              hi = fmaxf(hi, fmaxf(fabsf(f.x), fabsf(f.y)));
+            for (int k = 0; k < kHT / 2; ++k) {
+              const uint64_t z = mul_f32x2(x[k], x[k]);
+              const float2 f = unpack_f32x2(z);
+              zq[k & 1] = max3(zq[k & 1], f.x, f.y);
+              uint64_t q = fma_f32x2(z, pack_f32x2(p.cap_f[3], p.cap_f[3]),
+                                     pack_f32x2(p.cap_f[2], p.cap_f[2]));
+              q = fma_f32x2(q, z, pack_f32x2(p.cap_f[1], p.cap_f[1]));
+              q = fma_f32x2(q, z, pack_f32x2(p.cap_f[0], p.cap_f[0]));
+              x[k] = mul_f32x2(q, x[k]);
             }
-            if (__any_sync(0xffffffffu, !(hi * p.cap_in <= 0.5f))) {
+            if (__any_sync(0xffffffffu, !(fmaxf(zq[0], zq[1]) <= p.cap_z))) {
+              load_scores(tsh, x);
 #pragma unroll
-              for (int k = 0; k < kChunk / 2; ++k) {
+              for (int k = 0; k < kHT / 2; ++k) {
                 const float2 f = unpack_f32x2(x[k]);
-                x[k] = pack_f32x2(cap_tanh(f.x * p.cap_in), cap_tanh(f.y * p.cap_in));
-              }
-            } else {  // every |s| <= c / 2: the short polynomial, two scores at a time
-              const uint64_t cin = pack_f32x2(p.cap_in, p.cap_in);
-              const uint64_t c4 = pack_f32x2(kTanhLow4, kTanhLow4);
-              const uint64_t c3 = pack_f32x2(kTanhLow3, kTanhLow3);
-              const uint64_t c2 = pack_f32x2(kTanhLow2, kTanhLow2);
-              const uint64_t c1 = pack_f32x2(kTanhLow1, kTanhLow1);
-              const uint64_t c0 = pack_f32x2(kTanhLow0, kTanhLow0);
-#pragma unroll
-              for (int k = 0; k < kChunk / 2; ++k) {
-                const uint64_t y = mul_f32x2(x[k], cin), z = mul_f32x2(y, y);
-                uint64_t q = fma_f32x2(z, c4, c3);
-                q = fma_f32x2(q, z, c2);
-                q = fma_f32x2(q, z, c1);
-                q = fma_f32x2(q, z, c0);
-                x[k] = mul_f32x2(q, y);
+                x[k] = pack_f32x2(cap_tanh(f.x * p.cap_in) * p.cap_out,
+                                  cap_tanh(f.y * p.cap_in) * p.cap_out);
               }
             }
           }
-          const int tok = tok0 + kChunk * ch;
           if (p.slopes) {
-            const float d0 = float(pos - tok), raw = CAP ? p.cap_out : p.scale_log2;
+            const float d0 = float(pos - tok), raw = CAP ? 1.f : p.scale_log2;
             const uint64_t sc2 = pack_f32x2(raw, raw), sl2 = pack_f32x2(slope2, slope2);
-            if (p.tree && tok + kChunk > ctx) {
+            if (p.tree && tok + kHT > ctx) {
 #pragma unroll
-              for (int k = 0; k < kChunk / 2; ++k) {
+              for (int k = 0; k < kHT / 2; ++k) {
                 float d[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -614,14 +621,14 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < kChunk / 2; ++k)
+              for (int k = 0; k < kHT / 2; ++k)
                 x[k] = fma_f32x2(sl2, pack_f32x2(float(2 * k) - d0, float(2 * k + 1) - d0),
                                  mul_f32x2(x[k], sc2));
             }
           }
           if (!plain) {
 #pragma unroll
-            for (int w = 0; w < kChunk / 32; ++w) {
+            for (int w = 0; w < kHT / 32; ++w) {
               const int base = tok + 32 * w;
               uint32_t vis;
               if (p.tree) {
@@ -639,7 +646,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
               } else {
                 vis = bit_range(lo_row - base, min(pos + 1, L) - base);
               }
-              const uint32_t two = load_info >> (2 * (kChunk / 32 * ch + w));
+              const uint32_t two = load_info >> (2 * w);
               bad |= (vis & ((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u))) != 0;
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
@@ -651,80 +658,76 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           }
           float mq[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int k = 0; k < kChunk / 2; ++k) {
+          for (int k = 0; k < kHT / 2; ++k) {
             const float2 f = unpack_f32x2(x[k]);
-            mq[k & 1] = fmaxf(mq[k & 1], fmaxf(f.x, f.y));
+            mq[k & 1] = max3(mq[k & 1], f.x, f.y);
           }
-          mx = fmaxf(mx, fmaxf(mq[0], mq[1]));
-          if (change) store_chunk(ts + kChunk * ch, x);
-        }
-        if (change) tmem_wait_st();
-        mx *= sc;
-        // The base moves only past 2^8 (P stays at most 256); one vote per
-        // warp, since the TMEM accesses are warp-wide.
-        if (__any_sync(0xffffffffu, mx > m + kLazyLog2)) {
-          const float mn = fmaxf(m, mx);
-          const float alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn);
-          m = mn;
-          l *= alpha;
-          if (t >= (MT == 2 ? 1 : 2)) {  // O holds earlier tiles
+          const float mx = fmaxf(mq[0], mq[1]) * sc;
+          // The base moves only past 2^8 (P stays at most 256); one vote per
+          // warp, since the TMEM accesses are warp-wide.
+          if (__any_sync(0xffffffffu, mx > m + kLazyLog2)) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn);
+            m = mn;
+            l *= alpha;
+            const bool first = h == 0 && t < (MT == 2 ? 1 : 2);
+            if (!first) {  // O holds earlier half tiles: all of them, once their PV is done
+              const uint32_t done = 2 * sn + h - 1;  // PVs of this stream before this one's
+              if (!wait_all(Cfg::B_PV0 + s, done & 1)) break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
-              uint32_t o[16];
-              tmem_ld16(to + 16 * cc, o);
-              tmem_wait_ld();
+              for (int cc = 0; cc < 8; ++cc) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * cc, o);
+                tmem_wait_ld();
+                hold(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                asm volatile("" : "+r"(o[k]));
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                for (int k = 0; k < 16; ++k)
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st16(to + 16 * cc, o);
               }
-              tmem_st16(to + 16 * cc, o);
             }
           }
-        }
-        const float base = m == -CUDART_INF_F ? 0.f : m;
-        const uint64_t sc2 = pack_f32x2(sc, sc), nb2 = pack_f32x2(-base, -base);
-        uint64_t ls[2] = {0ull, 0ull};  // sums of the even and the odd tokens' P, twice
-#pragma unroll 1
-        for (int ch = 0; ch < 2; ++ch) {
-          uint64_t x[kChunk / 2];
-          load_chunk(ts + kChunk * ch, x);
-          uint32_t pk[kChunk / 2];
+          const float base = m == -CUDART_INF_F ? 0.f : m;
+          const uint64_t sc2 = pack_f32x2(sc, sc), nb2 = pack_f32x2(-base, -base);
+          uint64_t ls[2] = {0ull, 0ull};  // sums of the even and the odd tokens' P, twice
+          uint32_t pk[kHT / 2];
 #pragma unroll
-          for (int k = 0; k < kChunk / 2; ++k) {
+          for (int k = 0; k < kHT / 2; ++k) {
             const float2 f = unpack_f32x2(fma_f32x2(x[k], sc2, nb2));
             const float a = ex2_approx(f.x), e = ex2_approx(f.y);
             pk[k] = pack_bf16x2(a, e);
             ls[k & 1] = add_f32x2(ls[k & 1], pack_f32x2(a, e));
           }
-          // (the scores in these columns have been read by both passes)
-          tmem_st32(ts + kChunk / 2 * ch, pk);
-        }
-        {
-          const float2 a = unpack_f32x2(add_f32x2(ls[0], ls[1]));
-          l += a.x + a.y;
-        }
-        tmem_wait_st();
-        // V rows that were not loaded, lie past the end or before the oldest
-        // window are zeroed (P is 0 there, but 0 * NaN is not)
-        if (!plain && (MT == 1 || s == 0) &&
-            ((load_info >> 8) != 0 || tok0 + kWT > L || tok0 < lo_unit)) {
-          const uint32_t iv = Cfg::v_item(tile_no, t, n);
-          if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
-          const int tok = tok0 + row;
-          if (((load_info >> (8 + (row >> 4))) & 1u) || tok >= L || tok < lo_unit) {
-            const uint32_t vr = sbase + Cfg::kOffRing + (iv % NB) * kBuf + row * 128;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               vr + (k >> 3) * kHalf + (k & 7) * 16),
-                           "r"(0u)
-                           : "memory");
+          tmem_st32(tsh, pk);
+          {
+            const float2 a = unpack_f32x2(add_f32x2(ls[0], ls[1]));
+            l += a.x + a.y;
           }
-          fence_proxy_async_smem();
+          tmem_wait_st();
+          // V rows that were not loaded, lie past the end or before the oldest
+          // window are zeroed (P is 0 there, but 0 * NaN is not)
+          if (!plain && (MT == 1 || s == 0) &&
+              ((load_info >> 8) != 0 || tok + kHT > L || tok < lo_unit)) {
+            const uint32_t iv = Cfg::v_item(tile_no, t, n);
+            if (!wait_all(Cfg::B_FULL0 + iv % NB, (iv / NB) & 1)) break;
+            // one 128-byte half row per thread
+            const int vr = row & 63, at = tok + vr;
+            if (((load_info >> (8 + (vr >> 4))) & 1u) || at >= L || at < lo_unit) {
+              const uint32_t dst = sbase + Cfg::kOffRing + (iv % NB) * kBuf + (row >> 6) * kHalf +
+                                   (kHT * h + vr) * 128;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + k * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          mbar_arrive(bar(Cfg::B_P0 + 2 * s + h));
         }
-        tc_fence_before();
-        mbar_arrive(bar(Cfg::B_P0 + s));
+        if (!ok) break;
       }
       if (!ok) break;
       // the row's base and sum for the epilogue (once it has read the ones that
@@ -826,36 +829,38 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         if (!wait_all(Cfg::B_O0 + s, pieces & 1)) break;
         if (both && !wait_all(Cfg::B_O0 + 1, on1 & 1)) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {  // 16 columns
-          float f[16];
+        // 16 columns of the row's result, w0 O_0 + w1 O_1
+        auto columns = [&](int cc, float (&f)[16]) {
           uint32_t a[16];
           tmem_ld16(tl + kTmemO + 128 * s + 16 * cc, a);
           tmem_wait_ld();
+          hold(a);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            asm volatile("" : "+r"(a[k]));
-            f[k] = __uint_as_float(a[k]) * w0;
-          }
+          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(a[k]) * w0;
           if (both) {
             tmem_ld16(tl + kTmemO + 128 + 16 * cc, a);
             tmem_wait_ld();
+            hold(a);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              asm volatile("" : "+r"(a[k]));
-              f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
-            }
-          }
-          if (cc == 7) {  // read in full: the next piece may overwrite O
-            tc_fence_before();
-            // (stream 1 first: the MMA warp does not wait for it in every piece)
-            if (MT == 1) mbar_arrive(bar(Cfg::B_OFREE0 + 1));
-            mbar_arrive(bar(Cfg::B_OFREE0 + s));
+            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
           }
           if (none) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) f[k] = 0.f;
           }
+        };
+        // O is read in full: the next piece may overwrite it (stream 1 first:
+        // the MMA warp does not wait for it in every piece)
+        auto hand_back = [&] {
+          tc_fence_before();
+          if (MT == 1) mbar_arrive(bar(Cfg::B_OFREE0 + 1));
+          mbar_arrive(bar(Cfg::B_OFREE0 + s));
+        };
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          float f[16];
+          columns(cc, f);
+          if (cc == 7) hand_back();
           if (pc.partial) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)

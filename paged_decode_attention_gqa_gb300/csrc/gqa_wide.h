@@ -7,6 +7,11 @@ namespace zl {
 
 constexpr int kWideTile = 128;  // tokens per tile
 
+// tanh(y) / y for z = y^2 in [0, 1/4]: the cubic in z that interpolates it at
+// the 4 Chebyshev nodes of the interval, within 5.5e-7 (6.3e-7
+// evaluated in 32 bits): a score c tanh(s / c) is then off by 3e-7 of c at most.
+#define ZL_CAP_POLYNOMIAL {0.999999451, -0.333262842, 0.131899394, -0.0443927384}
+
 struct WideParams {
   CUtensorMap tmap_k;  // 4-D {D, page_size, Hkv, num_pages}, box {64, box, 1, 1}, 128B swizzle
   CUtensorMap tmap_v;
@@ -27,6 +32,9 @@ struct WideParams {
   int nblk;  // row blocks per kv head
   int64_t len_cap;
   float scale_log2, cap_in, cap_out;  // as in GqaParams
+  // The capped score in base 2 as x (cap_f[0] + cap_f[1] z + ..), z = x^2, of the
+  // dot product x; right where z <= cap_z (-1: nowhere)
+  float cap_f[4], cap_z;
   const float* slopes;
   int window;
   const uint32_t* tree;

@@ -16,11 +16,6 @@ constexpr float kTanh0 = 0.999999949f, kTanh1 = -0.33332828f, kTanh2 = 0.1332507
                 kTanh3 = -0.0534516464f, kTanh4 = 0.0202797083f, kTanh5 = -0.00619432483f,
                 kTanh6 = 0.0010380251f;
 
-// The same up to |y| = 1/2 (z <= 1/4) at degree 4, from 5 nodes: within 2e-8, 1.8e-7
-// evaluated in 32 bits.
-constexpr float kTanhLow0 = 0.999999987f, kTanhLow1 = -0.333330679f, kTanhLow2 = 0.133247505f,
-                kTanhLow3 = -0.0529842388f, kTanhLow4 = 0.0171313444f;
-
 // tanh(y) to about 2e-7 of max(|tanh y|, ..): the polynomial up to |y| = 1, and
 // 1 - 2 / (e^(2y) + 1) beyond, where e^(2y) overflowing to infinity gives 1 and
 // underflowing to 0 gives -1. (That difference cancels near zero.) A score is c
