@@ -173,9 +173,10 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
   const int row_tiles = (a->q_len + plan->tpt - 1) / plan->tpt;
   plan->mt = row_tiles > 1 ? 2 : 1;
   plan->nblk = (row_tiles + plan->mt - 1) / plan->mt;
-  // (the tcgen05 kernel counts tiles in 32 bits)
+  // (the tcgen05 kernel counts tiles, and each unit's fixed cost, in 32 bits)
   const double most_tiles = double(a->B) * a->Hkv * plan->nblk *
-                            (double(a->block_table_stride) * a->page_size / zl::kWideTile + 1);
+                            (double(a->block_table_stride) * a->page_size / zl::kWideTile + 1 +
+                             zl::kWideUnitCost);
   if (mods && !mods->weights && plan->g * a->q_len > kWideRows && most_tiles < 2e9) {
     plan->wide = true;
     plan->grid = a->num_ctas > 0 ? a->num_ctas : dev.sms;
@@ -187,7 +188,7 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
       plan->grid = int(std::min(int64_t(plan->grid), std::max<int64_t>(tiles, 1)));
     }
     const size_t rows = size_t(plan->grid) * 2 * plan->mt * 128;
-    plan->off_lse = round_up((size_t(a->B) + 1) * sizeof(int32_t), 256);
+    plan->off_lse = round_up(size_t(plan->grid) * sizeof(int4), 256);
     plan->off_o = plan->off_lse + round_up(rows * sizeof(float), 256);
     plan->bytes = plan->off_o + rows * zl::kGqaHeadDim * sizeof(float);
     return ZL_OK;
@@ -499,7 +500,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.seq_lens = a->seq_lens;
   p.bt_stride = a->block_table_stride;
   char* ws = static_cast<char*>(a->workspace);
-  p.ws_prefix = reinterpret_cast<int32_t*>(ws);
+  p.ws_cut = reinterpret_cast<int4*>(ws);
   p.ws_lse = reinterpret_cast<float*>(ws + plan.off_lse);
   p.ws_o = reinterpret_cast<float*>(ws + plan.off_o);
   p.err_flags = a->err_flags;

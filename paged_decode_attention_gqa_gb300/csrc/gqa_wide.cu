@@ -140,6 +140,12 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, uint64_t (&x)[kHT / 
   }
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+  else tmem_ld16(taddr, r);
+}
+
 // One contiguous run of tiles of one unit, as every role walks them.
 struct Piece {
   int b, kvh, blk, L, ntiles, tile0;
@@ -151,28 +157,36 @@ struct Piece {
 __device__ __forceinline__ int wide_first_tile(const WideParams& p, int L) {
   return p.window ? max(L - p.q_total - p.window + 1, 0) / kWT : 0;
 }
-__device__ __forceinline__ int wide_tiles(const WideParams& p, int L) {
-  if (!(L >= 0 && int64_t(L) <= p.len_cap)) return 0;
-  return (L + kWT - 1) / kWT - wide_first_tile(p, L);
+// Places of a unit on the work line (0 for a sequence without tiles).
+__device__ __forceinline__ int unit_places(const WideParams& p, int L) {
+  if (!(L > 0 && int64_t(L) <= p.len_cap)) return 0;
+  return (L + kWT - 1) / kWT - wide_first_tile(p, L) + kWideUnitCost;
 }
 
-// (Tile numbers fit 32 bits: the host takes this kernel only when they do.)
+// Work line: unit u of sequence b (u = kv head * nblk + row block) takes
+// kWideUnitCost places for its start and end (Q, the first scores, the masked
+// tiles, the epilogue), then one per tile, so that equal ranges take equal time.
+// `idx` lies in a unit; the piece from it to e_c or the unit's end, whichever
+// is first, has the tiles whose places it covers, and the first tiles' if it
+// ends among them. (Places fit 32 bits: the host takes this kernel only when
+// they do.)
 __device__ __forceinline__ Piece piece_at(const WideParams& p, const int* prefix, int idx, int s_c,
                                           int e_c) {
   Piece q;
   const int U = p.Hkv * p.nblk;
   q.b = locate_seq(prefix, p.B, U, idx);
-  const int first = prefix[q.b], n_unit = prefix[q.b + 1] - first;
-  const int off = idx - U * first, u = off / n_unit, j0 = off - u * n_unit;
+  const int first = prefix[q.b], len = prefix[q.b + 1] - first;
+  const int off = idx - U * first, u = off / len;
   q.kvh = u / p.nblk;
   q.blk = u - q.kvh * p.nblk;
-  const int unit_end = U * first + (u + 1) * n_unit;
-  q.next = min(e_c, unit_end);
-  q.ntiles = q.next - idx;
-  q.partial = j0 > 0 || q.next < unit_end;
+  const int unit0 = U * first + u * len;
+  q.next = min(e_c, unit0 + len);
+  const int t0 = max(idx - unit0 - kWideUnitCost, 0);
+  q.ntiles = max(q.next - unit0 - kWideUnitCost, 0) - t0;
+  q.partial = q.ntiles < len - kWideUnitCost;
   q.slot = idx == s_c ? 0 : 1;
   q.L = p.seq_lens[q.b];
-  q.tile0 = wide_first_tile(p, q.L) + j0;
+  q.tile0 = wide_first_tile(p, q.L) + t0;
   return q;
 }
 
@@ -232,7 +246,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     tma_prefetch_desc(&p.tmap_v);
     tma_prefetch_desc(&p.tmap_q);
   }
-  if (warp == 0) {  // tiles per sequence, exclusive prefix sum
+  if (warp == 0) {  // places of a unit of each sequence, exclusive prefix sum
     const int per = (B + 31) / 32, b0 = lane * per;
     int local = 0;
     for (int i = 0; i < per; ++i) {
@@ -240,7 +254,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         const int L = p.seq_lens[b0 + i];
         if (blockIdx.x == 0 && !(L >= 0 && int64_t(L) <= p.len_cap))
           raise_error(p.err_flags, kErrBadLen);
-        local += wide_tiles(p, L);
+        local += unit_places(p, L);
       }
     }
     int incl = local;
@@ -253,7 +267,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     for (int i = 0; i < per; ++i) {
       if (b0 + i < B) {
         prefix[b0 + i] = run;
-        run += wide_tiles(p, p.seq_lens[b0 + i]);
+        run += unit_places(p, p.seq_lens[b0 + i]);
       }
     }
     if (lane == 31) prefix[B] = incl;
@@ -264,12 +278,24 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   griddep_launch_dependents();  // the merge kernel waits for this whole grid
   const uint32_t tmem = *tmem_slot;
   const int c = blockIdx.x;
-  if (c == 0)
-    for (int b = tid; b <= B; b += kWideThreads) p.ws_prefix[b] = prefix[b];
   const int64_t W = int64_t(p.Hkv) * p.nblk * prefix[B];
   const TileCut cut(W, gridDim.x);
   const int s_c = c < int(cut.G) && W > 0 ? int(cut.start(c)) : 0;
   const int e_c = c < int(cut.G) && W > 0 ? int(cut.start(c + 1)) : 0;
+  if (tid == 0 && c > 0) {
+    // For the merge: whether this CTA's first place is the first boundary
+    // between the tiles of a unit, and if so of which one (sequence, unit),
+    // the last CTA with a part of it and the slot of the first one's (c - 1).
+    int4 cut_unit = make_int4(0, 0, -1, 0);
+    if (e_c > s_c) {
+      const int U = p.Hkv * p.nblk, b = locate_seq(prefix, B, U, s_c);
+      const int first = prefix[b], len = prefix[b + 1] - first, u = (s_c - U * first) / len;
+      const int unit0 = U * first + u * len, before = int(cut.start(c - 1));
+      if (s_c > unit0 + kWideUnitCost && before <= unit0 + kWideUnitCost)
+        cut_unit = make_int4(b, u, cut.owner(unit0 + len - 1), before >= unit0 ? 0 : 1);
+    }
+    p.ws_cut[c] = cut_unit;
+  }
 
   if (warp >= 8 && warp < 12) {
     if (warp == 8 || warp == 10) {
@@ -287,6 +313,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       bool ok = true;
       for (int idx = s_c; idx < e_c && ok;) {
         const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+        if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+          idx = pc.next;
+          continue;
+        }
         const int32_t* bt = p.block_table + int64_t(pc.b) * p.bt_stride;
         const int lo = p.window ? pc.L - p.q_total - p.window + 1 : 0;
         // this lane's block of tile t: its page, -1 (nothing there), -2 (bad page)
@@ -357,8 +387,12 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       // and depths in a buffer of their own.
       uint32_t pieces = 0;
       bool ok = true;
-      for (int idx = s_c; idx < e_c && ok; ++pieces) {
+      for (int idx = s_c; idx < e_c && ok;) {
         const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+        if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+          idx = pc.next;
+          continue;
+        }
         if (p.tree) {
           const int words = p.q_total * p.tree_words;
           const uint32_t* src = p.tree + int64_t(pc.b) * words;
@@ -391,6 +425,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           }
         }
         __syncwarp();
+        ++pieces;
         idx = pc.next;
       }
       if (!ok && lane == 0) {
@@ -456,6 +491,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     };
     for (int idx = s_c; idx < e_c && ok;) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+        idx = pc.next;
+        continue;
+      }
       const int n = pc.ntiles;
       if (!wait(Cfg::B_Q, pieces & 1)) break;
       // the first PV of a stream overwrites the O that the epilogue reads
@@ -534,8 +573,12 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       return ok;
     };
     uint32_t tile_no = 0, pieces = 0, sn = 0;  // tiles of the CTA, pieces, tiles of this stream
-    for (int idx = s_c; idx < e_c && ok; ++pieces) {
+    for (int idx = s_c; idx < e_c && ok;) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+        idx = pc.next;
+        continue;
+      }
       const int n = pc.ntiles, L = pc.L, ctx = L - p.q_total;
       // Row `row` of this stream's row tile: token row / g of the tile's tpt,
       // head row % g (rows past the last token have zeros in Q, rows past g tpt
@@ -737,6 +780,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       ml[par * 256 + s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
       mbar_arrive(bar(Cfg::B_ML0 + par));
       tile_no += n;
+      ++pieces;
       idx = pc.next;
     }
     if (!ok) {
@@ -761,7 +805,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     // this lane's 16-byte chunks of the 64-byte staging rows (chunk c of row r
     // at c ^ (r / 2 % 4): free of bank conflicts both ways)
     const uint32_t put = stage + lane * 64, sw = (lane >> 1) & 3;
-    auto flush = [&](char* const (&dst)[4], int64_t off) {
+    auto flush = [&](char* mine, int64_t off) {  // mine: where this lane's row goes, or nullptr
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -771,7 +815,9 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                      : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4))
                      : "memory");
-        if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + off) = u;
+        const uint64_t to_row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), r);
+        if (to_row)
+          *reinterpret_cast<uint4*>(reinterpret_cast<char*>(to_row) + off + (lane & 3) * 16) = u;
       }
       __syncwarp();
     };
@@ -782,8 +828,12 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
                    : "memory");
     };
     uint32_t pieces = 0, on1 = 0;  // pieces, and those with an O of stream 1 (MT = 1)
-    for (int idx = s_c; idx < e_c && ok; ++pieces) {
+    for (int idx = s_c; idx < e_c && ok;) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+      if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+        idx = pc.next;
+        continue;
+      }
       const bool both = MT == 1 && pc.ntiles > 1;  // stream 1 had a tile
       const uint32_t par = pieces & 1;
       if (!wait_all(Cfg::B_ML0 + par, (pieces >> 1) & 1)) break;
@@ -815,38 +865,30 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         w1 *= inv;
         if (__any_sync(0xffffffffu, row_bad && exists) && lane == 0)
           raise_error(p.err_flags, kErrBadPage);
-        // rows 8 i + lane / 4 of the warp, 16-byte chunk lane % 4
         char* mine = !exists ? nullptr
                      : pc.partial ? reinterpret_cast<char*>(p.ws_o + wrow * kGqaHeadDim)
                                   : reinterpret_cast<char*>(p.out + orow * kGqaHeadDim);
-        char* dst[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine),
-                                         8 * i + (lane >> 2));
-          dst[i] = a ? reinterpret_cast<char*>(a) + (lane & 3) * 16 : nullptr;
-        }
         if (!wait_all(Cfg::B_O0 + s, pieces & 1)) break;
         if (both && !wait_all(Cfg::B_O0 + 1, on1 & 1)) break;
         tc_fence_after();
-        // 16 columns of the row's result, w0 O_0 + w1 O_1
-        auto columns = [&](int cc, float (&f)[16]) {
-          uint32_t a[16];
-          tmem_ld16(tl + kTmemO + 128 * s + 16 * cc, a);
+        // kStep columns of the row's result, w0 O_0 + w1 O_1, read at once (a
+        // read takes about 300 cycles under the softmax threads' own,
+        // whatever its width; for MT = 1 two O's have to fit the registers)
+        constexpr int kStep = MT == 2 ? 32 : 16;
+        auto columns = [&](int cc, float (&f)[kStep]) {
+          uint32_t a[kStep], d[kStep];
+          tmem_ld<kStep>(tl + kTmemO + 128 * s + kStep * cc, a);
+          if (both) tmem_ld<kStep>(tl + kTmemO + 128 + kStep * cc, d);
           tmem_wait_ld();
           hold(a);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(a[k]) * w0;
+          for (int k = 0; k < kStep; ++k) f[k] = none ? 0.f : __uint_as_float(a[k]) * w0;
           if (both) {
-            tmem_ld16(tl + kTmemO + 128 + 16 * cc, a);
-            tmem_wait_ld();
-            hold(a);
+            hold(d);
+            if (!none) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = fmaf(__uint_as_float(a[k]), w1, f[k]);
-          }
-          if (none) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = 0.f;
+              for (int k = 0; k < kStep; ++k) f[k] = fmaf(__uint_as_float(d[k]), w1, f[k]);
+            }
           }
         };
         // O is read in full: the next piece may overwrite it (stream 1 first:
@@ -856,25 +898,41 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           if (MT == 1) mbar_arrive(bar(Cfg::B_OFREE0 + 1));
           mbar_arrive(bar(Cfg::B_OFREE0 + s));
         };
+        if (pc.partial) {
 #pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-          float f[16];
-          columns(cc, f);
-          if (cc == 7) hand_back();
-          if (pc.partial) {
+          for (int cc = 0; cc < 128 / kStep; ++cc) {
+            float f[kStep];
+            columns(cc, f);
+            if (cc == 128 / kStep - 1) hand_back();
+#pragma unroll
+            for (int h = 0; h < kStep / 16; ++h) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                stash(q, __float_as_uint(f[16 * h + 4 * q]),
+                      __float_as_uint(f[16 * h + 4 * q + 1]),
+                      __float_as_uint(f[16 * h + 4 * q + 2]),
+                      __float_as_uint(f[16 * h + 4 * q + 3]));
+              flush(mine, int64_t(kStep / 16 * cc + h) * 64);
+            }
+          }
+        } else {  // packed first, so that O is handed back before the stores
+          uint32_t w[64];
+#pragma unroll
+          for (int cc = 0; cc < 128 / kStep; ++cc) {
+            float f[kStep];
+            columns(cc, f);
+#pragma unroll
+            for (int k = 0; k < kStep / 2; ++k)
+              w[kStep / 2 * cc + k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+          }
+          hand_back();
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              stash(q, __float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]),
-                    __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3]));
-            flush(dst, int64_t(cc) * 64);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-              stash((cc & 1) * 2 + q, pack_bf16x2(f[8 * q], f[8 * q + 1]),
-                    pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
-                    pack_bf16x2(f[8 * q + 4], f[8 * q + 5]),
-                    pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
-            if (cc & 1) flush(dst, int64_t(cc >> 1) * 64);
+              stash(q, w[16 * cc + 4 * q], w[16 * cc + 4 * q + 1], w[16 * cc + 4 * q + 2],
+                    w[16 * cc + 4 * q + 3]);
+            flush(mine, int64_t(cc) * 64);
           }
         }
         if (exists) {
@@ -883,6 +941,7 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         }
       }
       on1 += both ? 1 : 0;
+      ++pieces;
       idx = pc.next;
     }
     if (!ok) {
@@ -916,55 +975,61 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   }
 }
 
-// Joins the partials of the units cut between CTAs, one warp per row. Block
-// (c, y) looks at the boundary between CTAs c - 1 and c: if it is the first
-// one inside a unit, the block merges 8 of the unit's rows over the unit's
-// CTAs, in their order.
+// Joins the partials of the units cut between CTAs, kMergeRows rows per warp.
+// Block (c - 1, y) takes rows 32 y .. of the unit whose first cut is CTA c's
+// first place, if there is one (the attention kernel wrote that down), and
+// adds its parts in the order of the CTAs.
 template <int MT>
-__global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ WideParams p,
-                                                      int ctas) {
+__global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ WideParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x + 1, U = p.Hkv * p.nblk;
-  const int64_t W = int64_t(U) * p.ws_prefix[p.B];
-  if (W == 0) return;
-  const TileCut cut(W, ctas);
-  if (c >= int(cut.G)) return;
-  const int64_t x = cut.start(c);
-  const int b = locate_seq(p.ws_prefix, p.B, U, x);
-  const int first = p.ws_prefix[b], n = p.ws_prefix[b + 1] - first;
-  const int u = int((x - int64_t(U) * first) / n);
-  const int64_t U0 = int64_t(U) * first + int64_t(u) * n;
-  if (x == U0 || cut.start(c - 1) > U0) {
-    // not cut here, or an earlier boundary cuts it too (a CTA whose range
-    // starts inside the unit)
-    return;
+  const int c = blockIdx.x + 1;
+  const int4 u = __ldcg(p.ws_cut + c);
+  if (u.z < 0) return;
+  const int b = u.x, kvh = u.y / p.nblk, blk = u.y - kvh * p.nblk;
+  const int row0 = blockIdx.y * 32 + warp * kMergeRows;
+  int64_t orow[kMergeRows];
+  bool live[kMergeRows], any = false;
+#pragma unroll
+  for (int k = 0; k < kMergeRows; ++k) {
+    const int row = row0 + k, r = row & 127, qi = (blk * MT + row / 128) * p.tpt + r / p.g;
+    live[k] = r < p.g * p.tpt && qi < p.q_total;
+    any |= live[k];
+    orow[k] = (int64_t(b) * p.q_total + qi) * p.Hq + kvh * p.g + r % p.g;
   }
-  const int c_hi = cut.owner(U0 + n - 1);
-  const int row = blockIdx.y * 8 + warp;
-  const int tile = (u % p.nblk) * MT + row / 128, r = row % 128;
-  const int qi = tile * p.tpt + r / p.g;
-  if (r >= p.g * p.tpt || qi >= p.q_total) return;
-  MergeAcc<1> acc;
+  if (!any) return;
+  MergeAcc<kMergeRows> acc;
   acc.init();
-  for (int cc = c - 1; cc <= c_hi; ++cc) {
-    const int slot = cc == c - 1 && U0 > cut.start(cc) ? 1 : 0;
-    const int64_t wrow = (int64_t(cc) * 2 + slot) * (MT * 128) + row;
-    acc.add(0, __ldcg(p.ws_lse + wrow),
-            __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * kGqaHeadDim) + lane));
+  for (int cc = c - 1; cc <= u.z; ++cc) {
+    const int64_t wrow = (int64_t(cc) * 2 + (cc == c - 1 ? u.w : 0)) * (MT * 128) + row0;
+    float l[kMergeRows];
+    float4 o[kMergeRows];
+#pragma unroll
+    for (int k = 0; k < kMergeRows; ++k) {
+      if (live[k]) {
+        l[k] = __ldcg(p.ws_lse + wrow + k);
+        o[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (wrow + k) * kGqaHeadDim) + lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeRows; ++k)
+      if (live[k]) acc.add(k, l[k], o[k]);
   }
-  const bool none = acc.bad || !(acc.den[0] > 0.f);
-  const float inv = none ? 0.f : 1.f / acc.den[0];
-  const int64_t orow = (int64_t(b) * p.q_total + qi) * p.Hq + (u / p.nblk) * p.g + r % p.g;
-  uint2 o = make_uint2(0u, 0u);
-  if (!none)
-    o = make_uint2(pack_bf16x2(acc.acc[0].x * inv, acc.acc[0].y * inv),
-                   pack_bf16x2(acc.acc[0].z * inv, acc.acc[0].w * inv));
-  reinterpret_cast<uint2*>(p.out + orow * kGqaHeadDim)[lane] = o;
-  if (p.lse && lane == 0)
-    p.lse[orow] = none ? -CUDART_INF_F
-                       : (acc.mx[0] + log2f(acc.den[0])) * 0.69314718055994531f;
+#pragma unroll
+  for (int k = 0; k < kMergeRows; ++k) {
+    if (!live[k]) continue;
+    const bool none = ((acc.bad >> k) & 1u) || !(acc.den[k] > 0.f);
+    const float inv = none ? 0.f : 1.f / acc.den[k];
+    uint2 o = make_uint2(0u, 0u);
+    if (!none)
+      o = make_uint2(pack_bf16x2(acc.acc[k].x * inv, acc.acc[k].y * inv),
+                     pack_bf16x2(acc.acc[k].z * inv, acc.acc[k].w * inv));
+    reinterpret_cast<uint2*>(p.out + orow[k] * kGqaHeadDim)[lane] = o;
+    if (p.lse && lane == 0)
+      p.lse[orow[k]] = none ? -CUDART_INF_F
+                            : (acc.mx[k] + log2f(acc.den[k])) * 0.69314718055994531f;
+  }
 }
 
 template <int MT, bool CAP>
@@ -995,10 +1060,10 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
   if ((e = cudaLaunchKernelEx(&cfg, gqa_wide_kernel<MT, CAP>, p)) != cudaSuccess) return e;
   if (attn_end && (e = cudaEventRecord(attn_end, stream)) != cudaSuccess) return e;
   if (grid < 2) return cudaSuccess;  // nothing is cut
-  cfg.gridDim = dim3(unsigned(grid - 1), unsigned(MT * 128 / 8));
+  cfg.gridDim = dim3(unsigned(grid - 1), unsigned(MT * 128 / 32));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, gqa_wide_merge<MT>, p, grid);
+  return cudaLaunchKernelEx(&cfg, gqa_wide_merge<MT>, p);
 }
 
 }  // namespace

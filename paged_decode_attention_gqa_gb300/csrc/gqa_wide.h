@@ -6,6 +6,10 @@
 namespace zl {
 
 constexpr int kWideTile = 128;  // tokens per tile
+// What a unit costs beside its tiles, in tiles, for the cut between CTAs.
+// (64 sequences of 512-4096 tokens, 64 drafted tokens: 196, 177, 172, 172, 178 us
+// at 0, 1, 2, 3 and 5; 16 drafted tokens: 137, 128, 129, 130, 132 us.)
+constexpr int kWideUnitCost = 2;
 
 // tanh(y) / y for z = y^2 in [0, 1/4]: the cubic in z that interpolates it at
 // the 4 Chebyshev nodes of the interval, within 5.5e-7 (6.3e-7
@@ -21,7 +25,7 @@ struct WideParams {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int64_t bt_stride;
-  int32_t* ws_prefix;  // [B + 1] tile prefix sums, for the merge
+  int4* ws_cut;        // [CTAs] the unit each boundary cuts first, for the merge
   float* ws_lse;       // [CTAs][2][mt * 128] base-2 lse of partials (NaN = bad)
   float* ws_o;         // [..][128] normalised partial outputs
   uint32_t* err_flags;

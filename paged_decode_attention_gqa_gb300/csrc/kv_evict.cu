@@ -1,13 +1,19 @@
 // Eviction by accumulated weights (zl_kv_evict in the header), in two launches.
 //
-// select: one block per (sequence, kv head) finds the K-th largest weight of
-// the tokens between the sinks and the recent ones by a radix select on 32-bit
-// keys that order as the floats do (11 + 11 + 10 bits, a histogram in shared
-// memory each), then lists the kept positions in order: a token is kept if its
-// key is above the threshold, or equals it and fewer than the missing number
-// of equal ones came before it. Each warp owns a contiguous stretch, counts
-// it, and after a scan over the warps writes its places; no atomics decide an
-// order, so the result is always the same. The same block moves the weights.
+// select: one cluster of CTAs per (sequence, kv head) finds the K-th largest
+// weight of the tokens between the sinks and the recent ones by a radix select
+// on 32-bit keys that order as the floats do (11 + 11 + 10 bits, a histogram in
+// each CTA's shared memory, summed over the cluster), then lists the kept
+// positions in order: a token is kept if its key is above the threshold, or
+// equals it and fewer than the missing number of equal ones came before it.
+// Each CTA owns a contiguous part of the row, each warp a stretch of that;
+// counts are summed over warps and CTAs and every warp then writes its places,
+// so no atomic decides an order and the result is always the same. A CTA keeps
+// its part of the weights in shared memory: they are read from memory once.
+// The time is the chain of passes and their barriers, not the 4 bytes per
+// token (one CTA of 1024 threads per row, reading the weights in every pass,
+// took 209 us for 64 rows of 32k-131k tokens and 31 us for 512 rows of
+// 2k-4k).
 //
 // move: rows are 16-byte chunks. In place, kept[j] >= j, so the rows of one
 // (sequence, kv head, column part) may move in ascending chunks: a chunk's
@@ -40,6 +46,8 @@ struct EvictParams {
   int64_t wo_seq, wo_head;
   uint32_t* err_flags;
   int w_tokens, Hkv, budget, sink, recent;
+  int cluster;    // CTAs per row of the select launch
+  int sel_cache;  // weights each of them keeps in shared memory (0: none)
   // move launch: column parts of K (then of V) of `part` chunks, segments of
   // kSegment rows (out of place; 1 in place)
   int part, k_parts, parts, segments;
@@ -52,9 +60,9 @@ __device__ __forceinline__ bool evict_len_ok(const EvictParams& p, int L) {
 }
 
 // ------------------------------------------------------------------- select
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kSelCache = 16384;  // weights a CTA keeps in shared memory at most
+constexpr int kSelCluster = 8;    // CTAs per row at most (the portable cluster size)
 
 // A key that orders as the weights do: larger weight, larger key; -0 as +0,
 // NaN lowest.
@@ -64,55 +72,71 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads)
-evict_select_kernel(const __grid_constant__ EvictParams p) {
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kWarps = T / 32;
+  extern __shared__ float cache[];
   __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t warp_sum[kSelWarps], warp_eq[kSelWarps];
+  __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps], cta_gt, cta_eq;
   __shared__ uint32_t s_prefix, s_need;
   griddep_wait();
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int CS = p.cluster, rank = int(cluster_ctarank());
+  const int h = int(blockIdx.x) / CS, b = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int L = p.seq_lens[b];
   int32_t* kept = p.kept + (int64_t(b) * p.Hkv + h) * p.budget;
   const float* w = p.weights + int64_t(b) * p.w_seq + int64_t(h) * p.w_head;
   float* wo = p.weights_out + int64_t(b) * p.wo_seq + int64_t(h) * p.wo_head;
+  // (the whole cluster takes the same way out)
   if (!evict_len_ok(p, L)) {
-    if (h == 0 && tid == 0 && p.err_flags) atomicOr(p.err_flags, 2u);
-    for (int j = tid; j < p.budget; j += kSelThreads) kept[j] = -1;
+    if (h == 0 && rank == 0 && tid == 0 && p.err_flags) atomicOr(p.err_flags, 2u);
+    for (int j = rank * T + tid; j < p.budget; j += CS * T) kept[j] = -1;
     return;
   }
   if (L <= p.budget) {
-    for (int j = tid; j < p.budget; j += kSelThreads) kept[j] = j < L ? j : -1;
+    for (int j = rank * T + tid; j < p.budget; j += CS * T) kept[j] = j < L ? j : -1;
     if (wo != w)
-      for (int j = tid; j < L; j += kSelThreads) wo[j] = w[j];
+      for (int j = rank * T + tid; j < L; j += CS * T) wo[j] = w[j];
     return;
   }
   const int M = L - p.sink - p.recent;                 // candidates
   const int K = p.budget - p.sink - p.recent;          // kept of them: K < M
-  const float* c = w + p.sink;
-  for (int j = tid; j < p.sink; j += kSelThreads) kept[j] = j;
-  for (int j = tid; j < p.recent; j += kSelThreads)
+  const int part = ((M + CS - 1) / CS + 31) / 32 * 32;
+  const int lo = min(M, rank * part), n = min(M, lo + part) - lo;  // this CTA's
+  const float* c = w + p.sink + lo;
+  const bool cached = part <= p.sel_cache;  // the same for the whole cluster
+  auto weight_at = [&](int i) -> float { return cached ? cache[i] : c[i]; };
+  for (int j = rank * T + tid; j < p.sink; j += CS * T) kept[j] = j;
+  for (int j = rank * T + tid; j < p.recent; j += CS * T)
     kept[p.budget - p.recent + j] = L - p.recent + j;
+  if (cached)
+    for (int i = tid; i < n; i += T) cache[i] = c[i];
+  uint32_t prefix = 0, need = uint32_t(K), gt_before = 0, eq_before = 0;
   if (K > 0) {
     // the K-th largest key, most significant digits first: `prefix` holds the
     // digits found, `need` how many of the keys that share them are kept
-    uint32_t prefix = 0, need = uint32_t(K);
     int shift = 21;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int bits = pass < 2 ? 11 : 10;
       const uint32_t nb = 1u << bits;
-      for (uint32_t i = tid; i < nb; i += kSelThreads) hist[i] = 0;
+      for (uint32_t i = tid; i < nb; i += T) hist[i] = 0;
       __syncthreads();
       const int high = shift + bits;  // 32 in the first pass
-      for (int i0 = 0; i0 < M; i0 += kSelThreads * 4) {
+      for (int i0 = 0; i0 < n; i0 += T * 4) {
         uint32_t key[4];
         bool in[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * kSelThreads + tid;
-          in[u] = i < M;
-          key[u] = in[u] ? weight_key(c[i]) : 0u;
+          const int i = i0 + u * T + tid;
+          in[u] = i < n;
+          key[u] = in[u] ? weight_key(weight_at(i)) : 0u;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -127,86 +151,172 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
           if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
         }
       }
-      __syncthreads();
+      if (CS > 1) cluster_sync();
+      else __syncthreads();
       // the digit: the largest one with at least `need` keys at or above it.
-      // Thread i owns bins [2i, 2i + 1]; suffix sums over the threads.
-      const uint32_t per = nb / kSelThreads;  // 2 or 1
-      uint32_t mine = 0;
-      for (uint32_t k = 0; k < per; ++k) mine += hist[tid * per + k];
+      // Thread i owns `per` bins from i * per; suffix sums over the threads.
+      constexpr int kPer = kBins / T;
+      const int per = int(nb) / T > 0 ? int(nb) / T : 1;
+      uint32_t cnt[kPer], mine = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        cnt[k] = 0;
+        const uint32_t bin = uint32_t(tid * per + k);
+        if (k < per && bin < nb) {
+          if (CS > 1) {
+            const uint32_t addr = smem_u32(&hist[bin]);
+            for (int r = 0; r < CS; ++r) cnt[k] += ld_cluster(mapa_shared(addr, r));
+          } else {
+            cnt[k] = hist[bin];
+          }
+        }
+        mine += cnt[k];
+      }
       uint32_t suf = mine;  // over lanes >= this one
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const uint32_t x = __shfl_down_sync(0xffffffffu, suf, off);
         if (lane + off < 32) suf += x;
       }
-      if (lane == 0) warp_sum[warp] = suf;
+      if (lane == 0) warp_gt[warp] = suf;
       __syncthreads();
-      uint32_t above = suf - mine;  // keys in bins above this thread's
-      for (int k = warp + 1; k < kSelWarps; ++k) above += warp_sum[k];
+      // keys in the bins above this thread's
+      uint32_t above = suf - mine;
+      {
+        uint32_t x = lane < kWarps && lane > warp ? warp_gt[lane] : 0u;
+        above += __reduce_add_sync(0xffffffffu, x);
+      }
       if (above < need && need <= above + mine) {
-        for (int k = int(per) - 1; k >= 0; --k) {
-          const uint32_t cnt = hist[tid * per + k];
-          if (need <= above + cnt) {
+#pragma unroll
+        for (int k = kPer - 1; k >= 0; --k) {
+          if (above < need && need <= above + cnt[k]) {
             s_prefix = (prefix << bits) | uint32_t(tid * per + k);
             s_need = need - above;
-            break;
+            need = 0;  // found: nothing below matches
           }
-          above += cnt;
+          above += cnt[k];
         }
       }
-      __syncthreads();
+      // every CTA has read the histograms before any clears its own
+      if (CS > 1) cluster_sync();
+      else __syncthreads();
       prefix = s_prefix;
       need = s_need;
       shift -= pass == 0 ? 11 : 10;
     }
-    // `prefix` is the threshold key: every key above it is kept, and the first
-    // `need` of those that equal it
-    const uint32_t T = prefix;
-    const int seg = ((M + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;  // a warp's stretch
-    const int a0 = min(M, warp * seg), a1 = min(M, a0 + seg);
+  }
+  // `prefix` is the threshold key: every key above it is kept, and the first
+  // `need` of those that equal it
+  const uint32_t thr = prefix;
+  const int seg = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;  // a warp's stretch
+  const int a0 = min(n, warp * seg), a1 = min(n, a0 + seg);
+  if (K > 0) {
     uint32_t gt = 0, eq = 0;
     for (int i = a0 + lane; i < a1; i += 32) {
-      const uint32_t key = weight_key(c[i]);
-      gt += key > T ? 1u : 0u;
-      eq += key == T ? 1u : 0u;
+      const uint32_t key = weight_key(weight_at(i));
+      gt += key > thr ? 1u : 0u;
+      eq += key == thr ? 1u : 0u;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      gt += __shfl_xor_sync(0xffffffffu, gt, off);
-      eq += __shfl_xor_sync(0xffffffffu, eq, off);
-    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
-      warp_sum[warp] = gt;
+      warp_gt[warp] = gt;
       warp_eq[warp] = eq;
     }
     __syncthreads();
-    uint32_t gt0 = 0, eq0 = 0;  // before this warp's stretch
-    for (int k = 0; k < warp; ++k) {
-      gt0 += warp_sum[k];
-      eq0 += warp_eq[k];
+    // before this warp's stretch, within the CTA and in the CTAs before it
+    const uint32_t wg = lane < kWarps ? warp_gt[lane] : 0u, we = lane < kWarps ? warp_eq[lane] : 0u;
+    gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
+    eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
+    if (CS > 1) {
+      const uint32_t all_gt = __reduce_add_sync(0xffffffffu, wg);
+      const uint32_t all_eq = __reduce_add_sync(0xffffffffu, we);
+      if (tid == 0) {
+        cta_gt = all_gt;
+        cta_eq = all_eq;
+      }
+    }
+  }
+  // Also: every CTA holds its part of the weights, so that moving them in place
+  // overwrites nothing that is still to be read.
+  if (CS > 1) cluster_sync();
+  else __syncthreads();
+  if (K > 0) {
+    if (CS > 1) {
+      uint32_t g = 0, e = 0;
+      if (lane < rank) {
+        g = ld_cluster(mapa_shared(smem_u32(&cta_gt), lane));
+        e = ld_cluster(mapa_shared(smem_u32(&cta_eq), lane));
+      }
+      gt_before += __reduce_add_sync(0xffffffffu, g);
+      eq_before += __reduce_add_sync(0xffffffffu, e);
     }
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = a0; i0 < a1; i0 += 32) {
       const int i = i0 + lane;
-      const uint32_t key = i < a1 ? weight_key(c[i]) : 0u;
-      const uint32_t g = __ballot_sync(0xffffffffu, i < a1 && key > T);
-      const uint32_t e = __ballot_sync(0xffffffffu, i < a1 && key == T);
-      const uint32_t gb = gt0 + __popc(g & below), eb = eq0 + __popc(e & below);
+      const float x = i < a1 ? weight_at(i) : 0.f;
+      const uint32_t key = weight_key(x);
+      const uint32_t g = __ballot_sync(0xffffffffu, i < a1 && key > thr);
+      const uint32_t e = __ballot_sync(0xffffffffu, i < a1 && key == thr);
+      const uint32_t gb = gt_before + __popc(g & below), eb = eq_before + __popc(e & below);
       const bool take = ((g >> lane) & 1u) || (((e >> lane) & 1u) && eb < need);
-      if (take) kept[p.sink + gb + min(eb, need)] = p.sink + i;
-      gt0 += __popc(g);
-      eq0 += __popc(e);
+      if (take) {
+        const uint32_t at = p.sink + gb + min(eb, need);
+        kept[at] = p.sink + lo + i;
+        if (cached) wo[at] = x;
+      }
+      gt_before += __popc(g);
+      eq_before += __popc(e);
     }
   }
-  __syncthreads();
-  // Weights move like the rows: ascending, a chunk read before it is written.
-  for (int j0 = 0; j0 < p.budget; j0 += kSelThreads) {
+  // The other weights: the sinks stay or are copied; the recent ones move down
+  // in ascending chunks, each read before it is written (their places lie
+  // below every recent one that is still to be read). Where the parts do not
+  // fit the caches, one CTA moves the whole row that way, by the list.
+  if (CS > 1) cluster_sync();  // also: no CTA leaves while another reads its counts
+  else __syncthreads();
+  if (rank != CS - 1) return;
+  if (cached && wo != w)
+    for (int j = tid; j < p.sink; j += T) wo[j] = w[j];
+  for (int j0 = cached ? p.budget - p.recent : 0; j0 < p.budget; j0 += T) {
     const int j = j0 + tid;
     float x = 0.f;
-    if (j < p.budget) x = w[kept[j]];
+    if (j < p.budget) x = w[cached ? L - p.budget + j : __ldcg(kept + j)];
     __syncthreads();
     if (j < p.budget) wo[j] = x;
   }
+}
+
+template <int T>
+cudaError_t select_launch(EvictParams& p, int B, cudaStream_t stream) {
+  constexpr size_t kMax = size_t(kSelCache) * sizeof(float);
+  static bool done[64] = {};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!done[device]) {
+    if ((e = cudaFuncSetAttribute(evict_select_kernel<T>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMax))) !=
+        cudaSuccess)
+      return e;
+    done[device] = true;
+  }
+  const int part = ((p.w_tokens + p.cluster - 1) / p.cluster + 31) / 32 * 32;
+  p.sel_cache = part <= kSelCache ? part : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.Hkv * p.cluster), unsigned(B));
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = size_t(p.sel_cache) * sizeof(float);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(p.cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<T>, p);
 }
 
 // --------------------------------------------------------------------- move
@@ -295,8 +405,16 @@ cudaError_t evict_launch(EvictParams& p, int B, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
     return e;
-  evict_select_kernel<<<dim3(p.Hkv, B), kSelThreads, 0, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // CTAs per row: as many as the caches of a row need, and more while the rows
+  // alone leave SMs idle and each CTA still has a few weights per thread.
+  p.cluster = 1;
+  while (p.cluster < kSelCluster &&
+         (p.w_tokens > p.cluster * kSelCache ||
+          (int64_t(B) * p.Hkv * p.cluster < sms && p.w_tokens > p.cluster * 4096)))
+    p.cluster *= 2;
+  e = p.w_tokens <= p.cluster * 4096 ? select_launch<256>(p, B, stream)
+                                     : select_launch<1024>(p, B, stream);
+  if (e != cudaSuccess) return e;
   const bool in_place = p.dst_table == p.block_table;
   p.segments = in_place ? 1 : (p.budget + kSegment - 1) / kSegment;
   // A row's 16-byte chunks in parts of 16 (256 bytes); in place with few
