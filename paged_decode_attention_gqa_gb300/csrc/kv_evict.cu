@@ -2,18 +2,18 @@
 //
 // select: one cluster of CTAs per (sequence, kv head) finds the K-th largest
 // weight of the tokens between the sinks and the recent ones by a radix select
-// on 32-bit keys that order as the floats do (11 + 11 + 10 bits, a histogram in
-// each CTA's shared memory, summed over the cluster), then lists the kept
-// positions in order: a token is kept if its key is above the threshold, or
-// equals it and fewer than the missing number of equal ones came before it.
-// Each CTA owns a contiguous part of the row, each warp a stretch of that;
-// counts are summed over warps and CTAs and every warp then writes its places,
-// so no atomic decides an order and the result is always the same. A CTA keeps
-// its part of the weights in shared memory: they are read from memory once.
-// The time is the chain of passes and their barriers, not the 4 bytes per
-// token (one CTA of 1024 threads per row, reading the weights in every pass,
-// took 209 us for 64 rows of 32k-131k tokens and 31 us for 512 rows of
-// 2k-4k).
+// on 32-bit keys that order as the floats do (a histogram of the keys' next
+// digit in each CTA's shared memory, summed over the cluster), then lists the
+// kept positions in order: a token is kept if its key is above the threshold,
+// or equals it and fewer than the missing number of equal ones came before it.
+// Each CTA owns a contiguous part of the row, each thread 16 tokens of it in a
+// row: its counts and a scan over threads and CTAs give the place of every kept
+// token, so no atomic decides an order and the result is always the same. A
+// CTA keeps its part of the weights in shared memory; they are read from memory
+// once. What bounds it is the chain of passes and their barriers and the
+// instructions per token, not the 4 bytes: with one CTA per row, ballots per
+// token and the weights read again in every pass it took 209 us for 64 rows of
+// 32k-131k tokens and 31 us for 512 rows of 2k-4k.
 //
 // move: rows are 16-byte chunks. In place, kept[j] >= j, so the rows of one
 // (sequence, kv head, column part) may move in ascending chunks: a chunk's
@@ -47,7 +47,6 @@ struct EvictParams {
   uint32_t* err_flags;
   int w_tokens, Hkv, budget, sink, recent;
   int cluster;    // CTAs per row of the select launch
-  int sel_cache;  // weights each of them keeps in shared memory (0: none)
   // move launch: column parts of K (then of V) of `part` chunks, segments of
   // kSegment rows (out of place; 1 in place)
   int part, k_parts, parts, segments;
@@ -60,16 +59,15 @@ __device__ __forceinline__ bool evict_len_ok(const EvictParams& p, int L) {
 }
 
 // ------------------------------------------------------------------- select
-constexpr int kBins = 2048;
-constexpr int kSelCache = 16384;  // weights a CTA keeps in shared memory at most
+constexpr int kRun = 16;          // consecutive tokens of a thread
 constexpr int kSelCluster = 8;    // CTAs per row at most (the portable cluster size)
 
 // A key that orders as the weights do: larger weight, larger key; -0 as +0,
 // NaN lowest.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (isnan(w)) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+  return isnan(w) ? 0u : k;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
@@ -78,12 +76,24 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   return v;
 }
 
-template <int T>
+constexpr int kBins = 256;        // of a digit: 4 digits of 8 bits
+constexpr int kHistBytes = kBins * 32 * 4;
+
+// T threads. Every lane counts in a histogram of its own: the weights' leading
+// digits fall into a few bins, and additions to one address, by lanes of a warp
+// or by warps, are done one after the other. CACHED: this CTA's part fits
+// kRun tokens per thread; then a thread holds their keys in registers through
+// all passes (computing them again in each pass was 390 instructions per token
+// in all), and shared memory the weights. Otherwise they are read again.
+template <int T, bool CACHED>
 __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = T / 32;
-  extern __shared__ float cache[];
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps], cta_gt, cta_eq;
+  static_assert(T >= kBins, "a thread for every bin");
+  extern __shared__ uint32_t lane_hist[];  // [kBins][32]
+  // token i of this CTA's part at i + i / kRun (no bank conflicts)
+  float* cache = reinterpret_cast<float*>(lane_hist + kBins * 32);
+  __shared__ uint32_t hist[2][kBins];
+  __shared__ uint32_t warp_sum[kWarps], cta_gt, cta_eq;
   __shared__ uint32_t s_prefix, s_need;
   griddep_wait();
   const int CS = p.cluster, rank = int(cluster_ctarank());
@@ -107,140 +117,146 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
   }
   const int M = L - p.sink - p.recent;                 // candidates
   const int K = p.budget - p.sink - p.recent;          // kept of them: K < M
-  const int part = ((M + CS - 1) / CS + 31) / 32 * 32;
+  const int part = ((M + CS - 1) / CS + kRun - 1) / kRun * kRun;
   const int lo = min(M, rank * part), n = min(M, lo + part) - lo;  // this CTA's
   const float* c = w + p.sink + lo;
-  const bool cached = part <= p.sel_cache;  // the same for the whole cluster
-  auto weight_at = [&](int i) -> float { return cached ? cache[i] : c[i]; };
+  auto sync = [&] {
+    if (CS > 1) cluster_sync();
+    else __syncthreads();
+  };
   for (int j = rank * T + tid; j < p.sink; j += CS * T) kept[j] = j;
   for (int j = rank * T + tid; j < p.recent; j += CS * T)
     kept[p.budget - p.recent + j] = L - p.recent + j;
-  if (cached)
-    for (int i = tid; i < n; i += T) cache[i] = c[i];
-  uint32_t prefix = 0, need = uint32_t(K), gt_before = 0, eq_before = 0;
+  // Keys of tokens [i0, i0 + kRun) of this CTA's part, of which m are there.
+  uint32_t key[kRun];
+  int m = 0;
+  auto load_run = [&](int i0) {
+    m = min(max(n - i0, 0), kRun);
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      const float x = e >= m ? 0.f : CACHED ? cache[i0 + i0 / kRun + e] : c[i0 + e];
+      key[e] = weight_key(x);
+    }
+  };
+  if (CACHED) {
+    for (int i0 = tid; i0 < n; i0 += T * 8) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * T < n) x[u] = c[i0 + u * T];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * T;
+        if (i < n) cache[i + i / kRun] = x[u];
+      }
+    }
+    __syncthreads();
+    load_run(tid * kRun);
+  }
+  // Runs `f(i0)` with the keys of each of this thread's runs in place (a run
+  // that is not there has m = 0).
+  auto for_runs = [&](auto&& f) {
+    if (CACHED) {
+      f(tid * kRun);
+    } else {
+#pragma unroll 1
+      for (int base = 0; base < n; base += T * kRun) {
+        load_run(base + tid * kRun);
+        f(base + tid * kRun);
+      }
+    }
+  };
+  uint32_t prefix = 0, need = uint32_t(K);
   if (K > 0) {
     // the K-th largest key, most significant digits first: `prefix` holds the
     // digits found, `need` how many of the keys that share them are kept
-    int shift = 21;
+    const int bin = tid;  // of this thread, if below kBins
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10;
-      const uint32_t nb = 1u << bits;
-      for (uint32_t i = tid; i < nb; i += T) hist[i] = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < kBins * 32; i += T) lane_hist[i] = 0;
       __syncthreads();
-      const int high = shift + bits;  // 32 in the first pass
-      for (int i0 = 0; i0 < n; i0 += T * 4) {
-        uint32_t key[4];
-        bool in[4];
+      // (in the first pass every key matches: nothing is found yet)
+      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+      const uint32_t want = shift == 24 ? 0u : prefix << (shift + 8);
+      for_runs([&](int) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * T + tid;
-          in[u] = i < n;
-          key[u] = in[u] ? weight_key(weight_at(i)) : 0u;
-        }
+        for (int e = 0; e < kRun; ++e)
+          if (e < m && (key[e] & mask) == want)
+            atomicAdd(&lane_hist[((key[e] >> shift) & 255u) * 32 + lane], 1u);
+      });
+      __syncthreads();
+      // (two buffers: the cluster's barrier in the next pass comes between this
+      // pass's reads and the next writes of the same one)
+      uint32_t* sums = hist[(shift >> 3) & 1];
+      uint32_t mine = 0;
+      if (bin < kBins) {
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) mine += lane_hist[bin * 32 + ((k + lane) & 31)];
+        sums[bin] = mine;
+      }
+      if (CS > 1) {  // over the cluster
+        cluster_sync();
+        if (bin < kBins) {
+          const uint32_t addr = smem_u32(&sums[bin]);
+          uint32_t x[kSelCluster];  // all in flight before the first is added
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool take = in[u] && (high == 32 || (key[u] >> high) == prefix);
-          const uint32_t bin = (key[u] >> shift) & (nb - 1u);
-          // many equal weights (tokens nobody attended to): one add for a warp
-          const uint32_t m = __ballot_sync(0xffffffffu, take);
-          if (!m) continue;
-          const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
-          const uint32_t same = __ballot_sync(0xffffffffu, take && bin == lead);
-          if (take && bin != lead) atomicAdd(&hist[bin], 1u);
-          if (lane == __ffs(m) - 1) atomicAdd(&hist[lead], __popc(same));
+          for (int r = 0; r < kSelCluster; ++r)
+            x[r] = r < CS ? ld_cluster(mapa_shared(addr, r)) : 0u;
+          mine = 0;
+#pragma unroll
+          for (int r = 0; r < kSelCluster; ++r) mine += x[r];
         }
       }
-      if (CS > 1) cluster_sync();
-      else __syncthreads();
-      // the digit: the largest one with at least `need` keys at or above it.
-      // Thread i owns `per` bins from i * per; suffix sums over the threads.
-      constexpr int kPer = kBins / T;
-      const int per = int(nb) / T > 0 ? int(nb) / T : 1;
-      uint32_t cnt[kPer], mine = 0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        cnt[k] = 0;
-        const uint32_t bin = uint32_t(tid * per + k);
-        if (k < per && bin < nb) {
-          if (CS > 1) {
-            const uint32_t addr = smem_u32(&hist[bin]);
-            for (int r = 0; r < CS; ++r) cnt[k] += ld_cluster(mapa_shared(addr, r));
-          } else {
-            cnt[k] = hist[bin];
-          }
-        }
-        mine += cnt[k];
-      }
+      // the digit: the largest one with at least `need` keys at or above it
       uint32_t suf = mine;  // over lanes >= this one
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const uint32_t x = __shfl_down_sync(0xffffffffu, suf, off);
         if (lane + off < 32) suf += x;
       }
-      if (lane == 0) warp_gt[warp] = suf;
+      if (lane == 0) warp_sum[warp] = suf;
       __syncthreads();
       // keys in the bins above this thread's
-      uint32_t above = suf - mine;
-      {
-        uint32_t x = lane < kWarps && lane > warp ? warp_gt[lane] : 0u;
-        above += __reduce_add_sync(0xffffffffu, x);
+      const uint32_t above =
+          suf - mine +
+          __reduce_add_sync(0xffffffffu,
+                            lane < kBins / 32 && lane > warp ? warp_sum[lane] : 0u);
+      if (bin < kBins && above < need && need <= above + mine) {
+        s_prefix = (prefix << 8) | uint32_t(bin);
+        s_need = need - above;
       }
-      if (above < need && need <= above + mine) {
-#pragma unroll
-        for (int k = kPer - 1; k >= 0; --k) {
-          if (above < need && need <= above + cnt[k]) {
-            s_prefix = (prefix << bits) | uint32_t(tid * per + k);
-            s_need = need - above;
-            need = 0;  // found: nothing below matches
-          }
-          above += cnt[k];
-        }
-      }
-      // every CTA has read the histograms before any clears its own
-      if (CS > 1) cluster_sync();
-      else __syncthreads();
+      __syncthreads();
       prefix = s_prefix;
       need = s_need;
-      shift -= pass == 0 ? 11 : 10;
     }
   }
   // `prefix` is the threshold key: every key above it is kept, and the first
   // `need` of those that equal it
   const uint32_t thr = prefix;
-  const int seg = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;  // a warp's stretch
-  const int a0 = min(n, warp * seg), a1 = min(n, a0 + seg);
-  if (K > 0) {
-    uint32_t gt = 0, eq = 0;
-    for (int i = a0 + lane; i < a1; i += 32) {
-      const uint32_t key = weight_key(weight_at(i));
-      gt += key > thr ? 1u : 0u;
-      eq += key == thr ? 1u : 0u;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      warp_gt[warp] = gt;
-      warp_eq[warp] = eq;
-    }
+  uint32_t gt_before = 0, eq_before = 0;
+  // Counts of the current run: above the threshold in the low half (a round of
+  // the block has at most 2^14 tokens), equal to it in the high half.
+  auto run_counts = [&]() -> uint32_t {
+    uint32_t x = 0;
+#pragma unroll
+    for (int e = 0; e < kRun; ++e)
+      x += e >= m ? 0u : key[e] > thr ? 1u : key[e] == thr ? 0x10000u : 0u;
+    return x;
+  };
+  if (K > 0 && CS > 1) {  // how many this CTA has, for the CTAs after it
+    if (tid == 0) cta_gt = cta_eq = 0;
     __syncthreads();
-    // before this warp's stretch, within the CTA and in the CTAs before it
-    const uint32_t wg = lane < kWarps ? warp_gt[lane] : 0u, we = lane < kWarps ? warp_eq[lane] : 0u;
-    gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
-    eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
-    if (CS > 1) {
-      const uint32_t all_gt = __reduce_add_sync(0xffffffffu, wg);
-      const uint32_t all_eq = __reduce_add_sync(0xffffffffu, we);
-      if (tid == 0) {
-        cta_gt = all_gt;
-        cta_eq = all_eq;
+    for_runs([&](int) {
+      const uint32_t x = __reduce_add_sync(0xffffffffu, run_counts());
+      if (lane == 0) {
+        atomicAdd(&cta_gt, x & 0xffffu);
+        atomicAdd(&cta_eq, x >> 16);
       }
-    }
+    });
   }
   // Also: every CTA holds its part of the weights, so that moving them in place
   // overwrites nothing that is still to be read.
-  if (CS > 1) cluster_sync();
-  else __syncthreads();
+  sync();
   if (K > 0) {
     if (CS > 1) {
       uint32_t g = 0, e = 0;
@@ -248,66 +264,79 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
         g = ld_cluster(mapa_shared(smem_u32(&cta_gt), lane));
         e = ld_cluster(mapa_shared(smem_u32(&cta_eq), lane));
       }
-      gt_before += __reduce_add_sync(0xffffffffu, g);
-      eq_before += __reduce_add_sync(0xffffffffu, e);
+      gt_before = __reduce_add_sync(0xffffffffu, g);
+      eq_before = __reduce_add_sync(0xffffffffu, e);
     }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = a0; i0 < a1; i0 += 32) {
-      const int i = i0 + lane;
-      const float x = i < a1 ? weight_at(i) : 0.f;
-      const uint32_t key = weight_key(x);
-      const uint32_t g = __ballot_sync(0xffffffffu, i < a1 && key > thr);
-      const uint32_t e = __ballot_sync(0xffffffffu, i < a1 && key == thr);
-      const uint32_t gb = gt_before + __popc(g & below), eb = eq_before + __popc(e & below);
-      const bool take = ((g >> lane) & 1u) || (((e >> lane) & 1u) && eb < need);
-      if (take) {
-        const uint32_t at = p.sink + gb + min(eb, need);
-        kept[at] = p.sink + lo + i;
-        if (cached) wo[at] = x;
+    for_runs([&](int i0) {
+      const uint32_t mine = run_counts();
+      uint32_t pre = mine;  // over lanes <= this one
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, pre, off);
+        if (lane >= off) pre += y;
       }
-      gt_before += __popc(g);
-      eq_before += __popc(e);
-    }
+      if (lane == 31) warp_sum[warp] = pre;
+      __syncthreads();
+      const uint32_t ws = lane < kWarps ? warp_sum[lane] : 0u;
+      pre += __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u) - mine;  // before this run
+      uint32_t gt = gt_before + (pre & 0xffffu), eq = eq_before + (pre >> 16);
+      if (mine) {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+          const bool g = e < m && key[e] > thr, q = e < m && key[e] == thr;
+          if (g || (q && eq < need)) {
+            const uint32_t at = p.sink + gt + min(eq, need);
+            kept[at] = p.sink + lo + i0 + e;
+            if (CACHED) wo[at] = cache[i0 + i0 / kRun + e];
+          }
+          gt += g ? 1u : 0u;
+          eq += q ? 1u : 0u;
+        }
+      }
+      if (!CACHED) {
+        const uint32_t round = __reduce_add_sync(0xffffffffu, ws);
+        gt_before += round & 0xffffu;
+        eq_before += round >> 16;
+        __syncthreads();  // warp_sum is read
+      }
+    });
   }
   // The other weights: the sinks stay or are copied; the recent ones move down
   // in ascending chunks, each read before it is written (their places lie
   // below every recent one that is still to be read). Where the parts do not
   // fit the caches, one CTA moves the whole row that way, by the list.
-  if (CS > 1) cluster_sync();  // also: no CTA leaves while another reads its counts
-  else __syncthreads();
+  sync();  // also: no CTA leaves while another reads its counts
   if (rank != CS - 1) return;
-  if (cached && wo != w)
+  if (CACHED && wo != w)
     for (int j = tid; j < p.sink; j += T) wo[j] = w[j];
-  for (int j0 = cached ? p.budget - p.recent : 0; j0 < p.budget; j0 += T) {
+  for (int j0 = CACHED ? p.budget - p.recent : 0; j0 < p.budget; j0 += T) {
     const int j = j0 + tid;
     float x = 0.f;
-    if (j < p.budget) x = w[cached ? L - p.budget + j : __ldcg(kept + j)];
+    if (j < p.budget) x = w[CACHED ? L - p.budget + j : __ldcg(kept + j)];
     __syncthreads();
     if (j < p.budget) wo[j] = x;
   }
 }
 
-template <int T>
-cudaError_t select_launch(EvictParams& p, int B, cudaStream_t stream) {
-  constexpr size_t kMax = size_t(kSelCache) * sizeof(float);
+template <int T, bool CACHED>
+cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t stream) {
+  constexpr size_t kMost = kHistBytes + (CACHED ? size_t(T) * (kRun + 1) * sizeof(float) : 0);
   static bool done[64] = {};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!done[device]) {
-    if ((e = cudaFuncSetAttribute(evict_select_kernel<T>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMax))) !=
+    if ((e = cudaFuncSetAttribute(evict_select_kernel<T, CACHED>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost))) !=
         cudaSuccess)
       return e;
     done[device] = true;
   }
-  const int part = ((p.w_tokens + p.cluster - 1) / p.cluster + 31) / 32 * 32;
-  p.sel_cache = part <= kSelCache ? part : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.Hkv * p.cluster), unsigned(B));
   cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = size_t(p.sel_cache) * sizeof(float);
+  cfg.dynamicSmemBytes = kHistBytes + (CACHED ? size_t(part + part / kRun) * sizeof(float) : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -316,7 +345,23 @@ cudaError_t select_launch(EvictParams& p, int B, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<T, CACHED>, p);
+}
+
+// CTAs per row: as many as hold the row at kRun tokens per thread, and more
+// while the rows alone leave SMs idle and each CTA still has work for its
+// threads. Small blocks for short rows (their barriers cost less).
+cudaError_t select_rows(EvictParams& p, int B, int sms, cudaStream_t stream) {
+  constexpr int kSmall = 256, kLarge = 1024;
+  p.cluster = 1;
+  while (p.cluster < kSelCluster &&
+         (p.w_tokens > p.cluster * kLarge * kRun ||
+          (int64_t(B) * p.Hkv * p.cluster < sms && p.w_tokens > p.cluster * kSmall * kRun)))
+    p.cluster *= 2;
+  const int part = ((p.w_tokens + p.cluster - 1) / p.cluster + kRun - 1) / kRun * kRun;
+  if (part <= kSmall * kRun) return select_launch<kSmall, true>(p, part, B, stream);
+  if (part <= kLarge * kRun) return select_launch<kLarge, true>(p, part, B, stream);
+  return select_launch<kLarge, false>(p, part, B, stream);
 }
 
 // --------------------------------------------------------------------- move
@@ -405,15 +450,7 @@ cudaError_t evict_launch(EvictParams& p, int B, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
     return e;
-  // CTAs per row: as many as the caches of a row need, and more while the rows
-  // alone leave SMs idle and each CTA still has a few weights per thread.
-  p.cluster = 1;
-  while (p.cluster < kSelCluster &&
-         (p.w_tokens > p.cluster * kSelCache ||
-          (int64_t(B) * p.Hkv * p.cluster < sms && p.w_tokens > p.cluster * 4096)))
-    p.cluster *= 2;
-  e = p.w_tokens <= p.cluster * 4096 ? select_launch<256>(p, B, stream)
-                                     : select_launch<1024>(p, B, stream);
+  e = select_rows(p, B, sms, stream);
   if (e != cudaSuccess) return e;
   const bool in_place = p.dst_table == p.block_table;
   p.segments = in_place ? 1 : (p.budget + kSegment - 1) / kSegment;
