@@ -18,6 +18,7 @@ import contextlib
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -386,133 +387,212 @@ def call_ex(params: Params, scores: ScoreParams, stream=None):
                                    ctypes.c_void_p(stream.cuda_stream)), "zl_decode_attn_ex")
 
 
-def _expect(t, name, dtype, shape, device, contiguous=True):
-    """Check a tensor argument of the entry points below (None passes)."""
-    if t is None:
-        return
+# The binding's part of a small call (a decode step of a few short sequences) is
+# longer than its kernels, so the entry points below check each tensor with one
+# test of all it must be, and pack the parameter structs in one step. (ctypes
+# field by field, torch.cuda.current_stream() and a check per property took 37 us
+# of such a call.)
+_PARAMS = struct.Struct("@N3P3qPq3P9ifPNPi2PIi2P0P")
+_SCORES = struct.Struct("@Nfi3P2qif0P")
+_EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iP0P")
+_COMMIT = struct.Struct("@N2P3qPq2PqPP8iP0P")
+for _s, _c in ((_PARAMS, Params), (_SCORES, ScoreParams), (_EVICT, EvictParams),
+               (_COMMIT, CommitParams)):
+    assert _s.size == ctypes.sizeof(_c), _c.__name__
+
+
+def _pack(form, *values) -> bytes:
+    try:
+        return form.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"a size, count or stride is no integer, or out of range: {e}") from e
+
+
+def _refuse(t, name, dtype, shape, device, contiguous):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the pools on {device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags,
-                  same_width=True):
-    """The checks every call over a paged cache shares; returns (B, Hkv)."""
+def _expect(t, name, dtype, shape, device, contiguous=True):
+    """Check a tensor argument; returns its address."""
+    if (t.dtype != dtype or t.shape != shape or t.device != device
+            or (contiguous and not t.is_contiguous())):
+        _refuse(t, name, dtype, shape, device, contiguous)
+    return t.data_ptr()
+
+
+def _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags):
+    """The checks every call over a paged cache shares; returns (device, B, Hkv,
+    page, token, head strides, block-table stride, err_flags address)."""
     dev = k_pool.device
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"the pools are on {dev}, which is not the current device")
     if k_pool.dim() != 4 or (v_pool is not None and v_pool.dim() != 4):
         raise ValueError("pools are 4-D: [pages, slot, head, dim] (NHD) or "
                          "[pages, head, slot, dim] (HND)")
+    shape, st = k_pool.shape, k_pool.stride()
+    if layout == "NHD":
+        slots, Hkv, ts, hs = shape[1], shape[2], st[1], st[2]
+    elif layout == "HND":
+        slots, Hkv, ts, hs = shape[2], shape[1], st[2], st[1]
+    else:
+        raise ValueError(f"unknown layout {layout!r}")
+    if k_pool.dtype != torch.bfloat16:
+        raise ValueError(f"k_pool must be torch.bfloat16, not {k_pool.dtype}")
+    if st[3] != 1:
+        raise ValueError("pool rows must be contiguous")
     if v_pool is not None:
-        shape = k_pool.shape if same_width else k_pool.shape[:3] + v_pool.shape[3:]
-        _expect(v_pool, "v_pool", torch.bfloat16, shape, dev, contiguous=False)
-        if v_pool.stride(3) != 1:
-            raise ValueError("pool rows must be contiguous")
-    _expect(k_pool, "k_pool", torch.bfloat16, k_pool.shape, dev, contiguous=False)
-    slots, Hkv = (k_pool.shape[1], k_pool.shape[2]) if layout == "NHD" else (
-        k_pool.shape[2], k_pool.shape[1])
+        _expect(v_pool, "v_pool", torch.bfloat16, shape[:3] + v_pool.shape[3:], dev, False)
+        if v_pool.stride() != st:
+            raise ValueError("K and V pools must share strides, and their rows be contiguous")
     if slots != page_size:
         raise ValueError(f"the pools hold {slots} slots per page, page_size is {page_size}")
-    B = seq_lens.shape[0]
+    if seq_lens.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("seq_lens is 1-D and block_table 2-D")
+    B, width = block_table.shape
     _expect(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be 2-D")
-    _expect(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev,
-            contiguous=False)
-    if block_table.stride(1) != 1 or (B > 1 and block_table.stride(0) < block_table.shape[1]):
+    _expect(block_table, "block_table", torch.int32, (B, width), dev, False)
+    bts = block_table.stride()
+    if bts[1] != 1 or (B > 1 and bts[0] < width):
         raise ValueError("block_table rows must be contiguous and distinct")
+    err = None
     if err_flags is not None:
         if err_flags.dtype not in (torch.int32, torch.uint32) or err_flags.numel() < 1:
             raise ValueError("err_flags must be a 32-bit integer tensor")
         if err_flags.device != dev:
             raise ValueError(f"err_flags is on {err_flags.device}, the pools on {dev}")
-    return B, Hkv
+        err = err_flags.data_ptr()
+    return dev, B, Hkv, st[0], ts, hs, bts[0] if B > 1 else width, err
 
 
 def _token_rows(t, name, B, Hkv, device):
-    """fp32 [B, Hkv, tokens] with contiguous token rows that do not overlap."""
+    """fp32 [B, Hkv, tokens] with contiguous token rows; returns (address,
+    sequence stride, head stride, tokens)."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [B, Hkv, tokens]")
-    _expect(t, name, torch.float32, (B, Hkv, t.shape[2]), device, contiguous=False)
-    if t.shape[2] < 1 or (t.shape[2] > 1 and t.stride(2) != 1):
+    n = t.shape[2]
+    at = _expect(t, name, torch.float32, (B, Hkv, n), device, False)
+    st = t.stride()
+    if n < 1 or (n > 1 and st[2] != 1):
         raise ValueError(f"{name} needs contiguous rows of at least one token")
+    return at, st[0], st[1], n
 
 
-def _table_stride(block_table):
-    """A row's reach: the stride, or the width where a row is all there is."""
-    return block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+def _on(device, stream):
+    """The raw stream a call goes to (the device's current one by default), and
+    the context its scratch is allocated in: memory from torch's allocator is
+    reused in the order of that stream."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the pools are on {device}, which is not the current device")
+    cur = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None or stream.cuda_stream == cur:
+        return cur, _NO_CONTEXT
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _on(stream):
-    """The stream a call goes to, and the context its scratch is allocated in:
-    memory from torch's allocator is reused in the order of that stream."""
-    cur = torch.cuda.current_stream()
-    if stream is None or stream == cur:
-        return cur, contextlib.nullcontext()
-    return stream, torch.cuda.stream(stream)
+_NO_CONTEXT = contextlib.nullcontext()
+_raw: dict = {}
+_sizes: dict = {}  # workspace bytes of zl_decode_attn_ex by device and shapes
+
+
+def _raw_fn(name, nargs):
+    """The entry point taking packed structs (bytes) and plain addresses."""
+    fn = _raw.get(name)
+    if fn is None:
+        fn = lib()[name]  # a function object of its own: lib().name keeps its types
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.c_char_p] * nargs + [ctypes.c_void_p]
+        _raw[name] = fn
+    return fn
 
 
 def make_score_params(q, Hkv, *, softcap=0.0, alibi_slopes=None, window=0, tree_mask=None,
                       weights=None, weights_decay=1.0) -> ScoreParams:
-    """The score modifications of one decode_attn call (see there)."""
-    B, q_len, Hq, _ = q.shape
-    _expect(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), q.device)
-    if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int32, torch.uint32):
-            raise ValueError("tree_mask must be 32-bit words")
-        _expect(tree_mask, "tree_mask", tree_mask.dtype, (B, q_len, (q_len + 31) // 32), q.device)
-    m = ScoreParams()
-    m.struct_size = ctypes.sizeof(ScoreParams)
-    m.softcap, m.window = float(softcap), int(window)
-    m.alibi_slopes, m.tree_mask = _ptr(alibi_slopes), _ptr(tree_mask)
-    m.weights_decay = float(weights_decay)
-    if weights is not None:
-        _token_rows(weights, "weights", B, Hkv, q.device)
-        m.weights = weights.data_ptr()
-        m.weights_seq_stride, m.weights_head_stride = weights.stride(0), weights.stride(1)
-        m.weights_tokens = weights.shape[2]
+    """The score modifications of a decode_attn call (see there), for call_ex."""
+    m = ScoreParams.from_buffer_copy(_pack_scores(q.shape, Hkv, q.device, softcap, alibi_slopes,
+                                                  window, tree_mask, weights, weights_decay))
     m.tensors = (alibi_slopes, tree_mask, weights)
     return m
 
 
-def _run_ex(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, Hkv, out, lse,
-            workspace, err_flags, num_ctas, max_seq_len, layout, stream, events, k_new, v_new,
-            mods):
+def _pack_scores(q_shape, Hkv, dev, softcap, alibi_slopes, window, tree_mask, weights,
+                 weights_decay) -> bytes:
+    B, q_len, Hq, _ = q_shape
+    slopes = mask = w = None
+    ws = wh = wt = 0
+    if alibi_slopes is not None:
+        slopes = _expect(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), dev)
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.int32, torch.uint32):
+            raise ValueError("tree_mask must be 32-bit words")
+        mask = _expect(tree_mask, "tree_mask", tree_mask.dtype, (B, q_len, (q_len + 31) // 32),
+                       dev)
+    if weights is not None:
+        w, ws, wh, wt = _token_rows(weights, "weights", B, Hkv, dev)
+    return _pack(_SCORES, _SCORES.size, softcap, window, slopes or 0, mask or 0, w or 0, ws, wh, wt,
+                        weights_decay)
+
+
+def _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size, scale, out, lse, workspace,
+            err_flags, num_ctas, max_seq_len, layout, stream, events, k_new, v_new, softcap,
+            alibi_slopes, window, tree_mask, weights, weights_decay):
     """decode_attn with modified scores (zl_decode_attn_ex)."""
     if q.dim() != 4 or v_pool is None:
         raise ValueError("q must be [B, q_len, Hq, D], with K and V pools")
-    _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
-    B, q_len, Hq, D = q.shape
-    dev = k_pool.device
-    _expect(q, "q", torch.bfloat16, (seq_lens.shape[0], q_len, Hq, k_pool.shape[3]), dev)
-    _expect(out, "out", torch.bfloat16, (B, q_len, Hq, D), dev)
-    _expect(lse, "lse", torch.float32, (B, q_len, Hq), dev)
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _expect(t, name, torch.bfloat16, (B, q_len, Hkv, D), dev)
-    m = make_score_params(q, Hkv, **mods)
-    on, scratch = _on(stream)
+    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
+        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    shape = q.shape
+    _, q_len, Hq, D = shape
+    if v_pool.shape[3] != D:
+        raise ValueError("q and the pools' rows must be equally wide")
+    q_at = _expect(q, "q", torch.bfloat16, (B, q_len, Hq, k_pool.shape[3]), dev)
+    lse_at = kn = vn = None
+    if lse is not None:
+        lse_at = _expect(lse, "lse", torch.float32, (B, q_len, Hq), dev)
+    if k_new is not None:
+        kn = _expect(k_new, "k_new", torch.bfloat16, (B, q_len, Hkv, D), dev)
+    if v_new is not None:
+        vn = _expect(v_new, "v_new", torch.bfloat16, (B, q_len, Hkv, D), dev)
+    if out is not None:
+        _expect(out, "out", torch.bfloat16, shape, dev)
+    mods = _pack_scores(shape, Hkv, dev, softcap, alibi_slopes, window, tree_mask, weights,
+                        weights_decay)
+    on, scratch = _on(dev, stream)
+    begin, end = (events[0].cuda_event, events[1].cuda_event) if events is not None else (0, 0)
+
+    def pack(ws_at, ws_bytes):
+        return _pack(
+            _PARAMS, _PARAMS.size, q_at, k_pool.data_ptr(), v_pool.data_ptr(), ps, ts, hs,
+            block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), out_at, lse_at or 0, B, q_len,
+            Hq, Hkv, D, D, page_size, k_pool.shape[0], max_seq_len, scale, ws_at, ws_bytes,
+            err or 0, num_ctas, begin or 0, end or 0, 0, 0, kn or 0, vn or 0)
+
     with scratch:
         if out is None:
-            out = torch.empty((B, q_len, Hq, D), dtype=torch.bfloat16, device=dev)
-        p = make_params(q, k_pool, v_pool, block_table, seq_lens, out, page_size=page_size,
-                        scale=scale, Hkv=Hkv, D_v=D, lse=lse, err_flags=err_flags,
-                        num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout, events=events,
-                        k_new=k_new, v_new=v_new)
-        p.block_table_stride = _table_stride(block_table)
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out_at = out.data_ptr()
         if workspace is None:
             # a call's own: stream order alone separates it from other calls,
-            # and a captured graph keeps it
-            workspace = torch.empty(max(workspace_size_ex(p, m), 256), dtype=torch.uint8,
-                                    device=dev)
-        p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.numel() * workspace.element_size()
-        call_ex(p, m, on)
+            # and a captured graph keeps it. Its size follows from the shapes.
+            key = (dev.index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len,
+                   window, 0 if weights is None else weights.shape[2])
+            need = _sizes.get(key)
+            if need is None:
+                n = ctypes.c_size_t(0)
+                _check(_raw_fn("zl_decode_attn_ex_workspace_size", 2)(pack(0, 0), mods,
+                                                                      ctypes.addressof(n)),
+                       "zl_decode_attn_ex_workspace_size")
+                if len(_sizes) >= 4096:
+                    _sizes.clear()
+                need = _sizes[key] = n.value or 256
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        params = pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        _check(_raw_fn("zl_decode_attn_ex", 2)(params, mods, on), "zl_decode_attn_ex")
     return out
 
 
@@ -566,17 +646,14 @@ def decode_attn(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, o
     weight, summed over the query tokens and the heads of its kv head, is added
     to weights_decay times what it holds.
     """
-    Hkv = k_pool.shape[2] if layout == "NHD" else k_pool.shape[1]
-    if softcap or window or any(t is not None for t in (alibi_slopes, tree_mask, weights)):
+    if (softcap or window or alibi_slopes is not None or tree_mask is not None
+            or weights is not None):
         if single_launch or shared_prefix_pages:
             raise ZlError(ERR_UNSUPPORTED, "modified scores with single_launch or a shared prefix")
-        return _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size=page_size, scale=scale,
-                       Hkv=Hkv, out=out, lse=lse, workspace=workspace, err_flags=err_flags,
-                       num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout, stream=stream,
-                       events=events, k_new=k_new, v_new=v_new,
-                       mods=dict(softcap=softcap, alibi_slopes=alibi_slopes, window=window,
-                                 tree_mask=tree_mask, weights=weights,
-                                 weights_decay=weights_decay))
+        return _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size, scale, out, lse,
+                       workspace, err_flags, num_ctas, max_seq_len, layout, stream, events, k_new,
+                       v_new, softcap, alibi_slopes, window, tree_mask, weights, weights_decay)
+    Hkv = k_pool.shape[2] if layout == "NHD" else k_pool.shape[1]
     return _run(q, k_pool, v_pool, block_table, seq_lens, mla=False, page_size=page_size,
                 scale=scale, Hkv=Hkv, D_v=q.shape[3], out=out, lse=lse, workspace=workspace,
                 err_flags=err_flags, num_ctas=num_ctas, max_seq_len=max_seq_len, layout=layout,
@@ -669,30 +746,6 @@ def tree_mask(parents) -> torch.Tensor:
     return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
 
 
-def _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, *, page_size, layout,
-                 err_flags):
-    # (new_lens and other outputs left out are allocated once the checks have passed)
-    """The fields zl_kv_evict_params and zl_kv_commit_params share."""
-    B, Hkv = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags,
-                           same_width=False)
-    _expect(new_lens, "new_lens", torch.int32, (B,), k_pool.device)
-    ps, ts, hs = _pool_strides(k_pool, layout)
-    if v_pool is not None and _pool_strides(v_pool, layout) != (ps, ts, hs):
-        raise ValueError("K and V pools must share strides")
-    if k_pool.stride(3) != 1:
-        raise ValueError("pool rows must be contiguous")
-    p.struct_size = ctypes.sizeof(type(p))
-    p.k_pool, p.v_pool = _ptr(k_pool), _ptr(v_pool)
-    p.page_stride, p.token_stride, p.head_stride = ps, ts, hs
-    p.block_table, p.block_table_stride = _ptr(block_table), _table_stride(block_table)
-    p.seq_lens = _ptr(seq_lens)
-    p.B, p.Hkv, p.D_k = B, Hkv, k_pool.shape[3]
-    p.D_v = 0 if v_pool is None else v_pool.shape[3]
-    p.page_size, p.num_pages = page_size, k_pool.shape[0]
-    p.err_flags = _ptr(err_flags)
-    return B, Hkv
-
-
 def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budget, sink=0,
              recent=0, new_lens=None, kept=None, weights_out=None, dst_block_table=None,
              layout="NHD", err_flags=None, stream=None):
@@ -706,39 +759,42 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
     Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]: the kept
     positions, then -1).
     """
-    if weights is None or seq_lens.dim() != 1:
-        raise ValueError("weights is required, and seq_lens is 1-D")
-    p = EvictParams()
-    B, Hkv = _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, page_size=page_size,
-                          layout=layout, err_flags=err_flags)
-    _token_rows(weights, "weights", B, Hkv, k_pool.device)
-    _expect(kept, "kept", torch.int32, (B, Hkv, budget), k_pool.device)
-    p.weights, p.weights_tokens = weights.data_ptr(), weights.shape[2]
-    p.weights_seq_stride, p.weights_head_stride = weights.stride(0), weights.stride(1)
+    if weights is None:
+        raise ValueError("weights is required")
+    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
+        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    w, w_seq, w_head, tokens = _token_rows(weights, "weights", B, Hkv, dev)
+    wo = wo_seq = wo_head = dst = dst_stride = 0
     if weights_out is not None:
-        _token_rows(weights_out, "weights_out", B, Hkv, k_pool.device)
-        if weights_out.shape[2] < min(budget, weights.shape[2]):
+        wo, wo_seq, wo_head, out_tokens = _token_rows(weights_out, "weights_out", B, Hkv, dev)
+        if out_tokens < min(budget, tokens):
             raise ValueError("weights_out is shorter than what the budget may leave")
-        p.weights_out = weights_out.data_ptr()
-        p.weights_out_seq_stride = weights_out.stride(0)
-        p.weights_out_head_stride = weights_out.stride(1)
     if dst_block_table is not None:
-        _expect(dst_block_table, "dst_block_table", torch.int32, (B, dst_block_table.shape[1]),
-                k_pool.device, contiguous=False)
-        if dst_block_table.stride(1) != 1:
-            raise ValueError("block_table rows must be contiguous")
-        p.dst_block_table = dst_block_table.data_ptr()
-        p.dst_block_table_stride = _table_stride(dst_block_table)
-    p.budget, p.sink, p.recent = int(budget), int(sink), int(recent)
-    on, scratch = _on(stream)
+        if dst_block_table.dim() != 2:
+            raise ValueError("dst_block_table must be 2-D")
+        width = dst_block_table.shape[1]
+        dst = _expect(dst_block_table, "dst_block_table", torch.int32, (B, width), dev, False)
+        st = dst_block_table.stride()
+        if st[1] != 1 or (B > 1 and st[0] < width):
+            raise ValueError("dst_block_table rows must be contiguous and distinct")
+        dst_stride = st[0] if B > 1 else width
+    if new_lens is not None:
+        _expect(new_lens, "new_lens", torch.int32, (B,), dev)
+    if kept is not None:
+        _expect(kept, "kept", torch.int32, (B, Hkv, budget), dev)
+    on, scratch = _on(dev, stream)
     with scratch:
         if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=k_pool.device)
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
         if kept is None:
-            kept = torch.empty(B, Hkv, max(int(budget), 1), dtype=torch.int32,
-                               device=k_pool.device)
-    p.new_lens, p.kept = new_lens.data_ptr(), kept.data_ptr()
-    _check(lib().zl_kv_evict(ctypes.byref(p), ctypes.c_void_p(on.cuda_stream)), "zl_kv_evict")
+            kept = torch.empty(B, Hkv, max(budget, 1), dtype=torch.int32, device=dev)
+    params = _pack(
+        _EVICT, _EVICT.size, k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), ps, ts, hs,
+        block_table.data_ptr(), bt_stride, dst, dst_stride, seq_lens.data_ptr(),
+        new_lens.data_ptr(), kept.data_ptr(), w, w_seq, w_head, wo, wo_seq, wo_head, tokens, B,
+        Hkv, k_pool.shape[3], 0 if v_pool is None else v_pool.shape[3], page_size,
+        k_pool.shape[0], budget, sink, recent, err or 0)
+    _check(_raw_fn("zl_kv_evict", 1)(params, on), "zl_kv_evict")
     return new_lens, kept
 
 
@@ -751,23 +807,26 @@ def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_siz
     become the tokens after the context, in place. v_pool None: a latent-only
     pool. Returns new_lens int32 [B] (context plus accepted).
     """
-    if seq_lens.dim() != 1 or path.dim() != 2:
-        raise ValueError("seq_lens is 1-D and path 2-D")
-    p = CommitParams()
-    B, _ = _move_fields(p, k_pool, v_pool, block_table, seq_lens, new_lens, page_size=page_size,
-                        layout=layout, err_flags=err_flags)
-    _expect(path, "path", torch.int32, (B, path.shape[1]), k_pool.device, contiguous=False)
-    _expect(accepted, "accepted", torch.int32, (B,), k_pool.device)
-    if path.shape[1] > 1 and path.stride(1) != 1:
+    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
+        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    if path.dim() != 2:
+        raise ValueError("path must be 2-D")
+    n = path.shape[1]
+    path_at = _expect(path, "path", torch.int32, (B, n), dev, False)
+    st = path.stride()
+    if n > 1 and st[1] != 1:
         raise ValueError("path rows must be contiguous")
-    p.path, p.path_len = path.data_ptr(), path.shape[1]
-    p.path_stride = path.stride(0) if B > 1 else path.shape[1]
-    p.accepted = accepted.data_ptr()
-    p.q_len = int(q_len)
-    on, scratch = _on(stream)
+    acc = _expect(accepted, "accepted", torch.int32, (B,), dev)
+    if new_lens is not None:
+        _expect(new_lens, "new_lens", torch.int32, (B,), dev)
+    on, scratch = _on(dev, stream)
     with scratch:
         if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=k_pool.device)
-    p.new_lens = new_lens.data_ptr()
-    _check(lib().zl_kv_commit(ctypes.byref(p), ctypes.c_void_p(on.cuda_stream)), "zl_kv_commit")
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    params = _pack(
+        _COMMIT, _COMMIT.size, k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), ps, ts, hs,
+        block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), path_at, st[0] if B > 1 else n,
+        acc, new_lens.data_ptr(), n, B, q_len, Hkv, k_pool.shape[3],
+        0 if v_pool is None else v_pool.shape[3], page_size, k_pool.shape[0], err or 0)
+    _check(_raw_fn("zl_kv_commit", 1)(params, on), "zl_kv_commit")
     return new_lens

@@ -138,6 +138,17 @@ def test_bad_path_bit_matches_the_header():
     assert f"#define ZL_DEVERR_BAD_PATH {zl.DEVERR_BAD_PATH}u" in open(zl.HEADER).read()
 
 
+@pytest.mark.parametrize("form,mirror", [("_PARAMS", "Params"), ("_SCORES", "ScoreParams"),
+                                         ("_EVICT", "EvictParams"), ("_COMMIT", "CommitParams")])
+def test_packed_structs_match_the_mirrors(form, mirror):
+    """The binding packs the parameter structs in one step: every field where
+    the ctypes mirror has it."""
+    form, mirror = getattr(zl, form), getattr(zl, mirror)
+    n = len(mirror._fields_)
+    got = mirror.from_buffer_copy(form.pack(*range(1, n + 1)))
+    assert [float(getattr(got, name)) for name, _ in mirror._fields_] == list(range(1, n + 1))
+
+
 # ------------------------------------------------------------ the binding's checks
 def _tensors(B=2, q_len=3, Hq=8, Hkv=2, P=16, pages=6):
     return dict(q=torch.zeros(B, q_len, Hq, 128, dtype=torch.bfloat16),
@@ -180,6 +191,27 @@ def test_decode_attn_with_mods_refuses_other_modes():
             zl.decode_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], page_size=16, scale=0.1,
                            window=8, **kw)
         assert e.value.status == zl.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(window=2.5), dict(window=1 << 40), dict(softcap=3.0,
+                                                                             num_ctas=1 << 33)])
+def test_decode_attn_refuses_numbers_out_of_range(kw):
+    d = _tensors()
+    with pytest.raises(ValueError):
+        zl.decode_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], page_size=16, scale=0.1, **kw)
+
+
+def test_calls_off_the_gpu_are_refused():
+    d = _tensors()
+    w = torch.zeros(2, 2, 48)
+    path, acc = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    for call in (lambda: zl.decode_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], page_size=16,
+                                        scale=0.1, softcap=3.0),
+                 lambda: zl.kv_evict(d["k"], d["v"], d["bt"], d["sl"], w, page_size=16, budget=8),
+                 lambda: zl.kv_commit(d["k"], d["v"], d["bt"], d["sl"], path, acc, page_size=16,
+                                      q_len=3)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
 
 
 def test_evict_and_commit_refuse_wrong_tensors():
