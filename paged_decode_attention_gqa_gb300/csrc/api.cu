@@ -430,14 +430,33 @@ zl_status validate_pointers(const zl_decode_attn_params* a, bool need_v) {
 
 namespace {
 
+// The kernels' cap fields (kernels.h, gqa_wide.h) for scores c tanh(s / c).
+template <class Params>
+void set_cap(float scale, float c, Params* p) {
+  if (!(c > 0.f)) return;
+  p->cap_in = float(double(scale) / c);
+  p->cap_out = float(double(c) * kLog2e);
+  // coefficients and bound in the dot product's own units; where they leave
+  // the range of normal 32-bit numbers, every score takes the full function
+  const double in = double(scale) / c, poly[4] = ZL_CAP_POLYNOMIAL;
+  bool normal = true;
+  double f = in * c * kLog2e;
+  for (int i = 0; i < 4; ++i, f *= in * in) {
+    p->cap_f[i] = float(poly[i] * f);
+    normal = normal && std::isnormal(p->cap_f[i]);
+  }
+  p->cap_z = float(0.25 / (in * in));
+  if (!normal || !std::isnormal(p->cap_z)) {
+    std::memset(p->cap_f, 0, sizeof(p->cap_f));
+    p->cap_z = -1.f;
+  }
+}
+
 // The modified-score launches: every row group in one attention launch, its
 // merge, and the weights kernel when the call accumulates weights.
 zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, const GqaPlan& plan,
                    GqaParams& p, char* ws, cudaStream_t s) {
-  if (m.softcap > 0.f) {
-    p.cap_in = float(double(a->scale) / m.softcap);
-    p.cap_out = float(double(m.softcap) * kLog2e);
-  }
+  set_cap(a->scale, m.softcap, &p);
   p.slopes = m.alibi_slopes;
   p.window = m.window;
   p.tree = m.tree_mask;
@@ -516,24 +535,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.nblk = plan.nblk;
   p.len_cap = a->block_table_stride * int64_t(a->page_size);
   p.scale_log2 = float(double(a->scale) * kLog2e);
-  if (m.softcap > 0.f) {
-    p.cap_in = float(double(a->scale) / m.softcap);
-    p.cap_out = float(double(m.softcap) * kLog2e);
-    // coefficients and bound in the dot product's own units; where they leave
-    // the range of normal 32-bit numbers, every chunk takes the full function
-    const double in = double(a->scale) / m.softcap, poly[4] = ZL_CAP_POLYNOMIAL;
-    bool normal = true;
-    double f = in * m.softcap * kLog2e;
-    for (int i = 0; i < 4; ++i, f *= in * in) {
-      p.cap_f[i] = float(poly[i] * f);
-      normal = normal && std::isnormal(p.cap_f[i]);
-    }
-    p.cap_z = float(0.25 / (in * in));
-    if (!normal || !std::isnormal(p.cap_z)) {
-      std::memset(p.cap_f, 0, sizeof(p.cap_f));
-      p.cap_z = -1.f;
-    }
-  }
+  set_cap(a->scale, m.softcap, &p);
   p.slopes = m.alibi_slopes;
   p.window = m.window;
   p.tree = m.tree_mask;

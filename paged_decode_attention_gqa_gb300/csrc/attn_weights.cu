@@ -15,7 +15,8 @@ namespace zl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 4;  // tokens per thread, kThreads apart
+constexpr int kPer = 4;    // tokens per thread, kThreads apart
+constexpr int kRows = 4;   // query rows whose scores are read together
 
 __global__ void __launch_bounds__(kThreads)
 attn_weights_kernel(const __grid_constant__ WeightsParams p) {
@@ -34,14 +35,29 @@ attn_weights_kernel(const __grid_constant__ WeightsParams p) {
   if (t0 + kThreads * kPer > lo) {
     for (int i = 0; i < p.q_total; ++i) {
       const int64_t row0 = (int64_t(b) * p.q_total + i) * p.Hq + int64_t(h) * p.g;
-      for (int j = 0; j < p.g; ++j) {
-        const float2 stat = __ldg(p.row_stat + row0 + j);
-        if (stat.y == 0.f) continue;  // a row without weight, or over a bad page
-        const float* s = p.scores + (row0 + j) * p.score_stride;
+      // 16 loads in flight per thread (one row at a time took twice as long)
+      for (int j = 0; j < p.g; j += kRows) {
+        float2 stat[kRows];
+        float x[kRows][kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int tk = t + k * kThreads;
-          if (tk >= lo && tk < L) sum[k] += ex2_approx(__ldg(s + tk) - stat.x) * stat.y;
+        for (int r = 0; r < kRows; ++r) {
+          // (0, 0): a row without weight, or over a bad page, or past the last
+          stat[r] = j + r < p.g ? __ldg(p.row_stat + row0 + j + r) : make_float2(0.f, 0.f);
+          const float* s = p.scores + (row0 + min(j + r, p.g - 1)) * p.score_stride;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int tk = t + k * kThreads;
+            x[r][k] = tk >= lo && tk < L ? __ldcs(s + tk) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          if (stat[r].y == 0.f) continue;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int tk = t + k * kThreads;
+            if (tk >= lo && tk < L) sum[k] += ex2_approx(x[r][k] - stat[r].x) * stat[r].y;
+          }
         }
       }
     }

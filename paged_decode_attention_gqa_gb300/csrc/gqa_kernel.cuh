@@ -460,33 +460,60 @@ struct ModRow {
 // One row's scores over this thread's four tokens of a tile (2 t4, 2 t4 + 1, 2
 // t4 + 8, 2 t4 + 9): dot products -> base-2 scores, -inf where the row does
 // not see the token; mx = the row's max over the whole tile. Returns whether
-// the row sees any of the four.
-__device__ __forceinline__ bool mod_row_scores(const GqaParams& p, const ModRow& row,
+// the row sees any of the four. `inside`: every row of the launch sees the
+// whole tile, which lies before the query tokens (the same for the whole warp;
+// nearly every tile of a long context: the test per token took a tenth of the
+// call's time).
+__device__ __forceinline__ bool mod_row_scores(const GqaParams& p, const ModRow& row, bool inside,
                                                const float (&dot)[4], int tok0, int L, int t4,
                                                float (&x)[4], float& mx) {
-  const bool drafted = row.bits != nullptr && tok0 + kGqaTile > row.ctx;
-  bool any = false;
+  if (p.cap_in > 0.f) {
+    // the short polynomial up to half the cap, the full function beyond
+    float z[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = tok0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
-    int dist = row.pos - t;  // in positions
-    bool vis = dist >= 0 && t >= row.lo && t < L;
-    if (drafted) {
-      const int j = t - row.ctx;
-      if (j >= 0 && t < L) {
-        vis = (__ldg(row.bits + (j >> 5)) >> (j & 31)) & 1u;
-        if (vis && (p.window || p.slopes)) {
-          dist = row.pos - row.ctx - tree_depth(row.seq_bits + int64_t(j) * p.tree_words,
-                                                p.tree_words);
-          vis = !p.window || dist < p.window;
+    for (int k = 0; k < 4; ++k) {
+      z[k] = dot[k] * dot[k];
+      x[k] = dot[k] * fmaf(fmaf(fmaf(z[k], p.cap_f[3], p.cap_f[2]), z[k], p.cap_f[1]), z[k],
+                           p.cap_f[0]);
+    }
+    if (__any_sync(0xffffffffu, !(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) <= p.cap_z))) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = cap_tanh(dot[k] * p.cap_in) * p.cap_out;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = dot[k] * p.scale_log2;
+  }
+  bool any = inside;
+  if (inside) {
+    if (p.slopes) {
+      const float d = float(row.pos - tok0 - 2 * t4);  // distance of the first token
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = fmaf(-row.slope2, d - float((k & 1) + (k >> 1) * 8), x[k]);
+    }
+  } else {
+    const bool drafted = row.bits != nullptr && tok0 + kGqaTile > row.ctx;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = tok0 + 2 * t4 + (k & 1) + (k >> 1) * 8;
+      int dist = row.pos - t;  // in positions
+      bool vis = dist >= 0 && t >= row.lo && t < L;
+      if (drafted) {
+        const int j = t - row.ctx;
+        if (j >= 0 && t < L) {
+          vis = (__ldg(row.bits + (j >> 5)) >> (j & 31)) & 1u;
+          if (vis && (p.window || p.slopes)) {
+            dist = row.pos - row.ctx - tree_depth(row.seq_bits + int64_t(j) * p.tree_words,
+                                                  p.tree_words);
+            vis = !p.window || dist < p.window;
+          }
         }
       }
+      vis = vis && row.live;
+      any |= vis;
+      x[k] = vis ? fmaf(-row.slope2, float(dist), x[k]) : -CUDART_INF_F;
     }
-    vis = vis && row.live;
-    any |= vis;
-    float v = p.cap_in > 0.f ? cap_tanh(dot[k] * p.cap_in) * p.cap_out : dot[k] * p.scale_log2;
-    v = fmaf(-row.slope2, float(dist), v);
-    x[k] = vis ? v : -CUDART_INF_F;
   }
   mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -907,11 +934,13 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
         float mxa, mxb = -CUDART_INF_F;
         if constexpr (MODE == kModeMod) {
           const float sa[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
-          bool seen = mod_row_scores(p, mod_a, sa, tok0, L, t4, xa, mxa);
+          const bool inside = !stage_is_bad && tok0 + kGqaTile <= L - p.q_total &&
+                              (!p.window || tok0 >= L - p.window);
+          bool seen = mod_row_scores(p, mod_a, inside, sa, tok0, L, t4, xa, mxa);
           bad_a |= stage_is_bad && seen;
           if (ROWS16) {
             const float sb[4] = {s[0][2], s[0][3], s[1][2], s[1][3]};
-            seen = mod_row_scores(p, mod_b, sb, tok0, L, t4, xb, mxb);
+            seen = mod_row_scores(p, mod_b, inside, sb, tok0, L, t4, xb, mxb);
             bad_b |= stage_is_bad && seen;
           }
           if (p.scores) {

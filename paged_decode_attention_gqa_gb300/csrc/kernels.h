@@ -93,6 +93,9 @@ struct GqaParams {
   // Modified scores (the kModeMod instances; zero otherwise; see gqa_mod.cu).
   float cap_in;            // tanh cap c: scale / c, 0 = no cap
   float cap_out;           // c * log2(e)
+  // The capped score in base 2 as x (cap_f[0] + cap_f[1] z + ..), z = x^2, of the
+  // dot product x; right where z <= cap_z (-1: nowhere)
+  float cap_f[4], cap_z;
   const float* slopes;     // distance bias of each query head [Hq], or nullptr
   int window;              // tokens a query sees back from its position, 0 = all
   const uint32_t* tree;    // ancestor bits [B, q_total, tree_words], or nullptr (a chain)
