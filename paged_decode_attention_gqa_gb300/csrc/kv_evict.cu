@@ -59,7 +59,6 @@ __device__ __forceinline__ bool evict_len_ok(const EvictParams& p, int L) {
 }
 
 // ------------------------------------------------------------------- select
-constexpr int kRun = 16;          // consecutive tokens of a thread
 constexpr int kSelCluster = 8;    // CTAs per row at most (the portable cluster size)
 
 // A key that orders as the weights do: larger weight, larger key; -0 as +0,
@@ -79,14 +78,15 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
 constexpr int kBins = 256;        // of a digit: 4 digits of 8 bits
 constexpr int kHistBytes = kBins * 32 * 4;
 
-// T threads. Every lane counts in a histogram of its own: the weights' leading
+// T threads of kRun consecutive tokens each, kBlocks blocks per SM. Every lane counts in a histogram of its own: the weights' leading
 // digits fall into a few bins, and additions to one address, by lanes of a warp
 // or by warps, are done one after the other. CACHED: this CTA's part fits
 // kRun tokens per thread; then a thread holds their keys in registers through
 // all passes (computing them again in each pass was 390 instructions per token
 // in all), and shared memory the weights. Otherwise they are read again.
-template <int T, bool CACHED>
-__global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__ EvictParams p) {
+template <int T, int kRun, int kBlocks, bool CACHED>
+__global__ void __launch_bounds__(T, kBlocks)
+evict_select_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = T / 32;
   static_assert(T >= kBins, "a thread for every bin");
   extern __shared__ uint32_t lane_hist[];  // [kBins][32]
@@ -139,13 +139,13 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
     }
   };
   if (CACHED) {
-    for (int i0 = tid; i0 < n; i0 += T * 8) {  // eight loads in flight
-      float x[8];
+    for (int i0 = tid; i0 < n; i0 += T * 16) {  // sixteen loads in flight
+      float x[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < 16; ++u)
         if (i0 + u * T < n) x[u] = c[i0 + u * T];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 16; ++u) {
         const int i = i0 + u * T;
         if (i < n) cache[i + i / kRun] = x[u];
       }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(T) evict_select_kernel(const __grid_constant__
   }
 }
 
-template <int T, bool CACHED>
+template <int T, int kRun, int kBlocks, bool CACHED>
 cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t stream) {
   constexpr size_t kMost = kHistBytes + (CACHED ? size_t(T) * (kRun + 1) * sizeof(float) : 0);
   static bool done[64] = {};
@@ -327,7 +327,7 @@ cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
   if (!done[device]) {
-    if ((e = cudaFuncSetAttribute(evict_select_kernel<T, CACHED>,
+    if ((e = cudaFuncSetAttribute(evict_select_kernel<T, kRun, kBlocks, CACHED>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost))) !=
         cudaSuccess)
       return e;
@@ -336,7 +336,7 @@ cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t st
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.Hkv * p.cluster), unsigned(B));
   cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = kHistBytes + (CACHED ? size_t(part + part / kRun) * sizeof(float) : 0);
+  cfg.dynamicSmemBytes = kHistBytes + (CACHED ? size_t((part + kRun - 1) / kRun) * (kRun + 1) * sizeof(float) : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -345,23 +345,26 @@ cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t st
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<T, CACHED>, p);
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<T, kRun, kBlocks, CACHED>, p);
 }
 
-// CTAs per row: as many as hold the row at kRun tokens per thread, and more
-// while the rows alone leave SMs idle and each CTA still has work for its
-// threads. Small blocks for short rows (their barriers cost less).
+// CTAs per row: as many as hold the row, and more while the rows alone leave SMs
+// idle and each CTA still has work for its threads. Small blocks for short rows
+// (their barriers cost less); longer runs and two blocks per SM for long ones:
+// a row takes about 23 us of passes and barriers whatever its length, so what
+// counts is how many are under way (64 rows of 32k-131k tokens: 91 us with 1024
+// threads of 16 tokens, one block per SM).
 cudaError_t select_rows(EvictParams& p, int B, int sms, cudaStream_t stream) {
-  constexpr int kSmall = 256, kLarge = 1024;
+  constexpr int kSmall = 256 * 16, kLarge = 512 * 32;  // tokens a CTA holds
   p.cluster = 1;
   while (p.cluster < kSelCluster &&
-         (p.w_tokens > p.cluster * kLarge * kRun ||
-          (int64_t(B) * p.Hkv * p.cluster < sms && p.w_tokens > p.cluster * kSmall * kRun)))
+         (p.w_tokens > p.cluster * kLarge ||
+          (int64_t(B) * p.Hkv * p.cluster < sms && p.w_tokens > p.cluster * kSmall)))
     p.cluster *= 2;
-  const int part = ((p.w_tokens + p.cluster - 1) / p.cluster + kRun - 1) / kRun * kRun;
-  if (part <= kSmall * kRun) return select_launch<kSmall, true>(p, part, B, stream);
-  if (part <= kLarge * kRun) return select_launch<kLarge, true>(p, part, B, stream);
-  return select_launch<kLarge, false>(p, part, B, stream);
+  const int part = (p.w_tokens + p.cluster - 1) / p.cluster;
+  if (part <= kSmall) return select_launch<256, 16, 4, true>(p, part, B, stream);
+  if (part <= kLarge) return select_launch<512, 32, 2, true>(p, part, B, stream);
+  return select_launch<512, 32, 2, false>(p, part, B, stream);
 }
 
 // --------------------------------------------------------------------- move
