@@ -408,88 +408,101 @@ def _pack(form, *values) -> bytes:
         raise ValueError(f"a size, count or stride is no integer, or out of range: {e}") from e
 
 
-def _refuse(t, name, dtype, shape, device, contiguous):
+def _refuse(t, name, dtype, shape, index, contiguous):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pools on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the K pool on device {index}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _expect(t, name, dtype, shape, device, contiguous=True):
-    """Check a tensor argument; returns its address."""
-    if (t.dtype != dtype or t.shape != shape or t.device != device
-            or (contiguous and not t.is_contiguous())):
-        _refuse(t, name, dtype, shape, device, contiguous)
-    return t.data_ptr()
+def _expect(t, name, dtype, shape, index, contiguous=True):
+    """Check a tensor argument (index: the K pool's device, -1 the CPU); returns
+    its address."""
+    if (t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and (not contiguous or t.is_contiguous())):
+        return t.data_ptr()
+    return _refuse(t, name, dtype, shape, index, contiguous)
+
+
+_BF16, _F32, _I32, _U32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
 
 
 def _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags):
-    """The checks every call over a paged cache shares; returns (device, B, Hkv,
-    page, token, head strides, block-table stride, err_flags address)."""
-    dev = k_pool.device
-    if k_pool.dim() != 4 or (v_pool is not None and v_pool.dim() != 4):
+    """The checks every call over a paged cache shares; returns (device index, B,
+    Hkv, the pools' shape, V's width, strides in (page, token, head) order, the
+    addresses of both pools, the block table and its stride, seq_lens and
+    err_flags)."""
+    index, shape, st = k_pool.get_device(), k_pool.shape, k_pool.stride()
+    if len(shape) != 4 or (v_pool is not None and v_pool.dim() != 4):
         raise ValueError("pools are 4-D: [pages, slot, head, dim] (NHD) or "
                          "[pages, head, slot, dim] (HND)")
-    shape, st = k_pool.shape, k_pool.stride()
     if layout == "NHD":
-        slots, Hkv, ts, hs = shape[1], shape[2], st[1], st[2]
+        _, slots, Hkv, _ = shape
+        ps, ts, hs, one = st
     elif layout == "HND":
-        slots, Hkv, ts, hs = shape[2], shape[1], st[2], st[1]
+        _, Hkv, slots, _ = shape
+        ps, hs, ts, one = st
     else:
         raise ValueError(f"unknown layout {layout!r}")
-    if k_pool.dtype != torch.bfloat16:
-        raise ValueError(f"k_pool must be torch.bfloat16, not {k_pool.dtype}")
-    if st[3] != 1:
+    if k_pool.dtype is not _BF16:
+        raise ValueError(f"k_pool must be {_BF16}, not {k_pool.dtype}")
+    if one != 1:
         raise ValueError("pool rows must be contiguous")
+    v_at = width_v = 0
     if v_pool is not None:
-        _expect(v_pool, "v_pool", torch.bfloat16, shape[:3] + v_pool.shape[3:], dev, False)
+        width_v = v_pool.shape[3]
+        v_at = _expect(v_pool, "v_pool", _BF16, (*shape[:3], width_v), index, False)
         if v_pool.stride() != st:
             raise ValueError("K and V pools must share strides, and their rows be contiguous")
     if slots != page_size:
         raise ValueError(f"the pools hold {slots} slots per page, page_size is {page_size}")
-    if seq_lens.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("seq_lens is 1-D and block_table 2-D")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D")
     B, width = block_table.shape
-    _expect(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    _expect(block_table, "block_table", torch.int32, (B, width), dev, False)
-    bts = block_table.stride()
-    if bts[1] != 1 or (B > 1 and bts[0] < width):
+    sl_at = _expect(seq_lens, "seq_lens", _I32, (B,), index)
+    bt_stride, one = block_table.stride()
+    if B == 1:
+        bt_stride = width
+    if (block_table.dtype is not _I32 or block_table.get_device() != index or one != 1
+            or bt_stride < width):
+        _expect(block_table, "block_table", _I32, (B, width), index)
         raise ValueError("block_table rows must be contiguous and distinct")
-    err = None
+    err = 0
     if err_flags is not None:
-        if err_flags.dtype not in (torch.int32, torch.uint32) or err_flags.numel() < 1:
+        if err_flags.dtype is not _I32 and err_flags.dtype is not _U32 or err_flags.numel() < 1:
             raise ValueError("err_flags must be a 32-bit integer tensor")
-        if err_flags.device != dev:
-            raise ValueError(f"err_flags is on {err_flags.device}, the pools on {dev}")
+        if err_flags.get_device() != index:
+            raise ValueError(f"err_flags is on {err_flags.device}, the K pool on device {index}")
         err = err_flags.data_ptr()
-    return dev, B, Hkv, st[0], ts, hs, bts[0] if B > 1 else width, err
+    return (index, B, Hkv, shape, width_v, ps, ts, hs, k_pool.data_ptr(), v_at,
+            block_table.data_ptr(), bt_stride, sl_at, err)
 
 
-def _token_rows(t, name, B, Hkv, device):
+def _token_rows(t, name, B, Hkv, index):
     """fp32 [B, Hkv, tokens] with contiguous token rows; returns (address,
     sequence stride, head stride, tokens)."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [B, Hkv, tokens]")
     n = t.shape[2]
-    at = _expect(t, name, torch.float32, (B, Hkv, n), device, False)
-    st = t.stride()
-    if n < 1 or (n > 1 and st[2] != 1):
+    at = _expect(t, name, _F32, (B, Hkv, n), index, False)
+    seq, head, one = t.stride()
+    if n < 1 or (n > 1 and one != 1):
         raise ValueError(f"{name} needs contiguous rows of at least one token")
-    return at, st[0], st[1], n
+    return at, seq, head, n
 
 
-def _on(device, stream):
+def _on(index, stream):
     """The raw stream a call goes to (the device's current one by default), and
     the context its scratch is allocated in: memory from torch's allocator is
     reused in the order of that stream."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
-    if device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"the pools are on {device}, which is not the current device")
-    cur = torch._C._cuda_getCurrentRawStream(device.index)
+    if index < 0:
+        raise ValueError("the tensors are not on a CUDA device")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the pools are on CUDA device {index}, which is not the current one")
+    cur = torch._C._cuda_getCurrentRawStream(index)
     if stream is None or stream.cuda_stream == cur:
         return cur, _NO_CONTEXT
     return stream.cuda_stream, torch.cuda.stream(stream)
@@ -514,28 +527,28 @@ def _raw_fn(name, nargs):
 def make_score_params(q, Hkv, *, softcap=0.0, alibi_slopes=None, window=0, tree_mask=None,
                       weights=None, weights_decay=1.0) -> ScoreParams:
     """The score modifications of a decode_attn call (see there), for call_ex."""
-    m = ScoreParams.from_buffer_copy(_pack_scores(q.shape, Hkv, q.device, softcap, alibi_slopes,
-                                                  window, tree_mask, weights, weights_decay))
+    m = ScoreParams.from_buffer_copy(_pack_scores(
+        *q.shape[:3], Hkv, q.get_device(), softcap, alibi_slopes, window, tree_mask, weights,
+        weights_decay)[0])
     m.tensors = (alibi_slopes, tree_mask, weights)
     return m
 
 
-def _pack_scores(q_shape, Hkv, dev, softcap, alibi_slopes, window, tree_mask, weights,
-                 weights_decay) -> bytes:
-    B, q_len, Hq, _ = q_shape
-    slopes = mask = w = None
-    ws = wh = wt = 0
+def _pack_scores(B, q_len, Hq, Hkv, index, softcap, alibi_slopes, window, tree_mask, weights,
+                 weights_decay):
+    """zl_score_params as bytes, and the length of the weights rows (0: none)."""
+    slopes = mask = w = ws = wh = wt = 0
     if alibi_slopes is not None:
-        slopes = _expect(alibi_slopes, "alibi_slopes", torch.float32, (Hq,), dev)
+        slopes = _expect(alibi_slopes, "alibi_slopes", _F32, (Hq,), index)
     if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int32, torch.uint32):
+        if tree_mask.dtype is not _I32 and tree_mask.dtype is not _U32:
             raise ValueError("tree_mask must be 32-bit words")
         mask = _expect(tree_mask, "tree_mask", tree_mask.dtype, (B, q_len, (q_len + 31) // 32),
-                       dev)
+                       index)
     if weights is not None:
-        w, ws, wh, wt = _token_rows(weights, "weights", B, Hkv, dev)
-    return _pack(_SCORES, _SCORES.size, softcap, window, slopes or 0, mask or 0, w or 0, ws, wh, wt,
-                        weights_decay)
+        w, ws, wh, wt = _token_rows(weights, "weights", B, Hkv, index)
+    return _pack(_SCORES, _SCORES.size, softcap, window, slopes, mask, w, ws, wh, wt,
+                 weights_decay), wt
 
 
 def _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size, scale, out, lse, workspace,
@@ -544,55 +557,59 @@ def _run_ex(q, k_pool, v_pool, block_table, seq_lens, page_size, scale, out, lse
     """decode_attn with modified scores (zl_decode_attn_ex)."""
     if q.dim() != 4 or v_pool is None:
         raise ValueError("q must be [B, q_len, Hq, D], with K and V pools")
-    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
-        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    (index, B, Hkv, pool_shape, width_v, ps, ts, hs, k_at, v_at, bt_at, bt_stride, sl_at,
+     err) = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
     shape = q.shape
     _, q_len, Hq, D = shape
-    if v_pool.shape[3] != D:
+    if width_v != D:
         raise ValueError("q and the pools' rows must be equally wide")
-    q_at = _expect(q, "q", torch.bfloat16, (B, q_len, Hq, k_pool.shape[3]), dev)
-    lse_at = kn = vn = None
-    if lse is not None:
-        lse_at = _expect(lse, "lse", torch.float32, (B, q_len, Hq), dev)
-    if k_new is not None:
-        kn = _expect(k_new, "k_new", torch.bfloat16, (B, q_len, Hkv, D), dev)
-    if v_new is not None:
-        vn = _expect(v_new, "v_new", torch.bfloat16, (B, q_len, Hkv, D), dev)
+    q_at = _expect(q, "q", _BF16, (B, q_len, Hq, pool_shape[3]), index)
+    out_at = lse_at = kn = vn = begin = end = 0
     if out is not None:
-        _expect(out, "out", torch.bfloat16, shape, dev)
-    mods = _pack_scores(shape, Hkv, dev, softcap, alibi_slopes, window, tree_mask, weights,
-                        weights_decay)
-    on, scratch = _on(dev, stream)
-    begin, end = (events[0].cuda_event, events[1].cuda_event) if events is not None else (0, 0)
+        out_at = _expect(out, "out", _BF16, shape, index)
+    if lse is not None:
+        lse_at = _expect(lse, "lse", _F32, (B, q_len, Hq), index)
+    if k_new is not None:
+        kn = _expect(k_new, "k_new", _BF16, (B, q_len, Hkv, D), index)
+    if v_new is not None:
+        vn = _expect(v_new, "v_new", _BF16, (B, q_len, Hkv, D), index)
+    mods, tokens = _pack_scores(B, q_len, Hq, Hkv, index, softcap, alibi_slopes, window,
+                                tree_mask, weights, weights_decay)
+    if events is not None:
+        begin, end = events[0].cuda_event or 0, events[1].cuda_event or 0
+    on, scratch = _on(index, stream)
 
-    def pack(ws_at, ws_bytes):
+    def params(out_at, ws_at, ws_bytes):
         return _pack(
-            _PARAMS, _PARAMS.size, q_at, k_pool.data_ptr(), v_pool.data_ptr(), ps, ts, hs,
-            block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), out_at, lse_at or 0, B, q_len,
-            Hq, Hkv, D, D, page_size, k_pool.shape[0], max_seq_len, scale, ws_at, ws_bytes,
-            err or 0, num_ctas, begin or 0, end or 0, 0, 0, kn or 0, vn or 0)
+            _PARAMS, _PARAMS.size, q_at, k_at, v_at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at,
+            lse_at, B, q_len, Hq, Hkv, D, D, page_size, pool_shape[0], max_seq_len, scale, ws_at,
+            ws_bytes, err, num_ctas, begin, end, 0, 0, kn, vn)
 
     with scratch:
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        out_at = out.data_ptr()
+            out = torch.empty(shape, dtype=_BF16, device=q.device)
+            out_at = out.data_ptr()
         if workspace is None:
             # a call's own: stream order alone separates it from other calls,
             # and a captured graph keeps it. Its size follows from the shapes.
-            key = (dev.index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len,
-                   window, 0 if weights is None else weights.shape[2])
-            need = _sizes.get(key)
-            if need is None:
+            key = (index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len, window,
+                   tokens)
+            ws_bytes = _sizes.get(key)
+            if ws_bytes is None:
                 n = ctypes.c_size_t(0)
-                _check(_raw_fn("zl_decode_attn_ex_workspace_size", 2)(pack(0, 0), mods,
-                                                                      ctypes.addressof(n)),
-                       "zl_decode_attn_ex_workspace_size")
+                _check(_raw_fn("zl_decode_attn_ex_workspace_size", 2)(
+                    params(out_at, 0, 0), mods, ctypes.addressof(n)),
+                    "zl_decode_attn_ex_workspace_size")
                 if len(_sizes) >= 4096:
                     _sizes.clear()
-                need = _sizes[key] = n.value or 256
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        params = pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        _check(_raw_fn("zl_decode_attn_ex", 2)(params, mods, on), "zl_decode_attn_ex")
+                ws_bytes = _sizes[key] = n.value or 256
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        status = _raw_fn("zl_decode_attn_ex", 2)(
+            params(out_at, workspace.data_ptr(), ws_bytes), mods, on)
+        if status != OK:
+            _check(status, "zl_decode_attn_ex")
     return out
 
 
@@ -761,40 +778,44 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
     """
     if weights is None:
         raise ValueError("weights is required")
-    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
-        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
-    w, w_seq, w_head, tokens = _token_rows(weights, "weights", B, Hkv, dev)
+    (index, B, Hkv, shape, width_v, ps, ts, hs, k_at, v_at, bt_at, bt_stride, sl_at,
+     err) = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    w, w_seq, w_head, tokens = _token_rows(weights, "weights", B, Hkv, index)
     wo = wo_seq = wo_head = dst = dst_stride = 0
     if weights_out is not None:
-        wo, wo_seq, wo_head, out_tokens = _token_rows(weights_out, "weights_out", B, Hkv, dev)
+        wo, wo_seq, wo_head, out_tokens = _token_rows(weights_out, "weights_out", B, Hkv, index)
         if out_tokens < min(budget, tokens):
             raise ValueError("weights_out is shorter than what the budget may leave")
     if dst_block_table is not None:
         if dst_block_table.dim() != 2:
             raise ValueError("dst_block_table must be 2-D")
         width = dst_block_table.shape[1]
-        dst = _expect(dst_block_table, "dst_block_table", torch.int32, (B, width), dev, False)
-        st = dst_block_table.stride()
-        if st[1] != 1 or (B > 1 and st[0] < width):
+        dst = _expect(dst_block_table, "dst_block_table", _I32, (B, width), index, False)
+        dst_stride, one = dst_block_table.stride()
+        if B == 1:
+            dst_stride = width
+        if one != 1 or dst_stride < width:
             raise ValueError("dst_block_table rows must be contiguous and distinct")
-        dst_stride = st[0] if B > 1 else width
+    new_at = kept_at = 0
     if new_lens is not None:
-        _expect(new_lens, "new_lens", torch.int32, (B,), dev)
+        new_at = _expect(new_lens, "new_lens", _I32, (B,), index)
     if kept is not None:
-        _expect(kept, "kept", torch.int32, (B, Hkv, budget), dev)
-    on, scratch = _on(dev, stream)
-    with scratch:
-        if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        if kept is None:
-            kept = torch.empty(B, Hkv, max(budget, 1), dtype=torch.int32, device=dev)
-    params = _pack(
-        _EVICT, _EVICT.size, k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), ps, ts, hs,
-        block_table.data_ptr(), bt_stride, dst, dst_stride, seq_lens.data_ptr(),
-        new_lens.data_ptr(), kept.data_ptr(), w, w_seq, w_head, wo, wo_seq, wo_head, tokens, B,
-        Hkv, k_pool.shape[3], 0 if v_pool is None else v_pool.shape[3], page_size,
-        k_pool.shape[0], budget, sink, recent, err or 0)
-    _check(_raw_fn("zl_kv_evict", 1)(params, on), "zl_kv_evict")
+        kept_at = _expect(kept, "kept", _I32, (B, Hkv, budget), index)
+    on, scratch = _on(index, stream)
+    if new_lens is None or kept is None:
+        with scratch:
+            if new_lens is None:
+                new_lens = torch.empty(B, dtype=_I32, device=k_pool.device)
+                new_at = new_lens.data_ptr()
+            if kept is None:
+                kept = torch.empty(B, Hkv, max(budget, 1), dtype=_I32, device=k_pool.device)
+                kept_at = kept.data_ptr()
+    status = _raw_fn("zl_kv_evict", 1)(_pack(
+        _EVICT, _EVICT.size, k_at, v_at, ps, ts, hs, bt_at, bt_stride, dst, dst_stride, sl_at,
+        new_at, kept_at, w, w_seq, w_head, wo, wo_seq, wo_head, tokens, B, Hkv, shape[3], width_v,
+        page_size, shape[0], budget, sink, recent, err), on)
+    if status != OK:
+        _check(status, "zl_kv_evict")
     return new_lens, kept
 
 
@@ -807,26 +828,28 @@ def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_siz
     become the tokens after the context, in place. v_pool None: a latent-only
     pool. Returns new_lens int32 [B] (context plus accepted).
     """
-    dev, B, Hkv, ps, ts, hs, bt_stride, err = _expect_cache(
-        k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
+    (index, B, Hkv, shape, width_v, ps, ts, hs, k_at, v_at, bt_at, bt_stride, sl_at,
+     err) = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
     if path.dim() != 2:
         raise ValueError("path must be 2-D")
     n = path.shape[1]
-    path_at = _expect(path, "path", torch.int32, (B, n), dev, False)
-    st = path.stride()
-    if n > 1 and st[1] != 1:
+    path_at = _expect(path, "path", _I32, (B, n), index, False)
+    path_stride, one = path.stride()
+    if n > 1 and one != 1:
         raise ValueError("path rows must be contiguous")
-    acc = _expect(accepted, "accepted", torch.int32, (B,), dev)
+    acc = _expect(accepted, "accepted", _I32, (B,), index)
+    new_at = 0
     if new_lens is not None:
-        _expect(new_lens, "new_lens", torch.int32, (B,), dev)
-    on, scratch = _on(dev, stream)
-    with scratch:
-        if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    params = _pack(
-        _COMMIT, _COMMIT.size, k_pool.data_ptr(), 0 if v_pool is None else v_pool.data_ptr(), ps, ts, hs,
-        block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), path_at, st[0] if B > 1 else n,
-        acc, new_lens.data_ptr(), n, B, q_len, Hkv, k_pool.shape[3],
-        0 if v_pool is None else v_pool.shape[3], page_size, k_pool.shape[0], err or 0)
-    _check(_raw_fn("zl_kv_commit", 1)(params, on), "zl_kv_commit")
+        new_at = _expect(new_lens, "new_lens", _I32, (B,), index)
+    on, scratch = _on(index, stream)
+    if new_lens is None:
+        with scratch:
+            new_lens = torch.empty(B, dtype=_I32, device=k_pool.device)
+            new_at = new_lens.data_ptr()
+    status = _raw_fn("zl_kv_commit", 1)(_pack(
+        _COMMIT, _COMMIT.size, k_at, v_at, ps, ts, hs, bt_at, bt_stride, sl_at, path_at,
+        path_stride if B > 1 else n, acc, new_at, n, B, q_len, Hkv, shape[3], width_v, page_size,
+        shape[0], err), on)
+    if status != OK:
+        _check(status, "zl_kv_commit")
     return new_lens
