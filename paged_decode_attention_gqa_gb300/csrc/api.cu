@@ -183,9 +183,14 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
     if (a->num_ctas == 0 && a->max_seq_len > 0) {
       int64_t len = a->max_seq_len;
       if (mods->window > 0) len = std::min(len, int64_t(mods->window) + a->q_len + zl::kWideTile);
-      const int64_t tiles = int64_t(a->B) * a->Hkv * plan->nblk *
-                            ((len + zl::kWideTile - 1) / zl::kWideTile);
-      plan->grid = int(std::min(int64_t(plan->grid), std::max<int64_t>(tiles, 1)));
+      const int64_t units = int64_t(a->B) * a->Hkv * plan->nblk;
+      const int64_t tiles = (len + zl::kWideTile - 1) / zl::kWideTile;
+      if (units <= plan->grid && tiles <= zl::kWideWholeTiles) {
+        plan->unit_cut = true;  // one CTA per unit, no merge
+        plan->grid = int(units);
+      } else {
+        plan->grid = int(std::min(int64_t(plan->grid), std::max<int64_t>(units * tiles, 1)));
+      }
     }
     const size_t rows = size_t(plan->grid) * 2 * plan->mt * 128;
     plan->off_lse = round_up(size_t(plan->grid) * sizeof(int4), 256);
@@ -475,6 +480,10 @@ zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.tg = plan.tg;
   p.group_ctas = plan.unit_cut || plan.tg == 2 ? plan.grid : std::max(1, plan.grid / plan.ngroups);
   const int grid = plan.tg == 2 ? plan.grid : p.group_ctas * plan.ngroups;
+  DeviceInfo dev;
+  const zl_status st = current_device(&dev);
+  if (st != ZL_OK) return st;
+  p.split_merge = int64_t(plan.ngroups) * a->B * a->Hkv * plan.gh * plan.q_group <= 8 * dev.sms;
   cudaError_t e = zl::gqa_mod_launch(p, grid, s, reinterpret_cast<cudaEvent_t>(a->attn_begin),
                                      reinterpret_cast<cudaEvent_t>(a->attn_end));
   if (e == cudaSuccess && m.weights) {
@@ -533,6 +542,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.tpt = plan.tpt;
   p.mt = plan.mt;
   p.nblk = plan.nblk;
+  p.whole_units = plan.unit_cut ? 2 : a->num_ctas == 0 ? 1 : 0;
   p.len_cap = a->block_table_stride * int64_t(a->page_size);
   p.scale_log2 = float(double(a->scale) * kLog2e);
   set_cap(a->scale, m.softcap, &p);
@@ -565,7 +575,7 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
     // sequences are no error for it)
     if ((st = zl_kv_append(&ap, reinterpret_cast<zl_stream_t>(s))) != ZL_OK) return st;
   }
-  const cudaError_t e = zl::gqa_wide_launch(p, plan.grid, s,
+  const cudaError_t e = zl::gqa_wide_launch(p, plan.grid, plan.unit_cut, s,
                                             reinterpret_cast<cudaEvent_t>(a->attn_begin),
                                             reinterpret_cast<cudaEvent_t>(a->attn_end));
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;

@@ -140,6 +140,17 @@ struct TileCut {
   }
 };
 
+// CTAs that share W tiles of `units` units when `ctas` are there (modified
+// scores). A unit cut into many pieces is slow to merge: about 0.09 us a piece
+// for the warp that merges a row, read eight at a time, against 0.5 us a tile,
+// so W / G * 0.5 + G / units * 0.09 is least at G = sqrt(5.6 W units). With
+// eight warps to a row (few rows; split_merge) a piece costs an eighth. One
+// sequence of 7493 tokens with one kv head took 76 us cut into 469 pieces.
+__device__ __forceinline__ int cut_ctas(const GqaParams& p, int64_t W, int64_t units, int ctas) {
+  const float best = sqrtf((p.split_merge ? 45.f : 5.6f) * float(W) * float(units));
+  return best < float(ctas) ? max(int(best), 1) : ctas;
+}
+
 // Whether every unit of the launch is short enough for a CTA of its own (the
 // unit cut): at most kGqaUnitCutTiles tiles in the longest unit (n_max), and
 // no more units than the group's CTAs.
@@ -255,9 +266,10 @@ template <int NR, int P>
 __device__ __forceinline__ void merge_add_pieces(MergeAcc<NR>& m, const GqaParams& p,
                                                  const TileCut& cut, int cta0, int64_t U0,
                                                  int c_lo, int c_hi, int w, int R, int row_off,
-                                                 int r0, int nrows, int lane) {
+                                                 int r0, int nrows, int lane, int c_from = -1) {
+  // (c_from: the first piece to add, if that is not the unit's first)
   const int sl_lo = U0 > cut.start(c_lo) ? 1 : 0;
-  for (int cb = c_lo; cb <= c_hi; cb += P) {
+  for (int cb = c_from < 0 ? c_lo : c_from; cb <= c_hi; cb += P) {
     float lv[P][NR];
     float4 ov[P][NR];
 #pragma unroll
@@ -644,7 +656,8 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
   const int tok0 = rg.tok0, qlen = rg.qlen, gh = rg.gh;
   const int nhg = p.nhg;
   const int64_t W = int64_t(nhg) * prefix[V];
-  const TileCut cut(W, G);
+  // (modified scores only: the other calls keep their cut, and so their bits)
+  const TileCut cut(W, MODE == kModeMod ? cut_ctas(p, W, int64_t(V) * nhg, G) : G);
   // CTAs past the cut's G (more CTAs than tiles) take no tiles.
   int64_t s_c = c < int(cut.G) ? cut.start(c) : W;
   int64_t e_c = c < int(cut.G) ? cut.start(c + 1) : W;
@@ -1220,7 +1233,7 @@ __global__ void __launch_bounds__(128) gqa_merge_kernel(const __grid_constant__ 
   const int head0 = kvh * p.g + rg.hoff;  // the group's first query head
   const int PT = MODE == kModeShared ? p.prefix_tiles : 0;
   const int64_t W = int64_t(p.nhg) * (int64_t(NG) * PT + all);
-  const TileCut cut(W, G);
+  const TileCut cut(W, MODE == kModeMod ? cut_ctas(p, W, int64_t(p.B) * p.nhg, G) : G);
   const int64_t U0 = int64_t(p.nhg) * (int64_t(NG) * PT + before) + int64_t(hg) * n;
   const int c_lo = n ? cut.owner(U0) : 0, c_hi = n ? cut.owner(U0 + n - 1) : 0;
   if constexpr (MODE != kModeShared) {

@@ -17,6 +17,68 @@ namespace zl {
 
 namespace {
 
+// The merge of a modified-score call with few rows: a block per row, its
+// kSplitWarps warps taking the unit's pieces in equal runs; the runs' results
+// are then merged like pieces, in order. With a warp per row, 64 KB per SM of
+// partials wait on one chain of reads (8 sequences cut into 19 pieces each: 8
+// us; one sequence of 60000 tokens: 16).
+constexpr int kSplitWarps = 8;
+
+__global__ void __launch_bounds__(kSplitWarps * 32)
+gqa_merge_split_kernel(const __grid_constant__ GqaParams p, int G) {
+  __shared__ float s_lse[kSplitWarps];
+  __shared__ float4 s_o[kSplitWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rmax = p.gh * p.q_len;
+  const int64_t per_group = int64_t(p.B) * p.Hkv * rmax, item = blockIdx.x;
+  const int tg = int(item / per_group);
+  const int64_t gitem = item - tg * per_group;
+  const int unit = int(gitem / rmax), r0 = int(gitem % rmax);
+  const int b = unit / p.Hkv, kvh = unit % p.Hkv;
+  const RowGroup rg = row_group(p, tg);
+  int before = 0, all = 0, nmax = 0;
+  for (int s = lane; s < p.B; s += 32) {
+    const int t = seq_unit_tiles<kModeMod>(p, p.seq_lens[s]);
+    all += t;
+    before += s < b ? t : 0;
+    nmax = max(nmax, t);
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  nmax = __reduce_max_sync(0xffffffffu, nmax);
+  const int n = seq_unit_tiles<kModeMod>(p, p.seq_lens[b]);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (r0 >= rg.gh * rg.qlen || n == 0) return;
+  if (p.auto_cut && short_units(int64_t(p.B) * p.nhg, nmax, G)) return;
+  const int hg = kvh / p.hpc, w = kvh % p.hpc;
+  const int64_t W = int64_t(p.nhg) * all;
+  const TileCut cut(W, cut_ctas(p, W, int64_t(p.B) * p.nhg, G));
+  const int64_t U0 = int64_t(p.nhg) * before + int64_t(hg) * n;
+  const int c_lo = cut.owner(U0), c_hi = cut.owner(U0 + n - 1);
+  if (c_lo == c_hi) return;
+  const int per = (c_hi - c_lo + kSplitWarps) / kSplitWarps;  // pieces of a warp
+  const int from = c_lo + warp * per, to = min(c_hi, from + per - 1);
+  MergeAcc<1> m;
+  m.init();
+  if (from <= to)
+    merge_add_pieces<1, 8>(m, p, cut, tg * G, U0, c_lo, to, w, rmax, 0, r0, 1, lane, from);
+  {
+    const bool some = m.den[0] > 0.f;
+    const float inv = some ? __frcp_rn(m.den[0]) : 0.f;
+    s_o[warp][lane] = make_float4(m.acc[0].x * inv, m.acc[0].y * inv, m.acc[0].z * inv,
+                                  m.acc[0].w * inv);
+    if (lane == 0)
+      s_lse[warp] = m.bad ? CUDART_NAN_F : some ? m.mx[0] + log2f(m.den[0]) : -CUDART_INF_F;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  m.init();
+#pragma unroll
+  for (int k = 0; k < kSplitWarps; ++k) m.add(0, s_lse[k], s_o[k][lane]);
+  merge_write_out<kModeMod>(m, p, b, rg.tok0, kvh * p.g + rg.hoff, rg.gh, r0, 1, lane);
+}
+
 template <int HPC, bool R16, int TG>
 struct ModInstance {
   static cudaError_t launch(const GqaParams& p, int grid, cudaStream_t stream) {
@@ -62,7 +124,17 @@ cudaError_t gqa_mod_launch(const GqaParams& p, int grid, cudaStream_t stream,
   if (e != cudaSuccess) return e;
   if (attn_end && (e = cudaEventRecord(attn_end, stream)) != cudaSuccess) return e;
   if (p.unit_cut) return cudaSuccess;  // nothing to merge
-  return launch_merge<kModeMod>(p, stream);
+  if (!p.split_merge) return launch_merge<kModeMod>(p, stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(int64_t(p.ngroups) * p.B * p.Hkv * p.gh * p.q_len));
+  cfg.blockDim = dim3(kSplitWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gqa_merge_split_kernel, p, p.group_ctas);
 }
 
 }  // namespace zl

@@ -263,14 +263,18 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       const int x = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += x;
     }
-    int run = incl - local;
+    int run = incl - local, longest = 0;
     for (int i = 0; i < per; ++i) {
       if (b0 + i < B) {
+        const int n = unit_places(p, p.seq_lens[b0 + i]);
         prefix[b0 + i] = run;
-        run += unit_places(p, p.seq_lens[b0 + i]);
+        run += n;
+        longest = max(longest, n);
       }
     }
     if (lane == 31) prefix[B] = incl;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) info[0] = uint32_t(longest);
   }
   tc_fence_before();
   __syncthreads();
@@ -279,15 +283,33 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   const uint32_t tmem = *tmem_slot;
   const int c = blockIdx.x;
   const int64_t W = int64_t(p.Hkv) * p.nblk * prefix[B];
-  const TileCut cut(W, gridDim.x);
-  const int s_c = c < int(cut.G) && W > 0 ? int(cut.start(c)) : 0;
-  const int e_c = c < int(cut.G) && W > 0 ? int(cut.start(c + 1)) : 0;
+  // A piece more costs the merge about 0.4 us (two read at a time), a place 1.8
+  // us: places / G * 1.8 + G / units * 0.4 is least at G = sqrt(4.5 W units).
+  const int64_t units = int64_t(B) * p.Hkv * p.nblk;
+  const float best = sqrtf(4.5f * float(W) * float(units));
+  const TileCut cut(W, best < float(gridDim.x) ? max(int(best), 1) : int(gridDim.x));
+  int s_c = c < int(cut.G) && W > 0 ? int(cut.start(c)) : 0;
+  int e_c = c < int(cut.G) && W > 0 ? int(cut.start(c + 1)) : 0;
+  // Few short units: one CTA each, nothing cut (a cut costs the partials' way
+  // through memory and the merge's part of the call).
+  const bool whole = p.whole_units == 2 ||
+                     (p.whole_units == 1 && units <= gridDim.x &&
+                      int(info[0]) <= kWideWholeTiles + kWideUnitCost);
+  __syncthreads();  // info[0] is read: the K warp may use it
+  if (whole) {
+    s_c = e_c = 0;
+    if (c < units) {
+      const int U = p.Hkv * p.nblk, b = c / U, len = prefix[b + 1] - prefix[b];
+      s_c = U * prefix[b] + (c - b * U) * len;
+      e_c = s_c + len;
+    }
+  }
   if (tid == 0 && c > 0) {
     // For the merge: whether this CTA's first place is the first boundary
     // between the tiles of a unit, and if so of which one (sequence, unit),
     // the last CTA with a part of it and the slot of the first one's (c - 1).
     int4 cut_unit = make_int4(0, 0, -1, 0);
-    if (e_c > s_c) {
+    if (e_c > s_c && !whole) {
       const int U = p.Hkv * p.nblk, b = locate_seq(prefix, B, U, s_c);
       const int first = prefix[b], len = prefix[b + 1] - first, u = (s_c - U * first) / len;
       const int unit0 = U * first + u * len, before = int(cut.start(c - 1));
@@ -1001,20 +1023,28 @@ __global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ Wi
   if (!any) return;
   MergeAcc<kMergeRows> acc;
   acc.init();
-  for (int cc = c - 1; cc <= u.z; ++cc) {
-    const int64_t wrow = (int64_t(cc) * 2 + (cc == c - 1 ? u.w : 0)) * (MT * 128) + row0;
-    float l[kMergeRows];
-    float4 o[kMergeRows];
+  constexpr int kBatch = 2;  // parts whose loads are in flight together (most units have two)
+  for (int c0 = c - 1; c0 <= u.z; c0 += kBatch) {
+    float l[kBatch][kMergeRows];
+    float4 o[kBatch][kMergeRows];
 #pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-      if (live[k]) {
-        l[k] = __ldcg(p.ws_lse + wrow + k);
-        o[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (wrow + k) * kGqaHeadDim) + lane);
+    for (int q = 0; q < kBatch; ++q) {
+      const int cc = c0 + q;
+      const int64_t wrow = (int64_t(cc) * 2 + (cc == c - 1 ? u.w : 0)) * (MT * 128) + row0;
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k) {
+        if (cc <= u.z && live[k]) {
+          l[q][k] = __ldcg(p.ws_lse + wrow + k);
+          o[q][k] =
+              __ldcg(reinterpret_cast<const float4*>(p.ws_o + (wrow + k) * kGqaHeadDim) + lane);
+        }
       }
     }
 #pragma unroll
-    for (int k = 0; k < kMergeRows; ++k)
-      if (live[k]) acc.add(k, l[k], o[k]);
+    for (int q = 0; q < kBatch; ++q)
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k)
+        if (c0 + q <= u.z && live[k]) acc.add(k, l[q][k], o[q][k]);
   }
 #pragma unroll
   for (int k = 0; k < kMergeRows; ++k) {
@@ -1033,8 +1063,8 @@ __global__ void __launch_bounds__(256) gqa_wide_merge(const __grid_constant__ Wi
 }
 
 template <int MT, bool CAP>
-cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent_t attn_begin,
-                   cudaEvent_t attn_end) {
+cudaError_t launch(const WideParams& p, int grid, bool no_merge, cudaStream_t stream,
+                   cudaEvent_t attn_begin, cudaEvent_t attn_end) {
   static bool done[kMaxDevices] = {};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -1059,7 +1089,7 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
   cfg.dynamicSmemBytes = WideCfg<MT>::smem_bytes(p.B);
   if ((e = cudaLaunchKernelEx(&cfg, gqa_wide_kernel<MT, CAP>, p)) != cudaSuccess) return e;
   if (attn_end && (e = cudaEventRecord(attn_end, stream)) != cudaSuccess) return e;
-  if (grid < 2) return cudaSuccess;  // nothing is cut
+  if (grid < 2 || no_merge) return cudaSuccess;  // nothing is cut
   cfg.gridDim = dim3(unsigned(grid - 1), unsigned(MT * 128 / 32));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
@@ -1068,14 +1098,14 @@ cudaError_t launch(const WideParams& p, int grid, cudaStream_t stream, cudaEvent
 
 }  // namespace
 
-cudaError_t gqa_wide_launch(const WideParams& p, int grid, cudaStream_t stream,
+cudaError_t gqa_wide_launch(const WideParams& p, int grid, bool no_merge, cudaStream_t stream,
                             cudaEvent_t attn_begin, cudaEvent_t attn_end) {
   const bool cap = p.cap_in > 0.f;
   if (p.mt == 2)
-    return cap ? launch<2, true>(p, grid, stream, attn_begin, attn_end)
-               : launch<2, false>(p, grid, stream, attn_begin, attn_end);
-  return cap ? launch<1, true>(p, grid, stream, attn_begin, attn_end)
-             : launch<1, false>(p, grid, stream, attn_begin, attn_end);
+    return cap ? launch<2, true>(p, grid, no_merge, stream, attn_begin, attn_end)
+               : launch<2, false>(p, grid, no_merge, stream, attn_begin, attn_end);
+  return cap ? launch<1, true>(p, grid, no_merge, stream, attn_begin, attn_end)
+             : launch<1, false>(p, grid, no_merge, stream, attn_begin, attn_end);
 }
 
 }  // namespace zl

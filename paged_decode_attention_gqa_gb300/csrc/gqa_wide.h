@@ -10,6 +10,8 @@ constexpr int kWideTile = 128;  // tokens per tile
 // (64 sequences of 512-4096 tokens, 64 drafted tokens: 196, 177, 172, 172, 178 us
 // at 0, 1, 2, 3 and 5; 16 drafted tokens: 137, 128, 129, 130, 132 us.)
 constexpr int kWideUnitCost = 2;
+// Units of at most this many tiles, no more of them than CTAs, are not cut.
+constexpr int kWideWholeTiles = 4;
 
 // tanh(y) / y for z = y^2 in [0, 1/4]: the cubic in z that interpolates it at
 // the 4 Chebyshev nodes of the interval, within 5.5e-7 (6.3e-7
@@ -34,6 +36,9 @@ struct WideParams {
   int tpt;   // query tokens per row tile: 128 / g
   int mt;    // row tiles per row block: 1 (the call has only one) or 2
   int nblk;  // row blocks per kv head
+  // 2: a CTA per unit (the host knows a length bound and launches no merge); 1:
+  // the default grid, the kernel decides by kWideWholeTiles; 0: units are cut
+  int whole_units;
   int64_t len_cap;
   float scale_log2, cap_in, cap_out;  // as in GqaParams
   // The capped score in base 2 as x (cap_f[0] + cap_f[1] z + ..), z = x^2, of the
@@ -45,8 +50,9 @@ struct WideParams {
   int tree_words;
 };
 
-// The attention kernel on `grid` CTAs, then the merge of the units it cut.
-cudaError_t gqa_wide_launch(const WideParams& p, int grid, cudaStream_t stream,
+// The attention kernel on `grid` CTAs, then the merge of the units it cut
+// (no_merge: the caller knows that there are none).
+cudaError_t gqa_wide_launch(const WideParams& p, int grid, bool no_merge, cudaStream_t stream,
                             cudaEvent_t attn_begin, cudaEvent_t attn_end);
 
 }  // namespace zl

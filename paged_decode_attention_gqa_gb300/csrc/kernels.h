@@ -100,6 +100,7 @@ struct GqaParams {
   int window;              // tokens a query sees back from its position, 0 = all
   const uint32_t* tree;    // ancestor bits [B, q_total, tree_words], or nullptr (a chain)
   int tree_words;
+  int split_merge;         // 1: the merge takes eight warps to a row (few rows)
   int64_t len_cap;         // longest valid length (the block table's or the weights' reach)
   // Accumulated weights (scores = nullptr: none): each (query row, token)'s
   // base-2 score [B, q_total, Hq][score_stride], -inf where it is not visible,
