@@ -94,6 +94,18 @@ def test_evict_long(B, Hkv, L, budget):
     run_evict(w, weights_for(w, L, 2), budget=budget, sink=4, recent=budget // 3)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal"])
+def test_evict_rows_beyond_the_registers_of_a_cluster(kind):
+    """Rows of more than 131072 weights are read anew for each step of the search."""
+    w = wl.random_case(3125, B=3, Hq=1, Hkv=1, page_size=128, lens=[140000, 131073, 300],
+                       poison=False)
+    wt = weights_for(w, 140003, 9, kind)
+    run_evict(w, wt, budget=4097, sink=4, recent=1000)
+    free = np.setdiff1d(np.arange(w.num_pages), w.block_table[w.block_table >= 0])
+    dst = free[:3 * 33].reshape(3, 33).astype(np.int32)
+    run_evict(w, wt, budget=4097, recent=30, dst=dst)
+
+
 def test_evict_into_new_pages():
     w = wl.random_case(3130, B=4, Hq=8, Hkv=2, lens=[700, 120, 33, 0], pool_factor=3.0)
     free = np.setdiff1d(np.arange(w.num_pages), w.block_table[w.block_table >= 0])

@@ -340,3 +340,80 @@ def test_far_pages_and_large_batch():
     del k, v
     w = wl.random_case(2730, B=600, Hq=4, Hkv=2, max_len=40)
     run(w, softcap=6.0, window=20)
+
+
+# Calls of more than 32 query rows per kv head: another kernel, whose tiles are
+# 128 tokens wide and 128 rows high.
+
+
+@pytest.mark.parametrize("P,layout", [(16, "HND"), (32, "NHD"), (48, "NHD"), (48, "HND"),
+                                      (64, "HND"), (128, "NHD"), (256, "HND")])
+def test_many_rows_pages_and_layouts(P, layout):
+    w = wl.random_case(2800 + P, B=5, Hq=16, Hkv=4, page_size=P, layout=layout, q_len=12,
+                       lens=[12, P - 1, P, P + 1, 3 * P + 5])
+    mask = random_trees(np.random.default_rng(P), 5, 12)
+    run(w, **mods_of("all", 16))
+    run(w, mask=mask, **mods_of("all", 16))
+    run(w, mask=mask, window=P // 2 + 3)
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_len", [(128, 1, 1), (128, 1, 5), (64, 1, 4), (5, 1, 60),
+                                          (24, 2, 7), (7, 7, 90), (33, 1, 9), (100, 1, 3),
+                                          (9, 3, 128)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_many_rows_heads(Hq, Hkv, q_len, tree):
+    w = wl.random_case(2810, B=3, Hq=Hq, Hkv=Hkv, q_len=q_len,
+                       lens=[max(q_len, 1), q_len + 130, 700])
+    mask = random_trees(np.random.default_rng(3), 3, q_len) if tree else None
+    run(w, mask=mask, softcap=4.0, slopes=slopes_of(Hq))
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 31, 63, 64, 65, 90, 127, 128, 129, 190, 255, 256])
+@pytest.mark.parametrize("q_len", [33, 64, 65, 128])
+def test_drafted_tokens_across_tiles(ctx, q_len):
+    """Every place of the first drafted token in its tile: the distance bias and
+    the window go by depth there, not by place."""
+    w = wl.random_case(2820 + ctx, B=2, Hq=2, Hkv=2, q_len=q_len, lens=[ctx + q_len] * 2)
+    mask = random_trees(np.random.default_rng(ctx), 2, q_len)
+    run(w, mask=mask, slopes=torch.tensor([0.3, 0.01]))
+    run(w, mask=mask, slopes=torch.tensor([0.3, 0.01]), window=5, softcap=3.0)
+    # a chain, whose depths are the places
+    chain = zl.tree_mask(np.tile(np.arange(q_len) - 1, (2, 1)))
+    a = run(w, mask=chain, slopes=torch.tensor([0.3, 0.01]), window=70)
+    b = run(w, slopes=torch.tensor([0.3, 0.01]), window=70)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 2, 7, 60, 152])
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(20, 8, 2), (50, 32, 1)])
+def test_many_rows_any_split(ctas, q_len, Hq, Hkv):
+    w = wl.random_case(2830, B=4, Hq=Hq, Hkv=Hkv, lens=[4000, 33, 0, 900], q_len=q_len,
+                       page_size=32, values=True)
+    mask = random_trees(np.random.default_rng(8), 4, q_len)
+    for msl in (0, 4000):
+        run(w, num_ctas=ctas, max_seq_len=msl, mask=mask, **mods_of("alibi", Hq))
+
+
+def test_many_rows_many_sequences():
+    w = wl.random_case(2840, B=700, Hq=4, Hkv=1, max_len=60, q_len=12)
+    run(w, softcap=6.0, window=20)
+    run(w, mask=random_trees(np.random.default_rng(8), 700, 12))
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+@pytest.mark.parametrize("scale,cap", [(1e-3, 50.0), (0.09, 1e-3), (0.09, 1e4), (3.0, 50.0),
+                                       (1e-30, 1.0)])
+def test_caps_far_from_the_scores(q_len, scale, cap):
+    w = wl.random_case(2850, B=2, Hq=4, Hkv=2, lens=[64, 200], q_len=q_len, scale=scale)
+    run(w, softcap=cap)
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_len", [(8, 8, 1), (8, 1, 2), (4, 1, 20)])
+def test_bad_pages_in_calls_of_few_rows(Hq, Hkv, q_len):
+    """One sequence in many pieces, one of which meets a bad page."""
+    w = wl.random_case(2860, B=1, Hq=Hq, Hkv=Hkv, q_len=q_len, lens=[9000], poison=False)
+    for at in (0, 300, 9000 // 16):
+        bt = w.block_table.copy()
+        bt[0, at] = w.num_pages
+        run(w, block_table=bt, softcap=5.0, expect_bad=1)
+        run(w, block_table=bt, window=500, expect_bad=0 if at < 500 else 1)
