@@ -101,7 +101,12 @@ struct GqaPlan {
 };
 
 // Rows per kv head above which a modified-score call runs the tcgen05 kernel.
-constexpr int kWideRows = 32;
+// Both sides measured, drafted trees over 64 sequences of 512-4096 tokens, 32
+// heads on 8: 16 rows 120 us by either kernel; 20 rows 122 us here, 166 there;
+// 36 rows 123 and 230. With 4 sequences of 100-500 tokens and 32 rows 15.3 and
+// 21.3. (One sequence of 8000 tokens, 20 to 32 rows: 28 and 23, the side that
+// loses.)
+constexpr int kWideRows = 16;
 
 // Query tokens per sequence one call takes, and query heads per kv head (the
 // GQA path takes the (token, head) rows of a kv head in groups of at most 16).

@@ -342,7 +342,7 @@ def test_far_pages_and_large_batch():
     run(w, softcap=6.0, window=20)
 
 
-# Calls of more than 32 query rows per kv head: another kernel, whose tiles are
+# Calls of many query rows per kv head: another kernel, whose tiles are
 # 128 tokens wide and 128 rows high.
 
 
