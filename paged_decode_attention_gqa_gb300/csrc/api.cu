@@ -440,6 +440,17 @@ zl_status validate_pointers(const zl_decode_attn_params* a, bool need_v) {
 
 namespace {
 
+// Longest valid length of a sequence under modified scores (the kernels' sums of
+// a length and a tile stay in 32 bits), and the window as the kernels take it:
+// one that no sequence fills hides nothing, and its differences could leave 32
+// bits.
+int64_t mods_len_cap(const zl_decode_attn_params* a) {
+  return std::min<int64_t>(a->block_table_stride * int64_t(a->page_size), INT32_MAX - 4096);
+}
+int mods_window(const zl_decode_attn_params* a, const zl_score_params& m) {
+  return m.window >= mods_len_cap(a) ? 0 : m.window;
+}
+
 // The kernels' cap fields (kernels.h, gqa_wide.h) for scores c tanh(s / c).
 template <class Params>
 void set_cap(float scale, float c, Params* p) {
@@ -468,10 +479,10 @@ zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, con
                    GqaParams& p, char* ws, cudaStream_t s) {
   set_cap(a->scale, m.softcap, &p);
   p.slopes = m.alibi_slopes;
-  p.window = m.window;
+  p.window = mods_window(a, m);
   p.tree = m.tree_mask;
   p.tree_words = (a->q_len + 31) / 32;
-  p.len_cap = a->block_table_stride * int64_t(a->page_size);
+  p.len_cap = mods_len_cap(a);
   if (m.weights) {
     p.len_cap = std::min(p.len_cap, int64_t(m.weights_tokens));
     p.row_stat = reinterpret_cast<float2*>(ws + plan.off_stat);
@@ -507,7 +518,7 @@ zl_status mods_run(const zl_decode_attn_params* a, const zl_score_params& m, con
     w.Hq = a->Hq;
     w.Hkv = a->Hkv;
     w.g = plan.g;
-    w.window = m.window;
+    w.window = p.window;
     w.len_cap = p.len_cap;
     w.max_tokens = m.weights_tokens;
     e = zl::weights_launch(w, s);
@@ -548,11 +559,11 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
   p.mt = plan.mt;
   p.nblk = plan.nblk;
   p.whole_units = plan.unit_cut ? 2 : a->num_ctas == 0 ? 1 : 0;
-  p.len_cap = a->block_table_stride * int64_t(a->page_size);
+  p.len_cap = mods_len_cap(a);
   p.scale_log2 = float(double(a->scale) * kLog2e);
   set_cap(a->scale, m.softcap, &p);
   p.slopes = m.alibi_slopes;
-  p.window = m.window;
+  p.window = mods_window(a, m);
   p.tree = m.tree_mask;
   p.tree_words = (a->q_len + 31) / 32;
   if (a->k_new) {

@@ -417,3 +417,13 @@ def test_bad_pages_in_calls_of_few_rows(Hq, Hkv, q_len):
         bt[0, at] = w.num_pages
         run(w, block_table=bt, softcap=5.0, expect_bad=1)
         run(w, block_table=bt, window=500, expect_bad=0 if at < 500 else 1)
+
+
+@pytest.mark.parametrize("window", [299, 300, 1 << 20, (1 << 31) - 1])
+@pytest.mark.parametrize("q_len", [4, 24])
+def test_windows_longer_than_any_sequence(q_len, window):
+    """Nothing is hidden, also where fewer tokens are cached than drafted."""
+    w = wl.random_case(2870, B=4, Hq=8, Hkv=2, q_len=q_len, lens=[1, q_len - 1, 300, 150])
+    run(w, window=window)
+    mask = random_trees(np.random.default_rng(1), 4, q_len)
+    run(w, window=window, mask=mask, weights=torch.zeros(4, 2, 300))
