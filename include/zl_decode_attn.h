@@ -343,7 +343,8 @@ zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
  *
  * Everything else is as for zl_decode_attn, fused append included, with two
  * limits: flags must be 0 and shared_prefix_pages 0 (ZL_ERR_UNSUPPORTED). A
- * softcap outside [1e-6, 1e6] is ZL_ERR_UNSUPPORTED. Results depend only on
+ * softcap outside [1e-6, 1e6], or one that scale divided by is no normal 32-bit
+ * number, is ZL_ERR_UNSUPPORTED. Results depend only on
  * logical content, and repeated calls are bit-identical. K and V rows of
  * tokens that no query token's window reaches are never used and pages that
  * hold only such tokens need not be mapped; rows that some query sees and
@@ -364,9 +365,10 @@ typedef struct {
 zl_status zl_decode_attn_ex(const zl_decode_attn_params* params, const zl_score_params* scores,
                             zl_stream_t stream);
 
-/* Workspace bytes zl_decode_attn_ex needs; of the score params the pointers
-   only as present or absent. With weights it holds the scores of every query
-   row: B * q_len * Hq * weights_tokens * 4 bytes more. */
+/* Workspace bytes zl_decode_attn_ex needs, from the shapes, num_ctas,
+   max_seq_len, window, weights_tokens and which pointers are NULL. With weights
+   it holds the scores of every query row: B * q_len * Hq * weights_tokens * 4
+   bytes more. */
 zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
                                            const zl_score_params* scores, size_t* bytes);
 
@@ -430,7 +432,8 @@ zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream);
  * 0, 1, ...: their K and V rows move there, in place, and new_lens[b] =
  * seq_lens[b] - q_len + accepted[b].
  *   - path int32, row b of path_len entries at b * path_stride; accepted int32
- *     [B]; 0 <= accepted[b] <= min(q_len, path_len), q_len <= 128. Entries past accepted[b] are not read.
+ *     [B]; 0 <= accepted[b] <= min(q_len, path_len), q_len <= 128. Entries past
+ *     accepted[b] are not read.
  *   - Pools, strides, row widths, block table and v_pool = NULL as for
  *     zl_kv_append; no page of these sequences may be mapped by another one.
  *   - Device data errors: seq_lens[b] < q_len or above the block table's reach

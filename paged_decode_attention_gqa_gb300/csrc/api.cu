@@ -151,15 +151,16 @@ zl_status mods_validate(const zl_decode_attn_params* a, const zl_score_params* m
   if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap) || m->window < 0)
     return ZL_ERR_INVALID_ARG;
   // scale / c and c * log2(e) must be normal numbers
-  if (m->softcap > 0.f && (m->softcap < 1e-6f || m->softcap > 1e6f)) return ZL_ERR_UNSUPPORTED;
+  if (m->softcap > 0.f && (m->softcap < 1e-6f || m->softcap > 1e6f ||
+                           !std::isnormal(float(double(a->scale) / m->softcap))))
+    return ZL_ERR_UNSUPPORTED;
   if (!aligned(m->alibi_slopes, 4) || !aligned(m->tree_mask, 4) || !aligned(m->weights, 4))
     return ZL_ERR_INVALID_ARG;
   if (m->weights) {
     if (m->weights_tokens < 1 || !std::isfinite(m->weights_decay) || m->weights_decay < 0.f)
       return ZL_ERR_INVALID_ARG;
-    // rows of different sequences and heads must not overlap
-    if ((a->B > 1 && m->weights_seq_stride < m->weights_tokens) ||
-        (a->Hkv > 1 && m->weights_head_stride < m->weights_tokens))
+    if (!zl::rows_distinct(a->B, a->Hkv, m->weights_seq_stride, m->weights_head_stride,
+                           m->weights_tokens))
       return ZL_ERR_INVALID_ARG;
   }
   if (a->flags || a->shared_prefix_pages != 0) return ZL_ERR_UNSUPPORTED;

@@ -110,6 +110,15 @@ struct GqaParams {
   float2* row_stat;
 };
 
+// Rows of `tokens` elements, element (b, h) at b * seq + h * head, do not overlap
+// (one of the strides spans all rows of the other).
+inline bool rows_distinct(int64_t B, int64_t H, int64_t seq, int64_t head, int64_t tokens) {
+  if (B == 1) return H == 1 || head >= tokens;
+  if (H == 1) return seq >= tokens;
+  return seq >= head ? head >= tokens && (seq - tokens) / head >= H - 1
+                     : seq >= tokens && (head - tokens) / seq >= B - 1;
+}
+
 // The weights kernel that follows a launch with p.scores set.
 struct WeightsParams {
   const float* scores;

@@ -78,12 +78,13 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
 constexpr int kBins = 256;        // of a digit: 4 digits of 8 bits
 constexpr int kHistBytes = kBins * 32 * 4;
 
-// T threads of kRun consecutive tokens each, kBlocks blocks per SM. Every lane counts in a histogram of its own: the weights' leading
-// digits fall into a few bins, and additions to one address, by lanes of a warp
-// or by warps, are done one after the other. CACHED: this CTA's part fits
-// kRun tokens per thread; then a thread holds their keys in registers through
-// all passes (computing them again in each pass was 390 instructions per token
-// in all), and shared memory the weights. Otherwise they are read again.
+// T threads of kRun consecutive tokens each, kBlocks blocks per SM.
+// Every lane counts in a histogram of its own: the weights' leading digits fall
+// into a few bins, and additions to one address, by lanes of a warp or by
+// warps, are done one after the other. CACHED: this CTA's part fits kRun tokens
+// per thread; then a thread holds their keys in registers through all passes
+// (computing them again in each pass was 390 instructions per token in all), and
+// shared memory the weights. Otherwise they are read again.
 template <int T, int kRun, int kBlocks, bool CACHED>
 __global__ void __launch_bounds__(T, kBlocks)
 evict_select_kernel(const __grid_constant__ EvictParams p) {
@@ -336,7 +337,8 @@ cudaError_t select_launch(const EvictParams& p, int part, int B, cudaStream_t st
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.Hkv * p.cluster), unsigned(B));
   cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = kHistBytes + (CACHED ? size_t((part + kRun - 1) / kRun) * (kRun + 1) * sizeof(float) : 0);
+  cfg.dynamicSmemBytes =
+      kHistBytes + (CACHED ? size_t((part + kRun - 1) / kRun) * (kRun + 1) * sizeof(float) : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -491,13 +493,15 @@ extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* a, zl_stream_t stream
       int64_t(a->sink) + a->recent > a->budget || a->weights_tokens < 1)
     return ZL_ERR_INVALID_ARG;
   if (a->dst_block_table && a->dst_block_table_stride < 1) return ZL_ERR_INVALID_ARG;
-  // rows of different sequences and heads must not overlap
-  if ((a->B > 1 && a->weights_seq_stride < a->weights_tokens) ||
-      (a->Hkv > 1 && a->weights_head_stride < a->weights_tokens))
+  if (!zl::rows_distinct(a->B, a->Hkv, a->weights_seq_stride, a->weights_head_stride,
+                         a->weights_tokens))
     return ZL_ERR_INVALID_ARG;
   const int64_t out_tokens = a->budget < a->weights_tokens ? a->budget : a->weights_tokens;
-  if (a->weights_out && ((a->B > 1 && a->weights_out_seq_stride < out_tokens) ||
-                         (a->Hkv > 1 && a->weights_out_head_stride < out_tokens)))
+  if (a->weights_out && !zl::rows_distinct(a->B, a->Hkv, a->weights_out_seq_stride,
+                                           a->weights_out_head_stride, out_tokens))
+    return ZL_ERR_INVALID_ARG;
+  // (in place is NULL: the kernels that write elsewhere read without its order)
+  if (a->weights_out == a->weights || a->dst_block_table == a->block_table)
     return ZL_ERR_INVALID_ARG;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;

@@ -39,6 +39,13 @@ def _scores(**over):
     (dict(), dict(weights=FAKE, weights_decay=float("nan")), zl.ERR_INVALID_ARG),
     (dict(), dict(weights=FAKE, weights_head_stride=127), zl.ERR_INVALID_ARG),  # rows overlap
     (dict(), dict(weights=FAKE, weights_seq_stride=0), zl.ERR_INVALID_ARG),
+    # each stride holds a row, yet (sequence 0, head 1) and (1, 0) are the same
+    (dict(), dict(weights=FAKE, weights_head_stride=256, weights_seq_stride=256),
+     zl.ERR_INVALID_ARG),
+    (dict(), dict(weights=FAKE, weights_head_stride=128, weights_seq_stride=1023),
+     zl.ERR_INVALID_ARG),
+    (dict(scale=1e35), dict(softcap=1e-6), zl.ERR_UNSUPPORTED),  # scale / softcap overflows
+    (dict(scale=1e-35), dict(softcap=1e6), zl.ERR_UNSUPPORTED),
     (dict(flags=zl.SINGLE_LAUNCH), dict(softcap=30.0), zl.ERR_UNSUPPORTED),
     (dict(flags=zl.TEST_STALL), dict(), zl.ERR_UNSUPPORTED),
     (dict(shared_prefix_pages=1), dict(softcap=30.0), zl.ERR_UNSUPPORTED),
@@ -88,6 +95,10 @@ def _evict(**over):
     dict(recent=-1), dict(sink=25),               # sink + recent > budget
     dict(sink=1 << 30, recent=1 << 30, budget=1 << 30),
     dict(weights_tokens=0), dict(weights_head_stride=100), dict(weights_seq_stride=0),
+    dict(weights_head_stride=256, weights_seq_stride=256),       # rows overlap
+    dict(weights_out=2 * FAKE, weights_out_head_stride=32, weights_out_seq_stride=40),
+    dict(weights_out=FAKE, weights_out_head_stride=128, weights_out_seq_stride=1024),  # in place
+    dict(dst_block_table=FAKE, dst_block_table_stride=8),
     dict(weights_out=FAKE, weights_out_head_stride=8, weights_out_seq_stride=1024),
     dict(weights_out=FAKE, weights_out_head_stride=32, weights_out_seq_stride=0),
     dict(dst_block_table=FAKE, dst_block_table_stride=0),
