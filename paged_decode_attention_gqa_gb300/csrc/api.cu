@@ -100,13 +100,16 @@ struct GqaPlan {
   int tpt = 1, mt = 1, nblk = 1;
 };
 
-// Rows per kv head above which a modified-score call runs the tcgen05 kernel.
-// Both sides measured, drafted trees over 64 sequences of 512-4096 tokens, 32
-// heads on 8: 16 rows 120 us by either kernel; 20 rows 122 us here, 166 there;
-// 36 rows 123 and 230. With 4 sequences of 100-500 tokens and 32 rows 15.3 and
-// 21.3. (One sequence of 8000 tokens, 20 to 32 rows: 28 and 23, the side that
-// loses.)
+// Query rows per kv head above which a modified-score call runs the tcgen05
+// kernel; with at most kFewUnits (sequence, kv head) units only above
+// kWideRowsFew. Both sides measured, drafted trees, 4 heads to a kv head: 512
+// units of 512-4096 tokens, 16 rows 120 us by either kernel, 20 rows 122 by the
+// tcgen05 one and 166 by the other, 36 rows 123 and 230; 16 units of 200 tokens
+// and 32 rows 13.7 and 16.2, of 16000 tokens 43 and 52; 8 units of 200 tokens and
+// 20 or 32 rows 13.3 and 12.4 to 13.0, of 4000 tokens 24 and 21 to 23.
 constexpr int kWideRows = 16;
+constexpr int kWideRowsFew = 32;
+constexpr int kFewUnits = 8;
 
 // Query tokens per sequence one call takes, and query heads per kv head (the
 // GQA path takes the (token, head) rows of a kv head in groups of at most 16).
@@ -183,7 +186,9 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
   const double most_tiles = double(a->B) * a->Hkv * plan->nblk *
                             (double(a->block_table_stride) * a->page_size / zl::kWideTile + 1 +
                              zl::kWideUnitCost);
-  if (mods && !mods->weights && plan->g * a->q_len > kWideRows && most_tiles < 2e9) {
+  const int head_rows = plan->g * a->q_len;
+  if (mods && !mods->weights && most_tiles < 2e9 &&
+      head_rows > (int64_t(a->B) * a->Hkv <= kFewUnits ? kWideRowsFew : kWideRows)) {
     plan->wide = true;
     plan->grid = a->num_ctas > 0 ? a->num_ctas : dev.sms;
     if (a->num_ctas == 0 && a->max_seq_len > 0) {
@@ -198,10 +203,10 @@ zl_status gqa_plan(const zl_decode_attn_params* a, GqaPlan* plan,
         plan->grid = int(std::min(int64_t(plan->grid), std::max<int64_t>(units * tiles, 1)));
       }
     }
-    const size_t rows = size_t(plan->grid) * 2 * plan->mt * 128;
+    const size_t slots = size_t(plan->grid) * 2 * plan->mt * 128;
     plan->off_lse = round_up(size_t(plan->grid) * sizeof(int4), 256);
-    plan->off_o = plan->off_lse + round_up(rows * sizeof(float), 256);
-    plan->bytes = plan->off_o + rows * zl::kGqaHeadDim * sizeof(float);
+    plan->off_o = plan->off_lse + round_up(slots * sizeof(float), 256);
+    plan->bytes = plan->off_o + slots * zl::kGqaHeadDim * sizeof(float);
     return ZL_OK;
   }
   plan->fused = (a->flags & ZL_DECODE_SINGLE_LAUNCH) != 0;
