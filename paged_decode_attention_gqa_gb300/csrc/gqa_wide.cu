@@ -78,18 +78,14 @@ struct WideCfg {
   static_assert(kSmemMax <= 232448, "shared memory of one CTA");
 };
 
-// Wait on an mbarrier with the whole warp by polling; every lane gets the same
-// answer, false after a timeout or an abort.
-__device__ __forceinline__ bool wide_warp_wait(uint32_t bar, uint32_t parity,
-                                               const volatile int* abort_flag) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+// Wait on an mbarrier by polling, one thread; false after a timeout or an abort.
+__device__ __forceinline__ bool wide_poll(uint32_t bar, uint32_t parity,
+                                          const volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-    if ((i & 63u) == 0) {
-      const bool stop = *abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs;
-      if (__any_sync(0xffffffffu, stop)) return false;
-    }
+    if (mbar_test(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs)) return false;
   }
 }
 
@@ -470,32 +466,28 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
     const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
+    if (elect_one()) {  // one thread for all of it: no votes, no shuffles between an arrival and its MMAs
     uint32_t item = 0, pieces = 0;
     uint32_t pn[2] = {0, 0};  // tiles whose P was taken from each stream
     bool ok = true;
     auto wait = [&](int i, uint32_t parity) -> bool {
-      ok = ok && wide_warp_wait(bar(i), parity, abort_flag);
+      ok = ok && wide_poll(bar(i), parity, abort_flag);
       return ok;
     };
     auto wait_item = [&](uint32_t it) { return wait(Cfg::B_FULL0 + it % NB, (it / NB) & 1); };
     auto buf = [&](uint32_t it) -> uint32_t {
       return sbase + Cfg::kOffRing + (it % NB) * kBuf;
     };
-    // The low words of the shared-memory descriptors, and the TMEM address,
-    // through a shuffle: the compiler then knows them to be the same in every
-    // lane and keeps them, and what is added per step, in uniform registers.
-    // (From ordinary ones each MMA took about 70 cycles to issue.)
-    auto uni = [](uint32_t v) -> uint32_t { return __shfl_sync(0xffffffffu, v, 0); };
-    const uint32_t tm = uni(tmem);
+    const uint32_t tm = tmem;
     constexpr uint32_t kDescHi = desc_hi(1024);
     constexpr uint32_t kLboV = uint32_t(kHalf >> 4) << 16;  // V's next 64 columns
     // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step. (All 128
     // tokens at once: with 64, each MMA still reads 4 KB of Q and takes as long.)
     auto qk = [&](int s, uint32_t it, bool release, bool last) {
-      const uint32_t ad = uni((sbase + (MT == 2 ? s * kBuf : 0)) >> 4);
-      const uint32_t bd = uni(buf(it) >> 4), d = uni(tm + kTmemS + 128 * s);
+      const uint32_t ad = ((sbase + (MT == 2 ? s * kBuf : 0)) >> 4);
+      const uint32_t bd = (buf(it) >> 4), d = (tm + kTmemS + 128 * s);
       tc_fence_after();
-      if (elect_one()) {
+      {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           constexpr uint32_t kNext = kHalf >> 4;
@@ -506,14 +498,13 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
         if (last) umma_commit(bar(Cfg::B_QFREE));  // Q is read for the last time
       }
-      __syncwarp();
     };
     // O_s (+)= P_s[h] V_h, 16 tokens (8 TMEM columns of P) per step
     auto pv = [&](int s, int h, uint32_t it, bool first, bool release, bool last) {
-      const uint32_t bd = uni(((buf(it) + h * (kHT * 128)) >> 4) | kLboV);
-      const uint32_t d = uni(tm + kTmemO + 128 * s), a = uni(tm + kTmemS + 128 * s + kHT * h);
+      const uint32_t bd = (((buf(it) + h * (kHT * 128)) >> 4) | kLboV);
+      const uint32_t d = (tm + kTmemO + 128 * s), a = (tm + kTmemS + 128 * s + kHT * h);
       tc_fence_after();
-      if (elect_one()) {
+      {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           umma_ts(d, a + 8 * k, bd + k * (16 * 128 / 16), kDescHi, idesc_pv, !first || k > 0);
@@ -521,7 +512,6 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         if (last) umma_commit(bar(Cfg::B_O0 + s));
         if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
       }
-      __syncwarp();
     };
     for (int idx = s_c; idx < e_c && ok;) {
       const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
@@ -585,15 +575,16 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       ++pieces;
       idx = pc.next;
     }
-    if (!ok && lane == 0) {
+    if (!ok) {
       raise_error(p.err_flags, kErrTimeout);
       *abort_flag = 1;
     }
     // Every MMA done before TMEM is released.
-    if (elect_one()) umma_commit(bar(Cfg::B_FINAL));
-    __syncwarp();
+    umma_commit(bar(Cfg::B_FINAL));
     const volatile int never = 0;
     mbar_wait(bar(Cfg::B_FINAL), 0, &never);
+    }
+    __syncwarp();
   }
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
