@@ -5,29 +5,37 @@
 // / 16 times from shared memory and L2. Here up to 256 rows share each K/V
 // tile: S = Q K^T (M = 128 rows, N = 128 tokens) and O += P V (N = 128
 // columns) are tcgen05.mma with S, P and O in TMEM, so a tile of 128 tokens
-// (64 KB) is loaded once for all of them and the load is what bounds it: 64 KB
-// at this card's bandwidth are about 2800 cycles per SM, the products of 256
-// rows 2100, their exponentials 2000.
+// (64 KB) is loaded once for all of them. Per SM and tile the load takes about
+// 2800 cycles at this card's bandwidth, the products of 128 rows 1050, of 256
+// rows 2100.
+// Measured, 64 sequences of 512-4096 tokens with 32 heads on 8 kv heads: 16
+// drafted tokens (MT = 1) 125 us, 5.1 TB/s, bound by the load and the ends of
+// units; 64 (MT = 2) 166 us, 4.1 TB/s and 0.96 PFLOP/s, with a cap 211 us, bound
+// by each stream's chain: 2150 cycles of softmax for 128 rows x 128 tokens, then
+// 1360 from its P to the next S (PV of a half tile 256, QK 512, the rest waits
+// and issue). A tile with masks takes 5000-6500.
 //
 // Two softmax warpgroups keep the tensor pipe fed, each with its own S and O
 // ("streams"). MT = 2: stream s has rows [128 s, 128 s + 128) of the block and
 // takes every tile. MT = 1 (at most 128 rows): both streams have the same rows
-// and take the tiles in turn, and their two results are joined in TMEM at the
-// end of the piece. Either way one stream's softmax runs under the other
-// one's products.
+// and take the tiles in turn, and the epilogue joins their two results. Either
+// way one stream's softmax runs under the other one's products.
 //
 // Work is cut as in gqa_kernel.cuh: units (sequence, kv head, row block) of
 // 128-token tiles on one line, cut into equal ranges, one per CTA; cut units
 // leave normalised fp32 partials for the merge kernel.
 //
 // TMEM (512 columns): S of stream 0, 1 (128 each; P, 64 columns of bf16 pairs,
-// replaces S once it is read), O of stream 0, 1 (128 each). MMAs of one CTA
+// replaces S once it is read, in halves of 64 tokens, so that a half's PV runs
+// under the other half's softmax), O of stream 0, 1 (128 each). MMAs of one CTA
 // execute in the order of their issue, so QK of a stream's next tile may
 // follow the PV that reads its P without a wait; the commit after a QK covers
 // the PV before it, so a softmax thread that sees S of a tile may also rescale
 // O.
 #include "gqa_kernel.cuh"
 #include "gqa_wide.h"
+
+#include <type_traits>
 
 namespace zl {
 
@@ -55,8 +63,8 @@ struct WideCfg {
   enum : int {
     B_Q = 0, B_QFREE, B_FINAL, B_MASK0, B_ML0 = B_MASK0 + 2, B_EPI0 = B_ML0 + 2,
     B_S0 = B_EPI0 + 2, B_P0 = B_S0 + 2, B_PV0 = B_P0 + 4, B_O0 = B_PV0 + 2,
-    B_OFREE0 = B_O0 + 2, B_FULL0 = B_OFREE0 + 2, B_EMPTY0 = B_FULL0 + kRing, B_INFO0 = B_EMPTY0 + kRing,
-    B_COUNT = B_INFO0 + kInfo
+    B_OFREE0 = B_O0 + 2, B_FULL0 = B_OFREE0 + 2, B_EMPTY0 = B_FULL0 + kRing,
+    B_INFO0 = B_EMPTY0 + kRing, B_COUNT = B_INFO0 + kInfo
   };
   static constexpr int kOffMisc = kOffBar + 8 * B_COUNT;   // TMEM address, abort flag
   static constexpr int kOffInfo = kOffMisc + 16;           // kInfo words
@@ -463,129 +471,126 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
         *abort_flag = 1;
       }
     } else {
-    // ---------------------------------------------------------- MMA issuer
-    const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
-    const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
-    if (elect_one()) {  // one thread for all of it: no votes, no shuffles between an arrival and its MMAs
-    uint32_t item = 0, pieces = 0;
-    uint32_t pn[2] = {0, 0};  // tiles whose P was taken from each stream
-    bool ok = true;
-    auto wait = [&](int i, uint32_t parity) -> bool {
-      ok = ok && wide_poll(bar(i), parity, abort_flag);
-      return ok;
-    };
-    auto wait_item = [&](uint32_t it) { return wait(Cfg::B_FULL0 + it % NB, (it / NB) & 1); };
-    auto buf = [&](uint32_t it) -> uint32_t {
-      return sbase + Cfg::kOffRing + (it % NB) * kBuf;
-    };
-    const uint32_t tm = tmem;
-    constexpr uint32_t kDescHi = desc_hi(1024);
-    constexpr uint32_t kLboV = uint32_t(kHalf >> 4) << 16;  // V's next 64 columns
-    // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step. (All 128
-    // tokens at once: with 64, each MMA still reads 4 KB of Q and takes as long.)
-    auto qk = [&](int s, uint32_t it, bool release, bool last) {
-      const uint32_t ad = ((sbase + (MT == 2 ? s * kBuf : 0)) >> 4);
-      const uint32_t bd = (buf(it) >> 4), d = (tm + kTmemS + 128 * s);
-      tc_fence_after();
-      {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t idesc_qk = umma_idesc_bf16(128, kWT, false);
+      const uint32_t idesc_pv = umma_idesc_bf16(128, 128, true);
+      // one thread for all of it: no votes or shuffles between an arrival and its
+      // MMAs (with the warp in step a wait took 160 cycles and bounded the kernel)
+      if (elect_one()) {
+        uint32_t item = 0, pieces = 0;
+        uint32_t pn[2] = {0, 0};  // tiles whose P was taken from each stream
+        bool ok = true;
+        auto wait = [&](int i, uint32_t parity) -> bool {
+          ok = ok && wide_poll(bar(i), parity, abort_flag);
+          return ok;
+        };
+        auto wait_item = [&](uint32_t it) { return wait(Cfg::B_FULL0 + it % NB, (it / NB) & 1); };
+        auto buf = [&](uint32_t it) -> uint32_t {
+          return sbase + Cfg::kOffRing + (it % NB) * kBuf;
+        };
+        constexpr uint32_t kDescHi = desc_hi(1024);
+        constexpr uint32_t kLboV = uint32_t(kHalf >> 4) << 16;  // V's next 64 columns
+        // S_s = Q K^T, 16 dims (32 bytes of the swizzled row) per step. (All 128
+        // tokens at once: with 64, each MMA still reads 4 KB of Q and takes as long.)
+        auto qk = [&](int s, uint32_t it, bool release, bool last) {
+          const uint32_t ad = (sbase + (MT == 2 ? s * kBuf : 0)) >> 4, bd = buf(it) >> 4;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          constexpr uint32_t kNext = kHalf >> 4;
-          const uint32_t off = (k >> 2) * kNext + (k & 3) * 2;
-          umma_ss(d, ad + off, bd + off, kDescHi, idesc_qk, k > 0);
-        }
-        umma_commit(bar(Cfg::B_S0 + s));
-        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
-        if (last) umma_commit(bar(Cfg::B_QFREE));  // Q is read for the last time
-      }
-    };
-    // O_s (+)= P_s[h] V_h, 16 tokens (8 TMEM columns of P) per step
-    auto pv = [&](int s, int h, uint32_t it, bool first, bool release, bool last) {
-      const uint32_t bd = (((buf(it) + h * (kHT * 128)) >> 4) | kLboV);
-      const uint32_t d = (tm + kTmemO + 128 * s), a = (tm + kTmemS + 128 * s + kHT * h);
-      tc_fence_after();
-      {
+          for (int k = 0; k < 8; ++k) {
+            constexpr uint32_t kNext = kHalf >> 4;
+            const uint32_t off = (k >> 2) * kNext + (k & 3) * 2;
+            umma_ss(tmem + kTmemS + 128 * s, ad + off, bd + off, kDescHi, idesc_qk, k > 0);
+          }
+          umma_commit(bar(Cfg::B_S0 + s));
+          if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
+          if (last) umma_commit(bar(Cfg::B_QFREE));  // Q is read for the last time
+        };
+        // O_s (+)= P_s[h] V_h, 16 tokens (8 TMEM columns of P) per step
+        auto pv = [&](int s, int h, uint32_t it, bool first, bool release, bool last) {
+          const uint32_t bd = ((buf(it) + h * (kHT * 128)) >> 4) | kLboV;
+          const uint32_t d = tmem + kTmemO + 128 * s, a = tmem + kTmemS + 128 * s + kHT * h;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_ts(d, a + 8 * k, bd + k * (16 * 128 / 16), kDescHi, idesc_pv, !first || k > 0);
-        umma_commit(bar(Cfg::B_PV0 + s));
-        if (last) umma_commit(bar(Cfg::B_O0 + s));
-        if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
-      }
-    };
-    for (int idx = s_c; idx < e_c && ok;) {
-      const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
-      if (pc.ntiles == 0) {  // only places of a unit's fixed cost
-        idx = pc.next;
-        continue;
-      }
-      const int n = pc.ntiles;
-      if (!wait(Cfg::B_Q, pieces & 1)) break;
-      // the first PV of a stream overwrites the O that the epilogue reads
-      auto o_free = [&](int s) -> bool {
-        return pieces == 0 || wait(Cfg::B_OFREE0 + s, (pieces - 1) & 1);
-      };
-      if (MT == 2) {
-        if (!wait_item(item)) break;
-        qk(0, item, false, false);
-        qk(1, item, true, n == 1);
-        ++item;
-        for (int t = 0; t < n && ok; ++t) {
-          const uint32_t iv = item, ik = item + 1;
-          const bool more = t + 1 < n;
-          if (!wait_item(iv)) break;
-          // stream 1 runs about half a tile behind stream 0, so this is the
-          // order in which the P halves come
+          for (int k = 0; k < 4; ++k)
+            umma_ts(d, a + 8 * k, bd + k * (16 * 128 / 16), kDescHi, idesc_pv, !first || k > 0);
+          umma_commit(bar(Cfg::B_PV0 + s));
+          if (last) umma_commit(bar(Cfg::B_O0 + s));
+          if (release) umma_commit(bar(Cfg::B_EMPTY0 + it % NB));
+        };
+        for (int idx = s_c; idx < e_c && ok;) {
+          const Piece pc = piece_at(p, prefix, idx, s_c, e_c);
+          if (pc.ntiles == 0) {  // only places of a unit's fixed cost
+            idx = pc.next;
+            continue;
+          }
+          const int n = pc.ntiles;
+          if (!wait(Cfg::B_Q, pieces & 1)) break;
+          // the first PV of a stream overwrites the O that the epilogue reads
+          auto o_free = [&](int s) -> bool {
+            return pieces == 0 || wait(Cfg::B_OFREE0 + s, (pieces - 1) & 1);
+          };
+          if (MT == 2) {
+            if (!wait_item(item)) break;
+            qk(0, item, false, false);
+            qk(1, item, true, n == 1);
+            ++item;
+            for (int t = 0; t < n && ok; ++t) {
+              const uint32_t iv = item, ik = item + 1;
+              const bool more = t + 1 < n;
+              if (!wait_item(iv)) break;
+              // stream 1 runs about half a tile behind stream 0, so this is the
+              // order in which the P halves come
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            const int s = k >> 1, h = k & 1;
-            if (!wait(Cfg::B_P0 + k, pn[0] & 1) || (t == 0 && h == 0 && !o_free(s))) break;
-            pv(s, h, iv, t == 0 && h == 0, k == 3, h == 1 && !more);
-            if (h == 1 && more) {
-              if (s == 0 && !wait_item(ik)) break;
-              qk(s, ik, s == 1, s == 1 && t + 2 == n);
+              for (int k = 0; k < 4; ++k) {
+                const int s = k >> 1, h = k & 1;
+                if (!wait(Cfg::B_P0 + k, pn[0] & 1) || (t == 0 && h == 0 && !o_free(s))) break;
+                pv(s, h, iv, t == 0 && h == 0, k == 3, h == 1 && !more);
+                if (h == 1 && more) {
+                  if (s == 0 && !wait_item(ik)) break;
+                  qk(s, ik, s == 1, s == 1 && t + 2 == n);
+                }
+              }
+              ++pn[0];
+              item += more ? 2 : 1;
+            }
+          } else {
+            for (int t = 0; t < 2 && t < n; ++t) {
+              if (!wait_item(item)) break;
+              qk(t, item++, true, t + 1 == n);
+            }
+            for (int t = 0; t < n && ok; ++t) {
+              const int s = t & 1;
+              const bool more = t + 2 < n;
+              if (!wait_item(item)) break;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                if (!wait(Cfg::B_P0 + 2 * s + h, pn[s] & 1) || (t < 2 && h == 0 && !o_free(s)))
+                  break;
+                pv(s, h, item, t < 2 && h == 0, h == 1, h == 1 && !more);
+              }
+              if (!ok) break;
+              ++pn[s];
+              ++item;
+              if (more) {
+                if (!wait_item(item)) break;
+                qk(s, item++, true, t + 3 == n);
+              }
             }
           }
-          ++pn[0];
-          item += more ? 2 : 1;
+          ++pieces;
+          idx = pc.next;
         }
-      } else {
-        for (int t = 0; t < 2 && t < n; ++t) {
-          if (!wait_item(item)) break;
-          qk(t, item++, true, t + 1 == n);
+        if (!ok) {
+          raise_error(p.err_flags, kErrTimeout);
+          *abort_flag = 1;
         }
-        for (int t = 0; t < n && ok; ++t) {
-          const int s = t & 1;
-          const bool more = t + 2 < n;
-          if (!wait_item(item)) break;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (!wait(Cfg::B_P0 + 2 * s + h, pn[s] & 1) || (t < 2 && h == 0 && !o_free(s))) break;
-            pv(s, h, item, t < 2 && h == 0, h == 1, h == 1 && !more);
-          }
-          if (!ok) break;
-          ++pn[s];
-          ++item;
-          if (more) {
-            if (!wait_item(item)) break;
-            qk(s, item++, true, t + 3 == n);
-          }
-        }
+        // Every MMA done before TMEM is released.
+        umma_commit(bar(Cfg::B_FINAL));
+        const volatile int never = 0;
+        mbar_wait(bar(Cfg::B_FINAL), 0, &never);
       }
-      ++pieces;
-      idx = pc.next;
+      __syncwarp();
     }
-    if (!ok) {
-      raise_error(p.err_flags, kErrTimeout);
-      *abort_flag = 1;
-    }
-    // Every MMA done before TMEM is released.
-    umma_commit(bar(Cfg::B_FINAL));
-    const volatile int never = 0;
-    mbar_wait(bar(Cfg::B_FINAL), 0, &never);
-    }
-    __syncwarp();
-  }
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2;                          // stream
@@ -1093,7 +1098,8 @@ cudaError_t launch(const WideParams& p, int grid, bool no_merge, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!done[device]) {
-    if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT, CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((e = cudaFuncSetAttribute(gqa_wide_kernel<MT, CAP, BIAS>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(WideCfg<MT>::kSmemMax))) != cudaSuccess)
       return e;
     done[device] = true;
@@ -1128,7 +1134,8 @@ cudaError_t gqa_wide_launch(const WideParams& p, int grid, bool no_merge, cudaSt
                              : (p.slopes ? launch<MT, false, true> : launch<MT, false, false>);
     return f(p, grid, no_merge, stream, attn_begin, attn_end);
   };
-  return p.mt == 2 ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>());
+  return p.mt == 2 ? pick(std::integral_constant<int, 2>())
+                   : pick(std::integral_constant<int, 1>());
 }
 
 }  // namespace zl
