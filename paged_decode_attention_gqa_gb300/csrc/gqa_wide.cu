@@ -302,10 +302,20 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
   // Few short units: one CTA each, nothing cut (a cut costs the partials' way
   // through memory and the merge's part of the call).
   const bool whole = p.whole_units == 2 ||
-                     (p.whole_units == 1 && units <= gridDim.x &&
-                      int(info[0]) <= kWideWholeTiles + kWideUnitCost);
+                     (p.whole_units == 1 && int(info[0]) <= kWideWholeTiles + kWideUnitCost);
   __syncthreads();  // info[0] is read: the K warp may use it
-  if (whole) {
+  if (whole && units > gridDim.x) {
+    // more units than CTAs: ranges that begin and end at the nearest unit's start
+    const TileCut even(W, int(gridDim.x));
+    auto at_unit = [&](int64_t place) -> int {
+      if (place >= W) return int(W);
+      const int U = p.Hkv * p.nblk, b = locate_seq(prefix, B, U, place);
+      const int len = prefix[b + 1] - prefix[b], off = int(place) - U * prefix[b];
+      return U * prefix[b] + (off + len / 2) / len * len;
+    };
+    s_c = c < int(even.G) ? at_unit(even.start(c)) : 0;
+    e_c = c < int(even.G) ? at_unit(even.start(c + 1)) : 0;
+  } else if (whole) {
     s_c = e_c = 0;
     if (c < units) {
       const int U = p.Hkv * p.nblk, b = c / U, len = prefix[b + 1] - prefix[b];

@@ -10,7 +10,10 @@ constexpr int kWideTile = 128;  // tokens per tile
 // (64 sequences of 512-4096 tokens, 64 drafted tokens: 196, 177, 172, 172, 178 us
 // at 0, 1, 2, 3 and 5; 16 drafted tokens: 137, 128, 129, 130, 132 us.)
 constexpr int kWideUnitCost = 2;
-// Units of at most this many tiles, no more of them than CTAs, are not cut.
+// Units of at most this many tiles are not cut: a CTA each, or the line is cut
+// at the nearest unit's start. (256 units of 128-512 tokens, 16 drafted tokens, 4 heads:
+// 29.9 us cut, 28.7 whole, 512 units 47.9 and 43.9, with 64 drafted tokens 65.6
+// and 58.4; with 8 tiles allowed, 160 units of 512-1024 tokens 28.8 and 32.9.)
 constexpr int kWideWholeTiles = 4;
 
 // tanh(y) / y for z = y^2 in [0, 1/4]: the cubic in z that interpolates it at

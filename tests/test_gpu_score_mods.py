@@ -398,6 +398,14 @@ def test_many_rows_many_sequences():
     w = wl.random_case(2840, B=700, Hq=4, Hkv=1, max_len=60, q_len=12)
     run(w, softcap=6.0, window=20)
     run(w, mask=random_trees(np.random.default_rng(8), 700, 12))
+    # whole units, several to a CTA, some of them empty; then one that is too long
+    g = np.random.default_rng(2)
+    lens = g.integers(0, 500, size=300)
+    lens[::7] = 0
+    for last in (500, 700):
+        lens[-1] = last
+        w = wl.random_case(2841, B=300, Hq=8, Hkv=2, lens=lens, q_len=6)
+        run(w, mask=random_trees(np.random.default_rng(8), 300, 6), slopes=slopes_of(8))
 
 
 @pytest.mark.parametrize("q_len", [1, 40])
