@@ -19,9 +19,11 @@
 // (sequence, kv head, column part) may move in ascending chunks: a chunk's
 // sources lie at or above its first destination, and nothing later reads what
 // an earlier chunk overwrote, but a chunk has to be read in full before it is
-// written, and before any later chunk is. One block walks one column part;
-// the next chunk's loads are in flight while this one is stored. Into other
-// pages there is no such order and the rows are cut into segments as well.
+// written, and before any later chunk is. One block walks one column part, or
+// with few of them a cluster of up to 8 (7 sequences of 25k-55k tokens, 2 kv
+// heads: 200 us with one block, 114 so); the next chunk's loads are in flight while this
+// one is stored. Into other pages there is no such order and the rows are cut
+// into segments as well.
 #include "kv_move.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -48,8 +50,8 @@ struct EvictParams {
   int w_tokens, Hkv, budget, sink, recent;
   int cluster;    // CTAs per row of the select launch
   // move launch: column parts of K (then of V) of `part` chunks, segments of
-  // kSegment rows (out of place; 1 in place)
-  int part, k_parts, parts, segments;
+  // kSegment rows (out of place; 1 in place), CTAs that share a part (in place)
+  int part, k_parts, parts, segments, move_cluster;
 };
 
 __device__ __forceinline__ bool evict_len_ok(const EvictParams& p, int L) {
@@ -374,39 +376,44 @@ constexpr int kMoveThreads = 256;
 constexpr int kUnroll = 4;       // chunks of 16 bytes per thread and step
 constexpr int kSegment = 1024;   // rows whose places are looked up together
 
-// Column part q of a row: chunks [c0, c0 + part) of K or V.
+// Column part q of a row: chunks [c0, c0 + part) of K or V. In place the row's
+// cluster of move_cluster CTAs takes the kept rows in steps, each CTA its share of
+// a step; the step after is loaded before the barrier that lets this one be
+// stored.
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
 evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ int64_t s_src[kSegment], s_dst[kSegment];  // row starts in chunks; -1: no move
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int CS = IN_PLACE ? p.move_cluster : 1, rank = IN_PLACE ? int(blockIdx.x) % CS : 0;
   const int seg = IN_PLACE ? 0 : int(blockIdx.x) / p.parts;
-  const int q = IN_PLACE ? int(blockIdx.x) : int(blockIdx.x) % p.parts;
+  const int q = IN_PLACE ? int(blockIdx.x) / CS : int(blockIdx.x) % p.parts;
   const bool is_v = q >= p.k_parts;
   const int width = is_v ? p.pools.cv : p.pools.ck;
   const int col = (is_v ? q - p.k_parts : q) * p.part + tid % p.part;
   uint4* pool = is_v ? p.pools.v : p.pools.k;
   const int32_t* kept = p.kept + (int64_t(b) * p.Hkv + h) * p.budget;
-  if (blockIdx.x == 0 && h == 0 && tid == 0) {
-    const int L = p.seq_lens[b];
-    p.new_lens[b] = evict_len_ok(p, L) ? min(L, p.budget) : L;
-  }
-  const int step_rows = kMoveThreads / p.part * kUnroll;  // rows of one step of the block
+  const int L = p.seq_lens[b];
+  const bool ok = evict_len_ok(p, L);
+  if (blockIdx.x == 0 && h == 0 && tid == 0) p.new_lens[b] = ok ? min(L, p.budget) : L;
+  // (the whole cluster takes the same way out)
+  if (!ok || (IN_PLACE && L <= p.budget)) return;
+  const int step_rows = kMoveThreads / p.part * kUnroll;  // rows of a CTA in one step
   const int32_t* sbt = p.block_table + int64_t(b) * p.bt_stride;
   const int32_t* dbt = p.dst_table + int64_t(b) * p.dst_stride;
   bool bad = false;
   const int first = seg * kSegment;
-  const int last = IN_PLACE ? p.budget : min(p.budget, first + kSegment);
-  for (int base = first; base < last; base += kSegment) {
-    const int rows = min(kSegment, last - base);
-    bool more = false;  // some row of the segment is kept
-    for (int r = tid; r < rows; r += kMoveThreads) {
-      const int j = base + r, t = kept[j];
+  const int last = IN_PLACE ? p.budget : min(min(p.budget, L), first + kSegment);
+  for (int base = first; base < last; base += CS * kSegment) {
+    // the CTA's row r of this round is row `at(r)` of the kept ones
+    auto at = [&](int r) { return base + (r / step_rows * CS + rank) * step_rows + r % step_rows; };
+    for (int r = tid; r < kSegment; r += kMoveThreads) {
+      const int j = at(r);
       int64_t src = -1, dst = -1;
-      if (t >= 0) {
-        more = true;
+      if (j < last) {
+        const int t = kept[j];
         if (!IN_PLACE || t != j) {
           const int ps = __ldg(sbt + t / p.pools.page_size);
           const int pd = __ldg(dbt + j / p.pools.page_size);
@@ -421,32 +428,56 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
       s_src[r] = src;
       s_dst[r] = dst;
     }
-    if (!__syncthreads_or(more)) break;  // kept entries end before this segment
+    __syncthreads();
     // steps of step_rows rows: load the next step before storing this one
     uint4 cur[kUnroll], nxt[kUnroll];
     auto load = [&](int r0, uint4 (&v)[kUnroll]) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int r = r0 + u * (kMoveThreads / p.part) + tid / p.part;
-        if (r < rows && col < width && s_src[r] >= 0) v[u] = pool[s_src[r] + col];
+        if (r < kSegment && col < width && s_src[r] >= 0) v[u] = pool[s_src[r] + col];
       }
     };
+    const int steps = min(kSegment / step_rows,
+                          (last - base + CS * step_rows - 1) / (CS * step_rows));
     load(0, cur);
-    for (int r0 = 0; r0 < rows; r0 += step_rows) {
+    for (int i = 0; i < steps; ++i) {
+      const int r0 = i * step_rows;
       load(r0 + step_rows, nxt);
-      if (IN_PLACE) __syncthreads();  // this step's rows are read by every thread
+      if (IN_PLACE) {  // this step's rows are read by every thread
+        if (CS > 1) cluster_sync();
+        else __syncthreads();
+      }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int r = r0 + u * (kMoveThreads / p.part) + tid / p.part;
-        if (r < rows && col < width && s_src[r] >= 0) pool[s_dst[r] + col] = cur[u];
+        if (col < width && s_src[r] >= 0) pool[s_dst[r] + col] = cur[u];
         cur[u] = nxt[u];
       }
     }
-    // the next segment's rows lie above every row stored here, and its places
-    // go into the same shared arrays
+    // the next round's rows lie above every row stored here, and its places go
+    // into the same shared arrays
     __syncthreads();
   }
   if (bad && q == 0 && p.err_flags) atomicOr(p.err_flags, 1u);
+}
+
+template <bool IN_PLACE>
+cudaError_t move_launch(const EvictParams& p, int B, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.parts * p.segments * p.move_cluster), unsigned(p.Hkv), unsigned(B));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(p.move_cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.move_cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel<IN_PLACE>, p);
 }
 
 cudaError_t evict_launch(EvictParams& p, int B, cudaStream_t stream) {
@@ -460,21 +491,20 @@ cudaError_t evict_launch(EvictParams& p, int B, cudaStream_t stream) {
   const bool in_place = p.dst_table == p.block_table;
   p.segments = in_place ? 1 : (p.budget + kSegment - 1) / kSegment;
   // A row's 16-byte chunks in parts of 16 (256 bytes); in place with few
-  // (sequence, kv head) pairs narrower parts, down to a 32-byte sector, so
-  // that there are two blocks per SM.
+  // (sequence, kv head) pairs clusters of CTAs, then narrower parts, down to a
+  // 32-byte sector, so that there are two blocks per SM.
   p.part = 16;
+  p.move_cluster = 1;
   auto count = [&] {
     p.k_parts = (p.pools.ck + p.part - 1) / p.part;
     p.parts = p.k_parts + (p.pools.cv + p.part - 1) / p.part;
-    return int64_t(p.parts) * p.Hkv * B;
+    return int64_t(p.parts) * p.Hkv * B * p.move_cluster;
   };
+  // (a cluster's step is at least 64 rows a CTA: with fewer rows kept its CTAs idle)
+  while (count() < 2 * sms && in_place && p.move_cluster < 8 && p.budget > 64 * p.move_cluster)
+    p.move_cluster *= 2;
   while (count() < 2 * sms && in_place && p.part > 2) p.part /= 2;
-  const dim3 grid(p.parts * p.segments, p.Hkv, B);
-  if (in_place)
-    evict_move_kernel<true><<<grid, kMoveThreads, 0, stream>>>(p);
-  else
-    evict_move_kernel<false><<<grid, kMoveThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return in_place ? move_launch<true>(p, B, stream) : move_launch<false>(p, B, stream);
 }
 
 }  // namespace
