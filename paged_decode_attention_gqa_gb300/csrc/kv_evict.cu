@@ -21,9 +21,9 @@
 // an earlier chunk overwrote, but a chunk has to be read in full before it is
 // written, and before any later chunk is. One block walks one column part, or
 // with few of them a cluster of up to 8 (7 sequences of 25k-55k tokens, 2 kv
-// heads: 200 us with one block, 114 so); the next chunk's loads are in flight while this
-// one is stored. Into other pages there is no such order and the rows are cut
-// into segments as well.
+// heads: 200 us with one block, 114 so); the next chunk's loads are in flight
+// while this one is stored. Into other pages there is no such order and the rows
+// are cut into segments as well.
 #include "kv_move.cuh"
 #include "kernels.h"
 #include "ptx.cuh"

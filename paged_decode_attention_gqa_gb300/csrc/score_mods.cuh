@@ -16,10 +16,16 @@ constexpr float kTanh0 = 0.999999949f, kTanh1 = -0.33332828f, kTanh2 = 0.1332507
                 kTanh3 = -0.0534516464f, kTanh4 = 0.0202797083f, kTanh5 = -0.00619432483f,
                 kTanh6 = 0.0010380251f;
 
-// tanh(y) to about 2e-7 of max(|tanh y|, ..): the polynomial up to |y| = 1, and
-// 1 - 2 / (e^(2y) + 1) beyond, where e^(2y) overflowing to infinity gives 1 and
-// underflowing to 0 gives -1. (That difference cancels near zero.) A score is c
-// * tanh(s / c) and enters an exponent: what counts is its absolute error.
+// tanh(y) for |y| > 1 as 1 - 2 / (e^(2y) + 1), where e^(2y) overflowing to
+// infinity gives 1 and underflowing to 0 gives -1.
+__device__ __forceinline__ float tanh_far(float y) {
+  const float e = ex2_approx(y * 2.8853900817779268f);
+  return 1.f - __fdividef(2.f, e + 1.f);
+}
+
+// tanh(y) to about 2e-7 of max(|tanh y|, ..): the polynomial up to |y| = 1 and
+// tanh_far beyond (its difference cancels near zero). A score is c * tanh(s / c)
+// and enters an exponent: what counts is its absolute error.
 __device__ __forceinline__ float cap_tanh(float y) {
   const float z = y * y;
   float t = fmaf(z, kTanh6, kTanh5);
@@ -28,9 +34,7 @@ __device__ __forceinline__ float cap_tanh(float y) {
   t = fmaf(t, z, kTanh2);
   t = fmaf(t, z, kTanh1);
   t = fmaf(t, z, kTanh0);
-  const float e = ex2_approx(y * 2.8853900817779268f);
-  const float far = 1.f - __fdividef(2.f, e + 1.f);
-  return fabsf(y) <= 1.f ? t * y : far;
+  return fabsf(y) <= 1.f ? t * y : tanh_far(y);
 }
 
 // Depth of a drafted token below the context's last position plus one: its
