@@ -9,8 +9,8 @@
 // 2800 cycles at this card's bandwidth, the products of 128 rows 1050, of 256
 // rows 2100.
 // Measured, 64 sequences of 512-4096 tokens with 32 heads on 8 kv heads: 16
-// drafted tokens (MT = 1) 125 us, 5.1 TB/s, bound by the load and the ends of
-// units; 64 (MT = 2) 166 us, 4.1 TB/s and 0.96 PFLOP/s, with a cap 211 us, bound
+// drafted tokens (MT = 1) 122 us, 5.2 TB/s, bound by the load and the ends of
+// units; 64 (MT = 2) 167 us, 4.1 TB/s and 0.95 PFLOP/s, with a cap 212 us, bound
 // by each stream's chain: 2150 cycles of softmax for 128 rows x 128 tokens, then
 // 1360 from its P to the next S (PV of a half tile 256, QK 512, the rest waits
 // and issue). A tile with masks takes 5000-6500.
@@ -203,8 +203,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
 // One contiguous run of tiles of one unit, as every role walks them: from the
 // newest, `last`, to the oldest. (A distance bias makes the newest scores the
 // largest; oldest first, the running maximum rose and O was rescaled at nearly
-// every tile: 64 drafted tokens, 64 sequences 293 us
-// against 243.)
+// every tile: 64 drafted tokens, 64 sequences 293 us against 243.)
 struct Piece {
   int b, kvh, blk, L, ntiles, last;
   bool partial;
