@@ -435,3 +435,38 @@ def test_windows_longer_than_any_sequence(q_len, window):
     run(w, window=window)
     mask = random_trees(np.random.default_rng(1), 4, q_len)
     run(w, window=window, mask=mask, weights=torch.zeros(4, 2, 300))
+
+
+@pytest.mark.parametrize("Hq,Hkv,q_len,ctas,msl,weights", [
+    (8, 2, 1, 0, 0, False), (8, 2, 1, 1000, 0, True), (32, 8, 2, 0, 400, True),
+    (32, 1, 1, 0, 0, True), (8, 2, 24, 0, 0, False), (8, 2, 24, 700, 0, False),
+    (32, 1, 24, 3, 0, False), (8, 2, 24, 0, 400, False), (32, 2, 20, 0, 0, True)])
+def test_explicit_workspace_of_the_exact_size(Hq, Hkv, q_len, ctas, msl, weights):
+    """The parameter structs and a workspace of the caller's: the bytes asked for
+    suffice, none past them are touched, and one byte less is refused."""
+    w = wl.random_case(2880, B=4, Hq=Hq, Hkv=Hkv, q_len=q_len, lens=[400, 130, 0, 257])
+    q, k, v, bt, sl = (x.cuda() for x in (w.q, w.k_pool, w.v_pool,
+                                          torch.from_numpy(w.block_table),
+                                          torch.from_numpy(w.seq_lens)))
+    mods = dict(softcap=6.0, alibi_slopes=slopes_of(Hq).cuda(), window=300,
+                tree_mask=random_trees(np.random.default_rng(3), 4, q_len).cuda())
+    wa = torch.zeros(4, Hkv, 400, device="cuda") if weights else None
+    wb = None if wa is None else wa.clone()
+    call = dict(page_size=16, scale=w.scale, num_ctas=ctas, max_seq_len=msl)
+    want = zl.decode_attn(q, k, v, bt, sl, weights=wa, **call, **mods)
+    out = torch.empty_like(want)
+    p = zl.make_params(q, k, v, bt, sl, out, Hkv=Hkv, D_v=128, **call)
+    m = zl.make_score_params(q, Hkv, weights=wb, **mods)
+    n = zl.workspace_size_ex(p, m)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    p.workspace, p.workspace_bytes = buf.data_ptr(), n
+    zl.call_ex(p, m)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    if weights:
+        assert torch.equal(wa, wb)
+    assert bool((buf[n:] == 0xA5).all())
+    if n:
+        p.workspace_bytes = n - 1
+        with pytest.raises(zl.ZlError):
+            zl.call_ex(p, m)
