@@ -407,7 +407,7 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
   const int first = seg * kSegment;
   const int last = IN_PLACE ? p.budget : min(min(p.budget, L), first + kSegment);
   for (int base = first; base < last; base += CS * kSegment) {
-    // the CTA's row r of this round is row `at(r)` of the kept ones
+    // the CTA's row r of this pass is row `at(r)` of the kept ones
     auto at = [&](int r) { return base + (r / step_rows * CS + rank) * step_rows + r % step_rows; };
     for (int r = tid; r < kSegment; r += kMoveThreads) {
       const int j = at(r);
@@ -455,7 +455,7 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
         cur[u] = nxt[u];
       }
     }
-    // the next round's rows lie above every row stored here, and its places go
+    // the next pass's rows lie above every row stored here, and its places go
     // into the same shared arrays
     __syncthreads();
   }
