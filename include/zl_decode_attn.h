@@ -337,7 +337,11 @@ zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
  *                          of the softmax weight of token t
  * for t < seq_lens[b] (elements at and after it stay as they are; with
  * weights_decay 0 the old values are not read). Rows zeroed for a bad page add
- * nothing. A sequence longer than weights_tokens counts as a bad length
+ * nothing. A token's sum therefore starts from what the element held when the
+ * token was cached: keep the elements at and behind seq_lens[b] at 0 (a new
+ * buffer, a row given to another sequence; zl_kv_evict clears what it leaves
+ * behind the new length if told to). A sequence longer than weights_tokens
+ * counts as a bad length
  * (ZL_DEVERR_BAD_SEQ_LEN: zeros, weights untouched). Rows of different
  * sequences and heads must not overlap.
  *
@@ -389,7 +393,16 @@ zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
  *     users. Pages past the new length are the caller's to free.
  *   - weights_out NULL: in place; otherwise element (b, kh, j) at
  *     b * weights_out_seq_stride + kh * weights_out_head_stride + j, and it
- *     must not overlap weights. Only j < new_lens[b] is written.
+ *     must not overlap weights. With weights_clear 0 only j < new_lens[b] is
+ *     written.
+ *   - weights_clear: a sum belongs to the token at its position, so what lies
+ *     behind the new length belongs to no token, and the next token cached
+ *     there would start from it. Nonzero clears it: in place (any nonzero
+ *     value) elements [new_lens[b], seq_lens[b]) become 0, in weights_out
+ *     elements [new_lens[b], weights_clear), where weights_clear is the length
+ *     of its rows (at least min(budget, weights_tokens)). A loop that goes on
+ *     accumulating in the same rows wants this. A struct of the size without
+ *     this field counts as 0.
  *   - Pools, strides, row widths, block table and v_pool = NULL as for
  *     zl_kv_append. budget >= 1, sink + recent <= budget.
  *   - Device data errors: seq_lens[b] < 0, above the block table's reach or
@@ -420,6 +433,7 @@ typedef struct {
   int32_t B, Hkv, D_k, D_v, page_size, num_pages;
   int32_t budget, sink, recent;
   uint32_t* err_flags; /* optional */
+  int32_t weights_clear;
 } zl_kv_evict_params;
 
 zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream);

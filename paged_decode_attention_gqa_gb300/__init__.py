@@ -163,6 +163,7 @@ class EvictParams(ctypes.Structure):
         ("sink", ctypes.c_int32),
         ("recent", ctypes.c_int32),
         ("err_flags", ctypes.c_void_p),
+        ("weights_clear", ctypes.c_int32),
     ]
 
 
@@ -394,7 +395,7 @@ def call_ex(params: Params, scores: ScoreParams, stream=None):
 # of such a call.)
 _PARAMS = struct.Struct("@N3P3qPq3P9ifPNPi2PIi2P0P")
 _SCORES = struct.Struct("@Nfi3P2qif0P")
-_EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iP0P")
+_EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iPi0P")
 _COMMIT = struct.Struct("@N2P3qPq2PqPP8iP0P")
 for _s, _c in ((_PARAMS, Params), (_SCORES, ScoreParams), (_EVICT, EvictParams),
                (_COMMIT, CommitParams)):
@@ -661,7 +662,8 @@ def decode_attn(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, o
     drafted tree, bit j of row i set where token i sees drafted token j (see
     tree_mask()). weights fp32 [B, Hkv, tokens]: each cached token's softmax
     weight, summed over the query tokens and the heads of its kv head, is added
-    to weights_decay times what it holds.
+    to weights_decay times what it holds. A new token's sum starts from what its
+    element held, so keep the elements behind seq_lens at 0.
     """
     if (softcap or window or alibi_slopes is not None or tree_mask is not None
             or weights is not None):
@@ -765,7 +767,7 @@ def tree_mask(parents) -> torch.Tensor:
 
 def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budget, sink=0,
              recent=0, new_lens=None, kept=None, weights_out=None, dst_block_table=None,
-             layout="NHD", err_flags=None, stream=None):
+             clear_weights=False, layout="NHD", err_flags=None, stream=None):
     """Hold every (sequence, kv head) to ``budget`` cached tokens (zl_kv_evict).
 
     weights [B, Hkv, tokens] fp32, as decode_attn accumulates them: a sequence
@@ -773,8 +775,11 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
     and the ones between with the largest weights, in order; their K, V and
     weights move to the front. In place, or to the pages of dst_block_table
     (weights to weights_out when given). v_pool None: a latent-only pool.
-    Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]: the kept
-    positions, then -1).
+    clear_weights: the weights behind the new length, which belong to no token
+    any more, become 0 (in place up to the old length, in weights_out up to the
+    end of its rows); otherwise they stay, and the next tokens cached there
+    start from them. Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]:
+    the kept positions, then -1).
     """
     if weights is None:
         raise ValueError("weights is required")
@@ -782,10 +787,12 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
      err) = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
     w, w_seq, w_head, tokens = _token_rows(weights, "weights", B, Hkv, index)
     wo = wo_seq = wo_head = dst = dst_stride = 0
+    clear = tokens if clear_weights else 0
     if weights_out is not None:
         wo, wo_seq, wo_head, out_tokens = _token_rows(weights_out, "weights_out", B, Hkv, index)
         if out_tokens < min(budget, tokens):
             raise ValueError("weights_out is shorter than what the budget may leave")
+        clear = out_tokens if clear_weights else 0
     if dst_block_table is not None:
         if dst_block_table.dim() != 2:
             raise ValueError("dst_block_table must be 2-D")
@@ -813,7 +820,7 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
     status = _raw_fn("zl_kv_evict", 1)(_pack(
         _EVICT, _EVICT.size, k_at, v_at, ps, ts, hs, bt_at, bt_stride, dst, dst_stride, sl_at,
         new_at, kept_at, w, w_seq, w_head, wo, wo_seq, wo_head, tokens, B, Hkv, shape[3], width_v,
-        page_size, shape[0], budget, sink, recent, err), on)
+        page_size, shape[0], budget, sink, recent, err, clear), on)
     if status != OK:
         _check(status, "zl_kv_evict")
     return new_lens, kept

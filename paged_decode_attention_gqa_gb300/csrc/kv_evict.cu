@@ -28,6 +28,7 @@
 #include "kernels.h"
 #include "ptx.cuh"
 
+#include <cstddef>
 #include <cstring>
 
 namespace zl {
@@ -48,6 +49,9 @@ struct EvictParams {
   int64_t wo_seq, wo_head;
   uint32_t* err_flags;
   int w_tokens, Hkv, budget, sink, recent;
+  // 0: the weights behind the new length stay as they are; else they become 0,
+  // in place up to the old length, in weights_out up to this many
+  int w_clear;
   int cluster;    // CTAs per row of the select launch
   // move launch: column parts of K (then of V) of `part` chunks, segments of
   // kSegment rows (out of place; 1 in place), CTAs that share a part (in place)
@@ -115,7 +119,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   if (L <= p.budget) {
     for (int j = rank * T + tid; j < p.budget; j += CS * T) kept[j] = j < L ? j : -1;
     if (wo != w)
-      for (int j = rank * T + tid; j < L; j += CS * T) wo[j] = w[j];
+      for (int j = rank * T + tid; j < max(L, p.w_clear); j += CS * T) wo[j] = j < L ? w[j] : 0.f;
     return;
   }
   const int M = L - p.sink - p.recent;                 // candidates
@@ -309,6 +313,11 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   // below every recent one that is still to be read). Where the parts do not
   // fit the caches, one CTA moves the whole row that way, by the list.
   sync();  // also: no CTA leaves while another reads its counts
+  // Weights behind the new length, if they are to become 0. In place the last
+  // CTA still reads from [keep_from, L): those it clears itself, at the end.
+  const int keep_from = max(p.budget, wo != w ? p.w_clear : CACHED ? L - p.recent : p.budget);
+  if (p.w_clear)
+    for (int j = p.budget + rank * T + tid; j < keep_from; j += CS * T) wo[j] = 0.f;
   if (rank != CS - 1) return;
   if (CACHED && wo != w)
     for (int j = tid; j < p.sink; j += T) wo[j] = w[j];
@@ -319,6 +328,8 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
     __syncthreads();
     if (j < p.budget) wo[j] = x;
   }
+  if (p.w_clear && wo == w)  // (every thread is past its reads of [keep_from, L))
+    for (int j = keep_from + tid; j < L; j += T) wo[j] = 0.f;
 }
 
 template <int T, int kRun, int kBlocks, bool CACHED>
@@ -510,8 +521,11 @@ cudaError_t evict_launch(EvictParams& p, int B, cudaStream_t stream) {
 }  // namespace
 }  // namespace zl
 
-extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* a, zl_stream_t stream) {
-  if (!a || a->struct_size != sizeof(zl_kv_evict_params)) return ZL_ERR_INVALID_ARG;
+extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream) {
+  zl_kv_evict_params given;
+  if (!zl::take_params(params, offsetof(zl_kv_evict_params, weights_clear), &given))
+    return ZL_ERR_INVALID_ARG;
+  const zl_kv_evict_params* a = &given;
   zl::EvictParams p;
   std::memset(&p, 0, sizeof(p));
   const zl_status st = zl::move_pools(a, &p.pools);
@@ -526,7 +540,10 @@ extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* a, zl_stream_t stream
   if (!zl::rows_distinct(a->B, a->Hkv, a->weights_seq_stride, a->weights_head_stride,
                          a->weights_tokens))
     return ZL_ERR_INVALID_ARG;
-  const int64_t out_tokens = a->budget < a->weights_tokens ? a->budget : a->weights_tokens;
+  int64_t out_tokens = a->budget < a->weights_tokens ? a->budget : a->weights_tokens;
+  if (a->weights_clear < 0 || (a->weights_out && a->weights_clear && a->weights_clear < out_tokens))
+    return ZL_ERR_INVALID_ARG;
+  if (a->weights_clear > out_tokens) out_tokens = a->weights_clear;
   if (a->weights_out && !zl::rows_distinct(a->B, a->Hkv, a->weights_out_seq_stride,
                                            a->weights_out_head_stride, out_tokens))
     return ZL_ERR_INVALID_ARG;
@@ -552,6 +569,7 @@ extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* a, zl_stream_t stream
   p.budget = a->budget;
   p.sink = a->sink;
   p.recent = a->recent;
+  p.w_clear = a->weights_clear;
   const cudaError_t e = zl::evict_launch(p, a->B, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstring>
+
 namespace zl {
 
 // K and V pools; row (page, slot, head) starts at page * page_stride + slot *
@@ -30,6 +32,16 @@ inline bool aligned_to(const void* p, size_t a) {
 inline bool overlaps(const int32_t* a, const int32_t* b, int64_t n) {
   const intptr_t d = reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b);
   return d < n * 4 && -d < n * 4;
+}
+
+// A caller's parameter struct: of this header's size, or of the size it had
+// before the fields after `first_size` bytes came (they are zero then).
+template <class Params>
+bool take_params(const Params* a, size_t first_size, Params* out) {
+  if (!a || (a->struct_size != sizeof(Params) && a->struct_size != first_size)) return false;
+  std::memset(out, 0, sizeof(Params));
+  std::memcpy(out, a, a->struct_size);
+  return true;
 }
 
 // The checks and conversion of the pool fields (the same names in every

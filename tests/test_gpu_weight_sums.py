@@ -1,0 +1,198 @@
+"""A cached token's sum of weights stays its own through the decode loop: what
+the operators that move tokens leave behind the new length is no new token's
+start. The references carry the sums by token, not by position."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import paged_decode_attention_gqa_gb300 as zl
+from paged_decode_attention_gqa_gb300 import workloads as wl
+from plain_ops import attention, check, evict, f64
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def u16(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def as_f64(x):
+    return torch.from_numpy(x.view(np.int16)).view(BF16).double().numpy()
+
+
+class Sums:
+    """Sums of weights by token: the cache of every (sequence, kv head) is a list
+    of tokens in the order of their positions."""
+
+    def __init__(self, B, Hkv, lens):
+        self.B, self.H, self.n = B, Hkv, 0
+        self.val, self.tol = {}, {}
+        self.cache = [[[self.new() for _ in range(int(lens[b]))] for _ in range(Hkv)]
+                      for b in range(B)]
+
+    def new(self):
+        self.n += 1
+        self.val[self.n] = self.tol[self.n] = 0.0
+        return self.n
+
+    def append(self, n):
+        for b in range(self.B):
+            for h in range(self.H):
+                self.cache[b][h] += [self.new() for _ in range(n)]
+
+    def add(self, w, tol, decay):
+        """w, tol [B, Hkv, T]: one call's weights by position."""
+        for b in range(self.B):
+            for h in range(self.H):
+                for t, tok in enumerate(self.cache[b][h]):
+                    v = decay * self.val[tok] + w[b, h, t]
+                    # the old sum's error, this call's, and the fma's rounding
+                    self.tol[tok] = decay * self.tol[tok] + tol[b, h, t] + 2.0 ** -22 * abs(v)
+                    self.val[tok] = v
+
+    def keep(self, b, h, positions):
+        self.cache[b][h] = [self.cache[b][h][int(t)] for t in positions]
+
+    def rows(self, T):
+        """By position, zeros behind the length."""
+        v, tol = np.zeros((self.B, self.H, T)), np.zeros((self.B, self.H, T))
+        for b in range(self.B):
+            for h in range(self.H):
+                for t, tok in enumerate(self.cache[b][h]):
+                    v[b, h, t], tol[b, h, t] = self.val[tok], self.tol[tok]
+        return v, tol
+
+
+@pytest.mark.parametrize("swap", [False, True])
+def test_decode_and_evict_loop(swap):
+    """A token per step, its weights, then back to the budget. swap: the kept sums
+    go to the other of two buffers each time."""
+    B, Hq, Hkv, P, D, T, budget, steps = 2, 8, 2, 16, 128, 80, 48, 30
+    lens = np.array([44, 48], dtype=np.int32)
+    w = wl.random_case(3400, B=B, Hq=Hq, Hkv=Hkv, lens=[T, T], poison=False)
+    gt = torch.Generator().manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, generator=gt).to(BF16)  # noqa: E731
+    k, v, bt = w.k_pool.cuda(), w.v_pool.cuda(), torch.from_numpy(w.block_table).cuda()
+    kr, vr = u16(k).copy(), u16(v).copy()
+    bufs = [torch.zeros(B, Hkv, T, device="cuda") for _ in range(2)]
+    if swap:
+        bufs[1].fill_(7.0)  # what an earlier use of the buffer left
+    sums = Sums(B, Hkv, lens)
+    sl, slr = torch.from_numpy(lens).cuda(), lens.copy()
+    for step in range(steps):
+        wt = bufs[step % 2 if swap else 0]
+        sl, slr = sl + 1, slr + 1
+        sums.append(1)
+        q, kn, vn = rnd(B, 1, Hq, D), rnd(B, 1, Hkv, D), rnd(B, 1, Hkv, D)
+        zl.decode_attn(q.cuda(), k, v, bt, sl, page_size=P, scale=w.scale, weights=wt,
+                       weights_decay=0.9, k_new=kn.cuda(), v_new=vn.cuda())
+        for b in range(B):
+            t = slr[b] - 1
+            kr[w.block_table[b, t // P], t % P] = u16(kn)[b, 0]
+            vr[w.block_table[b, t // P], t % P] = u16(vn)[b, 0]
+        ref = attention(f64(q), as_f64(kr), as_f64(vr), w.block_table, slr, scale=w.scale,
+                        tokens=T)
+        sums.add(ref.weights, ref.weights_tol, 0.9)
+        check(f64(wt), *sums.rows(T), f"weights {step}")
+        before = wt.cpu().numpy()
+        out = bufs[(step + 1) % 2] if swap else None
+        sl, kept = zl.kv_evict(k, v, bt, sl, wt, page_size=P, budget=budget, sink=2, recent=6,
+                               weights_out=out, clear_weights=True)
+        kr, vr, _, keptr, slr, _ = evict(kr, vr, before, w.block_table, slr, page_size=P,
+                                         budget=budget, sink=2, recent=6, num_pages=w.num_pages)
+        assert np.array_equal(kept.cpu().numpy(), keptr)
+        for b in range(B):
+            for h in range(Hkv):
+                sums.keep(b, h, keptr[b, h][keptr[b, h] >= 0])
+        check(f64(wt if out is None else out), *sums.rows(T), f"kept weights {step}")
+
+
+def run_clear(w, wt, *, out_tokens=None, dst=None, **kw):
+    """kv_evict with clear_weights against the plain form, whose rows are then
+    cleared behind the new length."""
+    k, v = w.k_pool.cuda(), w.v_pool.cuda()
+    bt, sl = torch.from_numpy(w.block_table).cuda(), torch.from_numpy(w.seq_lens).cuda()
+    wd = wt.cuda()
+    out = None if out_tokens is None else torch.full((w.B, w.Hkv, out_tokens), 5.0)
+    od = None if out is None else out.cuda()
+    new, kept = zl.kv_evict(k, v, bt, sl, wd, page_size=w.page_size, clear_weights=True,
+                            weights_out=od, dst_block_table=None if dst is None
+                            else torch.from_numpy(dst).cuda(), **kw)
+    kr, vr, wr, keptr, newr, _ = evict(
+        u16(w.k_pool), u16(w.v_pool), wt.numpy(), w.block_table, w.seq_lens,
+        page_size=w.page_size, num_pages=w.num_pages, dst_table=dst,
+        weights_out=None if out is None else out.numpy(), sink=kw.get("sink", 0),
+        recent=kw.get("recent", 0), budget=kw["budget"])
+    for b in range(w.B):
+        wr[b, :, newr[b]:w.seq_lens[b] if out is None else out_tokens] = 0
+    assert np.array_equal(kept.cpu().numpy(), keptr)
+    assert np.array_equal(new.cpu().numpy(), newr)
+    assert np.array_equal((wd if od is None else od).cpu().numpy(), wr)
+    if od is not None:
+        assert torch.equal(wd.cpu(), wt)
+    assert np.array_equal(u16(k), kr) and np.array_equal(u16(v), vr)
+
+
+@pytest.mark.parametrize("out_tokens", [None, 64, 320])
+@pytest.mark.parametrize("budget,sink,recent", [(64, 0, 0), (64, 4, 16), (50, 7, 43), (1, 0, 0),
+                                                (33, 0, 33), (33, 33, 0), (60, 0, 60),
+                                                (299, 1, 2)])
+def test_clear_behind_the_new_length(out_tokens, budget, sink, recent):
+    if out_tokens == 64 and budget > 64:
+        pytest.skip("the rows would not hold the budget")
+    w = wl.random_case(3410, B=6, Hq=8, Hkv=2, lens=[300, 1, 0, 64, 65, 150])
+    wt = torch.rand(6, 2, 310, generator=torch.Generator().manual_seed(budget)) + 0.5
+    run_clear(w, wt, out_tokens=out_tokens, budget=budget, sink=sink, recent=recent)
+
+
+@pytest.mark.parametrize("L,T,budget,recent", [(20000, 20000, 9001, 8000), (20000, 20011, 500, 0),
+                                               (131073, 131080, 4097, 1000)])
+def test_clear_long_rows(L, T, budget, recent):
+    """Rows over a cluster of CTAs, and rows that no cluster holds."""
+    w = wl.random_case(3420, B=2, Hq=1, Hkv=1, page_size=128, lens=[L, 40], poison=False,
+                       pool_factor=3.0)
+    wt = torch.rand(2, 1, T, generator=torch.Generator().manual_seed(L)) + 0.5
+    run_clear(w, wt, budget=budget, sink=3, recent=recent)
+    run_clear(w, wt, budget=budget, sink=3, recent=recent, out_tokens=T)
+    free = np.setdiff1d(np.arange(w.num_pages), w.block_table[w.block_table >= 0])
+    n = (budget + 127) // 128
+    run_clear(w, wt, budget=budget, recent=recent, dst=free[:2 * n].reshape(2, n).astype(np.int32))
+
+
+def test_clear_leaves_bad_sequences_alone():
+    w = wl.random_case(3430, B=3, Hq=8, Hkv=2, lens=[100, 90, 80])
+    sl = torch.tensor([-1, 101, 80], dtype=torch.int32).cuda()
+    wt = torch.rand(3, 2, 100, generator=torch.Generator().manual_seed(1)) + 0.5
+    wd = wt.cuda()
+    zl.kv_evict(w.k_pool.cuda(), w.v_pool.cuda(), torch.from_numpy(w.block_table).cuda(), sl, wd,
+                page_size=16, budget=32, clear_weights=True)
+    assert torch.equal(wd[:2].cpu(), wt[:2])
+    assert not wd[2, :, 32:80].any() and torch.equal(wd[2, :, 80:].cpu(), wt[2, :, 80:])
+
+
+def test_evict_struct_without_the_last_field():
+    """A caller built before weights_clear was there: nothing is cleared."""
+    w = wl.random_case(3440, B=1, Hq=2, Hkv=1, lens=[40])
+    k, v, bt, sl = (x.cuda() for x in (w.k_pool, w.v_pool, torch.from_numpy(w.block_table),
+                                       torch.from_numpy(w.seq_lens)))
+    wt = torch.ones(1, 1, 40, device="cuda")
+    new = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(1, 1, 8, dtype=torch.int32, device="cuda")
+    p = zl.EvictParams()
+    p.struct_size = zl.EvictParams.weights_clear.offset
+    p.k_pool, p.v_pool = k.data_ptr(), v.data_ptr()
+    p.page_stride, p.token_stride, p.head_stride = k.stride(0), k.stride(1), k.stride(2)
+    p.block_table, p.block_table_stride, p.seq_lens = bt.data_ptr(), bt.shape[1], sl.data_ptr()
+    p.new_lens, p.kept, p.weights = new.data_ptr(), kept.data_ptr(), wt.data_ptr()
+    p.weights_tokens = p.weights_seq_stride = p.weights_head_stride = 40
+    p.B, p.Hkv, p.D_k, p.D_v, p.page_size, p.num_pages = 1, 1, 128, 128, 16, w.num_pages
+    p.budget, p.recent, p.weights_clear = 8, 8, 1  # the last lies outside the given size
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert zl.lib().zl_kv_evict(ctypes.byref(p), stream) == zl.OK
+    torch.cuda.synchronize()
+    assert new.tolist() == [8] and kept.tolist() == [[list(range(32, 40))]]
+    assert bool((wt == 1).all())
