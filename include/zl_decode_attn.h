@@ -339,9 +339,9 @@ zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
  * weights_decay 0 the old values are not read). Rows zeroed for a bad page add
  * nothing. A token's sum therefore starts from what the element held when the
  * token was cached: keep the elements at and behind seq_lens[b] at 0 (a new
- * buffer, a row given to another sequence; zl_kv_evict clears what it leaves
- * behind the new length if told to). A sequence longer than weights_tokens
- * counts as a bad length
+ * buffer, a row given to another sequence; zl_kv_commit and zl_kv_evict clear
+ * what they leave behind the new length if told to). A sequence longer than
+ * weights_tokens counts as a bad length
  * (ZL_DEVERR_BAD_SEQ_LEN: zeros, weights untouched). Rows of different
  * sequences and heads must not overlap.
  *
@@ -455,6 +455,14 @@ zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream);
  *     (ZL_DEVERR_BAD_PATH): nothing of the sequence moves and new_lens[b] =
  *     seq_lens[b]. A row whose source or destination page id is outside [0,
  *     num_pages) does not move (ZL_DEVERR_BAD_PAGE).
+ *   - weights, optional, fp32 with strides as in zl_score_params: the sums of
+ *     weights move with their tokens in every kv head (path[j]'s to position
+ *     seq_lens[b] - q_len + j), and elements [new_lens[b], seq_lens[b]), the
+ *     rejected tokens', become 0: the tokens cached there next start from 0. A
+ *     sequence longer than weights_tokens is a bad length. Sums move whatever
+ *     the pages are. (What the rejected tokens' own query rows added to the
+ *     sums of the tokens before them stays.) A struct of the size without these
+ *     fields has no weights.
  *   - Rows are copies: bit-exact. new_lens must not overlap seq_lens.
  */
 typedef struct {
@@ -472,6 +480,9 @@ typedef struct {
   int32_t path_len; /* entries of a path row */
   int32_t B, q_len, Hkv, D_k, D_v, page_size, num_pages;
   uint32_t* err_flags; /* optional */
+  float* weights; /* or NULL */
+  int64_t weights_seq_stride, weights_head_stride;
+  int32_t weights_tokens;
 } zl_kv_commit_params;
 
 zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t stream);

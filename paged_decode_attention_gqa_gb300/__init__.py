@@ -192,6 +192,10 @@ class CommitParams(ctypes.Structure):
         ("page_size", ctypes.c_int32),
         ("num_pages", ctypes.c_int32),
         ("err_flags", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("weights_seq_stride", ctypes.c_int64),
+        ("weights_head_stride", ctypes.c_int64),
+        ("weights_tokens", ctypes.c_int32),
     ]
 
 
@@ -396,7 +400,7 @@ def call_ex(params: Params, scores: ScoreParams, stream=None):
 _PARAMS = struct.Struct("@N3P3qPq3P9ifPNPi2PIi2P0P")
 _SCORES = struct.Struct("@Nfi3P2qif0P")
 _EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iPi0P")
-_COMMIT = struct.Struct("@N2P3qPq2PqPP8iP0P")
+_COMMIT = struct.Struct("@N2P3qPq2PqPP8i2P2qi0P")
 for _s, _c in ((_PARAMS, Params), (_SCORES, ScoreParams), (_EVICT, EvictParams),
                (_COMMIT, CommitParams)):
     assert _s.size == ctypes.sizeof(_c), _c.__name__
@@ -827,13 +831,16 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
 
 
 def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_size, q_len,
-              new_lens=None, layout="NHD", err_flags=None, stream=None):
+              new_lens=None, weights=None, layout="NHD", err_flags=None, stream=None):
     """Move the accepted path of a drafted tree behind the context (zl_kv_commit).
 
     The last q_len of each sequence's seq_lens[b] tokens are the drafted tree;
     its tokens path[b, :accepted[b]] (path int32 [B, n], accepted int32 [B])
     become the tokens after the context, in place. v_pool None: a latent-only
-    pool. Returns new_lens int32 [B] (context plus accepted).
+    pool. weights [B, Hkv, tokens] fp32, as decode_attn accumulates them: the
+    accepted tokens' sums move with them, the rejected ones' become 0 (without
+    it they stay where the drafted tokens were). Returns new_lens int32 [B]
+    (context plus accepted).
     """
     (index, B, Hkv, shape, width_v, ps, ts, hs, k_at, v_at, bt_at, bt_stride, sl_at,
      err) = _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags)
@@ -845,6 +852,9 @@ def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_siz
     if n > 1 and one != 1:
         raise ValueError("path rows must be contiguous")
     acc = _expect(accepted, "accepted", _I32, (B,), index)
+    w = w_seq = w_head = tokens = 0
+    if weights is not None:
+        w, w_seq, w_head, tokens = _token_rows(weights, "weights", B, Hkv, index)
     new_at = 0
     if new_lens is not None:
         new_at = _expect(new_lens, "new_lens", _I32, (B,), index)
@@ -856,7 +866,7 @@ def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_siz
     status = _raw_fn("zl_kv_commit", 1)(_pack(
         _COMMIT, _COMMIT.size, k_at, v_at, ps, ts, hs, bt_at, bt_stride, sl_at, path_at,
         path_stride if B > 1 else n, acc, new_at, n, B, q_len, Hkv, shape[3], width_v, page_size,
-        shape[0], err), on)
+        shape[0], err, w, w_seq, w_head, tokens), on)
     if status != OK:
         _check(status, "zl_kv_commit")
     return new_lens

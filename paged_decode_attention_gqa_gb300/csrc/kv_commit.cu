@@ -4,13 +4,15 @@
 //
 // One block per (sequence, kv head, 256-byte column part of K or V): at most
 // 128 rows of 256 bytes, 8 chunks of 16 bytes per thread, all read before any
-// is written, so any path is safe in place. The whole call is a few hundred
+// is written, so any path is safe in place. The first block of a (sequence, kv
+// head) also moves the tokens' sums of weights, the same way. The whole call is a few hundred
 // KB: it is bound by the chain of dependent reads (length, path, page, row),
 // which all blocks walk at once.
 #include "kv_move.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
+#include <cstddef>
 #include <cstring>
 
 namespace zl {
@@ -33,6 +35,9 @@ struct CommitParams {
   int32_t* new_lens;
   uint32_t* err_flags;
   int q_len, max_accepted, k_parts;
+  float* weights;  // [B][Hkv][w_tokens], strides in elements; nullptr: none
+  int64_t w_seq, w_head;
+  int w_tokens;
 };
 
 __global__ void __launch_bounds__(kThreads)
@@ -47,7 +52,8 @@ kv_commit_kernel(const __grid_constant__ CommitParams p) {
   const bool first = blockIdx.x == 0 && h == 0;  // reports for the sequence
 
   const int L = __ldg(p.seq_lens + b), n = __ldg(p.accepted + b);
-  const bool len_ok = L >= p.q_len && int64_t(L) <= p.bt_stride * p.pools.page_size;
+  const bool len_ok = L >= p.q_len && int64_t(L) <= p.bt_stride * p.pools.page_size &&
+                      (!p.weights || L <= p.w_tokens);
   bool path_ok = n >= 0 && n <= p.max_accepted;
   int src[kPasses];
 #pragma unroll
@@ -68,6 +74,12 @@ kv_commit_kernel(const __grid_constant__ CommitParams p) {
   const int ctx = L - p.q_len;
   if (first && tid == 0) p.new_lens[b] = ctx + n;
   const int32_t* bt = p.block_table + int64_t(b) * p.bt_stride;
+  // sums of the drafted tokens, from ctx on
+  float* w = p.weights && blockIdx.x == 0
+                 ? p.weights + int64_t(b) * p.w_seq + int64_t(h) * p.w_head + ctx
+                 : nullptr;
+  float sum = 0.f;
+  if (w && tid < n) sum = w[__ldg(p.path + int64_t(b) * p.path_stride + tid)];
   uint4 data[kPasses];
   uint4* dst[kPasses];
   bool bad = false;
@@ -85,7 +97,8 @@ kv_commit_kernel(const __grid_constant__ CommitParams p) {
     data[i] = pool[p.pools.row(ps, ts % p.pools.page_size, h) + col];
     dst[i] = pool + p.pools.row(pd, td % p.pools.page_size, h) + col;
   }
-  __syncthreads();  // every row of this part is read
+  __syncthreads();  // every row of this part is read, and every sum
+  if (w && tid < p.q_len) w[tid] = sum;  // 0 behind the accepted ones
 #pragma unroll
   for (int i = 0; i < kPasses; ++i)
     if (dst[i]) *dst[i] = data[i];
@@ -95,8 +108,11 @@ kv_commit_kernel(const __grid_constant__ CommitParams p) {
 }  // namespace
 }  // namespace zl
 
-extern "C" zl_status zl_kv_commit(const zl_kv_commit_params* a, zl_stream_t stream) {
-  if (!a || a->struct_size != sizeof(zl_kv_commit_params)) return ZL_ERR_INVALID_ARG;
+extern "C" zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t stream) {
+  zl_kv_commit_params given;
+  if (!zl::take_params(params, offsetof(zl_kv_commit_params, weights), &given))
+    return ZL_ERR_INVALID_ARG;
+  const zl_kv_commit_params* a = &given;
   zl::CommitParams p;
   std::memset(&p, 0, sizeof(p));
   const zl_status st = zl::move_pools(a, &p.pools);
@@ -104,6 +120,11 @@ extern "C" zl_status zl_kv_commit(const zl_kv_commit_params* a, zl_stream_t stre
   if (!a->path || !a->accepted || !zl::aligned_to(a->path, 4) || !zl::aligned_to(a->accepted, 4))
     return ZL_ERR_INVALID_ARG;
   if (a->q_len < 1 || a->path_len < 1 || a->path_stride < a->path_len)
+    return ZL_ERR_INVALID_ARG;
+  if (a->weights &&
+      (!zl::aligned_to(a->weights, 4) || a->weights_tokens < 1 ||
+       !zl::rows_distinct(a->B, a->Hkv, a->weights_seq_stride, a->weights_head_stride,
+                          a->weights_tokens)))
     return ZL_ERR_INVALID_ARG;
   if (a->q_len > zl::kMaxDrafted) return ZL_ERR_UNSUPPORTED;
   p.block_table = a->block_table;
@@ -115,6 +136,10 @@ extern "C" zl_status zl_kv_commit(const zl_kv_commit_params* a, zl_stream_t stre
   p.new_lens = a->new_lens;
   p.err_flags = a->err_flags;
   p.q_len = a->q_len;
+  p.weights = a->weights;
+  p.w_seq = a->weights_seq_stride;
+  p.w_head = a->weights_head_stride;
+  p.w_tokens = a->weights_tokens;
   p.max_accepted = a->path_len < a->q_len ? a->path_len : a->q_len;
   p.k_parts = (p.pools.ck + zl::kPart - 1) / zl::kPart;
   const int parts = p.k_parts + (p.pools.cv + zl::kPart - 1) / zl::kPart;

@@ -9,7 +9,7 @@ import torch
 
 import paged_decode_attention_gqa_gb300 as zl
 from paged_decode_attention_gqa_gb300 import workloads as wl
-from plain_ops import attention, check, evict, f64
+from plain_ops import attention, check, commit, evict, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +196,116 @@ def test_evict_struct_without_the_last_field():
     torch.cuda.synchronize()
     assert new.tolist() == [8] and kept.tolist() == [[list(range(32, 40))]]
     assert bool((wt == 1).all())
+
+
+def run_commit(w, path, acc, q_len, wt, *, seq_lens=None, block_table=None):
+    """kv_commit with weights: the plain form for the pools, sums by hand."""
+    bt = w.block_table if block_table is None else block_table
+    sl = w.seq_lens if seq_lens is None else seq_lens
+    k, v = w.k_pool.cuda(), w.v_pool.cuda()
+    big = torch.full((w.B, w.Hkv + 1, wt.shape[2] + 9), 3.0, device="cuda")
+    view = big[:, :w.Hkv, 5:5 + wt.shape[2]]  # rows inside a larger buffer
+    view.copy_(wt)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = zl.kv_commit(k, v, torch.from_numpy(bt).cuda(), torch.from_numpy(sl).cuda(),
+                       torch.from_numpy(path).cuda(), torch.from_numpy(acc).cuda(),
+                       page_size=w.page_size, q_len=q_len, weights=view, err_flags=err)
+    long = sl > wt.shape[2]
+    slr = np.where(long, -1, sl).astype(np.int32)  # a bad length for the plain form
+    kr, vr, newr, errr = commit(u16(w.k_pool), u16(w.v_pool), bt, slr, path, acc,
+                                page_size=w.page_size, q_len=q_len, num_pages=w.num_pages)
+    newr = np.where(long, sl, newr)
+    want = wt.numpy().copy()
+    for b in range(w.B):
+        ctx, n = int(sl[b]) - q_len, int(newr[b]) - int(sl[b]) + q_len
+        if newr[b] == sl[b] and (slr[b] < q_len or n != acc[b]):
+            continue  # refused: nothing moves
+        want[b, :, ctx:ctx + n] = wt.numpy()[b][:, ctx + path[b, :n]]
+        want[b, :, ctx + n:sl[b]] = 0
+    assert int(err.item()) == errr
+    assert np.array_equal(new.cpu().numpy(), newr)
+    assert np.array_equal(view.cpu().numpy(), want)
+    big[:, :w.Hkv, 5:5 + wt.shape[2]] = 3.0
+    assert bool((big == 3.0).all())
+    assert np.array_equal(u16(k), kr) and np.array_equal(u16(v), vr)
+    return errr
+
+
+@pytest.mark.parametrize("q_len", [1, 2, 16, 17, 64, 128])
+def test_commit_moves_the_sums(q_len):
+    w = wl.random_case(3450 + q_len, B=6, Hq=8, Hkv=2, poison=False,
+                       lens=[q_len, q_len + 1, 300, 200, 130, 129])
+    wt = torch.rand(6, 2, 301, generator=torch.Generator().manual_seed(q_len)) + 0.5
+    g = np.random.default_rng(q_len)
+    path = g.integers(0, q_len, size=(6, q_len)).astype(np.int32)  # unsorted, with repeats
+    acc = g.integers(0, q_len, size=6, endpoint=True).astype(np.int32)
+    acc[0], acc[1] = q_len, 0
+    assert run_commit(w, path, acc, q_len, wt) == 0
+
+
+def test_commit_of_bad_sequences_leaves_their_sums():
+    w = wl.random_case(3460, B=6, Hq=8, Hkv=2, lens=[100, 90, 80, 120, 64, 110], poison=False)
+    path = np.tile(np.array([2, 5, 9], dtype=np.int32), (6, 1))
+    acc = np.array([3, -1, 3, 3, 3, 2], dtype=np.int32)
+    path[2, 1] = 12
+    sl, bt = w.seq_lens.copy(), w.block_table.copy()
+    sl[4] = 11
+    bt[5, 109 // 16] = -1                    # a row that does not move; its sum does
+    wt = torch.rand(6, 2, 115, generator=torch.Generator().manual_seed(2)) + 0.5
+    assert run_commit(w, path, acc, 12, wt, seq_lens=sl, block_table=bt) == 2 + 16 + 1
+
+
+def test_verify_commit_and_evict_loop():
+    """Drafted trees verified with weights, their paths committed, the cache back to
+    the budget: every token keeps its own sum."""
+    B, Hq, Hkv, q_len, P, D, T, budget = 2, 8, 2, 7, 16, 128, 80, 48
+    lens = np.array([44, 48], dtype=np.int32)
+    w = wl.random_case(3470, B=B, Hq=Hq, Hkv=Hkv, lens=[T, T], poison=False)
+    g, gt = np.random.default_rng(6), torch.Generator().manual_seed(12)
+    rnd = lambda *s: torch.randn(*s, generator=gt).to(BF16)  # noqa: E731
+    k, v, bt = w.k_pool.cuda(), w.v_pool.cuda(), torch.from_numpy(w.block_table).cuda()
+    kr, vr = u16(k).copy(), u16(v).copy()
+    wt = torch.zeros(B, Hkv, T, device="cuda")
+    sums = Sums(B, Hkv, lens)
+    sl, slr = torch.from_numpy(lens).cuda(), lens.copy()
+    for step in range(8):
+        sl, slr = sl + q_len, slr + q_len
+        sums.append(q_len)
+        mask = zl.tree_mask([[-1] + [int(g.integers(-1, i)) for i in range(1, q_len)]
+                             for _ in range(B)])
+        q, kn, vn = rnd(B, q_len, Hq, D), rnd(B, q_len, Hkv, D), rnd(B, q_len, Hkv, D)
+        zl.decode_attn(q.cuda(), k, v, bt, sl, page_size=P, scale=w.scale, weights=wt,
+                       tree_mask=mask.cuda(), k_new=kn.cuda(), v_new=vn.cuda())
+        for b in range(B):
+            for i in range(q_len):
+                t = slr[b] - q_len + i
+                kr[w.block_table[b, t // P], t % P] = u16(kn)[b, i]
+                vr[w.block_table[b, t // P], t % P] = u16(vn)[b, i]
+        ref = attention(f64(q), as_f64(kr), as_f64(vr), w.block_table, slr, scale=w.scale,
+                        mask=mask, tokens=T)
+        sums.add(ref.weights, ref.weights_tol + q_len * 4 * 2.0 ** -22 * ref.weights, 1.0)
+        acc = g.integers(0, q_len, size=B, endpoint=True).astype(np.int32)
+        path = np.zeros((B, q_len), dtype=np.int32)
+        for b in range(B):
+            path[b, :acc[b]] = np.sort(g.choice(q_len, acc[b], replace=False))
+        sl = zl.kv_commit(k, v, bt, sl, torch.from_numpy(path).cuda(), torch.from_numpy(acc).cuda(),
+                          page_size=P, q_len=q_len, weights=wt)
+        kr, vr, newr, _ = commit(kr, vr, w.block_table, slr, path, acc, page_size=P, q_len=q_len,
+                                 num_pages=w.num_pages)
+        for b in range(B):
+            ctx = int(slr[b]) - q_len
+            for h in range(Hkv):
+                sums.keep(b, h, list(range(ctx)) + [ctx + int(x) for x in path[b, :acc[b]]])
+        slr = newr
+        check(f64(wt), *sums.rows(T), f"committed weights {step}")
+        before = wt.cpu().numpy()
+        sl, kept = zl.kv_evict(k, v, bt, sl, wt, page_size=P, budget=budget, sink=2, recent=6,
+                               clear_weights=True)
+        kr, vr, _, keptr, slr, _ = evict(kr, vr, before, w.block_table, slr, page_size=P,
+                                         budget=budget, sink=2, recent=6, num_pages=w.num_pages)
+        assert np.array_equal(kept.cpu().numpy(), keptr)
+        for b in range(B):
+            for h in range(Hkv):
+                sums.keep(b, h, keptr[b, h][keptr[b, h] >= 0])
+        check(f64(wt), *sums.rows(T), f"kept weights {step}")
+        assert np.array_equal(sl.cpu().numpy(), slr)

@@ -6,11 +6,15 @@ import pytest
 import torch
 
 import paged_decode_attention_gqa_gb300 as zl
-from test_ops_abi import FAKE, _evict
+from test_ops_abi import FAKE, _commit, _evict
 
 
 def evict_status(**over):
     return zl.lib().zl_kv_evict(ctypes.byref(_evict(**over)), None)
+
+
+def commit_status(**over):
+    return zl.lib().zl_kv_commit(ctypes.byref(_commit(**over)), None)
 
 
 def test_rows_to_clear():
@@ -30,3 +34,33 @@ def test_evict_struct_sizes():
         pytest.skip("a GPU is present")
     for size in (old, new):
         assert evict_status(struct_size=size) == zl.ERR_CUDA
+
+
+@pytest.mark.parametrize("over", [
+    dict(weights=FAKE + 2), dict(weights_tokens=0), dict(weights_head_stride=127),
+    dict(weights_seq_stride=0), dict(weights_seq_stride=1023),
+])
+def test_weights_of_a_commit(over):
+    rows = dict(weights=4 * FAKE, weights_tokens=128, weights_head_stride=128,
+                weights_seq_stride=1024)
+    assert commit_status(**{**rows, **over}) == zl.ERR_INVALID_ARG
+
+
+def test_commit_struct_sizes():
+    new, old = ctypes.sizeof(zl.CommitParams), zl.CommitParams.weights.offset
+    for size in (old - 8, old + 8, new + 8):
+        assert commit_status(struct_size=size) == zl.ERR_INVALID_ARG
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for size in (old, new):
+        assert commit_status(struct_size=size) == zl.ERR_CUDA
+
+
+def test_binding_checks_the_weights_of_a_commit():
+    k = torch.zeros(6, 16, 2, 128, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    path, acc = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    for w in (torch.zeros(2, 8, 48), torch.zeros(2, 2, 48, dtype=torch.float64),
+              torch.zeros(2, 48), torch.zeros(2, 2, 96)[:, :, ::2]):
+        with pytest.raises(ValueError, match="weights"):
+            zl.kv_commit(k, k, bt, sl, path, acc, page_size=16, q_len=3, weights=w)
