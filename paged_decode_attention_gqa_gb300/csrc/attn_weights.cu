@@ -11,6 +11,8 @@
 #include "kernels.h"
 #include "ptx.cuh"
 
+#include <math_constants.h>
+
 namespace zl {
 namespace {
 
@@ -62,6 +64,13 @@ attn_weights_kernel(const __grid_constant__ WeightsParams p) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         if (stat[k].y == 0.f) continue;
+        if (isnan(stat[k].y)) {  // a NaN row: every token that it sees
+          sum.x += x[k].x == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
+          sum.y += x[k].y == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
+          sum.z += x[k].z == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
+          sum.w += x[k].w == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
+          continue;
+        }
         sum.x += ex2_approx(x[k].x - stat[k].x) * stat[k].y;
         sum.y += ex2_approx(x[k].y - stat[k].x) * stat[k].y;
         sum.z += ex2_approx(x[k].z - stat[k].x) * stat[k].y;

@@ -223,7 +223,8 @@ __device__ __forceinline__ int split_cta_span(const TileCut& cut, int64_t U0, in
 // Running log-sum-exp merge of NR rows (base-2 lse): a running max, the
 // rescaled weight sum and the rescaled sum of normalised outputs. A source row
 // with lse NaN (its piece met a bad page) marks that row bad (bit k of
-// `bad`); lse -inf weighs 0.
+// `bad`); lse -inf weighs 0, and +inf (modified scores: a piece whose sum is no
+// number) makes the row's sum and outputs NaN.
 template <int NR>
 struct MergeAcc {
   float mx[NR], den[NR];
@@ -254,6 +255,13 @@ struct MergeAcc {
     }
   }
 };
+
+// Whether a row of softmax sum l has no weight. Modified scores keep a sum that
+// is no number (a NaN or +inf score): such a row is NaN, however it was cut.
+template <int MODE>
+__device__ __forceinline__ bool no_weight(float l) {
+  return MODE == kModeMod ? l == 0.f : !(l > 0.f);
+}
 
 // Adds the partials of rows [row_off + r0, row_off + r0 + nrows) (slot stride
 // R) of the pieces of a unit (first tile U0) held by CTAs c_lo..c_hi, in CTA
@@ -329,7 +337,7 @@ __device__ __forceinline__ void merge_write_out(const MergeAcc<NR>& m, const Gqa
     if (k < nrows) {
       const int r = r0 + k;
       const int64_t orow = (int64_t(b) * p.q_total + tok0 + r / gh) * p.Hq + head0 + r % gh;
-      const bool none = ((m.bad >> k) & 1u) || !(m.den[k] > 0.f);
+      const bool none = ((m.bad >> k) & 1u) || no_weight<MODE>(m.den[k]);
       const float inv = none ? 0.f : __frcp_rn(m.den[k]);
       uint2 packed = make_uint2(0u, 0u);
       if (!none) {
@@ -1068,9 +1076,11 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
       const bool bad = half ? bad_b : bad_a;
       // A row whose piece met a bad page, or a row that saw no token, is
       // written as zeros with lse = -inf (weight 0 in the merge).
-      const bool none = bad || !(l > 0.f);
+      const bool none = bad || no_weight<MODE>(l);
       const float inv = none ? 0.f : 1.f / l;
-      const float lse2 = none ? -CUDART_INF_F : m + log2f(l);
+      float lse2 = none ? -CUDART_INF_F : m + log2f(l);
+      // (a partial's NaN means a bad page)
+      if (MODE == kModeMod && partial && isnan(l)) lse2 = CUDART_INF_F;
       if (!partial && MODE == kModeShared) {
         // a whole unit: the row's result over this part (prefix or suffix),
         // for the merge kernel to combine

@@ -64,12 +64,15 @@ gqa_merge_split_kernel(const __grid_constant__ GqaParams p, int G) {
   if (from <= to)
     merge_add_pieces<1, 8>(m, p, cut, tg * G, U0, c_lo, to, w, rmax, 0, r0, 1, lane, from);
   {
-    const bool some = m.den[0] > 0.f;
+    const bool some = !no_weight<kModeMod>(m.den[0]);
     const float inv = some ? __frcp_rn(m.den[0]) : 0.f;
     s_o[warp][lane] = make_float4(m.acc[0].x * inv, m.acc[0].y * inv, m.acc[0].z * inv,
                                   m.acc[0].w * inv);
     if (lane == 0)
-      s_lse[warp] = m.bad ? CUDART_NAN_F : some ? m.mx[0] + log2f(m.den[0]) : -CUDART_INF_F;
+      s_lse[warp] = m.bad              ? CUDART_NAN_F
+                    : isnan(m.den[0]) ? CUDART_INF_F
+                    : some            ? m.mx[0] + log2f(m.den[0])
+                                      : -CUDART_INF_F;
   }
   __syncthreads();
   if (warp != 0) return;

@@ -890,10 +890,10 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       }
       if (!ok) break;
       // the row's base and sum for the epilogue (once it has read the ones that
-      // were here; l = NaN: the row saw a bad page)
+      // were here; base NaN, which no score makes it: the row saw a bad page)
       const uint32_t par = pieces & 1;
       if (pieces >= 2 && !wait_all(Cfg::B_EPI0 + par, ((pieces >> 1) - 1) & 1)) break;
-      ml[par * 256 + s * 128 + row] = make_float2(m, bad ? CUDART_NAN_F : l);
+      ml[par * 256 + s * 128 + row] = make_float2(bad ? CUDART_NAN_F : m, l);
       mbar_arrive(bar(Cfg::B_ML0 + par));
       tile_no += n;
       ++pieces;
@@ -972,9 +972,9 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           w1 = r[1].x == -CUDART_INF_F ? 0.f : ex2_approx(r[1].x - m);
           l = r[0].y * w0 + r[1].y * w1;
         }
-        const bool bad = isnan(r[0].y) || (MT == 1 && isnan(r[1].y));
-        const bool row_bad = MT == 1 ? bad : isnan(l);
-        const bool none = row_bad || !(l > 0.f);
+        const bool row_bad =
+            MT == 1 ? isnan(r[0].x) || isnan(r[1].x) : isnan(s ? r[1].x : r[0].x);
+        const bool none = row_bad || no_weight<kModeMod>(l);
         const float inv = none ? 0.f : 1.f / l;
         const float lse2 = none ? -CUDART_INF_F : m + log2f(l);
         w0 *= inv;
@@ -1052,7 +1052,9 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
           }
         }
         if (exists) {
-          if (pc.partial) p.ws_lse[wrow] = row_bad ? CUDART_NAN_F : lse2;
+          // (of a partial: NaN a bad page, +inf a sum that is no number)
+          if (pc.partial)
+            p.ws_lse[wrow] = row_bad ? CUDART_NAN_F : isnan(l) ? CUDART_INF_F : lse2;
           else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
         }
       }
@@ -1161,7 +1163,7 @@ gqa_wide_merge(const __grid_constant__ WideParams p, int G) {
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     if (!live[k]) continue;
-    const bool none = ((acc.bad >> k) & 1u) || !(acc.den[k] > 0.f);
+    const bool none = ((acc.bad >> k) & 1u) || no_weight<kModeMod>(acc.den[k]);
     const float inv = none ? 0.f : 1.f / acc.den[k];
     uint2 o = make_uint2(0u, 0u);
     if (!none)

@@ -31,7 +31,7 @@ struct WideParams {
   const int32_t* seq_lens;
   int64_t bt_stride;
   int4* ws_cut;        // [CTAs] the unit each boundary cuts first, for the merge
-  float* ws_lse;       // [CTAs][2][mt * 128] base-2 lse of partials (NaN = bad)
+  float* ws_lse;       // [CTAs][2][mt * 128] base-2 lse of partials (NaN bad, +inf NaN)
   float* ws_o;         // [..][128] normalised partial outputs
   uint32_t* err_flags;
   int B, q_total, Hq, Hkv, g, page_size, num_pages;
