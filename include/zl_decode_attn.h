@@ -414,7 +414,8 @@ zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
  *     new_lens[b] = seq_lens[b] (ZL_DEVERR_BAD_SEQ_LEN). A row whose source or
  *     destination page id is outside [0, num_pages) does not move
  *     (ZL_DEVERR_BAD_PAGE).
- *   - Rows are copies: bit-exact. new_lens must not overlap seq_lens.
+ *   - Rows are copies: bit-exact. new_lens must overlap neither seq_lens nor
+ *     kept.
  */
 typedef struct {
   size_t struct_size; /* sizeof(zl_kv_evict_params) */
@@ -466,7 +467,8 @@ zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t stream);
  *     the pages are. (What the rejected tokens' own query rows added to the
  *     sums of the tokens before them stays.) A struct of the size without these
  *     fields has no weights.
- *   - Rows are copies: bit-exact. new_lens must not overlap seq_lens.
+ *   - Rows are copies: bit-exact. new_lens must overlap none of seq_lens,
+ *     accepted and path.
  */
 typedef struct {
   size_t struct_size; /* sizeof(zl_kv_commit_params) */

@@ -126,6 +126,11 @@ extern "C" zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t
        !zl::rows_distinct(a->B, a->Hkv, a->weights_seq_stride, a->weights_head_stride,
                           a->weights_tokens)))
     return ZL_ERR_INVALID_ARG;
+  // (one block writes a sequence's new length while others still read its
+  // accepted count and path)
+  if (zl::overlaps(a->new_lens, a->B, a->accepted, a->B) ||
+      zl::overlaps(a->new_lens, a->B, a->path, (a->B - 1) * a->path_stride + a->path_len))
+    return ZL_ERR_INVALID_ARG;
   if (a->q_len > zl::kMaxDrafted) return ZL_ERR_UNSUPPORTED;
   p.block_table = a->block_table;
   p.bt_stride = a->block_table_stride;

@@ -537,6 +537,8 @@ extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t s
       int64_t(a->sink) + a->recent > a->budget || a->weights_tokens < 1)
     return ZL_ERR_INVALID_ARG;
   if (a->dst_block_table && a->dst_block_table_stride < 1) return ZL_ERR_INVALID_ARG;
+  if (zl::overlaps(a->new_lens, a->B, a->kept, int64_t(a->B) * a->Hkv * a->budget))
+    return ZL_ERR_INVALID_ARG;
   if (!zl::rows_distinct(a->B, a->Hkv, a->weights_seq_stride, a->weights_head_stride,
                          a->weights_tokens))
     return ZL_ERR_INVALID_ARG;

@@ -28,10 +28,10 @@ inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
-// [a, a + n) and [b, b + n) int32 arrays overlap.
-inline bool overlaps(const int32_t* a, const int32_t* b, int64_t n) {
+// int32 arrays of na elements at a and nb at b overlap.
+inline bool overlaps(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
   const intptr_t d = reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b);
-  return d < n * 4 && -d < n * 4;
+  return d < nb * 4 && -d < na * 4;
 }
 
 // A caller's parameter struct: of this header's size, or of the size it had
@@ -60,7 +60,7 @@ zl_status move_pools(const Params* a, MovePools* out) {
   if (a->page_stride <= 0 || a->token_stride <= 0 || a->head_stride <= 0 ||
       a->page_stride % 8 || a->token_stride % 8 || a->head_stride % 8)
     return ZL_ERR_INVALID_ARG;
-  if (overlaps(a->new_lens, a->seq_lens, a->B)) return ZL_ERR_INVALID_ARG;
+  if (overlaps(a->new_lens, a->B, a->seq_lens, a->B)) return ZL_ERR_INVALID_ARG;
   if (a->B > 65535 || a->Hkv > 65535) return ZL_ERR_UNSUPPORTED;  // grid dimensions
   out->k = static_cast<uint4*>(a->k_pool);
   out->v = static_cast<uint4*>(a->v_pool);

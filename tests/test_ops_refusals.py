@@ -64,3 +64,26 @@ def test_binding_checks_the_weights_of_a_commit():
               torch.zeros(2, 48), torch.zeros(2, 2, 96)[:, :, ::2]):
         with pytest.raises(ValueError, match="weights"):
             zl.kv_commit(k, k, bt, sl, path, acc, page_size=16, q_len=3, weights=w)
+
+
+@pytest.mark.parametrize("at", [0, 4, 12, -12])
+def test_new_lengths_over_an_input_of_the_commit(at):
+    """The lengths of 4 sequences written where accepted, or a row of the path, is
+    still read; beside them they are taken."""
+    free = dict(seq_lens=2 * FAKE, path=4 * FAKE, accepted=6 * FAKE)
+    assert commit_status(**free, new_lens=6 * FAKE + at) == zl.ERR_INVALID_ARG
+    assert commit_status(**free, new_lens=4 * FAKE + at) == zl.ERR_INVALID_ARG
+    # rows of 8 entries, 8 apart: the last one ends 128 bytes in
+    assert commit_status(**free, new_lens=4 * FAKE + 124) == zl.ERR_INVALID_ARG
+    if not torch.cuda.is_available():
+        for new in (6 * FAKE + 16, 6 * FAKE - 16, 4 * FAKE + 128, 4 * FAKE - 16):
+            assert commit_status(**free, new_lens=new) == zl.ERR_CUDA
+
+
+def test_new_lengths_over_the_kept_list():
+    free, size = dict(seq_lens=2 * FAKE, kept=4 * FAKE), 4 * 8 * 32 * 4
+    for new in (4 * FAKE, 4 * FAKE - 12, 4 * FAKE + size - 4):
+        assert evict_status(**free, new_lens=new) == zl.ERR_INVALID_ARG
+    if not torch.cuda.is_available():
+        for new in (4 * FAKE - 16, 4 * FAKE + size):
+            assert evict_status(**free, new_lens=new) == zl.ERR_CUDA
