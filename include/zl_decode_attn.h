@@ -407,7 +407,9 @@ zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
  *     accumulating in the same rows wants this. A struct of the size without
  *     this field counts as 0.
  *   - Pools, strides, row widths, block table and v_pool = NULL as for
- *     zl_kv_append. budget >= 1, sink + recent <= budget.
+ *     zl_kv_append. budget >= 1, sink + recent <= budget. budget,
+ *     weights_tokens and weights_clear above 2^31 - 1 - 16384 are
+ *     ZL_ERR_UNSUPPORTED.
  *   - Device data errors: seq_lens[b] < 0, above the block table's reach or
  *     above weights_tokens, or a new length above the destination table's
  *     reach: nothing of the sequence moves, its kept entries are -1 and

@@ -386,6 +386,11 @@ cudaError_t select_rows(EvictParams& p, int B, int sms, cudaStream_t stream) {
 constexpr int kMoveThreads = 256;
 constexpr int kUnroll = 4;       // chunks of 16 bytes per thread and step
 constexpr int kSegment = 1024;   // rows whose places are looked up together
+// Longest budget and weights rows: a pass of the move looks up kSegment rows for
+// each CTA of a cluster, and a pass of the selection's loops is a token per
+// thread of one, so numbers up to one pass beyond either stay in 32 bits.
+constexpr int kMaxTokens = INT32_MAX - 16384;
+static_assert(kSelCluster * kSegment <= 16384 && kSelCluster * 512 <= 16384, "one pass");
 
 // Column part q of a row: chunks [c0, c0 + part) of K or V. In place the row's
 // cluster of move_cluster CTAs takes the kept rows in steps, each CTA its share of
@@ -549,6 +554,9 @@ extern "C" zl_status zl_kv_evict(const zl_kv_evict_params* params, zl_stream_t s
   if (a->weights_out && !zl::rows_distinct(a->B, a->Hkv, a->weights_out_seq_stride,
                                            a->weights_out_head_stride, out_tokens))
     return ZL_ERR_INVALID_ARG;
+  if (a->budget > zl::kMaxTokens || a->weights_tokens > zl::kMaxTokens ||
+      a->weights_clear > zl::kMaxTokens)
+    return ZL_ERR_UNSUPPORTED;
   // (in place is NULL: the kernels that write elsewhere read without its order)
   if (a->weights_out == a->weights || a->dst_block_table == a->block_table)
     return ZL_ERR_INVALID_ARG;

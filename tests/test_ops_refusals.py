@@ -87,3 +87,14 @@ def test_new_lengths_over_the_kept_list():
     if not torch.cuda.is_available():
         for new in (4 * FAKE - 16, 4 * FAKE + size):
             assert evict_status(**free, new_lens=new) == zl.ERR_CUDA
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 8192, (1 << 31) - 16384])
+def test_lengths_near_the_32_bit_limit(n):
+    """The kernels count rows in 32 bits and go up to a pass beyond the last one."""
+    rows = dict(weights_tokens=n, weights_head_stride=1 << 31, weights_seq_stride=1 << 34)
+    out = dict(weights_out=1 << 30, weights_out_head_stride=1 << 31,
+               weights_out_seq_stride=1 << 34)
+    assert evict_status(budget=n, new_lens=1 << 50) == zl.ERR_UNSUPPORTED
+    assert evict_status(**rows) == zl.ERR_UNSUPPORTED
+    assert evict_status(weights_clear=n, **out) == zl.ERR_UNSUPPORTED
