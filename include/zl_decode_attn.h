@@ -348,14 +348,15 @@ zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
  * Everything else is as for zl_decode_attn, fused append included, with two
  * limits: flags must be 0 and shared_prefix_pages 0 (ZL_ERR_UNSUPPORTED). A
  * softcap outside [1e-6, 1e6], or one that scale divided by is no normal 32-bit
- * number, is ZL_ERR_UNSUPPORTED. Results depend only on
- * logical content, and repeated calls are bit-identical. K and V rows of
- * tokens that no query token's window reaches are never used and pages that
- * hold only such tokens need not be mapped; rows that some query sees and
- * others do not must be finite. A NaN or +inf score (after the cap) of a token
- * that a query row sees makes that row's out and lse NaN, and the weights of
- * the tokens it sees; it is no device error, and other rows do not change. A
- * -inf score weighs 0; a row with no other scores is one that sees no token.
+ * number, is ZL_ERR_UNSUPPORTED, and so are weights with weights_tokens above
+ * 2^31 - 1 - 4096 or Hkv above 65535. Results depend only on logical content,
+ * and repeated calls are bit-identical. K and V rows of tokens that no query
+ * token's window reaches are never used and pages that hold only such tokens
+ * need not be mapped; rows that some query sees and others do not must be
+ * finite. A NaN or +inf score (after the cap) of a token that a query row sees
+ * makes that row's out and lse NaN, and the weights of the tokens it sees; it
+ * is no device error, and other rows do not change. A -inf score weighs 0; a
+ * row with no other scores is one that sees no token.
  */
 typedef struct {
   size_t struct_size;        /* sizeof(zl_score_params) */

@@ -165,6 +165,8 @@ zl_status mods_validate(const zl_decode_attn_params* a, const zl_score_params* m
     if (!zl::rows_distinct(a->B, a->Hkv, m->weights_seq_stride, m->weights_head_stride,
                            m->weights_tokens))
       return ZL_ERR_INVALID_ARG;
+    // (the grid that sums them: whole blocks of tokens in 32 bits, a kv head each in y)
+    if (m->weights_tokens > zl::kMaxWeightsTokens || a->Hkv > 65535) return ZL_ERR_UNSUPPORTED;
   }
   if (a->flags || a->shared_prefix_pages != 0) return ZL_ERR_UNSUPPORTED;
   return ZL_OK;

@@ -133,6 +133,7 @@ struct WeightsParams {
   int max_tokens;          // tokens the grid covers (weights row length)
 };
 cudaError_t weights_launch(const WeightsParams& p, cudaStream_t stream);
+constexpr int kMaxWeightsTokens = INT32_MAX - 4096;  // whole blocks of 1024 stay in 32 bits
 
 constexpr int kMlaTile = 64;       // tokens per MLA tile (page sizes are multiples of it)
 constexpr int kMlaDqk = 576;       // latent 512 + rope 64

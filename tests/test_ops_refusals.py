@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import paged_decode_attention_gqa_gb300 as zl
-from test_ops_abi import FAKE, _commit, _evict
+from test_abi import _params
+from test_ops_abi import FAKE, _commit, _evict, _scores
 
 
 def evict_status(**over):
@@ -98,3 +99,16 @@ def test_lengths_near_the_32_bit_limit(n):
     assert evict_status(budget=n, new_lens=1 << 50) == zl.ERR_UNSUPPORTED
     assert evict_status(**rows) == zl.ERR_UNSUPPORTED
     assert evict_status(weights_clear=n, **out) == zl.ERR_UNSUPPORTED
+
+
+def test_weights_beyond_the_grid_that_sums_them():
+    """Refused before the attention is enqueued, not after it."""
+    for n, Hkv in (((1 << 31) - 1, 8), ((1 << 31) - 4096, 8), (128, 65536)):
+        p = _params(Hkv=Hkv, Hq=Hkv)
+        m = _scores(weights=FAKE, weights_tokens=n, weights_head_stride=1 << 32,
+                    weights_seq_stride=1 << 50)
+        size = ctypes.c_size_t(0)
+        assert zl.lib().zl_decode_attn_ex(ctypes.byref(p), ctypes.byref(m),
+                                          None) == zl.ERR_UNSUPPORTED
+        assert zl.lib().zl_decode_attn_ex_workspace_size(
+            ctypes.byref(p), ctypes.byref(m), ctypes.byref(size)) == zl.ERR_UNSUPPORTED
