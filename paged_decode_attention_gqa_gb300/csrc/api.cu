@@ -598,9 +598,8 @@ zl_status wide_run(const zl_decode_attn_params* a, const zl_score_params& m, con
     ap.D_v = a->D_v;
     ap.page_size = a->page_size;
     ap.num_pages = a->num_pages;
-    // no err_flags: a bad length or page is the attention's to report (short
-    // sequences are no error for it)
-    if ((st = zl_kv_append(&ap, reinterpret_cast<zl_stream_t>(s))) != ZL_OK) return st;
+    ap.err_flags = a->err_flags;
+    if ((st = zl::kv_append_run(&ap, false, s)) != ZL_OK) return st;
   }
   const cudaError_t e = zl::gqa_wide_launch(p, plan.grid, plan.unit_cut, s,
                                             reinterpret_cast<cudaEvent_t>(a->attn_begin),

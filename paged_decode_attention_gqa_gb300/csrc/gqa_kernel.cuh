@@ -739,6 +739,8 @@ gqa_decode_kernel(const __grid_constant__ GqaParams p) {
         const int h = __shfl_sync(0xffffffffu, hg, k);
         const int bd = __shfl_sync(0xffffffffu, bad, k);
         const int nn = __shfl_sync(0xffffffffu, nnew, k);
+        // (a drafted token that no row sees is not looked at, but not stored either)
+        if (MODE == kModeMod && nn > 0 && bd && lane == 0) raise_error(p.err_flags, kErrBadPage);
         if (nn > 0 && !bd) {
           // Store the new tokens' rows of this CTA's kv heads before the tile's
           // loads (every CTA that loads the tile stores the same bytes).

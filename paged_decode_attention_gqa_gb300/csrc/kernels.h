@@ -1,6 +1,8 @@
 // Internal interface between the C-ABI front end (api.cu) and the kernels.
 #pragma once
 
+#include "../../include/zl_decode_attn.h"
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -134,6 +136,10 @@ struct WeightsParams {
 };
 cudaError_t weights_launch(const WeightsParams& p, cudaStream_t stream);
 constexpr int kMaxWeightsTokens = INT32_MAX - 4096;  // whole blocks of 1024 stay in 32 bits
+
+// zl_kv_append; flag_lens false: for a call that reports lengths itself (fewer
+// tokens than new ones are no error for the attention).
+zl_status kv_append_run(const zl_kv_append_params* a, bool flag_lens, cudaStream_t stream);
 
 constexpr int kMlaTile = 64;       // tokens per MLA tile (page sizes are multiples of it)
 constexpr int kMlaDqk = 576;       // latent 512 + rope 64

@@ -29,6 +29,7 @@ struct AppendParams {
   int64_t bt_stride;
   const int32_t* seq_lens;
   uint32_t* err_flags;
+  bool flag_lens;      // a length that takes no new tokens is an error
   int64_t rows;        // B * q_len * Hkv
   int q_len, Hkv, ck, cv, page_size, num_pages;
 };
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     const int64_t b = bi / p.q_len;
     const int L = __ldg(p.seq_lens + b);
     if (L < p.q_len || int64_t(L) > p.bt_stride * p.page_size) {
-      if (lane == 0 && i == 0 && kh == 0 && p.err_flags) atomicOr(p.err_flags, 2u);
+      if (lane == 0 && i == 0 && kh == 0 && p.flag_lens && p.err_flags) atomicOr(p.err_flags, 2u);
       continue;
     }
     const int t = L - p.q_len + i;
@@ -94,12 +95,11 @@ zl_status validate(const zl_kv_append_params* a) {
 }
 
 }  // namespace
-}  // namespace zl
 
-extern "C" zl_status zl_kv_append(const zl_kv_append_params* a, zl_stream_t stream) {
-  const zl_status st = zl::validate(a);
+zl_status kv_append_run(const zl_kv_append_params* a, bool flag_lens, cudaStream_t stream) {
+  const zl_status st = validate(a);
   if (st != ZL_OK) return st;
-  zl::AppendParams p;
+  AppendParams p;
   std::memset(&p, 0, sizeof(p));
   p.k_new = static_cast<const uint4*>(a->k_new);
   p.v_new = static_cast<const uint4*>(a->v_new);
@@ -112,6 +112,7 @@ extern "C" zl_status zl_kv_append(const zl_kv_append_params* a, zl_stream_t stre
   p.bt_stride = a->block_table_stride;
   p.seq_lens = a->seq_lens;
   p.err_flags = a->err_flags;
+  p.flag_lens = flag_lens;
   p.rows = int64_t(a->B) * a->q_len * a->Hkv;
   p.q_len = a->q_len;
   p.Hkv = a->Hkv;
@@ -121,6 +122,12 @@ extern "C" zl_status zl_kv_append(const zl_kv_append_params* a, zl_stream_t stre
   p.num_pages = a->num_pages;
   const int64_t blocks = (p.rows + 7) / 8;  // 8 warps per block, one row per warp
   const int grid = int(blocks < 65535 ? blocks : 65535);
-  zl::kv_append_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  kv_append_kernel<<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+}
+
+}  // namespace zl
+
+extern "C" zl_status zl_kv_append(const zl_kv_append_params* a, zl_stream_t stream) {
+  return zl::kv_append_run(a, true, reinterpret_cast<cudaStream_t>(stream));
 }
