@@ -162,7 +162,9 @@ typedef struct {
      their page slots first, exactly as zl_kv_append would (new token i of
      sequence b is position seq_lens[b] - q_len + i; the pools must be
      writable), and attends over the result: a decode step needs no separate
-     append launch. After the call the pools hold the new rows, bit-exact,
+     append launch. (zl_decode_attn_ex with more than 16 query rows per kv
+     head, 32 in small calls, does the same by an append launch of its own
+     before attn_begin.) After the call the pools hold the new rows, bit-exact,
      except rows on a bad page (skipped and flagged, as zl_kv_append does) and
      the rows of a sequence with fewer than q_len tokens or a bad length
      (skipped; only a bad length is flagged, by the attention). With
@@ -294,7 +296,8 @@ zl_status zl_decode_attn_noalloc(const zl_decode_attn_params* params, zl_stream_
  *   - The writes are ordinary stores on the given stream; a decode call
  *     enqueued after it on the same stream sees them.
  *   - zl_decode_attn_params.k_new / v_new do the same stores inside the
- *     attention launch (one launch less per decode step).
+ *     attention launch (one launch less per decode step; see there for
+ *     zl_decode_attn_ex).
  */
 typedef struct {
   size_t struct_size; /* sizeof(zl_kv_append_params) */
@@ -376,7 +379,9 @@ zl_status zl_decode_attn_ex(const zl_decode_attn_params* params, const zl_score_
 /* Workspace bytes zl_decode_attn_ex needs, from the shapes, num_ctas,
    max_seq_len, window, weights_tokens and which pointers are NULL. With weights
    it holds the scores of every query row: B * q_len * Hq * weights_tokens * 4
-   bytes more. */
+   bytes more. (max_seq_len does not bound that, since no result depends on it.
+   Rows longer than the sequences need be given only in part: weights_tokens of
+   the longest sequence with the strides of the whole rows.) */
 zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
                                            const zl_score_params* scores, size_t* bytes);
 
@@ -387,7 +392,9 @@ zl_status zl_decode_attn_ex_workspace_size(const zl_decode_attn_params* params,
  * between, the budget - sink - recent with the largest weights (equal weights:
  * the earlier token; NaN counts as below every number). The kept rows move, in
  * order, to positions 0 .. budget - 1: K, V and weights. Each kv head chooses
- * for itself. A sequence of at most budget tokens keeps everything.
+ * for itself. A sequence of at most budget tokens keeps everything. A kept
+ * token's position for later calls (distance bias, window) is its new place in
+ * the cache; zl_score_params has no other.
  *   - new_lens[b] = min(L, budget). kept, int32 [B, Hkv, budget] contiguous:
  *     the kept positions, ascending, then -1. Both are written.
  *   - dst_block_table NULL: in place (no page of these sequences may be mapped

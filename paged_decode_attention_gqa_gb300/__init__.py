@@ -667,7 +667,9 @@ def decode_attn(q, k_pool, v_pool, block_table, seq_lens, *, page_size, scale, o
     tree_mask()). weights fp32 [B, Hkv, tokens]: each cached token's softmax
     weight, summed over the query tokens and the heads of its kv head, is added
     to weights_decay times what it holds. A new token's sum starts from what its
-    element held, so keep the elements behind seq_lens at 0.
+    element held, so keep the elements behind seq_lens at 0. The scratch of such
+    a call grows with the rows' length (4 bytes per query row and token): give
+    wide rows as weights[:, :, :n], n of at least the longest sequence.
     """
     if (softcap or window or alibi_slopes is not None or tree_mask is not None
             or weights is not None):
@@ -782,8 +784,9 @@ def kv_evict(k_pool, v_pool, block_table, seq_lens, weights, *, page_size, budge
     clear_weights: the weights behind the new length, which belong to no token
     any more, become 0 (in place up to the old length, in weights_out up to the
     end of its rows); otherwise they stay, and the next tokens cached there
-    start from them. Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]:
-    the kept positions, then -1).
+    start from them. Rows much wider than the sequences take longer to search:
+    give weights[:, :, :n] here too. Returns (new_lens int32 [B], kept int32
+    [B, Hkv, budget]: the kept positions, then -1).
     """
     if weights is None:
         raise ValueError("weights is required")

@@ -107,6 +107,11 @@ struct GqaPlan {
 // tcgen05 one and 166 by the other, 36 rows 123 and 230; 16 units of 200 tokens
 // and 32 rows 13.7 and 16.2, of 16000 tokens 43 and 52; 8 units of 200 tokens and
 // 20 or 32 rows 13.3 and 12.4 to 13.0, of 4000 tokens 24 and 21 to 23.
+// A call with weights always runs the other one, which stores the scores that the
+// weights are summed from. That is meant for few rows: 64 sequences of 512-4096
+// tokens, 32 heads on 8 kv heads, with weights 16 drafted tokens take 487 us and
+// 0.56 GB of scratch (135 us without weights, from a cold L2), 64 drafted tokens
+// 1877 us and 2.2 GB (171 without).
 constexpr int kWideRows = 16;
 constexpr int kWideRowsFew = 32;
 constexpr int kFewUnits = 8;

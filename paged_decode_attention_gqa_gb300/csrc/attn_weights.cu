@@ -6,8 +6,10 @@
 // for t < seq_lens[b]. The attention kernel keeps every base-2 score x it
 // computed and, per query row, the final softmax base m and 1 / l, so a weight
 // is 2^(x - m) / l: 4 bytes written and read per (row, token) instead of a
-// second pass over K (256 bytes per token and kv head). Each weight is summed in
-// a fixed order: no atomics, the same bits every time.
+// second pass over K (256 bytes per token and kv head). Up to 32 rows per kv
+// head those are the fewer bytes; with more (drafted trees) it is the form there
+// is, not the cheapest one. Each weight is summed in a fixed order: no atomics,
+// the same bits every time.
 #include "kernels.h"
 #include "ptx.cuh"
 

@@ -680,8 +680,8 @@ gqa_wide_kernel(const __grid_constant__ WideParams p) {
       }
       const int n = pc.ntiles, L = pc.L, ctx = L - p.q_total;
       // Row `row` of this stream's row tile: token row / g of the tile's tpt,
-      // head row % g (rows past the last token have zeros in Q, rows past g tpt
-      // whatever the buffer holds: both are computed and dropped).
+      // head row % g (rows past the last token or past g tpt have zeros in Q:
+      // they are computed and dropped).
       const int qi_all = (pc.blk * MT + (MT == 2 ? s : 0)) * p.tpt + row / p.g;
       const bool exists = row < p.g * p.tpt && qi_all < p.q_total;
       const int qi = exists ? qi_all : 0;

@@ -7,11 +7,15 @@
 // kept positions in order: a token is kept if its key is above the threshold,
 // or equals it and fewer than the missing number of equal ones came before it.
 // Each CTA owns a contiguous part of the row, each thread 16 tokens of it in a
-// row: its counts and a scan over threads and CTAs give the place of every kept
-// token, so no atomic decides an order and the result is always the same. A
-// CTA keeps its part of the weights in shared memory; they are read from memory
-// once. What bounds it is the chain of passes and their barriers and the
-// instructions per token, not the 4 bytes: with one CTA per row, ballots per
+// row (32 in long rows): its counts and a scan over threads and CTAs give the
+// place of every kept token, so no atomic decides an order and the result is
+// always the same. A CTA keeps its part of the weights in shared memory; they
+// are read from memory once. What bounds it is the chain of passes and their barriers and the
+// instructions per token, not the 4 bytes. The instance goes by the length of
+// the weights rows, which is all the host knows: rows far longer than the
+// sequences cost passes over nothing (64 x 8 rows of 2049-4096 tokens to 2048,
+// both launches: 200 us in rows of 4096, 249 of 32768, 464 of 131072, and 607
+// just above, where no cluster holds a row). With one CTA per row, ballots per
 // token and the weights read again in every pass it took 209 us for 64 rows of
 // 32k-131k tokens and 31 us for 512 rows of 2k-4k.
 //

@@ -163,6 +163,26 @@ def test_clear_long_rows(L, T, budget, recent):
     run_clear(w, wt, budget=budget, recent=recent, dst=free[:2 * n].reshape(2, n).astype(np.int32))
 
 
+@pytest.mark.parametrize("clear", [False, True])
+def test_evict_by_a_view_of_wider_rows(clear):
+    """weights[:, :, :n] of wide rows: the result of rows of n, nothing past n touched."""
+    w = wl.random_case(3425, B=3, Hq=8, Hkv=2, lens=[300, 120, 33])
+    wt = torch.rand(3, 2, 301, generator=torch.Generator().manual_seed(4)) + 0.5
+    got = []
+    for width in (301, 5000):
+        k, v = w.k_pool.cuda(), w.v_pool.cuda()
+        big = torch.full((3, 2, width), 9.0, device="cuda")
+        big[:, :, :301] = wt.cuda()
+        new, kept = zl.kv_evict(k, v, torch.from_numpy(w.block_table).cuda(),
+                                torch.from_numpy(w.seq_lens).cuda(), big[:, :, :301],
+                                page_size=16, budget=100, sink=2, recent=9, clear_weights=clear)
+        got.append((new, kept, k.view(torch.int16), v.view(torch.int16),
+                    big[:, :, :301].contiguous()))
+        assert bool((big[:, :, 301:] == 9.0).all())
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_clear_leaves_bad_sequences_alone():
     w = wl.random_case(3430, B=3, Hq=8, Hkv=2, lens=[100, 90, 80])
     sl = torch.tensor([-1, 101, 80], dtype=torch.int32).cuda()
