@@ -358,8 +358,9 @@ zl_status zl_kv_append(const zl_kv_append_params* params, zl_stream_t stream);
  * need not be mapped; rows that some query sees and others do not must be
  * finite. A NaN or +inf score (after the cap) of a token that a query row sees
  * makes that row's out and lse NaN, and the weights of the tokens it sees; it
- * is no device error, and other rows do not change. A -inf score weighs 0; a
- * row with no other scores is one that sees no token.
+ * is no device error, and other rows keep their results (within the usual
+ * rounding). A -inf score weighs 0; a row with no other scores is one that sees
+ * no token.
  */
 typedef struct {
   size_t struct_size;        /* sizeof(zl_score_params) */

@@ -5,9 +5,9 @@
 // One block per (sequence, kv head, 256-byte column part of K or V): at most
 // 128 rows of 256 bytes, 8 chunks of 16 bytes per thread, all read before any
 // is written, so any path is safe in place. The first block of a (sequence, kv
-// head) also moves the tokens' sums of weights, the same way. The whole call is a few hundred
-// KB: it is bound by the chain of dependent reads (length, path, page, row),
-// which all blocks walk at once.
+// head) also moves the tokens' sums of weights, the same way. The whole call is
+// a few hundred KB: it is bound by the chain of dependent reads (length, path,
+// page, row), which all blocks walk at once.
 #include "kv_move.cuh"
 #include "kernels.h"
 #include "ptx.cuh"

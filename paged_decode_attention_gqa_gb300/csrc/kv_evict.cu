@@ -10,8 +10,8 @@
 // row (32 in long rows): its counts and a scan over threads and CTAs give the
 // place of every kept token, so no atomic decides an order and the result is
 // always the same. A CTA keeps its part of the weights in shared memory; they
-// are read from memory once. What bounds it is the chain of passes and their barriers and the
-// instructions per token, not the 4 bytes. The instance goes by the length of
+// are read from memory once. What bounds it is the chain of passes and their
+// barriers and the instructions per token, not the 4 bytes. The instance goes by the length of
 // the weights rows, which is all the host knows: rows far longer than the
 // sequences cost passes over nothing (64 x 8 rows of 2049-4096 tokens to 2048,
 // both launches: 200 us in rows of 4096, 249 of 32768, 464 of 131072, and 607

@@ -1,6 +1,6 @@
 """Modified scores that are no finite numbers: the rows that see them are NaN,
 however the call is cut and whichever kernel runs it, no page is called bad,
-and every other row is what it is without them."""
+and every other row is within its bounds."""
 import numpy as np
 import pytest
 import torch
