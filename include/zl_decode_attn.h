@@ -503,6 +503,199 @@ typedef struct {
 
 zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t stream);
 
+/*
+ * A K/V cache held in 4 bits. One pool of bytes: row (page, slot, head) of
+ * ZL_Q4_ROW_BYTES bytes starts at page * page_stride + slot * token_stride +
+ * head * head_stride (bytes, multiples of 16; the base 16-byte aligned), so that
+ * [num_pages, page_size, Hkv, 144] ("NHD") and [num_pages, Hkv, page_size, 144]
+ * ("HND") are both expressible. Heads have 128 elements. A row holds
+ *   bytes   0 ..  63  K's codes: element d in byte d / 2, the even one low
+ *   bytes  64 .. 127  V's codes
+ *   bytes 128 .. 135  K's scales, one per 16 elements
+ *   bytes 136 .. 143  V's scales
+ * A code's bit 3 is the sign, its bits 0 .. 2 pick 0, 0.5, 1, 1.5, 2, 3, 4 or 6. A
+ * scale is a byte of 5 exponent bits (bias 15) and 3 mantissa bits: the fp16
+ * number of bits byte << 7. An element's value is code value * scale.
+ *
+ * Writing a block of 16 elements x: scale = max |x| / 6, rounded to the nearest
+ * such number (ties to even), at most 10240; code = x / scale rounded to the
+ * nearest of the values (ties to the even code; beyond 6: 6; its sign is x's, also
+ * where it is 0). With scale 0 (max |x| at most 6 * 2^-18) all are zeros. Both
+ * roundings are exact: which side of a border a quotient lies on is decided without
+ * error. A block that holds a NaN or an infinity gets scale byte 255 and codes 0:
+ * all 16 read back as NaN. A value has at most 6 significant bits, so it is exact in
+ * bf16 and, with the scales above, in fp16.
+ *
+ * The pool is also a bf16 pool of 72 elements per row without V (v_pool NULL, D_k
+ * 72, strides halved): zl_kv_commit and zl_kv_evict move its rows so.
+ *
+ * The block table, seq_lens, page_size and num_pages mean what they mean in
+ * zl_decode_attn_params, and the conventions at the top hold. All data of a
+ * sequence with a bad length (ZL_DEVERR_BAD_SEQ_LEN) or a token on a bad page
+ * (ZL_DEVERR_BAD_PAGE) is left as it was.
+ */
+#define ZL_Q4_ROW_BYTES 144
+
+/*
+ * Store new tokens' K and V rows in the pool, quantised.
+ *   - k_new, v_new: bf16, row (sequence b, token i, head h) of 128 elements at
+ *     (b * q_len + i) * k_stride (v_stride) + h * 128 elements; strides are
+ *     multiples of 8 and at least Hkv * 128, the bases 16-byte aligned.
+ *   - new_lens NULL: token i < q_len of sequence b is position seq_lens[b] - q_len
+ *     + i, as in zl_kv_append. Otherwise int32 [B]: sequence b has n = new_lens[b]
+ *     new tokens, its first n rows (the rest is padding, not read), token i at
+ *     position seq_lens[b] - n + i. seq_lens count the new tokens.
+ *   - Device data errors: seq_lens[b] below the number of new tokens or above
+ *     block_table_stride * page_size, or new_lens[b] outside [0, q_len], stores
+ *     nothing of the sequence (ZL_DEVERR_BAD_SEQ_LEN).
+ *   - No page of these sequences may be mapped by another one, or twice. The new
+ *     rows must not overlap the pool.
+ */
+typedef struct {
+  size_t struct_size; /* sizeof(zl_kv_append_q4_params) */
+  const void* k_new;
+  const void* v_new;
+  int64_t k_stride, v_stride;
+  void* pool;
+  int64_t page_stride, token_stride, head_stride; /* bytes */
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  const int32_t* new_lens; /* or NULL */
+  int32_t B, q_len, Hkv, page_size, num_pages;
+  uint32_t* err_flags; /* optional */
+} zl_kv_append_q4_params;
+
+zl_status zl_kv_append_q4(const zl_kv_append_q4_params* params, zl_stream_t stream);
+
+/*
+ * Read the cached tokens back: k_out, v_out bf16 [B, tokens, Hkv, 128],
+ * contiguous, 32-byte aligned; either may be NULL. Rows t < seq_lens[b] are
+ * written (exactly the values that the codes stand for), rows behind them are left
+ * as they were, and so is the row of a token on a bad page.
+ *   - Device data errors: seq_lens[b] < 0, above block_table_stride * page_size or
+ *     above tokens: nothing of the sequence is written (ZL_DEVERR_BAD_SEQ_LEN).
+ */
+typedef struct {
+  size_t struct_size; /* sizeof(zl_kv_read_q4_params) */
+  const void* pool;
+  int64_t page_stride, token_stride, head_stride; /* bytes */
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  void* k_out; /* or NULL */
+  void* v_out; /* or NULL */
+  int32_t B, tokens, Hkv, page_size, num_pages;
+  uint32_t* err_flags; /* optional */
+} zl_kv_read_q4_params;
+
+zl_status zl_kv_read_q4(const zl_kv_read_q4_params* params, zl_stream_t stream);
+
+/*
+ * zl_decode_attn over such a pool: out and lse from the values that it holds.
+ *   - q, out bf16 [B, q_len, Hq, 128], lse fp32 [B, q_len, Hq] or NULL, causal
+ *     positions, grouped heads, max_seq_len, num_ctas (0 = the default), scale,
+ *     workspace and device errors as for zl_decode_attn. Results do not depend on
+ *     max_seq_len except within fp32 rounding.
+ *   - Supported: Hq % Hkv == 0, Hq / Hkv <= 128, 1 <= q_len <= 128, page_size a
+ *     multiple of 16 (<= 1024), 1 <= B <= 4096; B * (tiles of 16 tokens that the
+ *     block table reaches) below 2^31, and times Hkv below 2^40.
+ *   - A query row that holds a NaN or an infinity and sees a token gives NaN (out
+ *     and lse), and so does a row that sees a K or V block of scale 255 (K: the
+ *     whole row; V: those 16 elements) or has a score beyond 32 bits. V rows that
+ *     some query tokens of a call see and others do not must be finite.
+ */
+typedef struct {
+  size_t struct_size; /* sizeof(zl_decode_attn_q4_params) */
+  const void* q;
+  const void* pool;
+  int64_t page_stride, token_stride, head_stride; /* bytes */
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  void* out;
+  float* lse; /* or NULL */
+  int32_t B, q_len, Hq, Hkv, page_size, num_pages;
+  int32_t max_seq_len;
+  float scale;
+  void* workspace; /* 256-byte aligned, contents need no initialisation */
+  size_t workspace_bytes;
+  uint32_t* err_flags; /* optional */
+  int32_t num_ctas;
+} zl_decode_attn_q4_params;
+
+zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* params, zl_stream_t stream);
+
+/* Workspace bytes zl_decode_attn_q4 needs, from the shapes, num_ctas and
+   max_seq_len. */
+zl_status zl_decode_attn_q4_workspace_size(const zl_decode_attn_q4_params* params, size_t* bytes);
+
+/*
+ * Queries and keys between the projection and the attention, in one pass: a norm
+ * over each head, the rotation by position, and the store in the cache.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     over the 128 elements of a head
+ * (a NULL weight: y = x), then for i < n_freq the pair (i, n_freq + i) of y, with
+ * interleaved (2 i, 2 i + 1), is turned by the angle positions[axis of i] * freq[i]:
+ *   (a, b) -> rope_scale * (a cos - b sin, b cos + a sin)
+ * The elements from 2 * n_freq on are not turned (nor scaled). Everything is
+ * computed in 32 bits, the angle exactly for any int32 position, and rounded to
+ * bf16 once.
+ *   - q, k, v: bf16, row (sequence b, token i, head h) of 128 elements at (b *
+ *     q_len + i) * q_stride (k_stride, v_stride) + h * 128: slices of a fused
+ *     projection's output are taken as they are. Strides multiples of 8, at least
+ *     the heads * 128; bases 16-byte aligned. So are q_out and k_out. q_out may be
+ *     q with q's stride, k_out may be k; otherwise what is written must overlap
+ *     nothing that is read.
+ *   - freq_turns: host array of n_freq numbers, freq[i] in turns per position
+ *     times 2^64 (freq radians / (2 pi), modulo 1, rounded); axes: host array of
+ *     n_freq axis numbers below n_axes, or NULL (all 0). n_freq a multiple of 16,
+ *     at most 64; 0: no rotation.
+ *   - positions: int32, axis a of token (b, i) at a * axis_stride + b * q_len + i;
+ *     NULL: seq_lens[b] - q_len + i on every axis (the token's place in the cache).
+ *   - cache ZL_CACHE_NONE: k_out gets the keys; v, the pools and the block table
+ *     are not used. ZL_CACHE_BF16: keys and the rows of v go to k_pool and v_pool as
+ *     zl_kv_append would put them (pool strides in elements). ZL_CACHE_Q4: to the
+ *     4-bit pool k_pool (v_pool NULL, strides in bytes) as zl_kv_append_q4 would put
+ *     the bf16 keys, bit for bit. k_out may then be NULL.
+ *   - Device data errors (with a cache): a sequence of fewer than q_len tokens or
+ *     beyond the block table's reach stores nothing in the cache
+ *     (ZL_DEVERR_BAD_SEQ_LEN), a token on a bad page neither
+ *     (ZL_DEVERR_BAD_PAGE); q_out and k_out are written all the same.
+ *   - Supported: Hq, Hkv <= 65535, n_axes <= 4.
+ */
+typedef enum { ZL_CACHE_NONE = 0, ZL_CACHE_BF16 = 1, ZL_CACHE_Q4 = 2 } zl_cache_kind;
+
+typedef struct {
+  size_t struct_size; /* sizeof(zl_qk_norm_rope_params) */
+  const void* q;
+  const void* k;
+  const void* v; /* with a cache */
+  int64_t q_stride, k_stride, v_stride;
+  void* q_out;
+  void* k_out;
+  int64_t q_out_stride, k_out_stride;
+  const float* q_weight; /* fp32 [128], 16-byte aligned, or NULL */
+  const float* k_weight; /* or NULL */
+  float eps;
+  float rope_scale;
+  const uint64_t* freq_turns; /* host */
+  const uint8_t* axes;        /* host, or NULL */
+  int32_t n_freq, n_axes, interleaved;
+  int32_t cache; /* zl_cache_kind */
+  const int32_t* positions; /* or NULL */
+  int64_t axis_stride;
+  void* k_pool;
+  void* v_pool;
+  int64_t page_stride, token_stride, head_stride;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* seq_lens;
+  int32_t B, q_len, Hq, Hkv, page_size, num_pages;
+  uint32_t* err_flags; /* optional */
+} zl_qk_norm_rope_params;
+
+zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* params, zl_stream_t stream);
+
 /* Static description of a status code. */
 const char* zl_status_string(zl_status status);
 

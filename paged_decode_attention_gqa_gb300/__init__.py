@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import re
 import struct
@@ -26,8 +27,11 @@ import torch
 from ._build import LIB_PATH, build  # noqa: F401  (build() is the public build step)
 
 __all__ = [
-    "ZlError", "Params", "AppendParams", "ScoreParams", "EvictParams", "CommitParams", "lib",
+    "ZlError", "Params", "AppendParams", "ScoreParams", "EvictParams", "CommitParams",
+    "AppendQ4Params", "ReadQ4Params", "DecodeQ4Params", "NormRopeParams", "lib",
     "decode_attn", "decode_attn_mla", "kv_append", "kv_evict", "kv_commit", "tree_mask",
+    "decode_attn_q4", "kv_append_q4", "kv_read_q4", "qk_norm_rope", "Rope", "rope_frequencies",
+    "Q4_ROW_BYTES",
     "workspace_size", "workspace_size_mla", "workspace_size_ex", "call", "call_ex",
     "call_noalloc", "build", "LIB_PATH",
     "DEVERR_BAD_PAGE", "DEVERR_BAD_SEQ_LEN", "DEVERR_TIMEOUT", "DEVERR_BAD_PATH", "HEADER",
@@ -43,6 +47,8 @@ TEST_STALL = 0x80000000  # ZL_DECODE_TEST_STALL (failure-detection test hook)
 DEVERR_BAD_PAGE, DEVERR_BAD_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_BAD_PREFIX = 1, 2, 4, 8
 DEVERR_BAD_PATH = 16
 NOALLOC_WORKSPACE_BYTES = 8 << 20  # ZL_NOALLOC_WORKSPACE_BYTES
+Q4_ROW_BYTES = 144  # ZL_Q4_ROW_BYTES
+CACHE_NONE, CACHE_BF16, CACHE_Q4 = range(3)  # zl_cache_kind
 
 
 class ZlError(RuntimeError):
@@ -199,6 +205,126 @@ class CommitParams(ctypes.Structure):
     ]
 
 
+class AppendQ4Params(ctypes.Structure):
+    """Mirror of zl_kv_append_q4_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("err_flags", ctypes.c_void_p),
+    ]
+
+
+class ReadQ4Params(ctypes.Structure):
+    """Mirror of zl_kv_read_q4_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("tokens", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("err_flags", ctypes.c_void_p),
+    ]
+
+
+class DecodeQ4Params(ctypes.Structure):
+    """Mirror of zl_decode_attn_q4_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("q", ctypes.c_void_p),
+        ("pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("err_flags", ctypes.c_void_p),
+        ("num_ctas", ctypes.c_int32),
+    ]
+
+
+class NormRopeParams(ctypes.Structure):
+    """Mirror of zl_qk_norm_rope_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("rope_scale", ctypes.c_float),
+        ("freq_turns", ctypes.c_void_p),
+        ("axes", ctypes.c_void_p),
+        ("n_freq", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("cache", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+        ("axis_stride", ctypes.c_int64),
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("seq_lens", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("err_flags", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -236,6 +362,16 @@ def lib():
             handle.zl_kv_evict.argtypes = [ctypes.POINTER(EvictParams), ctypes.c_void_p]
             handle.zl_kv_commit.restype = ctypes.c_int
             handle.zl_kv_commit.argtypes = [ctypes.POINTER(CommitParams), ctypes.c_void_p]
+            for name, mirror in (("zl_kv_append_q4", AppendQ4Params),
+                                 ("zl_kv_read_q4", ReadQ4Params),
+                                 ("zl_decode_attn_q4", DecodeQ4Params),
+                                 ("zl_qk_norm_rope", NormRopeParams)):
+                fn = getattr(handle, name)
+                fn.restype = ctypes.c_int
+                fn.argtypes = [ctypes.POINTER(mirror), ctypes.c_void_p]
+            handle.zl_decode_attn_q4_workspace_size.restype = ctypes.c_int
+            handle.zl_decode_attn_q4_workspace_size.argtypes = [ctypes.POINTER(DecodeQ4Params),
+                                                                ctypes.POINTER(ctypes.c_size_t)]
             handle.zl_status_string.restype = ctypes.c_char_p
             handle.zl_status_string.argtypes = [ctypes.c_int]
             _lib = handle
@@ -401,8 +537,13 @@ _PARAMS = struct.Struct("@N3P3qPq3P9ifPNPi2PIi2P0P")
 _SCORES = struct.Struct("@Nfi3P2qif0P")
 _EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iPi0P")
 _COMMIT = struct.Struct("@N2P3qPq2PqPP8i2P2qi0P")
+_APPEND_Q4 = struct.Struct("@N2P2qP3qPq2P5iP0P")
+_READ_Q4 = struct.Struct("@NP3qPq3P5iP0P")
+_DECODE_Q4 = struct.Struct("@N2P3qPq3P7ifPNPi0P")
+_NORM_ROPE = struct.Struct("@N3P3q2P2q2P2f2P4iPq2P3qPqP6iP0P")
 for _s, _c in ((_PARAMS, Params), (_SCORES, ScoreParams), (_EVICT, EvictParams),
-               (_COMMIT, CommitParams)):
+               (_COMMIT, CommitParams), (_APPEND_Q4, AppendQ4Params), (_READ_Q4, ReadQ4Params),
+               (_DECODE_Q4, DecodeQ4Params), (_NORM_ROPE, NormRopeParams)):
     assert _s.size == ctypes.sizeof(_c), _c.__name__
 
 
@@ -873,3 +1014,343 @@ def kv_commit(k_pool, v_pool, block_table, seq_lens, path, accepted, *, page_siz
     if status != OK:
         _check(status, "zl_kv_commit")
     return new_lens
+
+
+# ------------------------------------------------------------- a cache in 4 bits
+def _pool_layout(shape, st, layout):
+    """(slots, heads, page stride, token stride, head stride) of a 4-D pool."""
+    if len(shape) != 4:
+        raise ValueError("pools are 4-D: [pages, slot, head, dim] (NHD) or "
+                         "[pages, head, slot, dim] (HND)")
+    if st[3] != 1:
+        raise ValueError("pool rows must be contiguous")
+    if layout == "NHD":
+        return shape[1], shape[2], st[0], st[1], st[2]
+    if layout == "HND":
+        return shape[2], shape[1], st[0], st[2], st[1]
+    raise ValueError(f"unknown layout {layout!r}")
+
+
+def _expect_table(block_table, seq_lens, index, err_flags):
+    """Block table, lengths and error word; returns (B, addresses of the table, its
+    stride, of seq_lens and err_flags)."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D")
+    B, width = block_table.shape
+    sl_at = _expect(seq_lens, "seq_lens", _I32, (B,), index)
+    bt_at = _expect(block_table, "block_table", _I32, (B, width), index, False)
+    bt_stride, one = block_table.stride()
+    if B == 1:
+        bt_stride = width
+    if (width > 1 and one != 1) or bt_stride < width:
+        raise ValueError("block_table rows must be contiguous and distinct")
+    err = 0
+    if err_flags is not None:
+        if err_flags.dtype is not _I32 and err_flags.dtype is not _U32 or err_flags.numel() < 1:
+            raise ValueError("err_flags must be a 32-bit integer tensor")
+        if err_flags.get_device() != index:
+            raise ValueError(f"err_flags is on {err_flags.device}, the pool on device {index}")
+        err = err_flags.data_ptr()
+    return B, bt_at, bt_stride, sl_at, err
+
+
+def _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags):
+    """The checks every call over a 4-bit cache shares; returns (device index, B, Hkv,
+    num_pages, address, strides in (page, token, head) order, then the block table,
+    its stride, seq_lens and err_flags)."""
+    index = pool.get_device()
+    if pool.dtype is not torch.uint8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
+        raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes: "
+                         "[pages, slot, head, row] (NHD) or [pages, head, slot, row] (HND)")
+    slots, Hkv, ps, ts, hs = _pool_layout(pool.shape, pool.stride(), layout)
+    if slots != page_size:
+        raise ValueError(f"the pool holds {slots} slots per page, page_size is {page_size}")
+    B, bt_at, bt_stride, sl_at, err = _expect_table(block_table, seq_lens, index, err_flags)
+    return (index, B, Hkv, pool.shape[0], pool.data_ptr(), ps, ts, hs, bt_at, bt_stride, sl_at,
+            err)
+
+
+def _expect_rows(t, name, B, q_len, heads, index):
+    """bf16 [B, q_len, heads, 128] whose heads lie side by side and whose tokens are
+    evenly spaced (a slice of a fused projection's output is); returns (address, token
+    stride)."""
+    at = _expect(t, name, _BF16, (B, q_len, heads, 128), index, False)
+    if t.is_contiguous():
+        return at, heads * 128
+    sb, st, sh, one = t.stride()
+    if one != 1 or (heads > 1 and sh != 128):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    if q_len == 1:
+        st = sb if B > 1 else heads * 128
+    elif B > 1 and sb != q_len * st:
+        raise ValueError(f"{name}: the tokens must be evenly spaced across the batch")
+    return at, st
+
+
+def kv_append_q4(k_new, v_new, pool, block_table, seq_lens, *, page_size, new_lens=None,
+                 layout="NHD", err_flags=None, stream=None):
+    """Store new tokens' K and V rows in a 4-bit cache, quantised (zl_kv_append_q4).
+
+    k_new, v_new [B, q_len, Hkv, 128] bf16 (slices of a fused projection's output are
+    taken as they are); pool uint8 [pages, page_size, Hkv, 144] (layout "NHD") or
+    [pages, Hkv, page_size, 144] ("HND"); block_table and seq_lens as for kv_append
+    (seq_lens count the new tokens). new_lens int32 [B]: a padded batch; sequence b's
+    new tokens are its first new_lens[b] rows.
+    """
+    (index, B, Hkv, pages, at, ps, ts, hs, bt_at, bt_stride, sl_at,
+     err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B, q_len, Hkv, 128]")
+    q_len = k_new.shape[1]
+    k_at, k_st = _expect_rows(k_new, "k_new", B, q_len, Hkv, index)
+    v_at, v_st = _expect_rows(v_new, "v_new", B, q_len, Hkv, index)
+    n_at = 0
+    if new_lens is not None:
+        n_at = _expect(new_lens, "new_lens", _I32, (B,), index)
+    on, _ = _on(index, stream)
+    status = _raw_fn("zl_kv_append_q4", 1)(_pack(
+        _APPEND_Q4, _APPEND_Q4.size, k_at, v_at, k_st, v_st, at, ps, ts, hs, bt_at, bt_stride,
+        sl_at, n_at, B, q_len, Hkv, page_size, pages, err), on)
+    if status != OK:
+        _check(status, "zl_kv_append_q4")
+
+
+def kv_read_q4(pool, block_table, seq_lens, *, page_size, tokens=None, k_out=None, v_out=None,
+               layout="NHD", err_flags=None, stream=None):
+    """Read a 4-bit cache's tokens back as bf16 (zl_kv_read_q4).
+
+    Writes rows t < seq_lens[b] of k_out and v_out [B, tokens, Hkv, 128] bf16 (exactly
+    the values the codes stand for) and leaves the rows behind them as they are; tokens
+    must hold the longest sequence. Without k_out and v_out, both are made (zeros behind
+    the lengths) for the given ``tokens``; with one of them, only that is written.
+    Returns (k_out, v_out).
+    """
+    (index, B, Hkv, pages, at, ps, ts, hs, bt_at, bt_stride, sl_at,
+     err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
+    given = k_out if k_out is not None else v_out
+    if given is not None:
+        if given.dim() != 4:
+            raise ValueError("k_out and v_out must be [B, tokens, Hkv, 128]")
+        if tokens is not None and tokens != given.shape[1]:
+            raise ValueError(f"tokens is {tokens}, the outputs hold {given.shape[1]}")
+        tokens = given.shape[1]
+    elif tokens is None or tokens < 1:
+        raise ValueError("tokens (at least the longest sequence) or the outputs are required")
+    on, scratch = _on(index, stream)
+    if given is None:
+        with scratch:
+            k_out = torch.zeros(B, tokens, Hkv, 128, dtype=_BF16, device=pool.device)
+            v_out = torch.zeros_like(k_out)
+    k_at = v_at = 0
+    if k_out is not None:
+        k_at = _expect(k_out, "k_out", _BF16, (B, tokens, Hkv, 128), index)
+    if v_out is not None:
+        v_at = _expect(v_out, "v_out", _BF16, (B, tokens, Hkv, 128), index)
+    status = _raw_fn("zl_kv_read_q4", 1)(_pack(
+        _READ_Q4, _READ_Q4.size, at, ps, ts, hs, bt_at, bt_stride, sl_at, k_at, v_at, B, tokens,
+        Hkv, page_size, pages, err), on)
+    if status != OK:
+        _check(status, "zl_kv_read_q4")
+    return k_out, v_out
+
+
+def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None, lse=None,
+                   workspace=None, err_flags=None, num_ctas=0, max_seq_len=0, layout="NHD",
+                   stream=None):
+    """Paged decode attention over a 4-bit cache (zl_decode_attn_q4).
+
+    q [B, q_len, Hq, 128] bf16; pool uint8 [pages, page_size, Hkv, 144] (layout "NHD") or
+    [pages, Hkv, page_size, 144] ("HND"), as kv_append_q4 or qk_norm_rope fill it;
+    block_table int32 [B, max_pages], seq_lens int32 [B]: as for decode_attn, the q_len
+    query tokens being the last cached ones. Returns out [B, q_len, Hq, 128] bf16; lse
+    fp32 [B, q_len, Hq] is written when given.
+    """
+    (index, B, Hkv, pages, at, ps, ts, hs, bt_at, bt_stride, sl_at,
+     err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, q_len, Hq, 128]")
+    shape = q.shape
+    _, q_len, Hq, _ = shape
+    q_at = _expect(q, "q", _BF16, (B, q_len, Hq, 128), index)
+    out_at = lse_at = 0
+    if out is not None:
+        out_at = _expect(out, "out", _BF16, shape, index)
+    if lse is not None:
+        lse_at = _expect(lse, "lse", _F32, (B, q_len, Hq), index)
+    on, scratch = _on(index, stream)
+
+    def params(out_at, ws_at, ws_bytes):
+        return _pack(_DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at,
+                     out_at, lse_at, B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale,
+                     ws_at, ws_bytes, err, num_ctas)
+
+    with scratch:
+        if out is None:
+            out = torch.empty(shape, dtype=_BF16, device=q.device)
+            out_at = out.data_ptr()
+        if workspace is None:  # a call's own, as in _run_ex
+            key = ("q4", index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len)
+            ws_bytes = _sizes.get(key)
+            if ws_bytes is None:
+                n = ctypes.c_size_t(0)
+                _check(_raw_fn("zl_decode_attn_q4_workspace_size", 1)(
+                    params(out_at, 0, 0), ctypes.addressof(n)),
+                    "zl_decode_attn_q4_workspace_size")
+                if len(_sizes) >= 4096:
+                    _sizes.clear()
+                ws_bytes = _sizes[key] = n.value
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous and on the pool's device")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        status = _raw_fn("zl_decode_attn_q4", 1)(
+            params(out_at, workspace.data_ptr(), ws_bytes), on)
+        if status != OK:
+            _check(status, "zl_decode_attn_q4")
+    return out
+
+
+def rope_frequencies(dim=128, base=10000.0):
+    """The usual rotation frequencies of ``dim`` rotated elements, in radians per
+    position: base^(-2 i / dim), i < dim / 2 (a list of floats, for Rope)."""
+    return [float(base) ** (-2.0 * i / dim) for i in range(dim // 2)]
+
+
+class Rope:
+    """A rotation by position, laid out once for qk_norm_rope.
+
+    frequencies: radians per position of each rotated pair (numbers in 64 bits on the
+    host; 16, 32, 48 or 64 of them: twice as many elements of a head are rotated, the
+    first ones), scaled as a model wants them. axes: which row of the positions each
+    follows (default: all the first). interleaved: pairs are (2 i, 2 i + 1) instead of
+    (i, n + i). scale: factor of the rotated elements.
+    """
+
+    def __init__(self, frequencies, *, axes=None, interleaved=False, scale=1.0):
+        freq = [float(f) for f in frequencies]
+        axes = [0] * len(freq) if axes is None else [int(a) for a in axes]
+        if len(axes) != len(freq):
+            raise ValueError("axes must name one axis for every frequency")
+        if any(not math.isfinite(f) for f in freq) or any(not 0 <= a < 4 for a in axes):
+            raise ValueError("frequencies must be finite, axes 0 to 3")
+        self.n_freq, self.interleaved, self.scale = len(freq), bool(interleaved), float(scale)
+        self.n_axes = max(axes, default=0) + 1
+        # turns per position, 64 bits behind the point: f / (2 pi) in whole numbers, as
+        # a float's quotient would not hold the digits that position * turns needs
+        turns = []
+        for f in freq:
+            num, den = f.as_integer_ratio()
+            turns.append((2 * num * _INV_TWO_PI + (den << 192)) // (den << 193) % (1 << 64))
+        self._turns = (ctypes.c_uint64 * max(1, len(freq)))(*turns)
+        self._axes = (ctypes.c_uint8 * max(1, len(freq)))(*axes)
+        self.turns_at, self.axes_at = ctypes.addressof(self._turns), ctypes.addressof(self._axes)
+
+
+# 2^256 / (2 pi), from pi to 80 digits
+_INV_TWO_PI = ((10 ** 80 << 255)
+               // 314159265358979323846264338327950288419716939937510582097494459230781640628620899)
+_NO_ROPE = Rope([])
+
+
+def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                 q_out=None, k_out=None, v=None, k_pool=None, v_pool=None, pool=None,
+                 block_table=None, seq_lens=None, page_size=0, layout="NHD", err_flags=None,
+                 stream=None):
+    """Norm and rotation of queries and keys per head, in one pass (zl_qk_norm_rope).
+
+    q [B, q_len, Hq, 128], k [B, q_len, Hkv, 128] bf16 (slices of a fused projection's
+    output are taken as they are). q_weight, k_weight fp32 [128]: RMS norm over each head
+    with eps; None: no norm. rope (Rope): the rotation, None: none. positions int32
+    [B, q_len], or [axes, B, q_len] for a rope of several axes; None: the tokens' places
+    in the cache, seq_lens[b] - q_len + i. q_out and k_out may be q and k themselves.
+
+    With a cache the keys and the rows of v [B, q_len, Hkv, 128] also go to their page
+    slots: bf16 pools k_pool, v_pool as kv_append would store them, or the 4-bit ``pool``
+    as kv_append_q4 would. k_out is then written only when given. Returns (q_out, k_out).
+    """
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, q_len, heads, 128]")
+    index = q.get_device()
+    B, q_len, Hq, _ = q.shape
+    Hkv = k.shape[2]
+    q_at, q_st = _expect_rows(q, "q", B, q_len, Hq, index)
+    k_at, k_st = _expect_rows(k, "k", B, q_len, Hkv, index)
+    cache, v_at, v_st, kp = CACHE_NONE, 0, 0, None
+    vp_at = ps = ts = hs = bt_at = bt_stride = sl_at = err = pages = 0
+    if pool is not None:
+        if k_pool is not None or v_pool is not None:
+            raise ValueError("either the bf16 pools or the 4-bit one")
+        cache, kp = CACHE_Q4, pool
+        if pool.dtype is not torch.uint8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
+            raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes")
+    elif k_pool is not None or v_pool is not None:
+        if k_pool is None or v_pool is None:
+            raise ValueError("k_pool and v_pool are given together")
+        cache, kp = CACHE_BF16, k_pool
+        if k_pool.dtype is not _BF16 or k_pool.dim() != 4 or k_pool.shape[3] != 128:
+            raise ValueError("k_pool must be bf16 with rows of 128 elements")
+        vp_at = _expect(v_pool, "v_pool", _BF16, tuple(k_pool.shape), index, False)
+        if v_pool.stride() != k_pool.stride():
+            raise ValueError("K and V pools must share strides")
+    if cache:
+        if v is None or block_table is None or seq_lens is None:
+            raise ValueError("storing in a cache needs v, block_table and seq_lens")
+        if kp.get_device() != index:
+            raise ValueError(f"the pool is on {kp.device}, q on device {index}")
+        slots, heads, ps, ts, hs = _pool_layout(kp.shape, kp.stride(), layout)
+        if slots != page_size or heads != Hkv:
+            raise ValueError(f"the pool holds {slots} slots per page and {heads} heads; page_size "
+                             f"is {page_size}, k has {Hkv} heads")
+        v_at, v_st = _expect_rows(v, "v", B, q_len, Hkv, index)
+        rows, bt_at, bt_stride, sl_at, err = _expect_table(block_table, seq_lens, index, err_flags)
+        if rows != B:
+            raise ValueError(f"block_table has {rows} rows for {B} sequences")
+        pages = kp.shape[0]
+    elif seq_lens is not None:
+        sl_at = _expect(seq_lens, "seq_lens", _I32, (B,), index)
+    if rope is None:
+        rope = _NO_ROPE
+    pos_at = axis_st = 0
+    if positions is not None:
+        if positions.dim() == 2:
+            if rope.n_axes > 1:
+                raise ValueError(f"the rope follows {rope.n_axes} axes: positions must be "
+                                 "[axes, B, q_len]")
+            pos_at = _expect(positions, "positions", _I32, (B, q_len), index)
+        else:
+            n = positions.shape[0] if positions.dim() == 3 else 0
+            if n < rope.n_axes:
+                raise ValueError(f"positions must be [B, q_len], or [axes, B, q_len] with at least "
+                                 f"{rope.n_axes} axes")
+            pos_at = _expect(positions, "positions", _I32, (n, B, q_len), index)
+        axis_st = B * q_len
+    elif rope.n_freq and not sl_at:
+        raise ValueError("a rotation needs positions, or seq_lens")
+    qw = kw = 0
+    if q_weight is not None:
+        qw = _expect(q_weight, "q_weight", _F32, (128,), index)
+    if k_weight is not None:
+        kw = _expect(k_weight, "k_weight", _F32, (128,), index)
+    ko_at = ko_st = 0
+    if q_out is not None:
+        qo_at, qo_st = _expect_rows(q_out, "q_out", B, q_len, Hq, index)
+    if k_out is not None:
+        ko_at, ko_st = _expect_rows(k_out, "k_out", B, q_len, Hkv, index)
+    on, scratch = _on(index, stream)
+    if q_out is None or (k_out is None and not cache):
+        with scratch:
+            if q_out is None:
+                q_out = torch.empty((B, q_len, Hq, 128), dtype=_BF16, device=q.device)
+                qo_at, qo_st = q_out.data_ptr(), Hq * 128
+            if k_out is None and not cache:
+                k_out = torch.empty((B, q_len, Hkv, 128), dtype=_BF16, device=q.device)
+                ko_at, ko_st = k_out.data_ptr(), Hkv * 128
+    status = _raw_fn("zl_qk_norm_rope", 1)(_pack(
+        _NORM_ROPE, _NORM_ROPE.size, q_at, k_at, v_at, q_st, k_st, v_st, qo_at, ko_at, qo_st,
+        ko_st, qw, kw, eps, rope.scale, rope.turns_at, rope.axes_at, rope.n_freq, rope.n_axes,
+        rope.interleaved, cache, pos_at, axis_st, kp.data_ptr() if cache else 0, vp_at, ps, ts, hs,
+        bt_at, bt_stride, sl_at, B, q_len, Hq, Hkv, page_size, pages, err), on)
+    if status != OK:
+        _check(status, "zl_qk_norm_rope")
+    return q_out, k_out

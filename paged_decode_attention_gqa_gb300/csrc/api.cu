@@ -3,6 +3,7 @@
 #include "../../include/zl_decode_attn.h"
 #include "gqa_wide.h"
 #include "kernels.h"
+#include "q4_host.h"
 
 #include <cudaTypedefs.h>
 
@@ -78,6 +79,27 @@ zl_status current_device(DeviceInfo* info) {
   info->sms = sm_count[dev];
   return ZL_OK;
 }
+
+}  // namespace
+
+// For the entry points of other files (q4_host.h).
+zl_status zl::sm_count(int* sms) {
+  DeviceInfo dev;
+  const zl_status st = current_device(&dev);
+  if (st == ZL_OK) *sms = dev.sms;
+  return st;
+}
+CUresult zl::encode_tiled(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, void* base,
+                          const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return CUDA_ERROR_NOT_INITIALIZED;
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+  return encode(map, type, rank, base, dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+namespace {
 
 // ------------------------------------------------------------------ GQA plan
 struct GqaPlan {
