@@ -21,7 +21,7 @@
 // - P^T in the layout of the second product comes out of the first one by a
 //   transposition of 8 x 8 fragments (movmatrix).
 //
-// Every warp streams the tiles (16 tokens of one kv head) of its own ring through
+// Every warp streams the tiles (32 tokens of one kv head) of its own ring through
 // TMA, one stage a tile, and is its own producer: no barrier between warps, but for
 // the merge of slices below. A CTA has HB x S warps: HB kv heads side by side (a
 // "bundle": with heads next to each other in memory their rows share sectors), S
@@ -29,20 +29,42 @@
 // are laid end to end and cut into equal ranges, one per CTA; slice s takes every
 // S-th tile. Slices are merged in shared memory at the end of each unit, units that
 // are cut between CTAs by a second, programmatically dependent launch, in CTA order.
+//
+// What an SM issues decides: an mma.sync holds the issue port for 8 cycles, every other
+// instruction for one, and nothing overlaps that (in registers alone, 16 conversions,
+// 16 products and 4 mma take the sum of it). A ring per CTA with copies for all its
+// heads at once, its warps taking turns at issuing them, needs fewer instructions and
+// was slower all the same: the warps then wait for one another.
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"
 
 #include <math_constants.h>
 
+#include <atomic>
 #include <cmath>
+#include <type_traits>
 
 namespace zl {
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kHalf = 16;  // tokens of one copy, within a page (page sizes are multiples)
+constexpr int kTile = 32;  // tokens of a ring stage: two such halves, on pages of their own
+constexpr int kHalfBytes = kHalf * kQ4Row;
 constexpr int kTileBytes = kTile * kQ4Row;
-constexpr int kMaxWarps = 8;
+constexpr int kMaxBundle = 8;
+// Warps of a CTA: 8, two CTAs to an SM; with 16 columns (more registers) 4, three CTAs.
+constexpr int max_warps(int nt) { return nt == 1 ? 8 : 4; }
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 3; }
+// What a unit costs beside its tiles (queries, the masked tile, the epilogue: some 6 us of
+// a warp that shares its scheduler with three, where a tile takes 1.7), in tiles of each
+// slice: places of the line that hold no tile. (32 sequences of 1000-8000 tokens, 32 heads
+// on one kv head: without 36 us, with 2 32, with 4 28; 64 sequences verifying 4 tokens
+// each: 77, 75, 72.)
+constexpr int kUnitCost = 4;
+// Units of at most this many tiles per slice get a CTA each where there are CTAs
+// enough: streaming them costs less than the merge of their parts.
+constexpr int kWholeTiles = 4;
 constexpr int kMaxDevices = 64;
 constexpr double kLog2e = 1.4426950408889634;
 // A row's softmax base moves when a score exceeds it by more than kMove, to kSlack
@@ -52,24 +74,25 @@ constexpr float kMove = 15.f;
 constexpr float kSlack = 7.f;
 
 struct Q4Params {
-  CUtensorMap tmap;  // 4-D bytes {144, page_size, Hkv, num_pages}, box {144, 16, 1, 1}
+  CUtensorMap tmap;  // 4-D bytes {144, page_size, Hkv, num_pages}, box {144, 16 or 32, 1, 1}
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* lse;
   const int32_t* block_table;
   int64_t bt_stride;
   const int32_t* seq_lens;
-  // workspace: tile prefix sums [B + 1] and the longest unit; partials of cut units,
-  // slots [CTA][2][HB][rr]: normalised outputs, base-2 lse (NaN: bad, +inf: no number)
-  int32_t* ws_prefix;
+  // workspace: partials of cut units, slots [CTA][2][HB][rr]: normalised outputs,
+  // base-2 lse (NaN: bad, +inf: no number)
   float* ws_lse;
   float* ws_o;
   uint32_t* err_flags;
   int B, q_len, Hq, Hkv, g, page_size, num_pages;
-  int HB, S, stages;     // heads of a bundle, slices, ring stages per warp
+  int HB, S, stages;     // heads of a bundle, slices, ring stages
   int units_per_seq;     // bundles x row groups
   int rgroups, rr, rows; // row groups of rr rows, rows = g * q_len of a kv head
   int ctas;              // CTAs of the attention kernel
+  int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
+  int whole;             // 1: CTA c takes unit c and there is no merge (max_seq_len is short)
   float scale_log2;
 };
 
@@ -85,17 +108,36 @@ __device__ __forceinline__ int tiles_of(const Q4Params& p, int L) {
 // How the line of W tiles is cut: G ranges, or (short units) one unit per CTA.
 struct Cut {
   int64_t W;
-  int G;
+  uint32_t G, Wr;
+  int64_t Wq;  // W = Wq G + Wr
   bool whole;  // CTA c takes unit c
   __device__ __forceinline__ Cut(const Q4Params& p, int64_t tiles, int longest) {
     W = tiles * p.units_per_seq;
     const int64_t units = int64_t(p.B) * p.units_per_seq;
-    whole = units <= p.ctas && longest <= 4 * p.S;
-    G = int(min(int64_t(p.ctas), max(W / (2 * p.S), int64_t(1))));
+    whole = p.whole || (units <= p.ctas && longest <= kWholeTiles * p.S);
+    if (W < (INT64_C(1) << 31)) {  // (nearly always: 64-bit divisions are slow)
+      const uint32_t w = uint32_t(W);
+      G = min(uint32_t(p.ctas), max(w / uint32_t(p.S), 1u));
+      Wq = w / G;
+      Wr = w - uint32_t(Wq) * G;
+    } else {
+      G = uint32_t(p.ctas);
+      Wq = W / G;
+      Wr = uint32_t(W - Wq * G);
+    }
   }
-  __device__ __forceinline__ int64_t start(int c) const { return W * c / G; }
-  // The CTA whose range holds tile x: the largest c with start(c) <= x.
-  __device__ __forceinline__ int owner(int64_t x) const { return int(((x + 1) * G - 1) / W); }
+  // floor(c W / G) (c Wr < G^2 < 2^32)
+  __device__ __forceinline__ int64_t start(int c) const {
+    return int64_t(c) * Wq + (uint32_t(c) * Wr) / G;
+  }
+  // The CTA whose range holds tile x: the largest c with start(c) <= x, from an
+  // estimate that is off by one at most.
+  __device__ __forceinline__ int owner(int64_t x) const {
+    int c = min(int(float(x) * (float(G) / float(W))), int(G) - 1);
+    while (start(c) > x) --c;
+    while (c + 1 < int(G) && start(c + 1) <= x) ++c;
+    return c;
+  }
 };
 
 // Largest b with units_per_seq * prefix[b] <= idx (sequences without tiles are
@@ -111,11 +153,28 @@ __device__ __forceinline__ int locate(const int32_t* prefix, int B, int m, int64
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with nothing added to.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// a where m is set, b elsewhere, in one instruction.
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "r"(m));
+  return d;
 }
 
 // 8 x 8 fragment of 16-bit elements, transposed across the warp.
@@ -135,14 +194,26 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Fragment row r of the 16 tokens of a tile is token tile_token(r): even rows of
+// Fragment row r of the 16 tokens of a half is token half_token(r): even rows of
 // each half take tokens 0, 2, 4, 6 (second half: 1, 3, 5, 7), odd ones 12, 14, 8, 10
 // (13, 15, 9, 11). Rows of 36 words: with neighbouring rows 4 mod 8 tokens apart the
 // K reads, and with a lane's four V tokens 2 mod 8 apart the V reads, touch every
 // bank once.
-__device__ __forceinline__ int tile_token(int r) {
+__device__ __forceinline__ int half_token(int r) {
   const int k = r & 7;
   return ((k & 1) ? ((k + 3) & 7) + 8 : k) + (r >> 3);
+}
+
+// To 1 ulp, and to 2^-22 (the outputs are rounded to 2^-9 and lse is compared in 2^-20).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Merges n partials of a row, four columns per lane, in order.
@@ -177,21 +248,68 @@ __device__ __forceinline__ int64_t query_row(const Q4Params& p, int b, int h, in
   return (int64_t(b) * p.q_len + i) * p.Hq + h * p.g + (r - i * p.g);
 }
 
+// The line: each sequence with tiles takes that many places and those of the unit's cost,
+// for every of its units. Places before each sequence for one unit, prefix[0 .. B] in
+// shared memory, and the most tiles that one has; by the whole block.
+__device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, int* longest) {
+  __shared__ int part_sum[32], part_max[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int per = (p.B + 32 * warps - 1) / (32 * warps) * 32;  // a warp's run of sequences
+  const int b0 = warp * per;
+  int carry = 0, most = 0;
+  for (int i = 0; i < per && b0 + i < p.B; i += 32) {
+    const int b = b0 + i + lane;
+    const int n = b < p.B ? tiles_of(p, __ldcg(p.seq_lens + b)) : 0;
+    int incl = n > 0 ? n + kUnitCost * p.S : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += x;
+    }
+    most = max(most, n);
+    if (b < p.B) prefix[b + 1] = carry + incl;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+  if (lane == 0) {
+    part_sum[warp] = carry;
+    part_max[warp] = most;
+  }
+  __syncthreads();
+  int before = 0, top = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += part_sum[w];
+    top = max(top, part_max[w]);
+  }
+  for (int i = lane; i < per && b0 + i < p.B; i += 32) prefix[b0 + i + 1] += before;
+  if (threadIdx.x == 0) prefix[0] = 0;
+  *longest = top;
+  __syncthreads();
+}
+
 template <int NT>
-__global__ void __launch_bounds__(kMaxWarps * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(32 * max_warps(NT), ctas_per_sm(NT))
 q4_decode_kernel(const __grid_constant__ Q4Params p) {
+  // Registers: with 16 columns a warp holds 64 outputs, so the query fragments stay in
+  // shared memory and the halves of a tile go one after the other.
+  constexpr bool kQShared = NT > 1;
+  constexpr int kSide = NT > 1 ? 1 : 2;  // halves side by side
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int W = p.HB * p.S;  // warps
+  const int HB = p.HB, S = p.S, W = HB * S;  // W warps
   const int NS = p.stages;
   uint8_t* ring = smem + warp * NS * kTileBytes;
-  // slices' results at the end of a unit: base-2 lse [warp][NT * 8], outputs [..][128]
+  // slices' results at the end of a unit, 8 rows at a time: base-2 lse [warp][8],
+  // outputs [warp][8][128]
   float* merge_l = reinterpret_cast<float*>(smem + W * NS * kTileBytes);
-  float* merge_o = merge_l + (p.S > 1 ? W * NT * 8 : 0);
-  uint64_t* full_bars = reinterpret_cast<uint64_t*>(merge_o + (p.S > 1 ? W * NT * 8 * 128 : 0));
-  const uint32_t full = smem_u32(full_bars + warp * NS);
-  int32_t* prefix = reinterpret_cast<int32_t*>(full_bars + W * NS);  // [B + 1]
-  __shared__ int abort_flag, longest;
+  float* merge_o = merge_l + (S > 1 ? W * 8 : 0);
+  // NT = 2: the query fragments of each head
+  uint4* q_shared = reinterpret_cast<uint4*>(merge_o + (S > 1 ? W * 8 * 128 : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(q_shared + (NT > 1 ? HB * NT * 4 * 32 : 0));
+  const uint32_t full = smem_u32(bars + warp * NS);
+  int32_t* prefix = reinterpret_cast<int32_t*>(bars + W * NS);  // [B + 1]
+  __shared__ int abort_flag;
 
   if (tid == 0) abort_flag = 0;
   if (lane == 0) {
@@ -201,42 +319,111 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   }
   // nothing before this reads or writes global memory
   griddep_wait();
+  int longest;
+  scan_tiles(p, prefix, &longest);
 
-  if (warp == 0) {
-    const int per = (p.B + 31) / 32;
-    int local = 0, nmax = 0;
-    for (int i = 0; i < per; ++i) {
-      const int b = lane * per + i;
-      if (b < p.B) {
-        const int n = tiles_of(p, __ldg(p.seq_lens + b));
-        local += n;
-        nmax = max(nmax, n);
+  const int M = p.units_per_seq;
+  const int c = blockIdx.x;
+  // This CTA's part: len places of the line, from place r_c of sequence b_c's on (its units
+  // end to end). Both below 2^31 (host).
+  int b_c = 0, r_c = 0, len = 0;
+  {
+    const Cut cut(p, prefix[p.B], longest);
+    if (cut.whole) {
+      if (c < int64_t(p.B) * M) {
+        b_c = c / M;
+        len = prefix[b_c + 1] - prefix[b_c];
+        r_c = (c - b_c * M) * len;
+      }
+    } else if (c < int(cut.G) && cut.W > 0) {
+      const int64_t s_c = cut.start(c);
+      len = int(cut.start(c + 1) - s_c);
+      b_c = locate(prefix, p.B, M, s_c);
+      r_c = int(s_c - int64_t(M) * prefix[b_c]);
+    }
+  }
+  // places of all units of sequence b
+  auto seq_tiles = [&](int b) { return (prefix[b + 1] - prefix[b]) * M; };
+
+  const int hb = warp % HB, sl = warp / HB;
+  const int count = sl < len ? (len - 1 - sl) / S + 1 : 0;  // this warp's: sl, sl + S, ..
+
+  // With the copies of every SM under way a load that goes to HBM waits behind some 20 MB
+  // of them, 3 to 5 us. So the queries of a unit and the pages of the next tiles are
+  // brought into L2 ahead of their use; the first ones before the first copies.
+  auto prefetch_queries = [&](int b, int unit) {
+    const int h = (p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb;
+    const int r = (p.rgroups > 1 ? unit % p.rgroups * p.rr : 0) + (lane >> 1);
+    if ((lane >> 1) < p.rr && r < p.rows)
+      prefetch_l2(p.q + query_row(p, b, h, r) * 128 + (lane & 1) * 64);
+  };
+  if (sl == 0 && len > 0) {
+    while (r_c >= seq_tiles(b_c)) r_c -= seq_tiles(b_c++);
+    prefetch_queries(b_c, M > 1 ? r_c / (prefix[b_c + 1] - prefix[b_c]) : 0);
+  }
+
+  // ---- the warp as its own producer: lanes 2 i and 2 i + 1 hold page and place of
+  // the halves of its tile 16 j + i (place -1: no token there, or a bad page)
+  int page = 0, coord = -1;
+  int b_next = b_c, r_next = r_c + sl;  // the tile that the next batch begins with
+  bool any_bad = false;  // a half on a bad page so far (the same in every lane)
+  auto resolve = [&](int k0) {
+    while (r_next >= seq_tiles(b_next) && b_next + 1 < p.B) r_next -= seq_tiles(b_next++);
+    page = 0;
+    coord = -1;
+    if (k0 + (lane >> 1) < count) {
+      int b = b_next, r = r_next + (lane >> 1) * S;
+      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
+      const int n = prefix[b + 1] - prefix[b];
+      const int unit = M > 1 ? r / n : 0, t = (r - unit * n) * kTile + (lane & 1) * kHalf;
+      const int pg = t / p.page_size;
+      // (a half behind the last token has no page; the table's row is not read there)
+      const int L = __ldg(p.seq_lens + b);
+      if (t < L) {
+        page = __ldg(p.block_table + b * p.bt_stride + pg);
+        coord = (t - pg * p.page_size) |
+                (((p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb) << 10);
       }
     }
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += x;
-      nmax = max(nmax, __shfl_xor_sync(0xffffffffu, nmax, off));
+    if (k0 + 16 + (lane >> 1) < count) {  // the entry of the tile 16 further on
+      int b = b_next, r = r_next + (16 + (lane >> 1)) * S;
+      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
+      const int n = prefix[b + 1] - prefix[b];
+      const int t = min((M > 1 ? r % n : r) * kTile, __ldg(p.seq_lens + b) - 1);
+      prefetch_l2(p.block_table + b * p.bt_stride + t / p.page_size);
     }
-    int run = incl - local;
-    for (int i = 0; i < per; ++i) {
-      const int b = lane * per + i;
-      if (b < p.B) {
-        prefix[b] = run;
-        run += tiles_of(p, __ldg(p.seq_lens + b));
+    r_next += 16 * S;
+    const bool bad = page < 0 || page >= p.num_pages;
+    any_bad |= __any_sync(0xffffffffu, bad);
+    if (bad) {
+      flag(p.err_flags, ZL_DEVERR_BAD_PAGE);
+      coord = -1;
+    }
+  };
+  // Tile k into the stage at `to`; the same values in every lane, one lane issues (a
+  // copy per lane would be issued lane by lane).
+  auto issue = [&](int k, uint32_t to, uint32_t bar) {
+    const int src = 2 * (k & 15);
+    if (src == 0) resolve(k);
+    const int c0 = __shfl_sync(0xffffffffu, coord, src), p0 = __shfl_sync(0xffffffffu, page, src);
+    if (p.box32) {  // both halves lie on one page
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, c0 >= 0 ? kTileBytes : 0);
+        if (c0 >= 0) tma_load_4d(to, &p.tmap, bar, 0, c0 & 1023, c0 >> 10, p0);
+      }
+    } else {
+      const int c1 = __shfl_sync(0xffffffffu, coord, src + 1);
+      const int p1 = __shfl_sync(0xffffffffu, page, src + 1);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, (c0 >= 0 ? kHalfBytes : 0) + (c1 >= 0 ? kHalfBytes : 0));
+        if (c0 >= 0) tma_load_4d(to, &p.tmap, bar, 0, c0 & 1023, c0 >> 10, p0);
+        if (c1 >= 0) tma_load_4d(to + kHalfBytes, &p.tmap, bar, 0, c1 & 1023, c1 >> 10, p1);
       }
     }
-    if (lane == 31) prefix[p.B] = incl;
-    if (lane == 0) longest = nmax;
-  }
-  __syncthreads();
-  griddep_launch_dependents();
-  if (blockIdx.x == 0) {
-    for (int b = tid; b <= p.B; b += blockDim.x) p.ws_prefix[b] = prefix[b];
-    if (tid == 0) p.ws_prefix[p.B + 1] = longest;
-  }
+  };
+  const uint32_t ring_u32 = smem_u32(ring);
+  __syncwarp();
+  for (int k = 0; k < NS && k < count; ++k) issue(k, ring_u32 + k * kTileBytes, full + 8 * k);
 
   // Sequences without tiles: zeros.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -252,97 +439,66 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         p.lse[r0 + e] = -CUDART_INF_F;
   }
 
-  const int M = p.units_per_seq, S = p.S;
-  const Cut cut(p, prefix[p.B], longest);
-  int64_t s_c = 0, e_c = 0;
-  const int c = blockIdx.x;
-  if (cut.whole) {
-    if (c < int64_t(p.B) * M) {
-      const int b = c / M, n = prefix[b + 1] - prefix[b];
-      s_c = int64_t(M) * prefix[b] + int64_t(c - b * M) * n;
-      e_c = s_c + n;
-    }
-  } else if (c < cut.G && cut.W > 0) {
-    s_c = cut.start(c);
-    e_c = cut.start(c + 1);
-  }
-
-  const int hb = warp % p.HB, sl = warp / p.HB;
-  const int64_t first = s_c + sl;  // this warp's tiles: first, first + S, ..
-  const int64_t count = first < e_c ? (e_c - 1 - first) / S + 1 : 0;
-
-  // ---- the warp as its own producer: lane i holds page and place of tile 32 j + i
-  int page = 0, coord = 0, next_page = 0, next_coord = 0;
-  uint32_t bad_tiles = 0;   // of the batch being issued
-  uint32_t bad_stages = 0;  // stages that hold a tile on a bad page
-  auto resolve = [&](int64_t k0) {
-    const int64_t k = k0 + lane;
-    next_page = 0;
-    if (k < count) {
-      const int64_t idx = first + k * S;
-      const int b = locate(prefix, p.B, M, idx);
-      const int n = prefix[b + 1] - prefix[b];
-      const int64_t r = idx - int64_t(M) * prefix[b];
-      const int unit = int(r / n), t = int(r - int64_t(unit) * n) * kTile;
-      const int h = unit / p.rgroups * p.HB + hb;
-      next_page = __ldg(p.block_table + b * p.bt_stride + t / p.page_size);
-      next_coord = (t % p.page_size) | (h << 10);
-    }
-  };
-  auto issue = [&](int64_t k, int stage) {
-    const int src = int(k) & 31;
-    if (src == 0) {
-      page = next_page;
-      coord = next_coord;
-      const bool bad = page < 0 || page >= p.num_pages;
-      bad_tiles = __ballot_sync(0xffffffffu, bad);
-      if (bad) flag(p.err_flags, ZL_DEVERR_BAD_PAGE);
-      resolve(k + 32);
-    }
-    const bool bad = (bad_tiles >> src) & 1u;
-    bad_stages = (bad_stages & ~(1u << stage)) | (uint32_t(bad) << stage);
-    if (lane == src && !bad) {
-      mbar_arrive_expect_tx(full + 8 * stage, kTileBytes);
-      tma_load_4d(smem_u32(ring + stage * kTileBytes), &p.tmap, full + 8 * stage, 0, coord & 1023,
-                  coord >> 10, page);
-    } else if (lane == src) {
-      mbar_arrive(full + 8 * stage);
-    }
-  };
-  __syncwarp();
-  if (count > 0) {
-    resolve(0);
-    for (int k = 0; k < NS && k < count; ++k) issue(k, k);
-  }
-
   const int gid = lane >> 2, t4 = lane & 3;
-  const int tok_k = tile_token(gid);   // K: this lane's first row (the other is one on)
-  const int tok_a = tile_token(2 * t4), tok_b = tile_token(2 * t4 + 1);  // V: and one on each
-  int64_t k_done = 0;  // tiles of this warp consumed
-  int stage = 0;
-  uint32_t phase = 0;
-  bool dead = false, merged_before = false;
-  int64_t k_dead = 0;
+  const int tok_k = half_token(gid);   // K: this lane's first row (the other is one on)
+  const int tok_a = half_token(2 * t4), tok_b = half_token(2 * t4 + 1);  // V: and one on each
+  constexpr int half_step = kHalfBytes;
+  const uint8_t* tile_at = ring;  // the stage to be read next
+  uint32_t bar_at = full, phase = 0;
+  int left = count - NS;  // tiles not issued yet
+  bool dead = false;      // a wait gave up: nothing is waited for or issued any more
+  int left_dead = 0;
+  auto wait = [&] {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar_at, phase))) return;
+    if (__all_sync(0xffffffffu, mbar_wait(bar_at, phase, &abort_flag))) return;
+    if (lane == 0) {
+      flag(p.err_flags, ZL_DEVERR_TIMEOUT);
+      *const_cast<volatile int*>(&abort_flag) = 1;
+    }
+    dead = true;
+    left_dead = left;
+  };
+  // Hands the stage back, to the tile NS further on.
+  auto next = [&] {
+    __syncwarp();  // every lane has read the stage
+    if (left > 0 && !dead) issue(count - left, smem_u32(tile_at), bar_at);
+    --left;
+    tile_at += kTileBytes;
+    bar_at += 8;
+    if (bar_at == full + 8 * NS) {
+      tile_at = ring;
+      bar_at = full;
+      phase ^= 1u;
+    }
+  };
+  bool merged_before = false;
 
-  int64_t idx = s_c;
-  while (idx < e_c) {
-    const int b = locate(prefix, p.B, M, idx);
-    const int n = prefix[b + 1] - prefix[b];
-    const int64_t r0 = idx - int64_t(M) * prefix[b];
-    const int unit = int(r0 / n), j0 = int(r0 - int64_t(unit) * n);
-    const int64_t piece_end = min(e_c, idx - j0 + n);
-    const bool cut_unit = j0 > 0 || piece_end < idx - j0 + n;
-    const int slot = idx == s_c ? 0 : 1;
-    const int h = unit / p.rgroups * p.HB + hb;
+  int pos = 0;  // in this CTA's range
+  while (pos < len) {
+    while (r_c >= seq_tiles(b_c)) r_c -= seq_tiles(b_c++);
+    const int b = b_c;
+    const int places = prefix[b + 1] - prefix[b], n = places - kUnitCost * S;
+    const int unit = M > 1 ? r_c / places : 0, j0 = r_c - unit * places;
+    const int piece_end = min(len, pos - j0 + places);
+    const bool cut_unit = j0 > 0 || piece_end - pos < n;
+    const int slot = j0 > 0 || pos == 0 ? 0 : 1;  // (1: the unit begins behind the range's start)
+    const int h = unit / p.rgroups * HB + hb;
     const int row0 = unit % p.rgroups * p.rr;
     const int R = min(p.rr, p.rows - row0);
     const int L = __ldg(p.seq_lens + b);
+    if (sl == 0 && piece_end < len) {  // of the next unit
+      int b1 = b, u1 = unit + 1;
+      if (u1 == M) {
+        u1 = 0;
+        do ++b1; while (seq_tiles(b1) == 0);
+      }
+      prefetch_queries(b1, u1);
+    }
 
     // Q^T fragments: column gid is query row row0 + 8 nt + gid; this lane's 32
     // elements from 32 t4 on, as fp16 times a power of two.
-    uint32_t qf[NT][16];
-    float fac[NT][2];  // softmax scale of columns 2 t4 and 2 t4 + 1
-    int lim[NT][2];    // tokens they see
+    uint32_t qf[kQShared ? 1 : NT][16];
+    uint64_t fac2[NT];  // softmax scales of columns 2 t4 and 2 t4 + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = 8 * nt + gid;
@@ -354,30 +510,39 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         for (int i = 0; i < 4; ++i) w[i] = __ldg(src + i);
       }
       const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
-      float amax = 0.f;
+      // the largest magnitude, by its bits (NaN above infinity)
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m2 = __vmaxu2(m2, x[i] & 0x7FFF7FFFu);
+      uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // times 2^(14 - e), e the exponent of the largest (at least -100); a row that holds
+      // a NaN or an infinity becomes NaN
+      const int e = max(int(amax >> 7) - 127, -100);
+      const float up =
+          amax < 0x7F80u ? __uint_as_float(uint32_t(127 + 14 - e) << 23) : CUDART_NAN_F;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 v = unpack_bf16x2(x[i]);
-        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        qf[kQShared ? 0 : nt][i] = pack_f16x2(v.x * up, v.y * up);
       }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^(14 - e), e the exponent of the largest (at least -100)
-      const int e = max(int(__float_as_uint(amax) >> 23) - 127, -100);
-      const float up = __uint_as_float(uint32_t(127 + 14 - e) << 23);
+      if constexpr (kQShared) {  // (slices of a head write the same)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 v = unpack_bf16x2(x[i]);
-        // (x * 0 is NaN for an infinity: the row is NaN then, whatever it meets)
-        qf[nt][i] = pack_f16x2(fmaf(v.x, 0.f, v.x * up), fmaf(v.y, 0.f, v.y * up));
+        for (int w = 0; w < 4; ++w)
+          q_shared[((hb * NT + nt) * 4 + w) * 32 + lane] =
+              make_uint4(qf[0][4 * w], qf[0][4 * w + 1], qf[0][4 * w + 2], qf[0][4 * w + 3]);
       }
       const float down = p.scale_log2 * __uint_as_float(uint32_t(127 - 14 + e) << 23);
-      fac[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
-      fac[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) lim[nt][u] = L - p.q_len + 1 + (row0 + 8 * nt + 2 * t4 + u) / p.g;
+      fac2[nt] = pack_f32x2(__shfl_sync(0xffffffffu, down, 8 * t4),
+                            __shfl_sync(0xffffffffu, down, 8 * t4 + 4));
     }
+    // tokens that column 2 t4 + u of 8-column tile nt sees
+    auto limit = [&](int nt, int u) {
+      return L - p.q_len + 1 + (row0 + 8 * nt + 2 * t4 + u) / p.g;
+    };
     const int all_see = L - p.q_len + 1 + row0 / p.g;  // tokens that every row sees
+    __syncwarp();
 
     float o[NT][8][4];
     float base[NT][2], l[NT][2];  // base: minus it is added to a score (+inf: none yet)
@@ -394,87 +559,113 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       }
     }
 
-    // this slice's first tile of the piece
-    const int64_t behind = (idx - s_c) % S;
-    int64_t t = idx + (sl >= behind ? sl - behind : sl + S - behind);
-    for (; t < piece_end; t += S) {
-      const int tok0 = (j0 + int(t - idx)) * kTile;
-      if (!dead && !__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, phase, &abort_flag))) {
-        if (lane == 0) {
-          flag(p.err_flags, ZL_DEVERR_TIMEOUT);
-          *const_cast<volatile int*>(&abort_flag) = 1;
-        }
-        dead = true;
-        k_dead = k_done;
-      }
-      if (!dead && ((bad_stages >> stage) & 1u)) {
+    // One tile: tokens tok0 .. tok0 + 31 of the sequence; MASKED: some row does not see
+    // all of them. valid: how many there are.
+    auto run_tile = [&](auto masked_t, int first_tok, int first_valid) {
+      constexpr bool MASKED = decltype(masked_t)::value;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) bad_row[nt][u] |= tok0 < lim[nt][u];
-      } else if (!dead) {
-        const uint8_t* tile = ring + stage * kTileBytes;
-        const bool masked = tok0 + kTile > all_see;
-
-        // S^T: rows tok_k and tok_k + 1 of K, 32 elements of each
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      for (int part = 0; part < 2; part += kSide) {
+        const uint8_t* tile = tile_at + part * half_step;
+        const int tok0 = first_tok + part * kHalf, valid = first_valid - part * kHalf;
+        // S^T: of each half, rows tok_k and tok_k + 1 of K, 32 elements of each
+        float s[kSide][NT][4];
         {
-          const uint8_t* row = tile + tok_k * kQ4Row;
-          const uint4 ca = *reinterpret_cast<const uint4*>(row + 16 * t4);
-          const uint4 cb = *reinterpret_cast<const uint4*>(row + kQ4Row + 16 * t4);
-          const uint32_t sa = *reinterpret_cast<const uint16_t*>(row + kQ4KScales + 2 * t4);
-          const uint32_t sb = *reinterpret_cast<const uint16_t*>(row + kQ4Row + kQ4KScales + 2 * t4);
-          const uint32_t fa[2] = {(sa & 255u) * 0x00800080u, (sa >> 8) * 0x00800080u};
-          const uint32_t fb[2] = {(sb & 255u) * 0x00800080u, (sb >> 8) * 0x00800080u};
-          const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+          uint4 ca[kSide], cb[kSide];
+          uint32_t fa[kSide][2], fb[kSide][2];
+#pragma unroll
+          for (int hf = 0; hf < kSide; ++hf) {
+            const uint8_t* row = tile + hf * half_step + tok_k * kQ4Row;
+            ca[hf] = *reinterpret_cast<const uint4*>(row + 16 * t4);
+            cb[hf] = *reinterpret_cast<const uint4*>(row + kQ4Row + 16 * t4);
+            const uint8_t* sc = row + kQ4KScales + 2 * t4;
+            fa[hf][0] = sc[0] * 0x00800080u;
+            fa[hf][1] = sc[1] * 0x00800080u;
+            fb[hf][0] = sc[kQ4Row] * 0x00800080u;
+            fb[hf][1] = sc[kQ4Row + 1] * 0x00800080u;
+          }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t xa[4], xb[4];
-            q4_pairs(wa[w], xa);
-            q4_pairs(wb[w], xb);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              xa[i] = mul_f16x2(xa[i], fa[w >> 1]);
-              xb[i] = mul_f16x2(xb[i], fb[w >> 1]);
-            }
+            uint32_t qw[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(s[nt], xa[0], xb[0], xa[1], xb[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
-              mma_f16(s[nt], xa[2], xb[2], xa[3], xb[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+              if constexpr (kQShared) {
+                const uint4 v = q_shared[((hb * NT + nt) * 4 + w) * 32 + lane];
+                qw[nt][0] = v.x, qw[nt][1] = v.y, qw[nt][2] = v.z, qw[nt][3] = v.w;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qw[nt][i] = qf[nt][4 * w + i];
+              }
+            }
+#pragma unroll
+            for (int hf = 0; hf < kSide; ++hf) {
+              uint32_t xa[4], xb[4];
+              q4_pairs(w == 0 ? ca[hf].x : w == 1 ? ca[hf].y : w == 2 ? ca[hf].z : ca[hf].w, xa);
+              q4_pairs(w == 0 ? cb[hf].x : w == 1 ? cb[hf].y : w == 2 ? cb[hf].z : cb[hf].w, xb);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                xa[i] = mul_f16x2(xa[i], fa[hf][w >> 1]);
+                xb[i] = mul_f16x2(xb[i], fb[hf][w >> 1]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (w == 0)
+                  mma_f16_first(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qw[nt][0], qw[nt][1]);
+                else
+                  mma_f16(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qw[nt][0], qw[nt][1]);
+                mma_f16(s[hf][nt], xa[2], xb[2], xa[3], xb[3], qw[nt][2], qw[nt][3]);
+              }
             }
           }
         }
 
-        // Softmax. This lane: tokens tok_k, tok_k + 1 of columns 2 t4, 2 t4 + 1.
-        uint32_t pf[NT][2];
+        // Softmax. This lane: of each half tokens tok_k, tok_k + 1 of columns 2 t4, 2 t4 + 1.
+        uint32_t pf[kSide][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float y[4];
+          auto hidden = [&](int hf, int i) {
+            return MASKED && tok0 + 16 * hf + tok_k + (i >> 1) >= limit(nt, i & 1);
+          };
+          float y[kSide][4];
           auto scores = [&] {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // (not fused: the largest score less itself is 0 at any size)
-              y[i] = __fadd_rn(__fmul_rn(s[nt][i], fac[nt][i & 1]), base[nt][i & 1]);
-              if (masked && tok0 + tok_k + (i >> 1) >= lim[nt][i & 1]) y[i] = -CUDART_INF_F;
-            }
+            for (int hf = 0; hf < kSide; ++hf)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // (not fused: the largest score less itself is 0 at any size)
+                if ((i & 1) == 0) {
+                  const float2 v = unpack_f32x2(add_f32x2(
+                      mul_f32x2(pack_f32x2(s[hf][nt][i], s[hf][nt][i + 1]), fac2[nt]),
+                      pack_f32x2(base[nt][0], base[nt][1])));
+                  y[hf][i] = v.x;
+                  y[hf][i + 1] = v.y;
+                }
+              }
+#pragma unroll
+            for (int hf = 0; hf < kSide; ++hf)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (hidden(hf, i)) y[hf][i] = -CUDART_INF_F;
           };
           scores();
-          if (__any_sync(0xffffffffu, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) > kMove)) {
-            float mx[2];
+          float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3]));
+          if (kSide > 1)
+            top = fmaxf(top, fmaxf(fmaxf(y[kSide - 1][0], y[kSide - 1][1]),
+                                   fmaxf(y[kSide - 1][2], y[kSide - 1][3])));
+          if (__any_sync(0xffffffffu, top > kMove)) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              float x0 = __fmul_rn(s[nt][u], fac[nt][u]), x1 = __fmul_rn(s[nt][u + 2], fac[nt][u]);
-              if (masked && tok0 + tok_k >= lim[nt][u]) x0 = -CUDART_INF_F;
-              if (masked && tok0 + tok_k + 1 >= lim[nt][u]) x1 = -CUDART_INF_F;
-              mx[u] = fmaxf(x0, x1);
-              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 4));
-              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 8));
-              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 16));
+              float mx = -CUDART_INF_F;
+#pragma unroll
+              for (int hf = 0; hf < kSide; ++hf)
+#pragma unroll
+                for (int i = u; i < 4; i += 2)
+                  if (!hidden(hf, i)) mx = fmaxf(mx, __fmul_rn(s[hf][nt][i], u ? unpack_f32x2(fac2[nt]).y : unpack_f32x2(fac2[nt]).x));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
               // moves to kSlack below the largest where that is upwards
-              const float nb = kSlack - mx[u];
-              if (mx[u] != -CUDART_INF_F && nb < base[nt][u]) {
+              const float nb = kSlack - mx;
+              if (mx != -CUDART_INF_F && nb < base[nt][u]) {
                 const float alpha =
                     base[nt][u] == CUDART_INF_F ? 0.f : ex2_approx(nb - base[nt][u]);
                 base[nt][u] = nb;
@@ -489,61 +680,106 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
             scores();
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = ex2_approx(y[i]);
-          l[nt][0] += y[0] + y[2];
-          l[nt][1] += y[1] + y[3];
-          pf[nt][0] = transpose_8x8(pack_f16x2(y[0], y[1]));
-          pf[nt][1] = transpose_8x8(pack_f16x2(y[2], y[3]));
+          for (int hf = 0; hf < kSide; ++hf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[hf][i] = ex2_approx(y[hf][i]);
+            l[nt][0] += y[hf][0] + y[hf][2];
+            l[nt][1] += y[hf][1] + y[hf][3];
+            pf[hf][nt][0] = transpose_8x8(pack_f16x2(y[hf][0], y[hf][1]));
+            pf[hf][nt][1] = transpose_8x8(pack_f16x2(y[hf][2], y[hf][3]));
+          }
         }
 
-        // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first half of the 16
-        // tokens), a + 1, b + 1 (second half)
-        {
-          const uint8_t* ra = tile + tok_a * kQ4Row + kQ4VCodes + 8 * gid;
-          const uint8_t* rb = tile + tok_b * kQ4Row + kQ4VCodes + 8 * gid;
+        // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first 8 fragment rows of a
+        // half's 16 tokens), a + 1, b + 1 (the others)
+#pragma unroll
+        for (int hf = 0; hf < kSide; ++hf) {
+          const uint8_t* ra = tile + hf * half_step + tok_a * kQ4Row + kQ4VCodes + 8 * gid;
+          const uint8_t* rb = tile + hf * half_step + tok_b * kQ4Row + kQ4VCodes + 8 * gid;
           const uint2 a0 = *reinterpret_cast<const uint2*>(ra);
           const uint2 a1 = *reinterpret_cast<const uint2*>(ra + kQ4Row);
           const uint2 b0 = *reinterpret_cast<const uint2*>(rb);
           const uint2 b1 = *reinterpret_cast<const uint2*>(rb + kQ4Row);
-          const int at = kQ4VScales + gid;
-          uint32_t s0 = tile[tok_a * kQ4Row + at], s1 = tile[(tok_a + 1) * kQ4Row + at];
-          uint32_t s2 = tile[tok_b * kQ4Row + at], s3 = tile[(tok_b + 1) * kQ4Row + at];
-          if (masked) {  // what lies behind the sequence may hold anything
-            const int valid = L - tok0;
-            s0 = tok_a < valid ? s0 : 0u;
-            s1 = tok_a + 1 < valid ? s1 : 0u;
-            s2 = tok_b < valid ? s2 : 0u;
-            s3 = tok_b + 1 < valid ? s3 : 0u;
+          const uint8_t* sa = tile + hf * half_step + tok_a * kQ4Row + kQ4VScales + gid;
+          const uint8_t* sb = tile + hf * half_step + tok_b * kQ4Row + kQ4VScales + gid;
+          uint32_t s0 = sa[0], s1 = sa[kQ4Row], s2 = sb[0], s3 = sb[kQ4Row];
+          if (MASKED) {  // what lies behind the sequence may hold anything
+            s0 = 16 * hf + tok_a < valid ? s0 : 0u;
+            s1 = 16 * hf + tok_a + 1 < valid ? s1 : 0u;
+            s2 = 16 * hf + tok_b < valid ? s2 : 0u;
+            s3 = 16 * hf + tok_b + 1 < valid ? s3 : 0u;
           }
           const uint32_t f0 = s0 * 0x80u + s2 * 0x800000u, f1 = s1 * 0x80u + s3 * 0x800000u;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             const uint32_t wa0 = w ? a0.y : a0.x, wb0 = w ? b0.y : b0.x;
             const uint32_t wa1 = w ? a1.y : a1.x, wb1 = w ? b1.y : b1.x;
-            uint32_t x0[4], y0[4], x1[4], y1[4];  // even and odd elements of both halves
-            q4_pairs((wa0 & 0x0F0F0F0Fu) | ((wb0 << 4) & 0xF0F0F0F0u), x0);
-            q4_pairs(((wa0 >> 4) & 0x0F0F0F0Fu) | (wb0 & 0xF0F0F0F0u), y0);
-            q4_pairs((wa1 & 0x0F0F0F0Fu) | ((wb1 << 4) & 0xF0F0F0F0u), x1);
-            q4_pairs(((wa1 >> 4) & 0x0F0F0F0Fu) | (wb1 & 0xF0F0F0F0u), y1);
+            uint32_t x0[4], y0[4], x1[4], y1[4];  // even and odd elements
+            q4_pairs(select_bits(wa0, wb0 << 4, 0x0F0F0F0Fu), x0);
+            q4_pairs(select_bits(wa0 >> 4, wb0, 0x0F0F0F0Fu), y0);
+            q4_pairs(select_bits(wa1, wb1 << 4, 0x0F0F0F0Fu), x1);
+            q4_pairs(select_bits(wa1 >> 4, wb1, 0x0F0F0F0Fu), y1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t m0 = mul_f16x2(x0[i], f0), m1 = mul_f16x2(y0[i], f0);
               const uint32_t m2 = mul_f16x2(x1[i], f1), m3 = mul_f16x2(y1[i], f1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[nt][4 * w + i], m0, m1, m2, m3, pf[nt][0], pf[nt][1]);
+                mma_f16(o[nt][4 * w + i], m0, m1, m2, m3, pf[hf][nt][0], pf[hf][nt][1]);
             }
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (!dead && k_done + NS < count) issue(k_done + NS, stage);
-      ++k_done;
-      if (++stage == NS) {
-        stage = 0;
-        phase ^= 1u;
+    };
+
+    // this slice's tiles of the piece: todo of them from token tok0 on, the first `plain`
+    // of which every row sees whole
+    const int behind = pos % S;
+    const int t0 = pos + (sl >= behind ? sl - behind : sl + S - behind);
+    int todo = t0 < piece_end ? (piece_end - 1 - t0) / S + 1 : 0;
+    int tok0 = (j0 + t0 - pos) * kTile;
+    const int stride = S * kTile;  // tokens from one to the next
+    while (todo > 0) {
+      int plain = all_see >= tok0 + kTile ? min(todo, (all_see - kTile - tok0) / stride + 1) : 0;
+      for (; plain > 0 && !dead; --plain) {
+        wait();
+        if (dead || any_bad) break;
+        run_tile(std::false_type{}, tok0, kTile);
+        next();
+        --todo;
+        tok0 += stride;
       }
+      if (todo == 0) break;
+      // one of the others: the newest, or any where a page was bad
+      if (plain == 0 && !dead) wait();
+      if (!dead) {
+        int whole = kTile;  // tokens before a bad half
+        if (any_bad) {
+          const int at = tok0 + (lane & 1) * kHalf;
+          int pg = 0;
+          if (at < L) pg = __ldg(p.block_table + b * p.bt_stride + at / p.page_size);
+          const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.num_pages) & 3u;
+          whole = bad & 1u ? 0 : bad ? kHalf : kTile;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) bad_row[nt][u] |= bad && tok0 + whole < limit(nt, u);
+        }
+        // (a row that does not see the bad half still needs the good one)
+        if (whole > 0 && tok0 < L) run_tile(std::true_type{}, tok0, min(L - tok0, whole));
+      }
+      next();
+      --todo;
+      tok0 += stride;
     }
+
+    r_c += piece_end - pos;
+    const bool any_tile = j0 < n;
+    pos = piece_end;
+    // The merge may be placed on this SM from here on: earlier it would take the room of
+    // CTAs that have not begun.
+    if (pos == len) griddep_launch_dependents();
+    if (!any_tile) continue;  // (only places without tiles)
 
     // ---- end of the piece: sums over the 8 lanes of a column
 #pragma unroll
@@ -554,7 +790,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], 8);
         l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], 16);
       }
-    const int64_t part0 = ((int64_t(c) * 2 + slot) * p.HB + hb) * p.rr;
+    const int64_t part0 = ((int64_t(c) * 2 + slot) * HB + hb) * p.rr;
     if (S == 1) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -563,8 +799,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           const int r = 8 * nt + 2 * t4 + u;
           if (r >= R) continue;
           const bool none = bad_row[nt][u] || l[nt][u] == 0.f;
-          const float inv = none ? 0.f : __frcp_rn(l[nt][u]);
-          const float lse2 = none ? -CUDART_INF_F : log2f(l[nt][u]) - base[nt][u];
+          const float inv = none ? 0.f : rcp_approx(l[nt][u]);
+          const float lse2 = none ? -CUDART_INF_F : lg2_approx(l[nt][u]) - base[nt][u];
           float v[16];
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
@@ -593,19 +829,20 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           }
         }
     } else {
-      // Slices: each leaves its rows, then takes every S-th row over all of them.
-      if (merged_before) named_barrier(1 + hb, S * 32);
-      merged_before = true;
+      // Slices: each leaves its rows (8 at a time), then takes every S-th over all of them.
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        if (8 * nt >= R) break;
+        if (merged_before) named_barrier(1 + hb, S * 32);
+        merged_before = true;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int r = 8 * nt + 2 * t4 + u;
-          if (r >= R) continue;
+          const int r = 2 * t4 + u;
+          if (8 * nt + r >= R) continue;
           const bool none = bad_row[nt][u] || l[nt][u] == 0.f;
-          const float inv = none ? 0.f : __frcp_rn(l[nt][u]);
-          const float lse2 = none ? -CUDART_INF_F : log2f(l[nt][u]) - base[nt][u];
-          float* to = merge_o + (warp * NT * 8 + r) * 128 + 16 * gid;
+          const float inv = none ? 0.f : rcp_approx(l[nt][u]);
+          const float lse2 = none ? -CUDART_INF_F : lg2_approx(l[nt][u]) - base[nt][u];
+          float* to = merge_o + (warp * 8 + r) * 128 + 16 * gid;
 #pragma unroll
           for (int mt = 0; mt < 8; mt += 2)
             *reinterpret_cast<float4*>(to + 2 * mt) =
@@ -613,101 +850,140 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
                             none ? 0.f : o[nt][mt + 1][u] * inv,
                             none ? 0.f : o[nt][mt + 1][u + 2] * inv);
           if (gid == 0)
-            merge_l[warp * NT * 8 + r] = bad_row[nt][u] ? CUDART_NAN_F
-                                            : isnan(lse2)  ? CUDART_INF_F
-                                                           : lse2;
+            merge_l[warp * 8 + r] = bad_row[nt][u] ? CUDART_NAN_F
+                                    : isnan(lse2)  ? CUDART_INF_F
+                                                   : lse2;
         }
-      named_barrier(1 + hb, S * 32);
-      for (int r = sl; r < R; r += S) {
-        RowMerge m;
-        m.init();
-        for (int s = 0; s < S; ++s) {
-          const int at = (s * p.HB + hb) * NT * 8 + r;
-          m.add(merge_l[at], reinterpret_cast<const float4*>(merge_o + at * 128)[lane]);
-        }
-        const bool none = m.bad || m.den == 0.f;
-        const float inv = none ? 0.f : __frcp_rn(m.den);
-        const float lse2 = none ? -CUDART_INF_F : m.m + log2f(m.den);
-        const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(m.o.x * inv, m.o.y * inv, m.o.z * inv, m.o.w * inv);
-        if (cut_unit) {
-          reinterpret_cast<float4*>(p.ws_o + (part0 + r) * 128)[lane] = v;
-          if (lane == 0)
-            p.ws_lse[part0 + r] = m.bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
-        } else {
-          const int64_t row = query_row(p, b, h, row0 + r);
-          reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-          if (p.lse && lane == 0) p.lse[row] = lse2 * 0.69314718055994531f;
+        named_barrier(1 + hb, S * 32);
+        for (int r = sl; r < min(8, R - 8 * nt); r += S) {
+          RowMerge m;
+          m.init();
+          for (int s = 0; s < S; ++s) {
+            const int at = (s * HB + hb) * 8 + r;
+            m.add(merge_l[at], reinterpret_cast<const float4*>(merge_o + at * 128)[lane]);
+          }
+          const bool none = m.bad || m.den == 0.f;
+          const float inv = none ? 0.f : rcp_approx(m.den);
+          const float lse2 = none ? -CUDART_INF_F : m.m + lg2_approx(m.den);
+          const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : make_float4(m.o.x * inv, m.o.y * inv, m.o.z * inv, m.o.w * inv);
+          if (cut_unit) {
+            const int64_t at = part0 + 8 * nt + r;
+            reinterpret_cast<float4*>(p.ws_o + at * 128)[lane] = v;
+            if (lane == 0)
+              p.ws_lse[at] = m.bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
+          } else {
+            const int64_t row = query_row(p, b, h, row0 + 8 * nt + r);
+            reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            if (p.lse && lane == 0) p.lse[row] = lse2 * 0.69314718055994531f;
+          }
         }
       }
     }
-    idx = piece_end;
   }
   // A warp that stopped leaves no copy in flight (but for one that never ends).
   if (dead) {
     const volatile int never = 0;
-    for (int64_t k = k_dead; k < min(count, k_dead + NS); ++k)
-      mbar_wait(full + 8 * int(k % NS), uint32_t(k / NS) & 1u, &never);
+    const int k_dead = count - NS - left_dead;
+    for (int k = k_dead; k < min(count, k_dead + NS); ++k)
+      mbar_wait(full + 8 * (k % NS), uint32_t(k / NS) & 1u, &never);
   }
 }
 
-// Rows of units that were cut, one warp each: the parts in CTA order.
+// Rows of units that were cut: the parts in CTA order, PW warps to a row (each takes
+// every PW-th part), 8 / PW rows to a block.
+template <int PW>
 __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q4Params p) {
   griddep_launch_dependents();
+  extern __shared__ int32_t prefix[];  // [B + 1]
+  constexpr int kRows = 8 / PW;
+  __shared__ float2 part_ml[kRows][PW];  // maximum (NaN: bad) and sum
+  __shared__ float4 part_o[kRows][PW][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = warp % PW, local = warp / PW;
+  // (The lengths may be read before the attention is done: what came before it in the
+  // stream was, when the attention let this launch begin.)
+  int longest;
+  scan_tiles(p, prefix, &longest);
+  const int b = blockIdx.y;
+  const int n = prefix[b + 1] - prefix[b] - kUnitCost * p.S;  // tiles (below 1: none)
+  const Cut cut(p, prefix[p.B], longest);
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = int64_t(p.B) * p.Hkv * p.rows;
-  const int64_t w = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= rows) return;
-  const int r = int(w % p.rows);
-  const int64_t bh = w / p.rows;
-  const int h = int(bh % p.Hkv), b = int(bh / p.Hkv);
-  const int32_t n0 = __ldcg(p.ws_prefix + b), n = __ldcg(p.ws_prefix + b + 1) - n0;
-  if (n == 0) return;
-  const Cut cut(p, __ldcg(p.ws_prefix + p.B), __ldcg(p.ws_prefix + p.B + 1));
-  if (cut.whole) return;
-  const int bundle = h / p.HB, rg = r / p.rr;
-  const int64_t U0 =
-      int64_t(p.units_per_seq) * n0 + int64_t(bundle * p.rgroups + rg) * n;
-  const int lo = cut.owner(U0), hi = cut.owner(U0 + n - 1);
-  if (lo == hi) return;
-  RowMerge m;
-  m.init();
-  const int first_slot = U0 > cut.start(lo) ? 1 : 0;
-  for (int c0 = lo; c0 <= hi; c0 += 4) {
-    float l[4];
-    float4 o[4];
+  if (n < 1 || cut.whole) return;
+  const int64_t per_slot = int64_t(p.HB) * p.rr;
+  const int rows = p.Hkv * p.rows;  // of the sequence: (head, its row)
+  for (int id0 = blockIdx.x * kRows; id0 < rows; id0 += gridDim.x * kRows) {
+    const int id = id0 + local;
+    const int h = id / p.rows, r = id - h * p.rows;
+    RowMerge m;
+    m.init();
+    int lo = 0, hi = 0;
+    if (id < rows) {
+      const int bundle = h / p.HB, rg = r / p.rr;
+      const int64_t U0 = int64_t(p.units_per_seq) * prefix[b] +
+                         int64_t(bundle * p.rgroups + rg) * (prefix[b + 1] - prefix[b]);
+      lo = cut.owner(U0), hi = cut.owner(U0 + n - 1);
+      const int first_slot = U0 > cut.start(lo) ? 1 : 0;
+      const int64_t at0 = (h - bundle * p.HB) * p.rr + (r - rg * p.rr);
+      for (int c0 = lo < hi ? lo + w : hi + 1; c0 <= hi; c0 += 4 * PW) {
+        float l[4];
+        float4 o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + i;
-      if (c <= hi) {
-        const int64_t at =
-            ((int64_t(c) * 2 + (c == lo ? first_slot : 0)) * p.HB + (h - bundle * p.HB)) * p.rr +
-            (r - rg * p.rr);
-        l[i] = __ldcg(p.ws_lse + at);
-        o[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * 128) + lane);
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + i * PW;
+          if (c <= hi) {
+            const int64_t at = (int64_t(c) * 2 + (c == lo ? first_slot : 0)) * per_slot + at0;
+            l[i] = __ldcg(p.ws_lse + at);
+            o[i] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * 128) + lane);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i * PW <= hi) m.add(l[i], o[i]);
       }
     }
+    if constexpr (PW > 1) {
+      if (id0 != blockIdx.x * kRows) __syncthreads();  // (the last round has been read)
+      if (lane == 0) part_ml[local][w] = make_float2(m.bad ? CUDART_NAN_F : m.m, m.den);
+      part_o[local][w][lane] = m.o;
+      __syncthreads();
+      if (w > 0) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c0 + i <= hi) m.add(l[i], o[i]);
+      for (int i = 1; i < PW; ++i) {
+        const float2 ml = part_ml[local][i];
+        const float4 v = part_o[local][i][lane];
+        m.bad |= isnan(ml.x);
+        const float mn = fmaxf(m.m, ml.x);
+        if (mn == -CUDART_INF_F || isnan(ml.x)) continue;
+        const float a = ex2_approx(m.m - mn), c = ex2_approx(ml.x - mn);
+        m.den = fmaf(m.den, a, ml.y * c);
+        m.o.x = fmaf(v.x, c, m.o.x * a);
+        m.o.y = fmaf(v.y, c, m.o.y * a);
+        m.o.z = fmaf(v.z, c, m.o.z * a);
+        m.o.w = fmaf(v.w, c, m.o.w * a);
+        m.m = mn;
+      }
+    }
+    if (lo == hi) continue;  // not cut
+    const bool none = m.bad || m.den == 0.f;
+    const float inv = none ? 0.f : rcp_approx(m.den);
+    const int64_t row = query_row(p, b, h, r);
+    uint2 v = make_uint2(0u, 0u);
+    if (!none)
+      v = make_uint2(pack_bf16x2(m.o.x * inv, m.o.y * inv), pack_bf16x2(m.o.z * inv, m.o.w * inv));
+    reinterpret_cast<uint2*>(p.out + row * 128)[lane] = v;
+    if (p.lse && lane == 0)
+      p.lse[row] = none ? -CUDART_INF_F : (m.m + lg2_approx(m.den)) * 0.69314718055994531f;
   }
-  const bool none = m.bad || m.den == 0.f;
-  const float inv = none ? 0.f : __frcp_rn(m.den);
-  const int64_t row = query_row(p, b, h, r);
-  uint2 v = make_uint2(0u, 0u);
-  if (!none)
-    v = make_uint2(pack_bf16x2(m.o.x * inv, m.o.y * inv), pack_bf16x2(m.o.z * inv, m.o.w * inv));
-  reinterpret_cast<uint2*>(p.out + row * 128)[lane] = v;
-  if (p.lse && lane == 0)
-    p.lse[row] = none ? -CUDART_INF_F : (m.m + log2f(m.den)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------- host
 struct Plan {
-  int nt, g, rows, rgroups, rr, HB, S, stages, units_per_seq, ctas;
-  size_t smem, off_lse, off_o, bytes;
+  int nt, g, rows, rgroups, rr, HB, S, stages, units_per_seq, ctas, merge_warps;
+  int sms;
+  bool whole;  // known from max_seq_len: a CTA for every unit
+  size_t smem, off_o, bytes;
 };
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -715,7 +991,8 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 size_t smem_bytes(const Plan& pl, int B) {
   const size_t W = size_t(pl.HB) * pl.S;
   size_t n = W * pl.stages * (kTileBytes + 8) + (size_t(B) + 1) * 4;
-  if (pl.S > 1) n += W * pl.nt * 8 * (4 + 128 * 4);
+  if (pl.S > 1) n += W * 8 * (4 + 128 * 4);
+  if (pl.nt > 1) n += size_t(pl.HB) * pl.nt * 4 * 32 * 16;
   return n;
 }
 
@@ -729,10 +1006,10 @@ zl_status validate(const zl_decode_attn_q4_params* a) {
   if (a->Hq / a->Hkv > 128 || a->q_len > 128 || a->B > kMaxBatch || a->Hkv > 65535 ||
       a->num_ctas > 65535)
     return ZL_ERR_UNSUPPORTED;
-  if (a->page_size % kTile || a->page_size > 1024) return ZL_ERR_UNSUPPORTED;
+  if (a->page_size % kHalf || a->page_size > 1024) return ZL_ERR_UNSUPPORTED;
   // (tile sums in 32 bits; the line of tiles times the CTAs in 64)
   if (a->block_table_stride >= (INT64_C(1) << 31)) return ZL_ERR_UNSUPPORTED;
-  const int64_t tiles = a->block_table_stride * (a->page_size / kTile) * a->B;
+  const int64_t tiles = a->block_table_stride * (a->page_size / kHalf) * a->B;
   if (tiles >= (INT64_C(1) << 31) || tiles * a->Hkv >= (INT64_C(1) << 40))
     return ZL_ERR_UNSUPPORTED;
   return ZL_OK;
@@ -740,19 +1017,21 @@ zl_status validate(const zl_decode_attn_q4_params* a) {
 
 template <int NT>
 zl_status occupancy(size_t smem, int threads, int* n) {
-  static bool done[kMaxDevices] = {};
+  // asked once per device and form (the sizes are few: threads and, in 1 KB steps, the
+  // shared memory)
+  static std::atomic<int> known[kMaxDevices][16][256] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ZL_ERR_CUDA;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(q4_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             226 * 1024) != cudaSuccess)
-      return ZL_ERR_CUDA;
-    done[dev] = true;
-  }
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, q4_decode_kernel<NT>, threads, smem) !=
-      cudaSuccess)
+  std::atomic<int>& k = known[dev][threads / 32][smem / 1024];
+  if ((*n = k.load(std::memory_order_relaxed)) > 0) return ZL_OK;
+  if (cudaFuncSetAttribute(q4_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           226 * 1024) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, q4_decode_kernel<NT>, threads, smem) !=
+          cudaSuccess ||
+      *n < 1)
     return ZL_ERR_CUDA;
-  return *n > 0 ? ZL_OK : ZL_ERR_CUDA;
+  k.store(*n, std::memory_order_relaxed);
+  return ZL_OK;
 }
 
 zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
@@ -760,26 +1039,30 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   if (st != ZL_OK) return st;
   int sms;
   if ((st = sm_count(&sms)) != ZL_OK) return st;
+  pl->sms = sms;
   pl->g = a->Hq / a->Hkv;
   pl->rows = pl->g * a->q_len;
   pl->rgroups = (pl->rows + 15) / 16;
   pl->rr = (pl->rows + pl->rgroups - 1) / pl->rgroups;
   pl->rgroups = (pl->rows + pl->rr - 1) / pl->rr;
   pl->nt = pl->rr > 8 ? 2 : 1;
-  // heads of a bundle: the most, up to 8, that divide Hkv; one in small calls
+  // Bundle: of the divisors of Hkv up to 8 the one that leaves the fewest warps of a CTA
+  // idle, the largest of those; one head in small calls, where slices cut the time of a
+  // unit.
+  const int warps = max_warps(pl->nt);
   pl->HB = 1;
   const int64_t len = a->max_seq_len > 0 ? a->max_seq_len : 4096;
   const int64_t tiles = int64_t(a->B) * a->Hkv * pl->rgroups * ((len + kTile - 1) / kTile);
-  if (tiles >= int64_t(sms) * 64)
-    for (int d = 2; d <= 8; ++d)
-      if (a->Hkv % d == 0) pl->HB = d;
-  pl->S = kMaxWarps / pl->HB;
+  if (tiles >= int64_t(sms) * 32)
+    for (int d = 2; d <= kMaxBundle; ++d)
+      if (a->Hkv % d == 0 && warps / d * d >= warps / pl->HB * pl->HB) pl->HB = d;
+  pl->S = warps / pl->HB;
   pl->units_per_seq = a->Hkv / pl->HB * pl->rgroups;
-  // ring: what two CTAs (NT = 2: one) leave an SM, at most 8 stages
-  const size_t room = (pl->nt == 1 ? 112 : 200) * 1024;
-  pl->stages = 8;
-  while (pl->stages > 3 && smem_bytes(*pl, a->B) > room) --pl->stages;
-  pl->smem = smem_bytes(*pl, a->B);
+  // Two stages to a warp, 147 KB on an SM: more only make the requests of all SMs wait
+  // for one another (with three 64 sequences of 512-4096 tokens took 49 us, not 45, and
+  // 8 of 32k-131k 130, not 125).
+  pl->stages = 2;
+  pl->smem = round_up(smem_bytes(*pl, a->B), 1024);
   int per_sm = 0;
   const int threads = pl->HB * pl->S * 32;
   st = pl->nt == 1 ? occupancy<1>(pl->smem, threads, &per_sm)
@@ -787,12 +1070,25 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   if (st != ZL_OK) return st;
   pl->ctas = a->num_ctas > 0 ? a->num_ctas : per_sm * sms;
   if (a->num_ctas == 0 && a->max_seq_len > 0) {
-    const int64_t most = int64_t(a->B) * pl->units_per_seq * ((len + kTile - 1) / kTile);
+    const int64_t most =
+        int64_t(a->B) * pl->units_per_seq * ((len + kTile - 1) / kTile + kUnitCost * pl->S);
     pl->ctas = int(std::max<int64_t>(1, std::min<int64_t>(pl->ctas, most)));
   }
+  const int64_t units = int64_t(a->B) * pl->units_per_seq;
+  pl->whole = a->max_seq_len > 0 && units <= pl->ctas &&
+              (int64_t(a->max_seq_len) + kTile - 1) / kTile <= kWholeTiles * pl->S;
+  if (pl->whole) pl->ctas = int(units);
+  // a warp of the merge reads four parts at a time; more warps to a row where a unit
+  // is cut into more
+  const int64_t parts = pl->ctas / units + 2;
+  pl->merge_warps = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;
+  // (a CTA counts its tiles, and those of a sequence's units, in 32 bits)
+  const int64_t line =
+      (a->block_table_stride * a->page_size / kTile + 1 + kUnitCost * pl->S) * pl->units_per_seq;
+  if (line * a->B / pl->ctas >= (INT64_C(1) << 29) || line >= (INT64_C(1) << 29))
+    return ZL_ERR_UNSUPPORTED;
   const size_t slots = size_t(pl->ctas) * 2 * pl->HB * pl->rr;
-  pl->off_lse = round_up((size_t(a->B) + 2) * 4, 256);
-  pl->off_o = pl->off_lse + round_up(slots * 4, 256);
+  pl->off_o = round_up(slots * 4, 256);
   pl->bytes = pl->off_o + slots * 128 * 4;
   return ZL_OK;
 }
@@ -825,7 +1121,7 @@ zl_status encode_pool(const zl_decode_attn_q4_params* a, CUtensorMap* map) {
                               cuuint64_t(a->num_pages)};
   const cuuint64_t strides[3] = {cuuint64_t(a->token_stride), cuuint64_t(a->head_stride),
                                  cuuint64_t(a->page_stride)};
-  const cuuint32_t box[4] = {kQ4Row, kTile, 1, 1};
+  const cuuint32_t box[4] = {kQ4Row, cuuint32_t(a->page_size % kTile ? kHalf : kTile), 1, 1};
   const CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                                   const_cast<void*>(a->pool), dims, strides, box);
   if (r == CUDA_ERROR_NOT_INITIALIZED) return ZL_ERR_CUDA;
@@ -871,8 +1167,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.bt_stride = a->block_table_stride;
   p.seq_lens = a->seq_lens;
   char* ws = static_cast<char*>(a->workspace);
-  p.ws_prefix = reinterpret_cast<int32_t*>(ws);
-  p.ws_lse = reinterpret_cast<float*>(ws + pl.off_lse);
+  p.ws_lse = reinterpret_cast<float*>(ws);
   p.ws_o = reinterpret_cast<float*>(ws + pl.off_o);
   p.err_flags = a->err_flags;
   p.B = a->B;
@@ -890,11 +1185,13 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.rr = pl.rr;
   p.rows = pl.rows;
   p.ctas = pl.ctas;
+  p.box32 = a->page_size % kTile == 0;
+  p.whole = pl.whole;
   p.scale_log2 = float(double(a->scale) * kLog2e);
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pl.ctas));
-  cfg.blockDim = dim3(unsigned(pl.HB * pl.S * 32));
+  cfg.blockDim = dim3(unsigned(pl.HB * pl.S) * 32);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -905,10 +1202,18 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   cudaError_t e = pl.nt == 1 ? cudaLaunchKernelEx(&cfg, q4_decode_kernel<1>, p)
                              : cudaLaunchKernelEx(&cfg, q4_decode_kernel<2>, p);
   if (e != cudaSuccess) return ZL_ERR_CUDA;
-  const int64_t rows = int64_t(a->B) * a->Hkv * pl.rows;
-  cfg.gridDim = dim3(unsigned((rows + 7) / 8));
+  if (pl.whole) return ZL_OK;  // no unit is cut
+  const int64_t rows = int64_t(a->Hkv) * pl.rows;  // of a sequence
+  const int64_t blocks = (rows * pl.merge_warps + 7) / 8;  // four to an SM at most
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>(blocks, std::max(1, 4 * pl.sms / a->B))),
+                     unsigned(a->B));
   cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, q4_merge_kernel, p);
+  cfg.dynamicSmemBytes = (size_t(a->B) + 1) * 4;
+  switch (pl.merge_warps) {
+    case 8: e = cudaLaunchKernelEx(&cfg, q4_merge_kernel<8>, p); break;
+    case 4: e = cudaLaunchKernelEx(&cfg, q4_merge_kernel<4>, p); break;
+    case 2: e = cudaLaunchKernelEx(&cfg, q4_merge_kernel<2>, p); break;
+    default: e = cudaLaunchKernelEx(&cfg, q4_merge_kernel<1>, p);
+  }
   return e == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
