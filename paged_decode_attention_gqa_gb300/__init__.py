@@ -574,6 +574,7 @@ def _expect(t, name, dtype, shape, index, contiguous=True):
 
 
 _BF16, _F32, _I32, _U32 = torch.bfloat16, torch.float32, torch.int32, torch.uint32
+_U8 = torch.uint8
 
 
 def _expect_cache(k_pool, v_pool, block_table, seq_lens, layout, page_size, err_flags):
@@ -1058,25 +1059,23 @@ def _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags):
     """The checks every call over a 4-bit cache shares; returns (device index, B, Hkv,
     num_pages, address, strides in (page, token, head) order, then the block table,
     its stride, seq_lens and err_flags)."""
-    index = pool.get_device()
-    if pool.dtype is not torch.uint8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
+    index, shape, st = pool.get_device(), pool.shape, pool.stride()
+    if pool.dtype is not _U8 or len(shape) != 4 or shape[3] != Q4_ROW_BYTES:
         raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes: "
                          "[pages, slot, head, row] (NHD) or [pages, head, slot, row] (HND)")
-    slots, Hkv, ps, ts, hs = _pool_layout(pool.shape, pool.stride(), layout)
+    slots, Hkv, ps, ts, hs = _pool_layout(shape, st, layout)
     if slots != page_size:
         raise ValueError(f"the pool holds {slots} slots per page, page_size is {page_size}")
     B, bt_at, bt_stride, sl_at, err = _expect_table(block_table, seq_lens, index, err_flags)
-    return (index, B, Hkv, pool.shape[0], pool.data_ptr(), ps, ts, hs, bt_at, bt_stride, sl_at,
-            err)
+    return (index, B, Hkv, shape[0], pool.data_ptr(), ps, ts, hs, bt_at, bt_stride, sl_at, err)
 
 
 def _expect_rows(t, name, B, q_len, heads, index):
     """bf16 [B, q_len, heads, 128] whose heads lie side by side and whose tokens are
     evenly spaced (a slice of a fused projection's output is); returns (address, token
     stride)."""
-    at = _expect(t, name, _BF16, (B, q_len, heads, 128), index, False)
-    if t.is_contiguous():
-        return at, heads * 128
+    if t.dtype is not _BF16 or t.get_device() != index or t.shape != (B, q_len, heads, 128):
+        _refuse(t, name, _BF16, (B, q_len, heads, 128), index, False)
     sb, st, sh, one = t.stride()
     if one != 1 or (heads > 1 and sh != 128):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
@@ -1084,7 +1083,7 @@ def _expect_rows(t, name, B, q_len, heads, index):
         st = sb if B > 1 else heads * 128
     elif B > 1 and sb != q_len * st:
         raise ValueError(f"{name}: the tokens must be evenly spaced across the batch")
-    return at, st
+    return t.data_ptr(), st
 
 
 def kv_append_q4(k_new, v_new, pool, block_table, seq_lens, *, page_size, new_lens=None,
@@ -1178,36 +1177,35 @@ def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None
     if lse is not None:
         lse_at = _expect(lse, "lse", _F32, (B, q_len, Hq), index)
     on, scratch = _on(index, stream)
-
-    def params(out_at, ws_at, ws_bytes):
-        return _pack(_DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at,
-                     out_at, lse_at, B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale,
-                     ws_at, ws_bytes, err, num_ctas)
-
-    with scratch:
-        if out is None:
-            out = torch.empty(shape, dtype=_BF16, device=q.device)
-            out_at = out.data_ptr()
-        if workspace is None:  # a call's own, as in _run_ex
-            key = ("q4", index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len)
-            ws_bytes = _sizes.get(key)
-            if ws_bytes is None:
-                n = ctypes.c_size_t(0)
-                _check(_raw_fn("zl_decode_attn_q4_workspace_size", 1)(
-                    params(out_at, 0, 0), ctypes.addressof(n)),
-                    "zl_decode_attn_q4_workspace_size")
-                if len(_sizes) >= 4096:
-                    _sizes.clear()
-                ws_bytes = _sizes[key] = n.value
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        else:
-            if workspace.get_device() != index or not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous and on the pool's device")
-            ws_bytes = workspace.numel() * workspace.element_size()
-        status = _raw_fn("zl_decode_attn_q4", 1)(
-            params(out_at, workspace.data_ptr(), ws_bytes), on)
-        if status != OK:
-            _check(status, "zl_decode_attn_q4")
+    if workspace is None:
+        key = ("q4", index, B, q_len, Hq, Hkv, page_size, bt_stride, num_ctas, max_seq_len)
+        ws_bytes = _sizes.get(key)
+        if ws_bytes is None:
+            n = ctypes.c_size_t(0)
+            _check(_raw_fn("zl_decode_attn_q4_workspace_size", 1)(_pack(
+                _DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at,
+                lse_at, B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale, 0, 0, err,
+                num_ctas), ctypes.addressof(n)), "zl_decode_attn_q4_workspace_size")
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            ws_bytes = _sizes[key] = n.value
+    else:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the pool's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None or (workspace is None and ws_bytes):
+        with scratch:
+            if out is None:
+                out = torch.empty(shape, dtype=_BF16, device=q.device)
+                out_at = out.data_ptr()
+            if workspace is None and ws_bytes:  # a call's own, as in _run_ex
+                workspace = torch.empty(ws_bytes, dtype=_U8, device=q.device)
+    status = _raw_fn("zl_decode_attn_q4", 1)(_pack(
+        _DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at, lse_at,
+        B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale,
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, err, num_ctas), on)
+    if status != OK:
+        _check(status, "zl_decode_attn_q4")
     return out
 
 
@@ -1282,7 +1280,7 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
         if k_pool is not None or v_pool is not None:
             raise ValueError("either the bf16 pools or the 4-bit one")
         cache, kp = CACHE_Q4, pool
-        if pool.dtype is not torch.uint8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
+        if pool.dtype is not _U8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
             raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes")
     elif k_pool is not None or v_pool is not None:
         if k_pool is None or v_pool is None:

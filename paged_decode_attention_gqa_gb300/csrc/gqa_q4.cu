@@ -1089,7 +1089,7 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
     return ZL_ERR_UNSUPPORTED;
   const size_t slots = size_t(pl->ctas) * 2 * pl->HB * pl->rr;
   pl->off_o = round_up(slots * 4, 256);
-  pl->bytes = pl->off_o + slots * 128 * 4;
+  pl->bytes = pl->whole ? 0 : pl->off_o + slots * 128 * 4;
   return ZL_OK;
 }
 
@@ -1155,7 +1155,8 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
     return ZL_ERR_INVALID_ARG;
   Plan pl;
   if ((st = make_plan(a, &pl)) != ZL_OK) return st;
-  if (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < pl.bytes)
+  if (pl.bytes > 0 &&
+      (!a->workspace || !aligned_to(a->workspace, 256) || a->workspace_bytes < pl.bytes))
     return ZL_ERR_WORKSPACE;
   Q4Params p;
   std::memset(&p, 0, sizeof(p));

@@ -5,8 +5,12 @@
 // token. 8 lanes take a head: 16 elements each, as two chunks of 8 chosen so that
 // both elements of every rotated pair are the lane's own (half-split pairs: chunk l
 // and chunk l + n_freq / 8; interleaved or not rotated: chunks 2 l and 2 l + 1), so
-// only the sum of squares crosses lanes. A block takes a few tokens; the sines and
-// cosines of each are computed once for all its heads.
+// only the sum of squares crosses lanes. A warp takes a token (a part of its heads where
+// tokens are few), four heads at a time, queries, then keys, then values: the lane's
+// sines and cosines stay in registers, and rows are loaded two rounds ahead. (With blocks
+// of 8 tokens that read the angles from shared memory for every head those reads bounded
+// it, with rows one round ahead the latency of the loads: 16384 tokens of 40 heads 66 us
+// either way, 61.7 so, 5.4 TB/s.) Pairs of elements go through packed 32-bit operations.
 //
 // The angle: positions times turns. freq_turns is a frequency in turns, 64 bits
 // behind the point, so the product's low 64 bits are the angle without its whole
@@ -22,9 +26,7 @@
 namespace zl {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = kThreads / 8;  // heads a block works on at once
-constexpr int kMaxTokens = 8;        // tokens of a block
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxFreq = 64;
 
 struct NormRope {
@@ -43,170 +45,209 @@ struct NormRope {
   uint32_t* err_flags;
   int64_t tokens;       // B * q_len
   int q_len, Hq, Hkv, page_size, num_pages;
-  int cache, n_freq, interleaved;
-  int tokens_per_block, heads, heads_per_block;  // heads: Hq + Hkv (+ Hkv of v)
+  int n_freq, interleaved;
+  int heads;            // Hq + Hkv (+ Hkv of v)
+  int parts, part;      // parts of a token's heads, heads in each (a multiple of 4)
   uint64_t turns[kMaxFreq];
   uint8_t axes[kMaxFreq];
 };
 
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(
+// Two bf16 of a word as two 32-bit floats, low half first.
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return pack_f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool INTERLEAVED, int CACHE>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     const __grid_constant__ NormRope p) {
   griddep_launch_dependents();
-  __shared__ __align__(16) float cosine[kMaxTokens][kMaxFreq], sine[kMaxTokens][kMaxFreq];
-  __shared__ __align__(16) float weight[2][128];
-  __shared__ int64_t place[kMaxTokens];  // of the token's row in the pool, -1: not stored
-  const int64_t tok0 = int64_t(blockIdx.x) * p.tokens_per_block;
-  const int ntok = int(min(int64_t(p.tokens_per_block), p.tokens - tok0));
-
-  for (int e = threadIdx.x; e < ntok * p.n_freq; e += kThreads) {
-    const int tt = e / p.n_freq, f = e - tt * p.n_freq;
-    const int64_t tok = tok0 + tt;
-    int pos;
-    if (p.positions) {
-      pos = __ldg(p.positions + p.axes[f] * p.axis_stride + tok);
-    } else {
-      const int64_t b = tok / p.q_len;
-      pos = __ldg(p.seq_lens + b) - p.q_len + int(tok - b * p.q_len);
-    }
-    const uint64_t turn = uint64_t(int64_t(pos)) * p.turns[f] + 0x80000000ull;
-    float s, c;
-    sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    cosine[tt][f] = c * p.rope_scale;
-    sine[tt][f] = s * p.rope_scale;
-  }
+  __shared__ __align__(16) float cosine[kWarps][kMaxFreq], sine[kWarps][kMaxFreq];
+  // elements 8 c + 4 j .. + 3 at [j][c]: a quarter-warp's reads touch every bank once
+  __shared__ __align__(16) float weight[2][2][16][4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
+  const int pair_lanes = INTERLEAVED ? 0 : p.n_freq >> 3;  // lanes with half-split pairs
+  const bool turned = 8 * l < p.n_freq;
+  // chunks of a lane in a row of q or k (one of v: 2 l and 2 l + 1)
+  const int qa = l < pair_lanes ? l : 2 * l, qb = l < pair_lanes ? l + pair_lanes : 2 * l + 1;
   for (int e = threadIdx.x; e < 256; e += kThreads) {
     const float* w = p.weight[e >> 7];
-    weight[e >> 7][e & 127] = w ? __ldg(w + (e & 127)) : 1.f;
-  }
-  if (p.cache != ZL_CACHE_NONE && int(threadIdx.x) < ntok) {
-    const int64_t tok = tok0 + threadIdx.x, b = tok / p.q_len;
-    const int i = int(tok - b * p.q_len), L = __ldg(p.seq_lens + b);
-    int64_t at = -1;
-    uint32_t err = 0;
-    if (L < p.q_len || int64_t(L) > p.bt_stride * p.page_size) {
-      err = ZL_DEVERR_BAD_SEQ_LEN;
-    } else {
-      const int t = L - p.q_len + i;
-      const int page = __ldg(p.block_table + b * p.bt_stride + t / p.page_size);
-      if (page < 0 || page >= p.num_pages)
-        err = ZL_DEVERR_BAD_PAGE;
-      else
-        at = int64_t(page) * p.page_stride + int64_t(t % p.page_size) * p.token_stride;
-    }
-    if (err && blockIdx.y == 0 && p.err_flags) atomicOr(p.err_flags, err);
-    place[threadIdx.x] = at;
+    const int d = e & 127;
+    weight[e >> 7][(d >> 2) & 1][d >> 3][d & 3] = w ? __ldg(w + d) : 1.f;
   }
   __syncthreads();
 
-  const int l = threadIdx.x & 7;
-  const int h0 = blockIdx.y * p.heads_per_block;
-  const int nh = min(p.heads_per_block, p.heads - h0);
-  const int total = ntok * nh;
-  const int pair_lanes = p.interleaved ? 0 : p.n_freq >> 3;  // lanes with half-split pairs
-  for (int r0 = 0; r0 < total; r0 += kRows) {
-    const int r = r0 + int(threadIdx.x >> 3);
-    const bool live = r < total;  // (every lane stays for the shuffles)
-    const int tt = live ? r / nh : 0;
-    int h = live ? h0 + r - tt * nh : 0;
-    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-    h -= kind == 0 ? 0 : kind == 1 ? p.Hq : p.Hq + p.Hkv;
-    const int64_t tok = tok0 + tt;
-    const bool split = kind < 2 && l < pair_lanes;
-    const int ca = split ? l : 2 * l, cb = split ? l + pair_lanes : 2 * l + 1;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (live) {
-      const uint4* src = p.x[kind] + tok * p.stride[kind] + int64_t(h) * 16;
-      a = src[ca];
-      b = src[cb];
+  const int64_t units = p.tokens * p.parts, step = int64_t(gridDim.x) * kWarps;
+  for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < units; u += step) {
+    const int64_t tok = p.parts > 1 ? u / p.parts : u;
+    const int begin = int(u - tok * p.parts) * p.part, end = min(begin + p.part, p.heads);
+
+    // Row r of the token: a head of q, then of k, then of v.
+    auto head_of = [&](int r, int& h) {
+      h = r;
+      if (h < p.Hq) return 0;
+      h -= p.Hq;
+      if (CACHE == ZL_CACHE_NONE || h < p.Hkv) return 1;
+      h -= p.Hkv;
+      return 2;
+    };
+    uint4 a[2], b[2];  // of this round and the next
+    auto load = [&](int r, uint4& x, uint4& y) {
+      if (r >= end) return;
+      int h;
+      const int kind = head_of(r, h);
+      const uint4* src = p.x[kind] + tok * p.stride[kind] + h * 16;
+      x = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l : qa];
+      y = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l + 1 : qb];
+    };
+    int r = begin + (lane >> 3);
+    load(r, a[0], b[0]);
+    load(r + 4, a[1], b[1]);
+
+    // Angles: a lane computes those of two frequencies, and takes its own eight.
+    __syncwarp();  // (the last token's have been read)
+    const int64_t seq = !p.positions || CACHE != ZL_CACHE_NONE ? tok / p.q_len : 0;
+    const int i = int(tok - seq * p.q_len);
+    for (int f = lane; f < p.n_freq; f += 32) {
+      const int pos = p.positions ? __ldg(p.positions + p.axes[f] * p.axis_stride + tok)
+                                  : __ldg(p.seq_lens + seq) - p.q_len + i;
+      const uint64_t turn = uint64_t(int64_t(pos)) * p.turns[f] + 0x80000000ull;
+      float sn, cs;
+      sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+      cosine[warp][f] = cs * p.rope_scale;
+      sine[warp][f] = sn * p.rope_scale;
     }
-    uint32_t y[2][4] = {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
-    float x[2][8];
-    float ss = 0.f;
+    __syncwarp();
+    ulonglong2 co[2] = {}, si[2] = {};
+    if (turned) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack_bf16x2(y[c][i]);
-        x[c][2 * i] = v.x;
-        x[c][2 * i + 1] = v.y;
-        ss = fmaf(v.x, v.x, ss);
-        ss = fmaf(v.y, v.y, ss);
+      for (int c = 0; c < 2; ++c) {
+        co[c] = *reinterpret_cast<const ulonglong2*>(&cosine[warp][8 * l + 4 * c]);
+        si[c] = *reinterpret_cast<const ulonglong2*>(&sine[warp][8 * l + 4 * c]);
       }
-    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-    if (kind < 2) {  // (a row of v goes as it is)
-      if (p.weight[kind]) {
-        const float inv = rsqrtf(fmaf(ss, 1.f / 128.f, p.eps));
-        const float* wa = &weight[kind][8 * ca];
-        const float* wb = &weight[kind][8 * cb];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[0][i] = x[0][i] * inv * wa[i];
-          x[1][i] = x[1][i] * inv * wb[i];
-        }
+    }
+    int64_t place = -1;  // of the token in the pool, -1: not stored
+    if constexpr (CACHE != ZL_CACHE_NONE) {
+      const int L = __ldg(p.seq_lens + seq);
+      uint32_t err = 0;
+      if (L < p.q_len || int64_t(L) > p.bt_stride * p.page_size) {
+        err = ZL_DEVERR_BAD_SEQ_LEN;
+      } else {
+        const int t = L - p.q_len + i;
+        const int page = __ldg(p.block_table + seq * p.bt_stride + t / p.page_size);
+        if (page < 0 || page >= p.num_pages)
+          err = ZL_DEVERR_BAD_PAGE;
+        else
+          place = int64_t(page) * p.page_stride + int64_t(t % p.page_size) * p.token_stride;
       }
-      if (8 * l < p.n_freq) {
-        const float* co = &cosine[tt][8 * l];
-        const float* si = &sine[tt][8 * l];
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float& u = x[i >> 2][2 * (i & 3)];
-            float& v = x[i >> 2][2 * (i & 3) + 1];
-            const float u0 = u, v0 = v;
-            u = u0 * co[i] - v0 * si[i];
-            v = v0 * co[i] + u0 * si[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float u = x[0][i], v = x[1][i];
-            x[0][i] = u * co[i] - v * si[i];
-            x[1][i] = v * co[i] + u * si[i];
-          }
-        }
-      }
+      if (err && lane == 0 && begin == 0 && p.err_flags) atomicOr(p.err_flags, err);
+    }
+
+    for (; r - (lane >> 3) < end; r += 4) {
+      const bool live = r < end;  // (every lane stays for the shuffles)
+      int h;
+      const int kind = head_of(live ? r : begin, h);
+      const bool of_v = CACHE != ZL_CACHE_NONE && kind == 2;
+      const bool split = !of_v && l < pair_lanes;
+      const int ca = of_v ? 2 * l : qa, cb = of_v ? 2 * l + 1 : qb;
+      uint32_t y[2][4] = {{a[0].x, a[0].y, a[0].z, a[0].w}, {b[0].x, b[0].y, b[0].z, b[0].w}};
+      a[0] = a[1];
+      b[0] = b[1];
+      load(r + 8, a[1], b[1]);
+      uint64_t x[2][4], sums = 0;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[c][i] = pack_bf16x2(x[c][2 * i], x[c][2 * i + 1]);
-      uint4* to = p.out[kind];
-      if (live && to) {
-        to += tok * p.out_stride[kind] + int64_t(h) * 16;
-        to[ca] = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
-        to[cb] = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
+        for (int e = 0; e < 4; ++e) {
+          x[c][e] = widen(y[c][e]);
+          sums = fma_f32x2(x[c][e], x[c][e], sums);
+        }
+      const float2 two = unpack_f32x2(sums);
+      float ss = two.x + two.y;
+      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+      if (!of_v) {  // (a row of v goes as it is)
+        if (p.weight[kind]) {
+          const float inv = rsqrtf(fmaf(ss, 1.f / 128.f, p.eps));
+          const uint64_t inv2 = pack_f32x2(inv, inv);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const ulonglong2 w =
+                  *reinterpret_cast<const ulonglong2*>(weight[kind][j][c ? cb : ca]);
+              x[c][2 * j] = mul_f32x2(mul_f32x2(x[c][2 * j], inv2), w.x);
+              x[c][2 * j + 1] = mul_f32x2(mul_f32x2(x[c][2 * j + 1], inv2), w.y);
+            }
+        }
+        if (turned) {
+          if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint64_t c2 = e & 2 ? co[e >> 2].y : co[e >> 2].x;
+              const uint64_t s2 = e & 2 ? si[e >> 2].y : si[e >> 2].x;
+              const float c = e & 1 ? unpack_f32x2(c2).y : unpack_f32x2(c2).x;
+              const float s = e & 1 ? unpack_f32x2(s2).y : unpack_f32x2(s2).x;
+              const float2 v = unpack_f32x2(x[e >> 2][e & 3]);
+              x[e >> 2][e & 3] = pack_f32x2(v.x * c - v.y * s, v.y * c + v.x * s);
+            }
+          } else {
+            const uint64_t minus = pack_f32x2(-1.f, -1.f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t c = e & 1 ? co[e >> 1].y : co[e >> 1].x;
+              const uint64_t s = e & 1 ? si[e >> 1].y : si[e >> 1].x;
+              const uint64_t m = x[0][e], v = x[1][e];
+              x[0][e] = fma_f32x2(mul_f32x2(v, s), minus, mul_f32x2(m, c));
+              x[1][e] = fma_f32x2(m, s, mul_f32x2(v, c));
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack_f32x2(x[c][e]);
+            y[c][e] = pack_bf16x2(v.x, v.y);
+          }
+        uint4* to = p.out[kind];
+        if (live && (CACHE == ZL_CACHE_NONE || to)) {
+          to += tok * p.out_stride[kind] + h * 16;
+          to[ca] = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
+          to[cb] = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
+        }
       }
-    }
-    if (p.cache == ZL_CACHE_NONE) continue;
-    const int64_t at = place[tt];
-    const bool store = live && kind > 0 && at >= 0;
-    const int64_t row = at + int64_t(h) * p.head_stride;
-    if (p.cache == ZL_CACHE_BF16) {
-      if (store) {
-        uint4* to = reinterpret_cast<uint4*>(p.pool[kind - 1] + row);
-        to[ca] = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
-        to[cb] = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
-      }
-      continue;
-    }
-    // A scale's 16 elements are chunks 2 m and 2 m + 1: the lane's own two, or
-    // (half-split pairs; an even number of such lanes) one of its own and one of
-    // the next lane's.
-    uint32_t ma = q4_amax8(y[0]), mb = q4_amax8(y[1]);
-    const uint32_t oa = __shfl_xor_sync(0xffffffffu, ma, 1), ob = __shfl_xor_sync(0xffffffffu, mb, 1);
-    ma = max(ma, split ? oa : mb);
-    mb = split ? max(mb, ob) : ma;
-    if (store) {
-      const Q4Scale sa = q4_scale(ma), sb = q4_scale(mb);
-      uint8_t* to = p.pool[0] + row;
-      const int kv = kind - 1;
-      uint32_t* codes = reinterpret_cast<uint32_t*>(to + kv * kQ4VCodes);
-      codes[ca] = q4_codes(y[0], sa);
-      codes[cb] = q4_codes(y[1], sb);
-      if (!(ca & 1)) {
-        to[kQ4KScales + 8 * kv + (ca >> 1)] = uint8_t(sa.byte);
-        if (split) to[kQ4KScales + 8 * kv + (cb >> 1)] = uint8_t(sb.byte);
+      if constexpr (CACHE != ZL_CACHE_NONE) {
+        const bool store = live && kind > 0 && place >= 0;
+        const int64_t row = place + int64_t(h) * p.head_stride;
+        if constexpr (CACHE == ZL_CACHE_BF16) {
+          if (store) {
+            uint4* to = reinterpret_cast<uint4*>(p.pool[kind - 1] + row);
+            to[ca] = make_uint4(y[0][0], y[0][1], y[0][2], y[0][3]);
+            to[cb] = make_uint4(y[1][0], y[1][1], y[1][2], y[1][3]);
+          }
+        } else {
+          // A scale's 16 elements are chunks 2 m and 2 m + 1: the lane's own two, or
+          // (half-split pairs; an even number of such lanes) one of its own and one of
+          // the next lane's.
+          uint32_t ma = q4_amax8(y[0]), mb = q4_amax8(y[1]);
+          const uint32_t oa = __shfl_xor_sync(0xffffffffu, ma, 1);
+          const uint32_t ob = __shfl_xor_sync(0xffffffffu, mb, 1);
+          ma = max(ma, split ? oa : mb);
+          mb = split ? max(mb, ob) : ma;
+          if (store) {
+            const Q4Scale sa = q4_scale(ma), sb = q4_scale(mb);
+            uint8_t* to = p.pool[0] + row;
+            const int kv = kind - 1;
+            uint32_t* codes = reinterpret_cast<uint32_t*>(to + kv * kQ4VCodes);
+            codes[ca] = q4_codes(y[0], sa);
+            codes[cb] = q4_codes(y[1], sb);
+            if (!(ca & 1)) {
+              to[kQ4KScales + 8 * kv + (ca >> 1)] = uint8_t(sa.byte);
+              if (split) to[kQ4KScales + 8 * kv + (cb >> 1)] = uint8_t(sb.byte);
+            }
+          }
+        }
       }
     }
   }
@@ -334,7 +375,6 @@ extern "C" zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* a, zl_stream_
   p.q_len = a->q_len;
   p.Hq = a->Hq;
   p.Hkv = a->Hkv;
-  p.cache = a->cache;
   p.n_freq = a->n_freq;
   p.interleaved = a->interleaved ? 1 : 0;
   for (int i = 0; i < a->n_freq; ++i) {
@@ -342,16 +382,24 @@ extern "C" zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* a, zl_stream_
     p.axes[i] = a->axes ? a->axes[i] : 0;
   }
   p.heads = a->Hq + a->Hkv + (cached ? a->Hkv : 0);
-  // Tokens per block: 8 where that leaves four blocks to an SM, fewer otherwise;
-  // with few tokens a block takes 32 heads of one.
-  int tpb = kMaxTokens;
-  while (tpb > 1 && p.tokens < int64_t(tpb) * 4 * sms) tpb /= 2;
-  p.tokens_per_block = tpb;
-  p.heads_per_block = p.tokens < 2 * sms ? std::min(p.heads, kRows) : p.heads;
-  const int64_t bx = (p.tokens + tpb - 1) / tpb;
-  const int by = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
-  if (bx > INT32_MAX || by > 65535) return ZL_ERR_UNSUPPORTED;
-  qk_norm_rope_kernel<<<dim3(unsigned(bx), unsigned(by)), kThreads, 0,
-                        reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  // A warp to a token, or to a part of its heads (a multiple of 4) where that leaves SMs
+  // with fewer than 8 warps.
+  const int fours = (p.heads + 3) / 4;
+  p.parts = int(std::max<int64_t>(1, std::min<int64_t>(fours, 8 * sms / p.tokens)));
+  p.part = (fours + p.parts - 1) / p.parts * 4;
+  p.parts = (p.heads + p.part - 1) / p.part;
+  // three blocks are resident on an SM; with more units than warps these take several
+  const int64_t blocks = (p.tokens * p.parts + kWarps - 1) / kWarps;
+  const unsigned grid = unsigned(std::min<int64_t>(blocks, 3 * sms));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p); };
+  switch (a->cache * 2 + p.interleaved) {
+    case 0: launch(qk_norm_rope_kernel<false, ZL_CACHE_NONE>); break;
+    case 1: launch(qk_norm_rope_kernel<true, ZL_CACHE_NONE>); break;
+    case 2: launch(qk_norm_rope_kernel<false, ZL_CACHE_BF16>); break;
+    case 3: launch(qk_norm_rope_kernel<true, ZL_CACHE_BF16>); break;
+    case 4: launch(qk_norm_rope_kernel<false, ZL_CACHE_Q4>); break;
+    default: launch(qk_norm_rope_kernel<true, ZL_CACHE_Q4>);
+  }
   return cudaGetLastError() == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
