@@ -53,9 +53,11 @@ constexpr int kTile = 32;  // tokens of a ring stage: two such halves, on pages 
 constexpr int kHalfBytes = kHalf * kQ4Row;
 constexpr int kTileBytes = kTile * kQ4Row;
 constexpr int kMaxBundle = 8;
-// Warps of a CTA: 8, two CTAs to an SM; with 16 columns (more registers) 4, three CTAs.
-constexpr int max_warps(int nt) { return nt == 1 ? 8 : 4; }
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 3; }
+constexpr int kMaxWarps = 8;  // of a CTA
+// Two CTAs to an SM, of 128 registers; with 16 columns, whose outputs and queries alone
+// take 96, one of 245. (64 sequences verifying 4 tokens each: 63 us; with 12 warps of 168
+// registers, which spill, 70, and 73 with the queries in shared memory.)
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 // What a unit costs beside its tiles (queries, the masked tile, the epilogue: some 6 us of
 // a warp that shares its scheduler with three, where a tile takes 1.7), in tiles of each
 // slice: places of the line that hold no tile. (32 sequences of 1000-8000 tokens, 32 heads
@@ -289,12 +291,8 @@ __device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, i
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * max_warps(NT), ctas_per_sm(NT))
+__global__ void __launch_bounds__(32 * kMaxWarps, ctas_per_sm(NT))
 q4_decode_kernel(const __grid_constant__ Q4Params p) {
-  // Registers: with 16 columns a warp holds 64 outputs, so the query fragments stay in
-  // shared memory and the halves of a tile go one after the other.
-  constexpr bool kQShared = NT > 1;
-  constexpr int kSide = NT > 1 ? 1 : 2;  // halves side by side
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HB = p.HB, S = p.S, W = HB * S;  // W warps
@@ -304,9 +302,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   // outputs [warp][8][128]
   float* merge_l = reinterpret_cast<float*>(smem + W * NS * kTileBytes);
   float* merge_o = merge_l + (S > 1 ? W * 8 : 0);
-  // NT = 2: the query fragments of each head
-  uint4* q_shared = reinterpret_cast<uint4*>(merge_o + (S > 1 ? W * 8 * 128 : 0));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(q_shared + (NT > 1 ? HB * NT * 4 * 32 : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_o + (S > 1 ? W * 8 * 128 : 0));
   const uint32_t full = smem_u32(bars + warp * NS);
   int32_t* prefix = reinterpret_cast<int32_t*>(bars + W * NS);  // [B + 1]
   __shared__ int abort_flag;
@@ -442,7 +438,6 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   const int gid = lane >> 2, t4 = lane & 3;
   const int tok_k = half_token(gid);   // K: this lane's first row (the other is one on)
   const int tok_a = half_token(2 * t4), tok_b = half_token(2 * t4 + 1);  // V: and one on each
-  constexpr int half_step = kHalfBytes;
   const uint8_t* tile_at = ring;  // the stage to be read next
   uint32_t bar_at = full, phase = 0;
   int left = count - NS;  // tiles not issued yet
@@ -497,7 +492,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
 
     // Q^T fragments: column gid is query row row0 + 8 nt + gid; this lane's 32
     // elements from 32 t4 on, as fp16 times a power of two.
-    uint32_t qf[kQShared ? 1 : NT][16];
+    uint32_t qf[NT][16];
     uint64_t fac2[NT];  // softmax scales of columns 2 t4 and 2 t4 + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -525,13 +520,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 v = unpack_bf16x2(x[i]);
-        qf[kQShared ? 0 : nt][i] = pack_f16x2(v.x * up, v.y * up);
-      }
-      if constexpr (kQShared) {  // (slices of a head write the same)
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          q_shared[((hb * NT + nt) * 4 + w) * 32 + lane] =
-              make_uint4(qf[0][4 * w], qf[0][4 * w + 1], qf[0][4 * w + 2], qf[0][4 * w + 3]);
+        qf[nt][i] = pack_f16x2(v.x * up, v.y * up);
       }
       const float down = p.scale_log2 * __uint_as_float(uint32_t(127 - 14 + e) << 23);
       fac2[nt] = pack_f32x2(__shfl_sync(0xffffffffu, down, 8 * t4),
@@ -542,7 +531,6 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       return L - p.q_len + 1 + (row0 + 8 * nt + 2 * t4 + u) / p.g;
     };
     const int all_see = L - p.q_len + 1 + row0 / p.g;  // tokens that every row sees
-    __syncwarp();
 
     float o[NT][8][4];
     float base[NT][2], l[NT][2];  // base: minus it is added to a score (+inf: none yet)
@@ -561,172 +549,155 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
 
     // One tile: tokens tok0 .. tok0 + 31 of the sequence; MASKED: some row does not see
     // all of them. valid: how many there are.
-    auto run_tile = [&](auto masked_t, int first_tok, int first_valid) {
+    auto run_tile = [&](auto masked_t, int tok0, int valid) {
       constexpr bool MASKED = decltype(masked_t)::value;
+      const uint8_t* tile = tile_at;
+      // S^T: of each half, rows tok_k and tok_k + 1 of K, 32 elements of each
+      float s[2][NT][4];
+      {
+        uint4 ca[2], cb[2];
+        uint32_t fa[2][2], fb[2][2];
 #pragma unroll
-      for (int part = 0; part < 2; part += kSide) {
-        const uint8_t* tile = tile_at + part * half_step;
-        const int tok0 = first_tok + part * kHalf, valid = first_valid - part * kHalf;
-        // S^T: of each half, rows tok_k and tok_k + 1 of K, 32 elements of each
-        float s[kSide][NT][4];
-        {
-          uint4 ca[kSide], cb[kSide];
-          uint32_t fa[kSide][2], fb[kSide][2];
-#pragma unroll
-          for (int hf = 0; hf < kSide; ++hf) {
-            const uint8_t* row = tile + hf * half_step + tok_k * kQ4Row;
-            ca[hf] = *reinterpret_cast<const uint4*>(row + 16 * t4);
-            cb[hf] = *reinterpret_cast<const uint4*>(row + kQ4Row + 16 * t4);
-            const uint8_t* sc = row + kQ4KScales + 2 * t4;
-            fa[hf][0] = sc[0] * 0x00800080u;
-            fa[hf][1] = sc[1] * 0x00800080u;
-            fb[hf][0] = sc[kQ4Row] * 0x00800080u;
-            fb[hf][1] = sc[kQ4Row + 1] * 0x00800080u;
-          }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t qw[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (kQShared) {
-                const uint4 v = q_shared[((hb * NT + nt) * 4 + w) * 32 + lane];
-                qw[nt][0] = v.x, qw[nt][1] = v.y, qw[nt][2] = v.z, qw[nt][3] = v.w;
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qw[nt][i] = qf[nt][4 * w + i];
-              }
-            }
-#pragma unroll
-            for (int hf = 0; hf < kSide; ++hf) {
-              uint32_t xa[4], xb[4];
-              q4_pairs(w == 0 ? ca[hf].x : w == 1 ? ca[hf].y : w == 2 ? ca[hf].z : ca[hf].w, xa);
-              q4_pairs(w == 0 ? cb[hf].x : w == 1 ? cb[hf].y : w == 2 ? cb[hf].z : cb[hf].w, xb);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                xa[i] = mul_f16x2(xa[i], fa[hf][w >> 1]);
-                xb[i] = mul_f16x2(xb[i], fb[hf][w >> 1]);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if (w == 0)
-                  mma_f16_first(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qw[nt][0], qw[nt][1]);
-                else
-                  mma_f16(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qw[nt][0], qw[nt][1]);
-                mma_f16(s[hf][nt], xa[2], xb[2], xa[3], xb[3], qw[nt][2], qw[nt][3]);
-              }
-            }
-          }
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint8_t* row = tile + hf * kHalfBytes + tok_k * kQ4Row;
+          ca[hf] = *reinterpret_cast<const uint4*>(row + 16 * t4);
+          cb[hf] = *reinterpret_cast<const uint4*>(row + kQ4Row + 16 * t4);
+          const uint8_t* sc = row + kQ4KScales + 2 * t4;
+          fa[hf][0] = sc[0] * 0x00800080u;
+          fa[hf][1] = sc[1] * 0x00800080u;
+          fb[hf][0] = sc[kQ4Row] * 0x00800080u;
+          fb[hf][1] = sc[kQ4Row + 1] * 0x00800080u;
         }
-
-        // Softmax. This lane: of each half tokens tok_k, tok_k + 1 of columns 2 t4, 2 t4 + 1.
-        uint32_t pf[kSide][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          auto hidden = [&](int hf, int i) {
-            return MASKED && tok0 + 16 * hf + tok_k + (i >> 1) >= limit(nt, i & 1);
-          };
-          float y[kSide][4];
-          auto scores = [&] {
+        for (int w = 0; w < 4; ++w) {
 #pragma unroll
-            for (int hf = 0; hf < kSide; ++hf)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // (not fused: the largest score less itself is 0 at any size)
-                if ((i & 1) == 0) {
-                  const float2 v = unpack_f32x2(add_f32x2(
-                      mul_f32x2(pack_f32x2(s[hf][nt][i], s[hf][nt][i + 1]), fac2[nt]),
-                      pack_f32x2(base[nt][0], base[nt][1])));
-                  y[hf][i] = v.x;
-                  y[hf][i + 1] = v.y;
-                }
-              }
-#pragma unroll
-            for (int hf = 0; hf < kSide; ++hf)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (hidden(hf, i)) y[hf][i] = -CUDART_INF_F;
-          };
-          scores();
-          float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3]));
-          if (kSide > 1)
-            top = fmaxf(top, fmaxf(fmaxf(y[kSide - 1][0], y[kSide - 1][1]),
-                                   fmaxf(y[kSide - 1][2], y[kSide - 1][3])));
-          if (__any_sync(0xffffffffu, top > kMove)) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float mx = -CUDART_INF_F;
-#pragma unroll
-              for (int hf = 0; hf < kSide; ++hf)
-#pragma unroll
-                for (int i = u; i < 4; i += 2)
-                  if (!hidden(hf, i)) mx = fmaxf(mx, __fmul_rn(s[hf][nt][i], u ? unpack_f32x2(fac2[nt]).y : unpack_f32x2(fac2[nt]).x));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              // moves to kSlack below the largest where that is upwards
-              const float nb = kSlack - mx;
-              if (mx != -CUDART_INF_F && nb < base[nt][u]) {
-                const float alpha =
-                    base[nt][u] == CUDART_INF_F ? 0.f : ex2_approx(nb - base[nt][u]);
-                base[nt][u] = nb;
-                l[nt][u] *= alpha;
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                  o[nt][mt][u] *= alpha;
-                  o[nt][mt][u + 2] *= alpha;
-                }
-              }
-            }
-            scores();
-          }
-#pragma unroll
-          for (int hf = 0; hf < kSide; ++hf) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[hf][i] = ex2_approx(y[hf][i]);
-            l[nt][0] += y[hf][0] + y[hf][2];
-            l[nt][1] += y[hf][1] + y[hf][3];
-            pf[hf][nt][0] = transpose_8x8(pack_f16x2(y[hf][0], y[hf][1]));
-            pf[hf][nt][1] = transpose_8x8(pack_f16x2(y[hf][2], y[hf][3]));
-          }
-        }
-
-        // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first 8 fragment rows of a
-        // half's 16 tokens), a + 1, b + 1 (the others)
-#pragma unroll
-        for (int hf = 0; hf < kSide; ++hf) {
-          const uint8_t* ra = tile + hf * half_step + tok_a * kQ4Row + kQ4VCodes + 8 * gid;
-          const uint8_t* rb = tile + hf * half_step + tok_b * kQ4Row + kQ4VCodes + 8 * gid;
-          const uint2 a0 = *reinterpret_cast<const uint2*>(ra);
-          const uint2 a1 = *reinterpret_cast<const uint2*>(ra + kQ4Row);
-          const uint2 b0 = *reinterpret_cast<const uint2*>(rb);
-          const uint2 b1 = *reinterpret_cast<const uint2*>(rb + kQ4Row);
-          const uint8_t* sa = tile + hf * half_step + tok_a * kQ4Row + kQ4VScales + gid;
-          const uint8_t* sb = tile + hf * half_step + tok_b * kQ4Row + kQ4VScales + gid;
-          uint32_t s0 = sa[0], s1 = sa[kQ4Row], s2 = sb[0], s3 = sb[kQ4Row];
-          if (MASKED) {  // what lies behind the sequence may hold anything
-            s0 = 16 * hf + tok_a < valid ? s0 : 0u;
-            s1 = 16 * hf + tok_a + 1 < valid ? s1 : 0u;
-            s2 = 16 * hf + tok_b < valid ? s2 : 0u;
-            s3 = 16 * hf + tok_b + 1 < valid ? s3 : 0u;
-          }
-          const uint32_t f0 = s0 * 0x80u + s2 * 0x800000u, f1 = s1 * 0x80u + s3 * 0x800000u;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t wa0 = w ? a0.y : a0.x, wb0 = w ? b0.y : b0.x;
-            const uint32_t wa1 = w ? a1.y : a1.x, wb1 = w ? b1.y : b1.x;
-            uint32_t x0[4], y0[4], x1[4], y1[4];  // even and odd elements
-            q4_pairs(select_bits(wa0, wb0 << 4, 0x0F0F0F0Fu), x0);
-            q4_pairs(select_bits(wa0 >> 4, wb0, 0x0F0F0F0Fu), y0);
-            q4_pairs(select_bits(wa1, wb1 << 4, 0x0F0F0F0Fu), x1);
-            q4_pairs(select_bits(wa1 >> 4, wb1, 0x0F0F0F0Fu), y1);
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t xa[4], xb[4];
+            q4_pairs(w == 0 ? ca[hf].x : w == 1 ? ca[hf].y : w == 2 ? ca[hf].z : ca[hf].w, xa);
+            q4_pairs(w == 0 ? cb[hf].x : w == 1 ? cb[hf].y : w == 2 ? cb[hf].z : cb[hf].w, xb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t m0 = mul_f16x2(x0[i], f0), m1 = mul_f16x2(y0[i], f0);
-              const uint32_t m2 = mul_f16x2(x1[i], f1), m3 = mul_f16x2(y1[i], f1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[nt][4 * w + i], m0, m1, m2, m3, pf[hf][nt][0], pf[hf][nt][1]);
+              xa[i] = mul_f16x2(xa[i], fa[hf][w >> 1]);
+              xb[i] = mul_f16x2(xb[i], fb[hf][w >> 1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (w == 0)
+                mma_f16_first(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+              else
+                mma_f16(s[hf][nt], xa[0], xb[0], xa[1], xb[1], qf[nt][4 * w], qf[nt][4 * w + 1]);
+              mma_f16(s[hf][nt], xa[2], xb[2], xa[3], xb[3], qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            }
+          }
+        }
+      }
+
+      // Softmax. This lane: of each half tokens tok_k, tok_k + 1 of columns 2 t4, 2 t4 + 1.
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        auto hidden = [&](int hf, int i) {
+          return MASKED && tok0 + 16 * hf + tok_k + (i >> 1) >= limit(nt, i & 1);
+        };
+        float y[2][4];
+        auto scores = [&] {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // (not fused: the largest score less itself is 0 at any size)
+              if ((i & 1) == 0) {
+                const float2 v = unpack_f32x2(add_f32x2(
+                    mul_f32x2(pack_f32x2(s[hf][nt][i], s[hf][nt][i + 1]), fac2[nt]),
+                    pack_f32x2(base[nt][0], base[nt][1])));
+                y[hf][i] = v.x;
+                y[hf][i + 1] = v.y;
+              }
+            }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (hidden(hf, i)) y[hf][i] = -CUDART_INF_F;
+        };
+        scores();
+        const float top = fmaxf(fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[0][2], y[0][3])),
+                                fmaxf(fmaxf(y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3])));
+        if (__any_sync(0xffffffffu, top > kMove)) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int i = u; i < 4; i += 2)
+                if (!hidden(hf, i)) mx = fmaxf(mx, __fmul_rn(s[hf][nt][i], u ? unpack_f32x2(fac2[nt]).y : unpack_f32x2(fac2[nt]).x));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            // moves to kSlack below the largest where that is upwards
+            const float nb = kSlack - mx;
+            if (mx != -CUDART_INF_F && nb < base[nt][u]) {
+              const float alpha =
+                  base[nt][u] == CUDART_INF_F ? 0.f : ex2_approx(nb - base[nt][u]);
+              base[nt][u] = nb;
+              l[nt][u] *= alpha;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                o[nt][mt][u] *= alpha;
+                o[nt][mt][u + 2] *= alpha;
+              }
+            }
+          }
+          scores();
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[hf][i] = ex2_approx(y[hf][i]);
+          l[nt][0] += y[hf][0] + y[hf][2];
+          l[nt][1] += y[hf][1] + y[hf][3];
+          pf[hf][nt][0] = transpose_8x8(pack_f16x2(y[hf][0], y[hf][1]));
+          pf[hf][nt][1] = transpose_8x8(pack_f16x2(y[hf][2], y[hf][3]));
+        }
+      }
+
+      // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first 8 fragment rows of a
+      // half's 16 tokens), a + 1, b + 1 (the others)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint8_t* ra = tile + hf * kHalfBytes + tok_a * kQ4Row + kQ4VCodes + 8 * gid;
+        const uint8_t* rb = tile + hf * kHalfBytes + tok_b * kQ4Row + kQ4VCodes + 8 * gid;
+        const uint2 a0 = *reinterpret_cast<const uint2*>(ra);
+        const uint2 a1 = *reinterpret_cast<const uint2*>(ra + kQ4Row);
+        const uint2 b0 = *reinterpret_cast<const uint2*>(rb);
+        const uint2 b1 = *reinterpret_cast<const uint2*>(rb + kQ4Row);
+        const uint8_t* sa = tile + hf * kHalfBytes + tok_a * kQ4Row + kQ4VScales + gid;
+        const uint8_t* sb = tile + hf * kHalfBytes + tok_b * kQ4Row + kQ4VScales + gid;
+        uint32_t s0 = sa[0], s1 = sa[kQ4Row], s2 = sb[0], s3 = sb[kQ4Row];
+        if (MASKED) {  // what lies behind the sequence may hold anything
+          s0 = 16 * hf + tok_a < valid ? s0 : 0u;
+          s1 = 16 * hf + tok_a + 1 < valid ? s1 : 0u;
+          s2 = 16 * hf + tok_b < valid ? s2 : 0u;
+          s3 = 16 * hf + tok_b + 1 < valid ? s3 : 0u;
+        }
+        const uint32_t f0 = s0 * 0x80u + s2 * 0x800000u, f1 = s1 * 0x80u + s3 * 0x800000u;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t wa0 = w ? a0.y : a0.x, wb0 = w ? b0.y : b0.x;
+          const uint32_t wa1 = w ? a1.y : a1.x, wb1 = w ? b1.y : b1.x;
+          uint32_t x0[4], y0[4], x1[4], y1[4];  // even and odd elements
+          q4_pairs(select_bits(wa0, wb0 << 4, 0x0F0F0F0Fu), x0);
+          q4_pairs(select_bits(wa0 >> 4, wb0, 0x0F0F0F0Fu), y0);
+          q4_pairs(select_bits(wa1, wb1 << 4, 0x0F0F0F0Fu), x1);
+          q4_pairs(select_bits(wa1 >> 4, wb1, 0x0F0F0F0Fu), y1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t m0 = mul_f16x2(x0[i], f0), m1 = mul_f16x2(y0[i], f0);
+            const uint32_t m2 = mul_f16x2(x1[i], f1), m3 = mul_f16x2(y1[i], f1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][4 * w + i], m0, m1, m2, m3, pf[hf][nt][0], pf[hf][nt][1]);
           }
         }
       }
@@ -856,22 +827,37 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         }
         named_barrier(1 + hb, S * 32);
         for (int r = sl; r < min(8, R - 8 * nt); r += S) {
-          RowMerge m;
-          m.init();
+          // (the largest first: then nothing waits for the slice before)
+          float top = -CUDART_INF_F, den = 0.f;
+          bool bad = false;
           for (int s = 0; s < S; ++s) {
-            const int at = (s * HB + hb) * 8 + r;
-            m.add(merge_l[at], reinterpret_cast<const float4*>(merge_o + at * 128)[lane]);
+            const float ls = merge_l[(s * HB + hb) * 8 + r];
+            bad |= isnan(ls);
+            top = fmaxf(top, ls);
           }
-          const bool none = m.bad || m.den == 0.f;
-          const float inv = none ? 0.f : rcp_approx(m.den);
-          const float lse2 = none ? -CUDART_INF_F : m.m + lg2_approx(m.den);
-          const float4 v = none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : make_float4(m.o.x * inv, m.o.y * inv, m.o.z * inv, m.o.w * inv);
+          const bool none = bad || top == -CUDART_INF_F;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!none) {
+#pragma unroll 4
+            for (int s = 0; s < S; ++s) {
+              const int at = (s * HB + hb) * 8 + r;
+              const float wgt = ex2_approx(merge_l[at] - top);
+              const float4 os = reinterpret_cast<const float4*>(merge_o + at * 128)[lane];
+              den += wgt;
+              v.x = fmaf(wgt, os.x, v.x);
+              v.y = fmaf(wgt, os.y, v.y);
+              v.z = fmaf(wgt, os.z, v.z);
+              v.w = fmaf(wgt, os.w, v.w);
+            }
+            const float inv = rcp_approx(den);
+            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          }
+          const float lse2 = none ? -CUDART_INF_F : top + lg2_approx(den);
           if (cut_unit) {
             const int64_t at = part0 + 8 * nt + r;
             reinterpret_cast<float4*>(p.ws_o + at * 128)[lane] = v;
             if (lane == 0)
-              p.ws_lse[at] = m.bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
+              p.ws_lse[at] = bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
           } else {
             const int64_t row = query_row(p, b, h, row0 + 8 * nt + r);
             reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
@@ -992,7 +978,6 @@ size_t smem_bytes(const Plan& pl, int B) {
   const size_t W = size_t(pl.HB) * pl.S;
   size_t n = W * pl.stages * (kTileBytes + 8) + (size_t(B) + 1) * 4;
   if (pl.S > 1) n += W * 8 * (4 + 128 * 4);
-  if (pl.nt > 1) n += size_t(pl.HB) * pl.nt * 4 * 32 * 16;
   return n;
 }
 
@@ -1049,14 +1034,13 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   // Bundle: of the divisors of Hkv up to 8 the one that leaves the fewest warps of a CTA
   // idle, the largest of those; one head in small calls, where slices cut the time of a
   // unit.
-  const int warps = max_warps(pl->nt);
   pl->HB = 1;
   const int64_t len = a->max_seq_len > 0 ? a->max_seq_len : 4096;
   const int64_t tiles = int64_t(a->B) * a->Hkv * pl->rgroups * ((len + kTile - 1) / kTile);
   if (tiles >= int64_t(sms) * 32)
     for (int d = 2; d <= kMaxBundle; ++d)
-      if (a->Hkv % d == 0 && warps / d * d >= warps / pl->HB * pl->HB) pl->HB = d;
-  pl->S = warps / pl->HB;
+      if (a->Hkv % d == 0 && kMaxWarps / d * d >= kMaxWarps / pl->HB * pl->HB) pl->HB = d;
+  pl->S = kMaxWarps / pl->HB;
   pl->units_per_seq = a->Hkv / pl->HB * pl->rgroups;
   // Two stages to a warp, 147 KB on an SM: more only make the requests of all SMs wait
   // for one another (with three 64 sequences of 512-4096 tokens took 49 us, not 45, and
