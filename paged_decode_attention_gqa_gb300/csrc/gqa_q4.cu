@@ -58,12 +58,12 @@ constexpr int kMaxWarps = 8;  // of a CTA
 // take 96, one of 245. (64 sequences verifying 4 tokens each: 63 us; with 12 warps of 168
 // registers, which spill, 70, and 73 with the queries in shared memory.)
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
-// What a unit costs beside its tiles (queries, the masked tile, the epilogue: some 6 us of
+// What a unit costs beside its tiles (queries, the masked tile, the epilogue: some 4 us of
 // a warp that shares its scheduler with three, where a tile takes 1.7), in tiles of each
-// slice: places of the line that hold no tile. (32 sequences of 1000-8000 tokens, 32 heads
-// on one kv head: without 36 us, with 2 32, with 4 28; 64 sequences verifying 4 tokens
-// each: 77, 75, 72.)
-constexpr int kUnitCost = 4;
+// slice: places of the line that hold none. (64 sequences of 512-4096 tokens: with 2 44.1
+// us, with 4 44.9; verifying 4 tokens each, so 16 columns: 65.5 and 62.6; 32 heads on one
+// kv head: 27.2 and 25.2, without 36.)
+constexpr int unit_cost(int nt) { return nt == 1 ? 2 : 4; }
 // Units of at most this many tiles per slice get a CTA each where there are CTAs
 // enough: streaming them costs less than the merge of their parts.
 constexpr int kWholeTiles = 4;
@@ -93,6 +93,7 @@ struct Q4Params {
   int units_per_seq;     // bundles x row groups
   int rgroups, rr, rows; // row groups of rr rows, rows = g * q_len of a kv head
   int ctas;              // CTAs of the attention kernel
+  int cost;              // places of a unit that hold no tile, a multiple of S
   int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
   int whole;             // 1: CTA c takes unit c and there is no merge (max_seq_len is short)
   float scale_log2;
@@ -262,7 +263,7 @@ __device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, i
   for (int i = 0; i < per && b0 + i < p.B; i += 32) {
     const int b = b0 + i + lane;
     const int n = b < p.B ? tiles_of(p, __ldcg(p.seq_lens + b)) : 0;
-    int incl = n > 0 ? n + kUnitCost * p.S : 0;
+    int incl = n > 0 ? n + p.cost : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, off);
@@ -342,7 +343,46 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   auto seq_tiles = [&](int b) { return (prefix[b + 1] - prefix[b]) * M; };
 
   const int hb = warp % HB, sl = warp / HB;
-  const int count = sl < len ? (len - 1 - sl) / S + 1 : 0;  // this warp's: sl, sl + S, ..
+  // This warp's tiles: of the range's places sl, sl + S, .. those that hold one.
+  int count = 0;
+  {
+    int b = b_c, r = r_c;
+    for (int at = 0; at < len;) {
+      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
+      const int places = prefix[b + 1] - prefix[b], n = places - p.cost;
+      const int j = M > 1 ? r % places : r;
+      const int piece = min(len - at, places - j), real = max(min(piece, n - j), 0);
+      const int skip = at % S <= sl ? sl - at % S : sl + S - at % S;
+      if (skip < real) count += (real - 1 - skip) / S + 1;
+      at += piece;
+      r += piece;
+    }
+  }
+  // Moves (b, r) to the first place from r on, in steps of S, that holds a tile; returns how
+  // many of the unit's tiles lie from there on in such steps, and the tile's own number.
+  auto to_tile = [&](int& b, int& r, int& unit, int& j) -> int {
+    for (;;) {
+      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
+      const int places = prefix[b + 1] - prefix[b], n = places - p.cost;
+      unit = M > 1 ? r / places : 0;
+      j = r - unit * places;
+      if (j < n) return (n - j + S - 1) / S;
+      r += (places - j + S - 1) / S * S;
+    }
+  };
+  // The i-th of this warp's tiles behind the one at (b, r).
+  auto tile_behind = [&](int i, int& b, int& r, int& unit, int& j) {
+    for (;;) {
+      const int here = to_tile(b, r, unit, j);
+      if (i < here) {
+        r += i * S;
+        j += i * S;
+        return;
+      }
+      i -= here;
+      r += here * S;
+    }
+  };
 
   // With the copies of every SM under way a load that goes to HBM waits behind some 20 MB
   // of them, 3 to 5 us. So the queries of a unit and the pages of the next tiles are
@@ -361,34 +401,31 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   // ---- the warp as its own producer: lanes 2 i and 2 i + 1 hold page and place of
   // the halves of its tile 16 j + i (place -1: no token there, or a bad page)
   int page = 0, coord = -1;
-  int b_next = b_c, r_next = r_c + sl;  // the tile that the next batch begins with
+  int b_next = b_c, r_next = r_c + sl;  // where the next batch begins
   bool any_bad = false;  // a half on a bad page so far (the same in every lane)
   auto resolve = [&](int k0) {
-    while (r_next >= seq_tiles(b_next) && b_next + 1 < p.B) r_next -= seq_tiles(b_next++);
     page = 0;
     coord = -1;
+    int unit, j;
     if (k0 + (lane >> 1) < count) {
-      int b = b_next, r = r_next + (lane >> 1) * S;
-      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
-      const int n = prefix[b + 1] - prefix[b];
-      const int unit = M > 1 ? r / n : 0, t = (r - unit * n) * kTile + (lane & 1) * kHalf;
-      const int pg = t / p.page_size;
+      int b = b_next, r = r_next;
+      tile_behind(lane >> 1, b, r, unit, j);
+      const int t = j * kTile + (lane & 1) * kHalf, pg = t / p.page_size;
       // (a half behind the last token has no page; the table's row is not read there)
-      const int L = __ldg(p.seq_lens + b);
-      if (t < L) {
+      if (t < __ldg(p.seq_lens + b)) {
         page = __ldg(p.block_table + b * p.bt_stride + pg);
         coord = (t - pg * p.page_size) |
                 (((p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb) << 10);
       }
     }
-    if (k0 + 16 + (lane >> 1) < count) {  // the entry of the tile 16 further on
-      int b = b_next, r = r_next + (16 + (lane >> 1)) * S;
-      while (r >= seq_tiles(b)) r -= seq_tiles(b++);
-      const int n = prefix[b + 1] - prefix[b];
-      const int t = min((M > 1 ? r % n : r) * kTile, __ldg(p.seq_lens + b) - 1);
-      prefetch_l2(p.block_table + b * p.bt_stride + t / p.page_size);
+    if (k0 + 16 < count) {
+      tile_behind(16, b_next, r_next, unit, j);
+      if (k0 + 16 + (lane >> 1) < count) {  // the next batch's table entries
+        int b = b_next, r = r_next;
+        tile_behind(lane >> 1, b, r, unit, j);
+        prefetch_l2(p.block_table + b * p.bt_stride + j * kTile / p.page_size);
+      }
     }
-    r_next += 16 * S;
     const bool bad = page < 0 || page >= p.num_pages;
     any_bad |= __any_sync(0xffffffffu, bad);
     if (bad) {
@@ -472,7 +509,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   while (pos < len) {
     while (r_c >= seq_tiles(b_c)) r_c -= seq_tiles(b_c++);
     const int b = b_c;
-    const int places = prefix[b + 1] - prefix[b], n = places - kUnitCost * S;
+    const int places = prefix[b + 1] - prefix[b], n = places - p.cost;
     const int unit = M > 1 ? r_c / places : 0, j0 = r_c - unit * places;
     const int piece_end = min(len, pos - j0 + places);
     const bool cut_unit = j0 > 0 || piece_end - pos < n;
@@ -707,7 +744,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     // of which every row sees whole
     const int behind = pos % S;
     const int t0 = pos + (sl >= behind ? sl - behind : sl + S - behind);
-    int todo = t0 < piece_end ? (piece_end - 1 - t0) / S + 1 : 0;
+    const int real_end = min(piece_end, pos - j0 + n);  // (behind it: places without a tile)
+    int todo = t0 < real_end ? (real_end - 1 - t0) / S + 1 : 0;
     int tok0 = (j0 + t0 - pos) * kTile;
     const int stride = S * kTile;  // tokens from one to the next
     while (todo > 0) {
@@ -737,7 +775,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
             for (int u = 0; u < 2; ++u) bad_row[nt][u] |= bad && tok0 + whole < limit(nt, u);
         }
         // (a row that does not see the bad half still needs the good one)
-        if (whole > 0 && tok0 < L) run_tile(std::true_type{}, tok0, min(L - tok0, whole));
+        if (whole > 0) run_tile(std::true_type{}, tok0, min(L - tok0, whole));
       }
       next();
       --todo;
@@ -893,7 +931,7 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
   int longest;
   scan_tiles(p, prefix, &longest);
   const int b = blockIdx.y;
-  const int n = prefix[b + 1] - prefix[b] - kUnitCost * p.S;  // tiles (below 1: none)
+  const int n = prefix[b + 1] - prefix[b] - p.cost;  // tiles (below 1: none)
   const Cut cut(p, prefix[p.B], longest);
   griddep_wait();
   if (n < 1 || cut.whole) return;
@@ -1055,7 +1093,7 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   pl->ctas = a->num_ctas > 0 ? a->num_ctas : per_sm * sms;
   if (a->num_ctas == 0 && a->max_seq_len > 0) {
     const int64_t most =
-        int64_t(a->B) * pl->units_per_seq * ((len + kTile - 1) / kTile + kUnitCost * pl->S);
+        int64_t(a->B) * pl->units_per_seq * ((len + kTile - 1) / kTile + unit_cost(pl->nt) * pl->S);
     pl->ctas = int(std::max<int64_t>(1, std::min<int64_t>(pl->ctas, most)));
   }
   const int64_t units = int64_t(a->B) * pl->units_per_seq;
@@ -1065,10 +1103,10 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   // a warp of the merge reads four parts at a time; more warps to a row where a unit
   // is cut into more
   const int64_t parts = pl->ctas / units + 2;
-  pl->merge_warps = parts > 16 ? 8 : parts > 8 ? 4 : parts > 4 ? 2 : 1;
+  pl->merge_warps = parts > 24 ? 8 : parts > 12 ? 4 : parts > 6 ? 2 : 1;
   // (a CTA counts its tiles, and those of a sequence's units, in 32 bits)
   const int64_t line =
-      (a->block_table_stride * a->page_size / kTile + 1 + kUnitCost * pl->S) * pl->units_per_seq;
+      (a->block_table_stride * a->page_size / kTile + 1 + unit_cost(pl->nt) * pl->S) * pl->units_per_seq;
   if (line * a->B / pl->ctas >= (INT64_C(1) << 29) || line >= (INT64_C(1) << 29))
     return ZL_ERR_UNSUPPORTED;
   const size_t slots = size_t(pl->ctas) * 2 * pl->HB * pl->rr;
@@ -1170,6 +1208,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.rr = pl.rr;
   p.rows = pl.rows;
   p.ctas = pl.ctas;
+  p.cost = unit_cost(pl.nt) * pl.S;
   p.box32 = a->page_size % kTile == 0;
   p.whole = pl.whole;
   p.scale_log2 = float(double(a->scale) * kLog2e);
