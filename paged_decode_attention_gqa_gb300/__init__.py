@@ -1035,16 +1035,18 @@ def _pool_layout(shape, st, layout):
 def _expect_table(block_table, seq_lens, index, err_flags):
     """Block table, lengths and error word; returns (B, addresses of the table, its
     stride, of seq_lens and err_flags)."""
-    if block_table.dim() != 2:
+    shape, st = block_table.shape, block_table.stride()
+    if len(shape) != 2:
         raise ValueError("block_table must be 2-D")
-    B, width = block_table.shape
-    sl_at = _expect(seq_lens, "seq_lens", _I32, (B,), index)
-    bt_at = _expect(block_table, "block_table", _I32, (B, width), index, False)
-    bt_stride, one = block_table.stride()
-    if B == 1:
-        bt_stride = width
-    if (width > 1 and one != 1) or bt_stride < width:
+    B, width = shape
+    bt_stride = st[0] if B > 1 else width
+    if (block_table.dtype is not _I32 or block_table.get_device() != index
+            or (width > 1 and st[1] != 1) or bt_stride < width):
+        _expect(block_table, "block_table", _I32, (B, width), index, False)
         raise ValueError("block_table rows must be contiguous and distinct")
+    if (seq_lens.dtype is not _I32 or seq_lens.get_device() != index or seq_lens.shape != (B,)
+            or not seq_lens.is_contiguous()):
+        _refuse(seq_lens, "seq_lens", _I32, (B,), index, True)
     err = 0
     if err_flags is not None:
         if err_flags.dtype is not _I32 and err_flags.dtype is not _U32 or err_flags.numel() < 1:
@@ -1052,7 +1054,7 @@ def _expect_table(block_table, seq_lens, index, err_flags):
         if err_flags.get_device() != index:
             raise ValueError(f"err_flags is on {err_flags.device}, the pool on device {index}")
         err = err_flags.data_ptr()
-    return B, bt_at, bt_stride, sl_at, err
+    return B, block_table.data_ptr(), bt_stride, seq_lens.data_ptr(), err
 
 
 def _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags):
@@ -1107,7 +1109,7 @@ def kv_append_q4(k_new, v_new, pool, block_table, seq_lens, *, page_size, new_le
     if new_lens is not None:
         n_at = _expect(new_lens, "new_lens", _I32, (B,), index)
     on, _ = _on(index, stream)
-    status = _raw_fn("zl_kv_append_q4", 1)(_pack(
+    status = (_raw.get("zl_kv_append_q4") or _raw_fn("zl_kv_append_q4", 1))(_pack(
         _APPEND_Q4, _APPEND_Q4.size, k_at, v_at, k_st, v_st, at, ps, ts, hs, bt_at, bt_stride,
         sl_at, n_at, B, q_len, Hkv, page_size, pages, err), on)
     if status != OK:
@@ -1145,7 +1147,7 @@ def kv_read_q4(pool, block_table, seq_lens, *, page_size, tokens=None, k_out=Non
         k_at = _expect(k_out, "k_out", _BF16, (B, tokens, Hkv, 128), index)
     if v_out is not None:
         v_at = _expect(v_out, "v_out", _BF16, (B, tokens, Hkv, 128), index)
-    status = _raw_fn("zl_kv_read_q4", 1)(_pack(
+    status = (_raw.get("zl_kv_read_q4") or _raw_fn("zl_kv_read_q4", 1))(_pack(
         _READ_Q4, _READ_Q4.size, at, ps, ts, hs, bt_at, bt_stride, sl_at, k_at, v_at, B, tokens,
         Hkv, page_size, pages, err), on)
     if status != OK:
@@ -1200,7 +1202,7 @@ def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None
                 out_at = out.data_ptr()
             if workspace is None and ws_bytes:  # a call's own, as in _run_ex
                 workspace = torch.empty(ws_bytes, dtype=_U8, device=q.device)
-    status = _raw_fn("zl_decode_attn_q4", 1)(_pack(
+    status = (_raw.get("zl_decode_attn_q4") or _raw_fn("zl_decode_attn_q4", 1))(_pack(
         _DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at, lse_at,
         B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale,
         0 if workspace is None else workspace.data_ptr(), ws_bytes, err, num_ctas), on)
@@ -1344,7 +1346,7 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
             if k_out is None and not cache:
                 k_out = torch.empty((B, q_len, Hkv, 128), dtype=_BF16, device=q.device)
                 ko_at, ko_st = k_out.data_ptr(), Hkv * 128
-    status = _raw_fn("zl_qk_norm_rope", 1)(_pack(
+    status = (_raw.get("zl_qk_norm_rope") or _raw_fn("zl_qk_norm_rope", 1))(_pack(
         _NORM_ROPE, _NORM_ROPE.size, q_at, k_at, v_at, q_st, k_st, v_st, qo_at, ko_at, qo_st,
         ko_st, qw, kw, eps, rope.scale, rope.turns_at, rope.axes_at, rope.n_freq, rope.n_axes,
         rope.interleaved, cache, pos_at, axis_st, kp.data_ptr() if cache else 0, vp_at, ps, ts, hs,

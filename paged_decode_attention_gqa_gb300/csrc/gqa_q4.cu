@@ -933,6 +933,20 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
   const int b = blockIdx.y;
   const int n = prefix[b + 1] - prefix[b] - p.cost;  // tiles (below 1: none)
   const Cut cut(p, prefix[p.B], longest);
+  // The CTAs that hold a unit's tiles, and 1 in .z where the first of them began before the
+  // unit; of the sequence's first units ahead of the wait.
+  auto span_of = [&](int unit) {
+    const int64_t U0 =
+        int64_t(p.units_per_seq) * prefix[b] + int64_t(unit) * (prefix[b + 1] - prefix[b]);
+    const int lo = cut.owner(U0);
+    return make_int3(lo, cut.owner(U0 + n - 1), U0 > cut.start(lo) ? 1 : 0);
+  };
+  constexpr int kSpans = 64;
+  __shared__ int3 spans[kSpans];
+  if (n > 0 && !cut.whole)
+    for (int i = threadIdx.x; i < min(p.units_per_seq, kSpans); i += blockDim.x)
+      spans[i] = span_of(i);
+  __syncthreads();
   griddep_wait();
   if (n < 1 || cut.whole) return;
   const int64_t per_slot = int64_t(p.HB) * p.rr;
@@ -944,11 +958,11 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
     m.init();
     int lo = 0, hi = 0;
     if (id < rows) {
-      const int bundle = h / p.HB, rg = r / p.rr;
-      const int64_t U0 = int64_t(p.units_per_seq) * prefix[b] +
-                         int64_t(bundle * p.rgroups + rg) * (prefix[b + 1] - prefix[b]);
-      lo = cut.owner(U0), hi = cut.owner(U0 + n - 1);
-      const int first_slot = U0 > cut.start(lo) ? 1 : 0;
+      const int bundle = h / p.HB, rg = p.rgroups > 1 ? r / p.rr : 0;
+      const int unit = bundle * p.rgroups + rg;
+      const int3 span = unit < kSpans ? spans[unit] : span_of(unit);
+      lo = span.x, hi = span.y;
+      const int first_slot = span.z;
       const int64_t at0 = (h - bundle * p.HB) * p.rr + (r - rg * p.rr);
       for (int c0 = lo < hi ? lo + w : hi + 1; c0 <= hi; c0 += 4 * PW) {
         float l[4];
