@@ -34,7 +34,15 @@
 // instruction for one, and nothing overlaps that (in registers alone, 16 conversions,
 // 16 products and 4 mma take the sum of it). A ring per CTA with copies for all its
 // heads at once, its warps taking turns at issuing them, needs fewer instructions and
-// was slower all the same: the warps then wait for one another.
+// was slower all the same: the warps then wait for one another. Queries and page ids
+// brought into L2 ahead of their use cost more in registers and instructions than they
+// save (8 sequences of 32k-131k tokens: 126 us with them, 123 without).
+//
+// Measured, 32 query heads on 8 kv heads, from a graph: 8 sequences of 32k-131k tokens
+// 123 us, 5.9 TB/s of 6.8 that a copy reaches (HBM, and ends of CTAs from 103 us on); 64
+// of 512-4096 tokens 43 us (9 until the first tile is there, 27 of streaming, 7 of ends
+// and merge), verifying 4 drafted tokens each 59 us (matrix instructions: 64 a tile, from
+// 8 warps); one token each of 32 heads on one kv head, 8 sequences, 24 us.
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"
@@ -55,8 +63,9 @@ constexpr int kTileBytes = kTile * kQ4Row;
 constexpr int kMaxBundle = 8;
 constexpr int kMaxWarps = 8;  // of a CTA
 // Two CTAs to an SM, of 128 registers; with 16 columns, whose outputs and queries alone
-// take 96, one of 245. (64 sequences verifying 4 tokens each: 63 us; with 12 warps of 168
-// registers, which spill, 70, and 73 with the queries in shared memory.)
+// take 96, one of 245. (64 sequences verifying 4 tokens each: with 12 warps of 168
+// registers, which spill, 70 us where this took 63, and 73 with the queries in shared
+// memory.)
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 // What a unit costs beside its tiles (queries, the masked tile, the epilogue: some 4 us of
 // a warp that shares its scheduler with three, where a tile takes 1.7), in tiles of each
@@ -384,20 +393,6 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     }
   };
 
-  // With the copies of every SM under way a load that goes to HBM waits behind some 20 MB
-  // of them, 3 to 5 us. So the queries of a unit and the pages of the next tiles are
-  // brought into L2 ahead of their use; the first ones before the first copies.
-  auto prefetch_queries = [&](int b, int unit) {
-    const int h = (p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb;
-    const int r = (p.rgroups > 1 ? unit % p.rgroups * p.rr : 0) + (lane >> 1);
-    if ((lane >> 1) < p.rr && r < p.rows)
-      prefetch_l2(p.q + query_row(p, b, h, r) * 128 + (lane & 1) * 64);
-  };
-  if (sl == 0 && len > 0) {
-    while (r_c >= seq_tiles(b_c)) r_c -= seq_tiles(b_c++);
-    prefetch_queries(b_c, M > 1 ? r_c / (prefix[b_c + 1] - prefix[b_c]) : 0);
-  }
-
   // ---- the warp as its own producer: lanes 2 i and 2 i + 1 hold page and place of
   // the halves of its tile 16 j + i (place -1: no token there, or a bad page)
   int page = 0, coord = -1;
@@ -418,14 +413,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
                 (((p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb) << 10);
       }
     }
-    if (k0 + 16 < count) {
-      tile_behind(16, b_next, r_next, unit, j);
-      if (k0 + 16 + (lane >> 1) < count) {  // the next batch's table entries
-        int b = b_next, r = r_next;
-        tile_behind(lane >> 1, b, r, unit, j);
-        prefetch_l2(p.block_table + b * p.bt_stride + j * kTile / p.page_size);
-      }
-    }
+    if (k0 + 16 < count) tile_behind(16, b_next, r_next, unit, j);
     const bool bad = page < 0 || page >= p.num_pages;
     any_bad |= __any_sync(0xffffffffu, bad);
     if (bad) {
@@ -518,14 +506,6 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     const int row0 = unit % p.rgroups * p.rr;
     const int R = min(p.rr, p.rows - row0);
     const int L = __ldg(p.seq_lens + b);
-    if (sl == 0 && piece_end < len) {  // of the next unit
-      int b1 = b, u1 = unit + 1;
-      if (u1 == M) {
-        u1 = 0;
-        do ++b1; while (seq_tiles(b1) == 0);
-      }
-      prefetch_queries(b1, u1);
-    }
 
     // Q^T fragments: column gid is query row row0 + 8 nt + gid; this lane's 32
     // elements from 32 t4 on, as fp16 times a power of two.
@@ -688,15 +668,19 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           }
           scores();
         }
+        uint64_t sum = pack_f32x2(l[nt][0], l[nt][1]);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[hf][i] = ex2_approx(y[hf][i]);
-          l[nt][0] += y[hf][0] + y[hf][2];
-          l[nt][1] += y[hf][1] + y[hf][3];
+          sum = add_f32x2(sum, add_f32x2(pack_f32x2(y[hf][0], y[hf][1]),
+                                         pack_f32x2(y[hf][2], y[hf][3])));
           pf[hf][nt][0] = transpose_8x8(pack_f16x2(y[hf][0], y[hf][1]));
           pf[hf][nt][1] = transpose_8x8(pack_f16x2(y[hf][2], y[hf][3]));
         }
+        const float2 sums = unpack_f32x2(sum);
+        l[nt][0] = sums.x;
+        l[nt][1] = sums.y;
       }
 
       // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first 8 fragment rows of a
@@ -1129,30 +1113,7 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   return ZL_OK;
 }
 
-// Maps this thread encoded recently (a decode loop keeps its pool).
-struct MapKey {
-  const void* pool;
-  int64_t page_stride, token_stride, head_stride;
-  int32_t page_size, Hkv, num_pages;
-  bool operator==(const MapKey& o) const {
-    return pool == o.pool && page_stride == o.page_stride && token_stride == o.token_stride &&
-           head_stride == o.head_stride && page_size == o.page_size && Hkv == o.Hkv &&
-           num_pages == o.num_pages;
-  }
-};
-constexpr int kMapCache = 4;
-thread_local MapKey t_keys[kMapCache];
-thread_local CUtensorMap t_maps[kMapCache];
-thread_local int t_used = 0, t_next = 0;
-
 zl_status encode_pool(const zl_decode_attn_q4_params* a, CUtensorMap* map) {
-  const MapKey key{a->pool, a->page_stride, a->token_stride, a->head_stride,
-                   a->page_size, a->Hkv, a->num_pages};
-  for (int i = 0; i < t_used; ++i)
-    if (t_keys[i] == key) {
-      *map = t_maps[i];
-      return ZL_OK;
-    }
   const cuuint64_t dims[4] = {kQ4Row, cuuint64_t(a->page_size), cuuint64_t(a->Hkv),
                               cuuint64_t(a->num_pages)};
   const cuuint64_t strides[3] = {cuuint64_t(a->token_stride), cuuint64_t(a->head_stride),
@@ -1161,12 +1122,7 @@ zl_status encode_pool(const zl_decode_attn_q4_params* a, CUtensorMap* map) {
   const CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                                   const_cast<void*>(a->pool), dims, strides, box);
   if (r == CUDA_ERROR_NOT_INITIALIZED) return ZL_ERR_CUDA;
-  if (r != CUDA_SUCCESS) return ZL_ERR_UNSUPPORTED;
-  t_keys[t_next] = key;
-  t_maps[t_next] = *map;
-  t_next = (t_next + 1) % kMapCache;
-  if (t_used < kMapCache) ++t_used;
-  return ZL_OK;
+  return r == CUDA_SUCCESS ? ZL_OK : ZL_ERR_UNSUPPORTED;
 }
 
 }  // namespace

@@ -425,11 +425,6 @@ __device__ __forceinline__ void st_global_v8(void* dst, uint32_t a0, uint32_t a1
                : "memory");
 }
 
-// Bring the line that holds `src` into L2.
-__device__ __forceinline__ void prefetch_l2(const void* src) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-}
-
 // 32-byte load of memory that no kernel running meanwhile writes (the address must
 // be 32-byte aligned).
 __device__ __forceinline__ void ldg_v8(const void* src, uint32_t (&a)[4], uint32_t (&b)[4]) {
