@@ -685,6 +685,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
 
       // O^T: elements 16 gid .. 16 gid + 15 of V rows a, b (first 8 fragment rows of a
       // half's 16 tokens), a + 1, b + 1 (the others)
+      uint32_t nan_at = 0;  // tokens whose block of this lane's elements is NaN
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint8_t* ra = tile + hf * kHalfBytes + tok_a * kQ4Row + kQ4VCodes + 8 * gid;
@@ -701,6 +702,17 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           s1 = 16 * hf + tok_a + 1 < valid ? s1 : 0u;
           s2 = 16 * hf + tok_b < valid ? s2 : 0u;
           s3 = 16 * hf + tok_b + 1 < valid ? s3 : 0u;
+          // a NaN would reach rows that do not see its token (0 times it): kept apart
+          auto keep_apart = [&](uint32_t& sv, int tok) {
+            if (sv >= 0xF8u) {
+              nan_at |= 1u << (16 * hf + tok);
+              sv = 0u;
+            }
+          };
+          keep_apart(s0, tok_a);
+          keep_apart(s1, tok_a + 1);
+          keep_apart(s2, tok_b);
+          keep_apart(s3, tok_b + 1);
         }
         const uint32_t f0 = s0 * 0x80u + s2 * 0x800000u, f1 = s1 * 0x80u + s3 * 0x800000u;
 #pragma unroll
@@ -720,6 +732,20 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][4 * w + i], m0, m1, m2, m3, pf[hf][nt][0], pf[hf][nt][1]);
           }
+        }
+      }
+      if (MASKED && __any_sync(0xffffffffu, nan_at != 0)) {
+        nan_at |= __shfl_xor_sync(0xffffffffu, nan_at, 1);
+        nan_at |= __shfl_xor_sync(0xffffffffu, nan_at, 2);
+        if (nan_at) {
+          const int first = tok0 + __ffs(int(nan_at)) - 1;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (first < limit(nt, u))
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) o[nt][mt][u] = o[nt][mt][u + 2] = CUDART_NAN_F;
         }
       }
     };

@@ -194,6 +194,34 @@ def test_numbers_that_are_none(num_ctas):
     assert np.array_equal(out[0, 0, :4], good[0, 0, :4]) and np.array_equal(out[1], good[1])
 
 
+@pytest.mark.parametrize("num_ctas", [0, 3])
+@pytest.mark.parametrize("at", [0, 1, 2, 4])  # the drafted token with the block, from the newest
+@pytest.mark.parametrize("q_len,Hq", [(5, 2), (5, 6), (7, 2)])
+def test_a_nan_block_reaches_only_rows_that_see_it(q_len, Hq, at, num_ctas):
+    """K or V of a drafted token without a number: the tokens before it keep their bits."""
+    lens = [33, 47, 64, 300, 6]
+    c = Cache(31, lens, 2)
+    q = queries(c, q_len, Hq)
+    good, good_lse, _ = run(c, q, num_ctas=num_ctas)
+    g = Hq // 2
+    for kind in ("v", "k"):
+        pool = c.pool.copy()
+        for b, L in enumerate(lens):
+            page, slot = c.place(b, L - 1 - at)
+            c.pool[page, slot, 1, (136 if kind == "v" else 128) + 3] = 255
+        out, lse, err = run(c, q, num_ctas=num_ctas)
+        c.pool = pool
+        assert err == 0
+        bad = np.zeros(out.shape, bool)
+        bad[:, q_len - 1 - at:, g:, 48:64] = True
+        if kind == "k":
+            bad[:, q_len - 1 - at:, g:] = True
+            assert np.isnan(lse[:, q_len - 1 - at:, g:]).all()
+            lse[:, q_len - 1 - at:, g:] = good_lse[:, q_len - 1 - at:, g:]
+        assert np.isnan(out[bad]).all()
+        assert np.array_equal(out[~bad], good[~bad]) and np.array_equal(lse, good_lse)
+
+
 def test_bytes_behind_the_sequence_do_not_matter():
     c = Cache(29, [37, 18], 3)
     q = queries(c, 2, 6)
