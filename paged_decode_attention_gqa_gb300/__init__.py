@@ -1035,15 +1035,17 @@ def _pool_layout(shape, st, layout):
 def _expect_table(block_table, seq_lens, index, err_flags):
     """Block table, lengths and error word; returns (B, addresses of the table, its
     stride, of seq_lens and err_flags)."""
-    shape, st = block_table.shape, block_table.stride()
+    shape = block_table.shape
     if len(shape) != 2:
         raise ValueError("block_table must be 2-D")
-    B, width = shape
-    bt_stride = st[0] if B > 1 else width
+    B, bt_stride = shape
     if (block_table.dtype is not _I32 or block_table.get_device() != index
-            or (width > 1 and st[1] != 1) or bt_stride < width):
-        _expect(block_table, "block_table", _I32, (B, width), index, False)
-        raise ValueError("block_table rows must be contiguous and distinct")
+            or not block_table.is_contiguous()):
+        _expect(block_table, "block_table", _I32, shape, index, False)
+        width, st = bt_stride, block_table.stride()
+        bt_stride = st[0] if B > 1 else width
+        if (width > 1 and st[1] != 1) or bt_stride < width:
+            raise ValueError("block_table rows must be contiguous and distinct")
     if (seq_lens.dtype is not _I32 or seq_lens.get_device() != index or seq_lens.shape != (B,)
             or not seq_lens.is_contiguous()):
         _refuse(seq_lens, "seq_lens", _I32, (B,), index, True)
@@ -1072,12 +1074,14 @@ def _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags):
     return (index, B, Hkv, shape[0], pool.data_ptr(), ps, ts, hs, bt_at, bt_stride, sl_at, err)
 
 
-def _expect_rows(t, name, B, q_len, heads, index):
-    """bf16 [B, q_len, heads, 128] whose heads lie side by side and whose tokens are
-    evenly spaced (a slice of a fused projection's output is); returns (address, token
-    stride)."""
-    if t.dtype is not _BF16 or t.get_device() != index or t.shape != (B, q_len, heads, 128):
+def _expect_rows(t, name, shape, B, q_len, heads, index):
+    """bf16 [B, q_len, heads, 128] (shape: the tensor's own) whose heads lie side by side
+    and whose tokens are evenly spaced (a slice of a fused projection's output is); returns
+    (address, token stride)."""
+    if t.dtype is not _BF16 or t.get_device() != index or shape != (B, q_len, heads, 128):
         _refuse(t, name, _BF16, (B, q_len, heads, 128), index, False)
+    if t.is_contiguous():
+        return t.data_ptr(), heads * 128
     sb, st, sh, one = t.stride()
     if one != 1 or (heads > 1 and sh != 128):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
@@ -1100,11 +1104,12 @@ def kv_append_q4(k_new, v_new, pool, block_table, seq_lens, *, page_size, new_le
     """
     (index, B, Hkv, pages, at, ps, ts, hs, bt_at, bt_stride, sl_at,
      err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
-    if k_new.dim() != 4:
+    shape = k_new.shape
+    if len(shape) != 4:
         raise ValueError("k_new must be [B, q_len, Hkv, 128]")
-    q_len = k_new.shape[1]
-    k_at, k_st = _expect_rows(k_new, "k_new", B, q_len, Hkv, index)
-    v_at, v_st = _expect_rows(v_new, "v_new", B, q_len, Hkv, index)
+    q_len = shape[1]
+    k_at, k_st = _expect_rows(k_new, "k_new", shape, B, q_len, Hkv, index)
+    v_at, v_st = _expect_rows(v_new, "v_new", v_new.shape, B, q_len, Hkv, index)
     n_at = 0
     if new_lens is not None:
         n_at = _expect(new_lens, "new_lens", _I32, (B,), index)
@@ -1130,11 +1135,12 @@ def kv_read_q4(pool, block_table, seq_lens, *, page_size, tokens=None, k_out=Non
      err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
     given = k_out if k_out is not None else v_out
     if given is not None:
-        if given.dim() != 4:
+        shape = given.shape
+        if len(shape) != 4:
             raise ValueError("k_out and v_out must be [B, tokens, Hkv, 128]")
-        if tokens is not None and tokens != given.shape[1]:
-            raise ValueError(f"tokens is {tokens}, the outputs hold {given.shape[1]}")
-        tokens = given.shape[1]
+        if tokens is not None and tokens != shape[1]:
+            raise ValueError(f"tokens is {tokens}, the outputs hold {shape[1]}")
+        tokens = shape[1]
     elif tokens is None or tokens < 1:
         raise ValueError("tokens (at least the longest sequence) or the outputs are required")
     on, scratch = _on(index, stream)
@@ -1168,11 +1174,14 @@ def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None
     """
     (index, B, Hkv, pages, at, ps, ts, hs, bt_at, bt_stride, sl_at,
      err) = _expect_q4(pool, block_table, seq_lens, layout, page_size, err_flags)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, q_len, Hq, 128]")
     shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, q_len, Hq, 128]")
     _, q_len, Hq, _ = shape
-    q_at = _expect(q, "q", _BF16, (B, q_len, Hq, 128), index)
+    if (shape != (B, q_len, Hq, 128) or q.dtype is not _BF16 or q.get_device() != index
+            or not q.is_contiguous()):
+        _refuse(q, "q", _BF16, (B, q_len, Hq, 128), index, True)
+    q_at = q.data_ptr()
     out_at = lse_at = 0
     if out is not None:
         out_at = _expect(out, "out", _BF16, shape, index)
@@ -1269,57 +1278,64 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
     slots: bf16 pools k_pool, v_pool as kv_append would store them, or the 4-bit ``pool``
     as kv_append_q4 would. k_out is then written only when given. Returns (q_out, k_out).
     """
-    if q.dim() != 4 or k.dim() != 4:
+    q_shape, k_shape = q.shape, k.shape
+    if len(q_shape) != 4 or len(k_shape) != 4:
         raise ValueError("q and k must be [B, q_len, heads, 128]")
     index = q.get_device()
-    B, q_len, Hq, _ = q.shape
-    Hkv = k.shape[2]
-    q_at, q_st = _expect_rows(q, "q", B, q_len, Hq, index)
-    k_at, k_st = _expect_rows(k, "k", B, q_len, Hkv, index)
-    cache, v_at, v_st, kp = CACHE_NONE, 0, 0, None
-    vp_at = ps = ts = hs = bt_at = bt_stride = sl_at = err = pages = 0
-    if pool is not None:
-        if k_pool is not None or v_pool is not None:
-            raise ValueError("either the bf16 pools or the 4-bit one")
-        cache, kp = CACHE_Q4, pool
-        if pool.dtype is not _U8 or pool.dim() != 4 or pool.shape[3] != Q4_ROW_BYTES:
-            raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes")
-    elif k_pool is not None or v_pool is not None:
-        if k_pool is None or v_pool is None:
-            raise ValueError("k_pool and v_pool are given together")
-        cache, kp = CACHE_BF16, k_pool
-        if k_pool.dtype is not _BF16 or k_pool.dim() != 4 or k_pool.shape[3] != 128:
-            raise ValueError("k_pool must be bf16 with rows of 128 elements")
-        vp_at = _expect(v_pool, "v_pool", _BF16, tuple(k_pool.shape), index, False)
-        if v_pool.stride() != k_pool.stride():
-            raise ValueError("K and V pools must share strides")
-    if cache:
+    B, q_len, Hq, _ = q_shape
+    Hkv = k_shape[2]
+    q_at, q_st = _expect_rows(q, "q", q_shape, B, q_len, Hq, index)
+    k_at, k_st = _expect_rows(k, "k", k_shape, B, q_len, Hkv, index)
+    cache = CACHE_NONE
+    v_at = v_st = kp_at = vp_at = ps = ts = hs = bt_at = bt_stride = sl_at = err = pages = 0
+    if pool is not None or k_pool is not None or v_pool is not None:
+        if pool is not None:
+            if k_pool is not None or v_pool is not None:
+                raise ValueError("either the bf16 pools or the 4-bit one")
+            cache, kp, shape = CACHE_Q4, pool, pool.shape
+            if pool.dtype is not _U8 or len(shape) != 4 or shape[3] != Q4_ROW_BYTES:
+                raise ValueError(f"the pool must be uint8 with rows of {Q4_ROW_BYTES} bytes")
+            st = pool.stride()
+        else:
+            if k_pool is None or v_pool is None:
+                raise ValueError("k_pool and v_pool are given together")
+            cache, kp, shape = CACHE_BF16, k_pool, k_pool.shape
+            if k_pool.dtype is not _BF16 or len(shape) != 4 or shape[3] != 128:
+                raise ValueError("k_pool must be bf16 with rows of 128 elements")
+            st = k_pool.stride()
+            vp_at = _expect(v_pool, "v_pool", _BF16, shape, index, False)
+            if v_pool.stride() != st:
+                raise ValueError("K and V pools must share strides")
         if v is None or block_table is None or seq_lens is None:
             raise ValueError("storing in a cache needs v, block_table and seq_lens")
         if kp.get_device() != index:
             raise ValueError(f"the pool is on {kp.device}, q on device {index}")
-        slots, heads, ps, ts, hs = _pool_layout(kp.shape, kp.stride(), layout)
+        slots, heads, ps, ts, hs = _pool_layout(shape, st, layout)
         if slots != page_size or heads != Hkv:
             raise ValueError(f"the pool holds {slots} slots per page and {heads} heads; page_size "
                              f"is {page_size}, k has {Hkv} heads")
-        v_at, v_st = _expect_rows(v, "v", B, q_len, Hkv, index)
+        v_at, v_st = _expect_rows(v, "v", v.shape, B, q_len, Hkv, index)
         rows, bt_at, bt_stride, sl_at, err = _expect_table(block_table, seq_lens, index, err_flags)
         if rows != B:
             raise ValueError(f"block_table has {rows} rows for {B} sequences")
-        pages = kp.shape[0]
+        kp_at, pages = kp.data_ptr(), shape[0]
     elif seq_lens is not None:
         sl_at = _expect(seq_lens, "seq_lens", _I32, (B,), index)
     if rope is None:
         rope = _NO_ROPE
     pos_at = axis_st = 0
     if positions is not None:
-        if positions.dim() == 2:
+        shape = positions.shape
+        if len(shape) == 2:
             if rope.n_axes > 1:
                 raise ValueError(f"the rope follows {rope.n_axes} axes: positions must be "
                                  "[axes, B, q_len]")
-            pos_at = _expect(positions, "positions", _I32, (B, q_len), index)
+            if (shape != (B, q_len) or positions.dtype is not _I32
+                    or positions.get_device() != index or not positions.is_contiguous()):
+                _refuse(positions, "positions", _I32, (B, q_len), index, True)
+            pos_at = positions.data_ptr()
         else:
-            n = positions.shape[0] if positions.dim() == 3 else 0
+            n = shape[0] if len(shape) == 3 else 0
             if n < rope.n_axes:
                 raise ValueError(f"positions must be [B, q_len], or [axes, B, q_len] with at least "
                                  f"{rope.n_axes} axes")
@@ -1334,9 +1350,9 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
         kw = _expect(k_weight, "k_weight", _F32, (128,), index)
     ko_at = ko_st = 0
     if q_out is not None:
-        qo_at, qo_st = _expect_rows(q_out, "q_out", B, q_len, Hq, index)
+        qo_at, qo_st = _expect_rows(q_out, "q_out", q_out.shape, B, q_len, Hq, index)
     if k_out is not None:
-        ko_at, ko_st = _expect_rows(k_out, "k_out", B, q_len, Hkv, index)
+        ko_at, ko_st = _expect_rows(k_out, "k_out", k_out.shape, B, q_len, Hkv, index)
     on, scratch = _on(index, stream)
     if q_out is None or (k_out is None and not cache):
         with scratch:
@@ -1349,7 +1365,7 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
     status = (_raw.get("zl_qk_norm_rope") or _raw_fn("zl_qk_norm_rope", 1))(_pack(
         _NORM_ROPE, _NORM_ROPE.size, q_at, k_at, v_at, q_st, k_st, v_st, qo_at, ko_at, qo_st,
         ko_st, qw, kw, eps, rope.scale, rope.turns_at, rope.axes_at, rope.n_freq, rope.n_axes,
-        rope.interleaved, cache, pos_at, axis_st, kp.data_ptr() if cache else 0, vp_at, ps, ts, hs,
+        rope.interleaved, cache, pos_at, axis_st, kp_at, vp_at, ps, ts, hs,
         bt_at, bt_stride, sl_at, B, q_len, Hq, Hkv, page_size, pages, err), on)
     if status != OK:
         _check(status, "zl_qk_norm_rope")
