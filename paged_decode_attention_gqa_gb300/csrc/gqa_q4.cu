@@ -98,18 +98,26 @@ struct Q4Params {
   float* ws_o;
   uint32_t* err_flags;
   int B, q_len, Hq, Hkv, g, page_size, num_pages;
-  int HB, S, stages;     // heads of a bundle, slices, ring stages
+  int HB, S, log_s;      // heads of a bundle, slices (a power of two) and their exponent
+  int stages;            // of a ring
   int units_per_seq;     // bundles x row groups
   int rgroups, rr, rows; // row groups of rr rows, rows = g * q_len of a kv head
   int ctas;              // CTAs of the attention kernel
   int cost;              // places of a unit that hold no tile, a multiple of S
   int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
   int whole;             // 1: CTA c takes unit c and there is no merge (max_seq_len is short)
+  uint64_t page_inv;     // 2^36 / (halves of a page), rounded up
   float scale_log2;
 };
 
 __device__ __forceinline__ void flag(uint32_t* f, uint32_t bits) {
   if (f) atomicOr(f, bits);
+}
+
+// The page of token t, a multiple of 16 below 2^31 (right as t / 16 times what page_inv is
+// too large by, below 64, stays below 2^36).
+__device__ __forceinline__ int page_of(const Q4Params& p, int t) {
+  return int((uint64_t(uint32_t(t) / kHalf) * p.page_inv) >> 36);
 }
 
 __device__ __forceinline__ int tiles_of(const Q4Params& p, int L) {
@@ -129,7 +137,7 @@ struct Cut {
     whole = p.whole || (units <= p.ctas && longest <= kWholeTiles * p.S);
     if (W < (INT64_C(1) << 31)) {  // (nearly always: 64-bit divisions are slow)
       const uint32_t w = uint32_t(W);
-      G = min(uint32_t(p.ctas), max(w / uint32_t(p.S), 1u));
+      G = min(uint32_t(p.ctas), max(w >> p.log_s, 1u));
       Wq = w / G;
       Wr = w - uint32_t(Wq) * G;
     } else {
@@ -152,13 +160,19 @@ struct Cut {
   }
 };
 
-// Largest b with units_per_seq * prefix[b] <= idx (sequences without tiles are
-// skipped: the next prefix equals theirs).
+// Largest b below B with m * prefix[b] <= idx < m * prefix[B] (sequences without tiles are
+// skipped: the next prefix equals theirs), by a warp, 32 places a step.
 __device__ __forceinline__ int locate(const int32_t* prefix, int B, int m, int64_t idx) {
-  int lo = 0, hi = B;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (int64_t(m) * prefix[mid] <= idx) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // among lo .. lo + n - 1, lo the least
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = min(lane * step, n - 1);
+    const uint32_t below =
+        __ballot_sync(0xffffffffu, lane == 0 || int64_t(m) * prefix[lo + at] <= idx);
+    const int last = 31 - __clz(int(below));
+    const int next = min(last * step, n - 1);
+    lo += next;
+    n = min(step, n - next);
   }
   return lo;
 }
@@ -262,7 +276,9 @@ __device__ __forceinline__ int64_t query_row(const Q4Params& p, int b, int h, in
 
 // The line: each sequence with tiles takes that many places and those of the unit's cost,
 // for every of its units. Places before each sequence for one unit, prefix[0 .. B] in
-// shared memory, and the most tiles that one has; by the whole block.
+// shared memory, behind them where HALVES a bit for each sequence whose last tile has a
+// token in its second half, and the most tiles that one has; by the whole block.
+template <bool HALVES>
 __device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, int* longest) {
   __shared__ int part_sum[32], part_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -271,7 +287,12 @@ __device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, i
   int carry = 0, most = 0;
   for (int i = 0; i < per && b0 + i < p.B; i += 32) {
     const int b = b0 + i + lane;
-    const int n = b < p.B ? tiles_of(p, __ldcg(p.seq_lens + b)) : 0;
+    const int L = b < p.B ? __ldcg(p.seq_lens + b) : 0;
+    const int n = tiles_of(p, L);
+    if (HALVES) {
+      const uint32_t both = __ballot_sync(0xffffffffu, n > 0 && (L - 1) % kTile >= kHalf);
+      if (lane == 0) prefix[p.B + 1 + (b0 + i) / 32] = int32_t(both);
+    }
     int incl = n > 0 ? n + p.cost : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -305,16 +326,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, ctas_per_sm(NT))
 q4_decode_kernel(const __grid_constant__ Q4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int HB = p.HB, S = p.S, W = HB * S;  // W warps
+  const int HB = p.HB, S = p.S, log_s = p.log_s, W = HB * S;  // W warps
   const int NS = p.stages;
   uint8_t* ring = smem + warp * NS * kTileBytes;
-  // slices' results at the end of a unit, 8 rows at a time: base-2 lse [warp][8],
-  // outputs [warp][8][128]
+  // slices' results at the end of a unit: base-2 lse [warp][8 NT], outputs [warp][8 NT][128]
+  constexpr int kRows = 8 * NT;
   float* merge_l = reinterpret_cast<float*>(smem + W * NS * kTileBytes);
-  float* merge_o = merge_l + (S > 1 ? W * 8 : 0);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_o + (S > 1 ? W * 8 * 128 : 0));
+  float* merge_o = merge_l + (S > 1 ? W * kRows : 0);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_o + (S > 1 ? W * kRows * 128 : 0));
   const uint32_t full = smem_u32(bars + warp * NS);
-  int32_t* prefix = reinterpret_cast<int32_t*>(bars + W * NS);  // [B + 1]
+  int32_t* prefix = reinterpret_cast<int32_t*>(bars + W * NS);  // [B + 1], and B bits
   __shared__ int abort_flag;
 
   if (tid == 0) abort_flag = 0;
@@ -326,7 +347,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   // nothing before this reads or writes global memory
   griddep_wait();
   int longest;
-  scan_tiles(p, prefix, &longest);
+  scan_tiles<true>(p, prefix, &longest);
+  const int32_t* both = prefix + p.B + 1;
 
   const int M = p.units_per_seq;
   const int c = blockIdx.x;
@@ -351,7 +373,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   // places of all units of sequence b
   auto seq_tiles = [&](int b) { return (prefix[b + 1] - prefix[b]) * M; };
 
-  const int hb = warp % HB, sl = warp / HB;
+  const int sl = warp / HB, hb = warp - sl * HB;
   // This warp's tiles: of the range's places sl, sl + S, .. those that hold one.
   int count = 0;
   {
@@ -361,8 +383,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       const int places = prefix[b + 1] - prefix[b], n = places - p.cost;
       const int j = M > 1 ? r % places : r;
       const int piece = min(len - at, places - j), real = max(min(piece, n - j), 0);
-      const int skip = at % S <= sl ? sl - at % S : sl + S - at % S;
-      if (skip < real) count += (real - 1 - skip) / S + 1;
+      const int skip = (sl - at) & (S - 1);
+      if (skip < real) count += ((real - 1 - skip) >> log_s) + 1;
       at += piece;
       r += piece;
     }
@@ -375,8 +397,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       const int places = prefix[b + 1] - prefix[b], n = places - p.cost;
       unit = M > 1 ? r / places : 0;
       j = r - unit * places;
-      if (j < n) return (n - j + S - 1) / S;
-      r += (places - j + S - 1) / S * S;
+      if (j < n) return (n - j + S - 1) >> log_s;
+      r += (places - j + S - 1) & -S;
     }
   };
   // The i-th of this warp's tiles behind the one at (b, r).
@@ -405,9 +427,10 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     if (k0 + (lane >> 1) < count) {
       int b = b_next, r = r_next;
       tile_behind(lane >> 1, b, r, unit, j);
-      const int t = j * kTile + (lane & 1) * kHalf, pg = t / p.page_size;
+      const int t = j * kTile + (lane & 1) * kHalf, pg = page_of(p, t);
       // (a half behind the last token has no page; the table's row is not read there)
-      if (t < __ldg(p.seq_lens + b)) {
+      if (!(lane & 1) || j + 1 + p.cost < prefix[b + 1] - prefix[b] ||
+          (both[b / 32] >> (b % 32) & 1)) {
         page = __ldg(p.block_table + b * p.bt_stride + pg);
         coord = (t - pg * p.page_size) |
                 (((p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb) << 10);
@@ -752,14 +775,14 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
 
     // this slice's tiles of the piece: todo of them from token tok0 on, the first `plain`
     // of which every row sees whole
-    const int behind = pos % S;
-    const int t0 = pos + (sl >= behind ? sl - behind : sl + S - behind);
+    const int t0 = pos + ((sl - pos) & (S - 1));
     const int real_end = min(piece_end, pos - j0 + n);  // (behind it: places without a tile)
-    int todo = t0 < real_end ? (real_end - 1 - t0) / S + 1 : 0;
+    int todo = t0 < real_end ? ((real_end - 1 - t0) >> log_s) + 1 : 0;
     int tok0 = (j0 + t0 - pos) * kTile;
     const int stride = S * kTile;  // tokens from one to the next
     while (todo > 0) {
-      int plain = all_see >= tok0 + kTile ? min(todo, (all_see - kTile - tok0) / stride + 1) : 0;
+      int plain =
+          all_see >= tok0 + kTile ? min(todo, ((all_see - kTile - tok0) >> (log_s + 5)) + 1) : 0;
       for (; plain > 0 && !dead; --plain) {
         wait();
         if (dead || any_bad) break;
@@ -776,7 +799,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         if (any_bad) {
           const int at = tok0 + (lane & 1) * kHalf;
           int pg = 0;
-          if (at < L) pg = __ldg(p.block_table + b * p.bt_stride + at / p.page_size);
+          if (at < L) pg = __ldg(p.block_table + b * p.bt_stride + page_of(p, at));
           const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.num_pages) & 3u;
           whole = bad & 1u ? 0 : bad ? kHalf : kTile;
 #pragma unroll
@@ -848,20 +871,19 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           }
         }
     } else {
-      // Slices: each leaves its rows (8 at a time), then takes every S-th over all of them.
+      // Slices: each leaves its rows, then takes every S-th over all of them.
+      if (merged_before) named_barrier(1 + hb, S * 32);
+      merged_before = true;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (8 * nt >= R) break;
-        if (merged_before) named_barrier(1 + hb, S * 32);
-        merged_before = true;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int r = 2 * t4 + u;
-          if (8 * nt + r >= R) continue;
+          const int r = 8 * nt + 2 * t4 + u;
+          if (r >= R) continue;
           const bool none = bad_row[nt][u] || l[nt][u] == 0.f;
           const float inv = none ? 0.f : rcp_approx(l[nt][u]);
           const float lse2 = none ? -CUDART_INF_F : lg2_approx(l[nt][u]) - base[nt][u];
-          float* to = merge_o + (warp * 8 + r) * 128 + 16 * gid;
+          float* to = merge_o + (warp * kRows + r) * 128 + 16 * gid;
 #pragma unroll
           for (int mt = 0; mt < 8; mt += 2)
             *reinterpret_cast<float4*>(to + 2 * mt) =
@@ -869,49 +891,47 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
                             none ? 0.f : o[nt][mt + 1][u] * inv,
                             none ? 0.f : o[nt][mt + 1][u + 2] * inv);
           if (gid == 0)
-            merge_l[warp * 8 + r] = bad_row[nt][u] ? CUDART_NAN_F
-                                    : isnan(lse2)  ? CUDART_INF_F
-                                                   : lse2;
+            merge_l[warp * kRows + r] = bad_row[nt][u] ? CUDART_NAN_F
+                                        : isnan(lse2)  ? CUDART_INF_F
+                                                       : lse2;
         }
-        named_barrier(1 + hb, S * 32);
-        for (int r = sl; r < min(8, R - 8 * nt); r += S) {
-          // (the largest first: then nothing waits for the slice before)
-          float top = -CUDART_INF_F, den = 0.f;
-          bool bad = false;
-          for (int s = 0; s < S; ++s) {
-            const float ls = merge_l[(s * HB + hb) * 8 + r];
-            bad |= isnan(ls);
-            top = fmaxf(top, ls);
-          }
-          const bool none = bad || top == -CUDART_INF_F;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!none) {
+      named_barrier(1 + hb, S * 32);
+      for (int r = sl; r < R; r += S) {
+        // (the largest first: then nothing waits for the slice before)
+        float top = -CUDART_INF_F, den = 0.f;
+        bool bad = false;
+        for (int s = 0; s < S; ++s) {
+          const float ls = merge_l[(s * HB + hb) * kRows + r];
+          bad |= isnan(ls);
+          top = fmaxf(top, ls);
+        }
+        const bool none = bad || top == -CUDART_INF_F;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!none) {
 #pragma unroll 4
-            for (int s = 0; s < S; ++s) {
-              const int at = (s * HB + hb) * 8 + r;
-              const float wgt = ex2_approx(merge_l[at] - top);
-              const float4 os = reinterpret_cast<const float4*>(merge_o + at * 128)[lane];
-              den += wgt;
-              v.x = fmaf(wgt, os.x, v.x);
-              v.y = fmaf(wgt, os.y, v.y);
-              v.z = fmaf(wgt, os.z, v.z);
-              v.w = fmaf(wgt, os.w, v.w);
-            }
-            const float inv = rcp_approx(den);
-            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          for (int s = 0; s < S; ++s) {
+            const int at = (s * HB + hb) * kRows + r;
+            const float wgt = ex2_approx(merge_l[at] - top);
+            const float4 os = reinterpret_cast<const float4*>(merge_o + at * 128)[lane];
+            den += wgt;
+            v.x = fmaf(wgt, os.x, v.x);
+            v.y = fmaf(wgt, os.y, v.y);
+            v.z = fmaf(wgt, os.z, v.z);
+            v.w = fmaf(wgt, os.w, v.w);
           }
-          const float lse2 = none ? -CUDART_INF_F : top + lg2_approx(den);
-          if (cut_unit) {
-            const int64_t at = part0 + 8 * nt + r;
-            reinterpret_cast<float4*>(p.ws_o + at * 128)[lane] = v;
-            if (lane == 0)
-              p.ws_lse[at] = bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
-          } else {
-            const int64_t row = query_row(p, b, h, row0 + 8 * nt + r);
-            reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            if (p.lse && lane == 0) p.lse[row] = lse2 * 0.69314718055994531f;
-          }
+          const float inv = rcp_approx(den);
+          v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
+        const float lse2 = none ? -CUDART_INF_F : top + lg2_approx(den);
+        if (cut_unit) {
+          const int64_t at = part0 + r;
+          reinterpret_cast<float4*>(p.ws_o + at * 128)[lane] = v;
+          if (lane == 0) p.ws_lse[at] = bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
+        } else {
+          const int64_t row = query_row(p, b, h, row0 + r);
+          reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          if (p.lse && lane == 0) p.lse[row] = lse2 * 0.69314718055994531f;
         }
       }
     }
@@ -939,7 +959,7 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
   // (The lengths may be read before the attention is done: what came before it in the
   // stream was, when the attention let this launch begin.)
   int longest;
-  scan_tiles(p, prefix, &longest);
+  scan_tiles<false>(p, prefix, &longest);
   const int b = blockIdx.y;
   const int n = prefix[b + 1] - prefix[b] - p.cost;  // tiles (below 1: none)
   const Cut cut(p, prefix[p.B], longest);
@@ -1038,8 +1058,8 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 size_t smem_bytes(const Plan& pl, int B) {
   const size_t W = size_t(pl.HB) * pl.S;
-  size_t n = W * pl.stages * (kTileBytes + 8) + (size_t(B) + 1) * 4;
-  if (pl.S > 1) n += W * 8 * (4 + 128 * 4);
+  size_t n = W * pl.stages * (kTileBytes + 8) + (size_t(B) + 1 + (size_t(B) + 31) / 32) * 4;
+  if (pl.S > 1) n += W * 8 * pl.nt * (4 + 128 * 4);
   return n;
 }
 
@@ -1102,7 +1122,8 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   if (tiles >= int64_t(sms) * 32)
     for (int d = 2; d <= kMaxBundle; ++d)
       if (a->Hkv % d == 0 && kMaxWarps / d * d >= kMaxWarps / pl->HB * pl->HB) pl->HB = d;
-  pl->S = kMaxWarps / pl->HB;
+  pl->S = 1;  // a power of two
+  while (2 * pl->S * pl->HB <= kMaxWarps) pl->S *= 2;
   pl->units_per_seq = a->Hkv / pl->HB * pl->rgroups;
   // Two stages to a warp, 147 KB on an SM: more only make the requests of all SMs wait
   // for one another (with three 64 sequences of 512-4096 tokens took 49 us, not 45, and
@@ -1198,6 +1219,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.num_pages = a->num_pages;
   p.HB = pl.HB;
   p.S = pl.S;
+  while (1 << p.log_s < pl.S) ++p.log_s;
   p.stages = pl.stages;
   p.units_per_seq = pl.units_per_seq;
   p.rgroups = pl.rgroups;
@@ -1207,6 +1229,8 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.cost = unit_cost(pl.nt) * pl.S;
   p.box32 = a->page_size % kTile == 0;
   p.whole = pl.whole;
+  const uint64_t halves = uint64_t(a->page_size / kHalf);
+  p.page_inv = ((UINT64_C(1) << 36) + halves - 1) / halves;
   p.scale_log2 = float(double(a->scale) * kLog2e);
 
   cudaLaunchConfig_t cfg = {};
