@@ -431,7 +431,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       // (a half behind the last token has no page; the table's row is not read there)
       if (!(lane & 1) || j + 1 + p.cost < prefix[b + 1] - prefix[b] ||
           (both[b / 32] >> (b % 32) & 1)) {
-        page = __ldg(p.block_table + b * p.bt_stride + pg);
+        page = p.block_table[b * p.bt_stride + pg];
         coord = (t - pg * p.page_size) |
                 (((p.rgroups > 1 ? unit / p.rgroups : unit) * HB + hb) << 10);
       }
@@ -472,7 +472,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   // Sequences without tiles: zeros.
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
-    const int L = __ldg(p.seq_lens + b);
+    const int L = p.seq_lens[b];
     if (tid == 0 && L != 0) flag(p.err_flags, ZL_DEVERR_BAD_SEQ_LEN);
     const int64_t r0 = int64_t(b) * p.q_len * p.Hq;
     uint4* o = reinterpret_cast<uint4*>(p.out + r0 * 128);
@@ -528,7 +528,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     const int h = unit / p.rgroups * HB + hb;
     const int row0 = unit % p.rgroups * p.rr;
     const int R = min(p.rr, p.rows - row0);
-    const int L = __ldg(p.seq_lens + b);
+    const int L = p.seq_lens[b];
 
     // Q^T fragments: column gid is query row row0 + 8 nt + gid; this lane's 32
     // elements from 32 t4 on, as fp16 times a power of two.
@@ -542,7 +542,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         const uint4* src =
             reinterpret_cast<const uint4*>(p.q + query_row(p, b, h, row0 + r) * 128) + 4 * t4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(src + i);
+        for (int i = 0; i < 4; ++i) w[i] = src[i];
       }
       const uint32_t* x = reinterpret_cast<const uint32_t*>(w);
       // the largest magnitude, by its bits (NaN above infinity)
@@ -799,7 +799,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         if (any_bad) {
           const int at = tok0 + (lane & 1) * kHalf;
           int pg = 0;
-          if (at < L) pg = __ldg(p.block_table + b * p.bt_stride + page_of(p, at));
+          if (at < L) pg = p.block_table[b * p.bt_stride + page_of(p, at)];
           const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.num_pages) & 3u;
           whole = bad & 1u ? 0 : bad ? kHalf : kTile;
 #pragma unroll

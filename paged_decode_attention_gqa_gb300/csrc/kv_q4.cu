@@ -29,12 +29,13 @@ struct AppendQ4 {
 
 // Blocks (x, b): the rows (token, head) of sequence b, two to a warp.
 __global__ void __launch_bounds__(256) append_q4_kernel(const __grid_constant__ AppendQ4 p) {
-  // (the attention that follows waits for this grid before it reads memory)
+  // (what follows waits for this grid before it touches memory, as this grid does here)
   griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31, kv = (lane >> 3) & 1, j = lane & 7;
   const int b = blockIdx.y;
-  const int L = __ldg(p.seq_lens + b);
-  const int n = p.new_lens ? __ldg(p.new_lens + b) : p.q_len;
+  const int L = p.seq_lens[b];
+  const int n = p.new_lens ? p.new_lens[b] : p.q_len;
   if (n < 0 || n > p.q_len || L < n || int64_t(L) > p.bt_stride * p.page_size) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.err_flags)
       atomicOr(p.err_flags, ZL_DEVERR_BAD_SEQ_LEN);
@@ -47,15 +48,15 @@ __global__ void __launch_bounds__(256) append_q4_kernel(const __grid_constant__ 
   for (uint32_t r = blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4); r < rows; r += step) {
     const uint32_t i = r / uint32_t(p.Hkv), h = r - i * uint32_t(p.Hkv);
     const int t = L - n + int(i);
-    const int page = __ldg(p.block_table + b * p.bt_stride + t / p.page_size);
+    const int page = p.block_table[b * p.bt_stride + t / p.page_size];
     const uint4* at = src + (int64_t(b) * p.q_len + i) * stride + int64_t(h) * 16 + 2 * j;
     uint32_t x[2][4];
     if (p.wide) {
-      ldg_v8(at, x[0], x[1]);
+      ld_global_v8(at, x[0], x[1]);
     } else {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint4 v = __ldg(at + c);
+        const uint4 v = at[c];
         x[c][0] = v.x, x[c][1] = v.y, x[c][2] = v.z, x[c][3] = v.w;
       }
     }
@@ -86,9 +87,10 @@ struct ReadQ4 {
 
 __global__ void __launch_bounds__(256) read_q4_kernel(const __grid_constant__ ReadQ4 p) {
   griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31, kv = (lane >> 3) & 1, j = lane & 7;
   const int b = blockIdx.y;
-  const int L = __ldg(p.seq_lens + b);
+  const int L = p.seq_lens[b];
   if (L < 0 || L > p.tokens || int64_t(L) > p.bt_stride * p.page_size) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.err_flags)
       atomicOr(p.err_flags, ZL_DEVERR_BAD_SEQ_LEN);
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const __grid_constant__ Re
   const uint32_t step = gridDim.x * (blockDim.x >> 4);
   for (uint32_t r = blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4); r < rows; r += step) {
     const uint32_t t = r / uint32_t(p.Hkv), h = r - t * uint32_t(p.Hkv);
-    const int page = __ldg(p.block_table + b * p.bt_stride + t / uint32_t(p.page_size));
+    const int page = p.block_table[b * p.bt_stride + t / uint32_t(p.page_size)];
     if (page < 0 || page >= p.num_pages) {
       if (h == 0 && (lane & 15) == 0 && p.err_flags) atomicOr(p.err_flags, ZL_DEVERR_BAD_PAGE);
       continue;
@@ -172,9 +174,8 @@ extern "C" zl_status zl_kv_append_q4(const zl_kv_append_q4_params* a, zl_stream_
   p.num_pages = a->num_pages;
   p.wide = aligned_to(a->k_new, 32) && aligned_to(a->v_new, 32) && a->k_stride % 16 == 0 &&
            a->v_stride % 16 == 0;
-  append_q4_kernel<<<row_grid(int64_t(a->q_len) * a->Hkv, a->B, sms), 256, 0,
-                     reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  return launch_after(append_q4_kernel, row_grid(int64_t(a->q_len) * a->Hkv, a->B, sms), 256,
+                      stream, p);
 }
 
 extern "C" zl_status zl_kv_read_q4(const zl_kv_read_q4_params* a, zl_stream_t stream) {
@@ -204,7 +205,6 @@ extern "C" zl_status zl_kv_read_q4(const zl_kv_read_q4_params* a, zl_stream_t st
   p.Hkv = a->Hkv;
   p.page_size = a->page_size;
   p.num_pages = a->num_pages;
-  read_q4_kernel<<<row_grid(int64_t(a->tokens) * a->Hkv, a->B, sms), 256, 0,
-                   reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+  return launch_after(read_q4_kernel, row_grid(int64_t(a->tokens) * a->Hkv, a->B, sms), 256,
+                      stream, p);
 }

@@ -425,10 +425,9 @@ __device__ __forceinline__ void st_global_v8(void* dst, uint32_t a0, uint32_t a1
                : "memory");
 }
 
-// 32-byte load of memory that no kernel running meanwhile writes (the address must
-// be 32-byte aligned).
-__device__ __forceinline__ void ldg_v8(const void* src, uint32_t (&a)[4], uint32_t (&b)[4]) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+// 32-byte load (the address must be 32-byte aligned).
+__device__ __forceinline__ void ld_global_v8(const void* src, uint32_t (&a)[4], uint32_t (&b)[4]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(b[0]), "=r"(b[1]),
                  "=r"(b[2]), "=r"(b[3])
                : "l"(src));

@@ -29,4 +29,22 @@ zl_status q4_check_pool(const Params* a) {
   return ZL_OK;
 }
 
+// Launches a kernel that begins with griddep_wait: its blocks may be placed while what
+// comes before it in the stream ends. (Append and read-back of 8 chunks of 512 tokens, call
+// after call: 49.4 us launched in the ordinary way, 44.4 so.)
+template <class Params>
+zl_status launch_after(void (*kernel)(Params), dim3 grid, int threads, zl_stream_t stream,
+                       const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
+}
+
 }  // namespace zl

@@ -61,6 +61,7 @@ template <bool INTERLEAVED, int CACHE>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     const __grid_constant__ NormRope p) {
   griddep_launch_dependents();
+  griddep_wait();
   __shared__ __align__(16) float cosine[kWarps][kMaxFreq], sine[kWarps][kMaxFreq];
   // elements 8 c + 4 j .. + 3 at [j][c]: a quarter-warp's reads touch every bank once
   __shared__ __align__(16) float weight[2][2][16][4];
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
   for (int e = threadIdx.x; e < 256; e += kThreads) {
     const float* w = p.weight[e >> 7];
     const int d = e & 127;
-    weight[e >> 7][(d >> 2) & 1][d >> 3][d & 3] = w ? __ldg(w + d) : 1.f;
+    weight[e >> 7][(d >> 2) & 1][d >> 3][d & 3] = w ? w[d] : 1.f;
   }
   __syncthreads();
 
@@ -108,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     const int64_t seq = !p.positions || CACHE != ZL_CACHE_NONE ? tok / p.q_len : 0;
     const int i = int(tok - seq * p.q_len);
     for (int f = lane; f < p.n_freq; f += 32) {
-      const int pos = p.positions ? __ldg(p.positions + p.axes[f] * p.axis_stride + tok)
-                                  : __ldg(p.seq_lens + seq) - p.q_len + i;
+      const int pos = p.positions ? p.positions[p.axes[f] * p.axis_stride + tok]
+                                  : p.seq_lens[seq] - p.q_len + i;
       const uint64_t turn = uint64_t(int64_t(pos)) * p.turns[f] + 0x80000000ull;
       float sn, cs;
       sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
@@ -127,13 +128,13 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     }
     int64_t place = -1;  // of the token in the pool, -1: not stored
     if constexpr (CACHE != ZL_CACHE_NONE) {
-      const int L = __ldg(p.seq_lens + seq);
+      const int L = p.seq_lens[seq];
       uint32_t err = 0;
       if (L < p.q_len || int64_t(L) > p.bt_stride * p.page_size) {
         err = ZL_DEVERR_BAD_SEQ_LEN;
       } else {
         const int t = L - p.q_len + i;
-        const int page = __ldg(p.block_table + seq * p.bt_stride + t / p.page_size);
+        const int page = p.block_table[seq * p.bt_stride + t / p.page_size];
         if (page < 0 || page >= p.num_pages)
           err = ZL_DEVERR_BAD_PAGE;
         else
@@ -391,15 +392,13 @@ extern "C" zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* a, zl_stream_
   // three blocks are resident on an SM; with more units than warps these take several
   const int64_t blocks = (p.tokens * p.parts + kWarps - 1) / kWarps;
   const unsigned grid = unsigned(std::min<int64_t>(blocks, 3 * sms));
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p); };
+  auto launch = [&](auto kernel) { return launch_after(kernel, dim3(grid), kThreads, stream, p); };
   switch (a->cache * 2 + p.interleaved) {
-    case 0: launch(qk_norm_rope_kernel<false, ZL_CACHE_NONE>); break;
-    case 1: launch(qk_norm_rope_kernel<true, ZL_CACHE_NONE>); break;
-    case 2: launch(qk_norm_rope_kernel<false, ZL_CACHE_BF16>); break;
-    case 3: launch(qk_norm_rope_kernel<true, ZL_CACHE_BF16>); break;
-    case 4: launch(qk_norm_rope_kernel<false, ZL_CACHE_Q4>); break;
-    default: launch(qk_norm_rope_kernel<true, ZL_CACHE_Q4>);
+    case 0: return launch(qk_norm_rope_kernel<false, ZL_CACHE_NONE>);
+    case 1: return launch(qk_norm_rope_kernel<true, ZL_CACHE_NONE>);
+    case 2: return launch(qk_norm_rope_kernel<false, ZL_CACHE_BF16>);
+    case 3: return launch(qk_norm_rope_kernel<true, ZL_CACHE_BF16>);
+    case 4: return launch(qk_norm_rope_kernel<false, ZL_CACHE_Q4>);
+    default: return launch(qk_norm_rope_kernel<true, ZL_CACHE_Q4>);
   }
-  return cudaGetLastError() == cudaSuccess ? ZL_OK : ZL_ERR_CUDA;
 }
