@@ -39,10 +39,10 @@
 // save (8 sequences of 32k-131k tokens: 126 us with them, 123 without).
 //
 // Measured, 32 query heads on 8 kv heads, from a graph: 8 sequences of 32k-131k tokens
-// 123 us, 5.9 TB/s of 6.8 that a copy reaches (HBM, and ends of CTAs from 103 us on); 64
-// of 512-4096 tokens 43 us (9 until the first tile is there, 27 of streaming, 7 of ends
-// and merge), verifying 4 drafted tokens each 59 us (matrix instructions: 64 a tile, from
-// 8 warps); one token each of 32 heads on one kv head, 8 sequences, 24 us.
+// 122 us, 6.0 TB/s of 6.8 that a copy reaches (HBM); 64 of 512-4096 tokens 42 us (7 until
+// the first tile is there, 28 of streaming, 7 of ends and merge), verifying 4 drafted
+// tokens each 58 us (matrix instructions: 64 a tile, from 8 warps); 32 of 1000-8000 tokens
+// with 32 heads on one kv head 23 us.
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"

@@ -4,7 +4,10 @@
 // Both move bytes: per token and kv head 512 bytes of bf16 on one side, 144 on the
 // other. A quarter-warp of 8 lanes takes a K or a V row, each lane one block of 16
 // elements (32 bytes of bf16, 8 of codes, a scale byte), so that no block is shared
-// between lanes and a row's 64 bytes of codes go out side by side.
+// between lanes and a row's 64 bytes of codes go out side by side. HBM bounds both: 8
+// chunks of 512 tokens of 8 heads appended and 2048-8192 tokens read back 44 us for 254 MB,
+// 5.7 TB/s where a copy reaches 6.8; 4 prompts of up to 16384 tokens written and read
+// 104 us, 5.9 TB/s. (Two rows at a time per thread: 115.)
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"

@@ -10,7 +10,7 @@
 // sines and cosines stay in registers, and rows are loaded two rounds ahead. (With blocks
 // of 8 tokens that read the angles from shared memory for every head those reads bounded
 // it, with rows one round ahead the latency of the loads: 16384 tokens of 40 heads 66 us
-// either way, 61.7 so, 5.4 TB/s.) Pairs of elements go through packed 32-bit operations.
+// either way, 61.5 so, 5.5 TB/s.) Pairs of elements go through packed 32-bit operations.
 //
 // The angle: positions times turns. freq_turns is a frequency in turns, 64 bits
 // behind the point, so the product's low 64 bits are the angle without its whole
@@ -60,7 +60,8 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
 template <bool INTERLEAVED, int CACHE>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     const __grid_constant__ NormRope p) {
-  griddep_launch_dependents();
+  // (no griddep_launch_dependents: blocks that wait beside these cost more than they save,
+  // 64 us a prompt of 16384 tokens and 61.5 without, call after call)
   griddep_wait();
   __shared__ __align__(16) float cosine[kWarps][kMaxFreq], sine[kWarps][kMaxFreq];
   // elements 8 c + 4 j .. + 3 at [j][c]: a quarter-warp's reads touch every bank once
