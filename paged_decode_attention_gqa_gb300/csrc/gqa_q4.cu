@@ -1114,14 +1114,18 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   pl->rgroups = (pl->rows + pl->rr - 1) / pl->rr;
   pl->nt = pl->rr > 8 ? 2 : 1;
   // Bundle: of the divisors of Hkv up to 8 the one that leaves the fewest warps of a CTA
-  // idle, the largest of those; one head in small calls, where slices cut the time of a
-  // unit.
+  // idle, the largest of those. In small calls, where slices cut the time of a unit, the
+  // least with which every CTA has one unit at most: each takes some 3 us beside its tiles.
+  // (51 sequences of 8-32 tokens, 5 query tokens, 32 heads on 8: 38 us with one head to a
+  // CTA, 8.7 so; 64 of 64-256 tokens 18 and 11.)
   pl->HB = 1;
   const int64_t len = a->max_seq_len > 0 ? a->max_seq_len : 4096;
-  const int64_t tiles = int64_t(a->B) * a->Hkv * pl->rgroups * ((len + kTile - 1) / kTile);
-  if (tiles >= int64_t(sms) * 32)
-    for (int d = 2; d <= kMaxBundle; ++d)
-      if (a->Hkv % d == 0 && kMaxWarps / d * d >= kMaxWarps / pl->HB * pl->HB) pl->HB = d;
+  const int64_t single = int64_t(a->B) * a->Hkv * pl->rgroups;  // units of one head
+  const bool large = single * ((len + kTile - 1) / kTile) >= int64_t(sms) * 32;
+  for (int d = 2; d <= kMaxBundle; ++d)
+    if (a->Hkv % d == 0 && kMaxWarps / d * d >= kMaxWarps / pl->HB * pl->HB &&
+        (large || single > int64_t(ctas_per_sm(pl->nt)) * sms * pl->HB))
+      pl->HB = d;
   pl->S = 1;  // a power of two
   while (2 * pl->S * pl->HB <= kMaxWarps) pl->S *= 2;
   pl->units_per_seq = a->Hkv / pl->HB * pl->rgroups;

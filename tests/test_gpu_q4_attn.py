@@ -83,6 +83,16 @@ def test_large_calls_put_heads_side_by_side():
         check(c, q, max_seq_len=200000, num_ctas=11)
 
 
+@pytest.mark.parametrize("B,hi,q_len,Hq,Hkv", [(51, 32, 5, 32, 8), (64, 120, 1, 32, 8),
+                                               (40, 90, 1, 12, 6), (90, 60, 2, 8, 4)])
+@pytest.mark.parametrize("bound", [False, True])
+def test_many_short_sequences(B, hi, q_len, Hq, Hkv, bound):
+    """More heads than CTAs, each of a few tiles."""
+    lens = [q_len + (i * 37) % (hi - q_len + 1) for i in range(B - 2)] + [hi, 0]
+    c = Cache(33, lens, Hkv)
+    check(c, queries(c, q_len, Hq), max_seq_len=hi if bound else 0)
+
+
 def test_remapped_pages_give_the_same_bits():
     c = Cache(21, [400, 90], 2)
     q = queries(c, 1, 8)
