@@ -662,7 +662,7 @@ zl_status zl_decode_attn_q4_workspace_size(const zl_decode_attn_q4_params* param
  *     beyond the block table's reach stores nothing in the cache
  *     (ZL_DEVERR_BAD_SEQ_LEN), a token on a bad page neither
  *     (ZL_DEVERR_BAD_PAGE); q_out and k_out are written all the same.
- *   - Supported: Hq, Hkv <= 65535, n_axes <= 4.
+ *   - Supported: Hq, Hkv <= 65535, n_axes <= 4, B * q_len <= 2^30.
  */
 typedef enum { ZL_CACHE_NONE = 0, ZL_CACHE_BF16 = 1, ZL_CACHE_Q4 = 2 } zl_cache_kind;
 

@@ -7,10 +7,11 @@
 // and chunk l + n_freq / 8; interleaved or not rotated: chunks 2 l and 2 l + 1), so
 // only the sum of squares crosses lanes. A warp takes a token (a part of its heads where
 // tokens are few), four heads at a time, queries, then keys, then values: the lane's
-// sines and cosines stay in registers, and rows are loaded two rounds ahead. (With blocks
-// of 8 tokens that read the angles from shared memory for every head those reads bounded
-// it, with rows one round ahead the latency of the loads: 16384 tokens of 40 heads 66 us
-// either way, 61.5 so, 5.5 TB/s.) Pairs of elements go through packed 32-bit operations.
+// sines and cosines stay in registers, and rows are loaded two rounds ahead, across
+// tokens, as the positions are. (16384 tokens of 40 heads: with blocks of 8 tokens that read
+// the angles from shared memory for every head, and with rows one round ahead, 66 us; ahead
+// within a token only, 61; so 59.7, 5.6 TB/s. Where a token has 6 heads, 62372 tokens, 79 and
+// 50.) Pairs of elements go through packed 32-bit operations.
 //
 // The angle: positions times turns. freq_turns is a frequency in turns, 64 bits
 // behind the point, so the product's low 64 bits are the angle without its whole
@@ -61,62 +62,105 @@ template <bool INTERLEAVED, int CACHE>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     const __grid_constant__ NormRope p) {
   // (no griddep_launch_dependents: blocks that wait beside these cost more than they save,
-  // 64 us a prompt of 16384 tokens and 61.5 without, call after call)
+  // 64 us a prompt of 16384 tokens where this took 61.5, call after call)
   griddep_wait();
   __shared__ __align__(16) float cosine[kWarps][kMaxFreq], sine[kWarps][kMaxFreq];
   // elements 8 c + 4 j .. + 3 at [j][c]: a quarter-warp's reads touch every bank once
   __shared__ __align__(16) float weight[2][2][16][4];
+  // (lanes read different ones, which the parameters' memory hands out one by one)
+  __shared__ uint64_t turns[kMaxFreq];
+  __shared__ int64_t axis_at[kMaxFreq];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
   const int pair_lanes = INTERLEAVED ? 0 : p.n_freq >> 3;  // lanes with half-split pairs
   const bool turned = 8 * l < p.n_freq;
   // chunks of a lane in a row of q or k (one of v: 2 l and 2 l + 1)
   const int qa = l < pair_lanes ? l : 2 * l, qb = l < pair_lanes ? l + pair_lanes : 2 * l + 1;
+  const int units = int(p.tokens * p.parts), step = gridDim.x * kWarps;
+  // What unit u is: token, heads begin .. end - 1 of it.
+  auto unit_at = [&](int u, int& tok, int& begin, int& end) {
+    tok = p.parts > 1 ? u / p.parts : u;
+    begin = (u - tok * p.parts) * p.part;
+    end = min(begin + p.part, p.heads);
+  };
+  // Row r of a token: a head of q, then of k, then of v.
+  auto head_of = [&](int r, int& h) {
+    h = r;
+    if (h < p.Hq) return 0;
+    h -= p.Hq;
+    if (CACHE == ZL_CACHE_NONE || h < p.Hkv) return 1;
+    h -= p.Hkv;
+    return 2;
+  };
+  // The position that frequency f goes by.
+  auto position = [&](int tok, int f) {
+    if (f >= p.n_freq) return 0;
+    if (p.positions) return p.positions[axis_at[f] + tok];
+    const int seq = tok / p.q_len;
+    return p.seq_lens[seq] - p.q_len + (tok - seq * p.q_len);
+  };
+  // Rows are loaded two rounds ahead, those of the next unit too: the round to be loaded is
+  // row r_a (of this lane) of unit u_a.
+  int u_a = blockIdx.x * kWarps + warp, tok_a = 0, r_a = 0, end_a = 0;
+  if (u_a < units) {
+    unit_at(u_a, tok_a, r_a, end_a);
+    r_a += lane >> 3;
+  }
+  uint4 a[2], b[2];  // of this round and the next
+  auto load = [&](uint4& x, uint4& y) {
+    if (u_a >= units) return;
+    if (r_a < end_a) {
+      int h;
+      const int kind = head_of(r_a, h);
+      const uint4* src = p.x[kind] + tok_a * p.stride[kind] + h * 16;
+      x = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l : qa];
+      y = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l + 1 : qb];
+    }
+    r_a += 4;
+    if (r_a - (lane >> 3) < end_a) return;
+    u_a += step;
+    unit_at(u_a, tok_a, r_a, end_a);
+    r_a += lane >> 3;
+  };
+  const int first = tok_a;
+  load(a[0], b[0]);
+  load(a[1], b[1]);
   for (int e = threadIdx.x; e < 256; e += kThreads) {
     const float* w = p.weight[e >> 7];
     const int d = e & 127;
     weight[e >> 7][(d >> 2) & 1][d >> 3][d & 3] = w ? w[d] : 1.f;
   }
+  for (int f = threadIdx.x; f < p.n_freq; f += kThreads) {
+    turns[f] = p.turns[f];
+    axis_at[f] = p.axes[f] * p.axis_stride;
+  }
   __syncthreads();
+  int pos[2] = {};  // of this lane's two frequencies, for the unit to come
+  if (blockIdx.x * kWarps + warp < units) {
+    pos[0] = position(first, lane);
+    pos[1] = position(first, lane + 32);
+  }
 
-  const int64_t units = p.tokens * p.parts, step = int64_t(gridDim.x) * kWarps;
-  for (int64_t u = int64_t(blockIdx.x) * kWarps + warp; u < units; u += step) {
-    const int64_t tok = p.parts > 1 ? u / p.parts : u;
-    const int begin = int(u - tok * p.parts) * p.part, end = min(begin + p.part, p.heads);
-
-    // Row r of the token: a head of q, then of k, then of v.
-    auto head_of = [&](int r, int& h) {
-      h = r;
-      if (h < p.Hq) return 0;
-      h -= p.Hq;
-      if (CACHE == ZL_CACHE_NONE || h < p.Hkv) return 1;
-      h -= p.Hkv;
-      return 2;
-    };
-    uint4 a[2], b[2];  // of this round and the next
-    auto load = [&](int r, uint4& x, uint4& y) {
-      if (r >= end) return;
-      int h;
-      const int kind = head_of(r, h);
-      const uint4* src = p.x[kind] + tok * p.stride[kind] + h * 16;
-      x = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l : qa];
-      y = src[CACHE != ZL_CACHE_NONE && kind == 2 ? 2 * l + 1 : qb];
-    };
+  for (int u = blockIdx.x * kWarps + warp; u < units; u += step) {
+    int tok, begin, end;
+    unit_at(u, tok, begin, end);
     int r = begin + (lane >> 3);
-    load(r, a[0], b[0]);
-    load(r + 4, a[1], b[1]);
 
     // Angles: a lane computes those of two frequencies, and takes its own eight.
     __syncwarp();  // (the last token's have been read)
-    const int64_t seq = !p.positions || CACHE != ZL_CACHE_NONE ? tok / p.q_len : 0;
-    const int i = int(tok - seq * p.q_len);
-    for (int f = lane; f < p.n_freq; f += 32) {
-      const int pos = p.positions ? p.positions[p.axes[f] * p.axis_stride + tok]
-                                  : p.seq_lens[seq] - p.q_len + i;
-      const uint64_t turn = uint64_t(int64_t(pos)) * p.turns[f] + 0x80000000ull;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int f = lane + 32 * e;
+      if (f >= p.n_freq) break;
+      const uint64_t turn = uint64_t(int64_t(pos[e])) * turns[f] + 0x80000000ull;
       float sn, cs;
       sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
       cosine[warp][f] = cs * p.rope_scale;
       sine[warp][f] = sn * p.rope_scale;
+    }
+    if (u + step < units) {
+      const int next = p.parts > 1 ? (u + step) / p.parts : u + step;
+      pos[0] = position(next, lane);
+      pos[1] = position(next, lane + 32);
     }
     __syncwarp();
     ulonglong2 co[2] = {}, si[2] = {};
@@ -129,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
     }
     int64_t place = -1;  // of the token in the pool, -1: not stored
     if constexpr (CACHE != ZL_CACHE_NONE) {
+      const int seq = tok / p.q_len, i = tok - seq * p.q_len;
       const int L = p.seq_lens[seq];
       uint32_t err = 0;
       if (L < p.q_len || int64_t(L) > p.bt_stride * p.page_size) {
@@ -154,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(
       uint32_t y[2][4] = {{a[0].x, a[0].y, a[0].z, a[0].w}, {b[0].x, b[0].y, b[0].z, b[0].w}};
       a[0] = a[1];
       b[0] = b[1];
-      load(r + 8, a[1], b[1]);
+      load(a[1], b[1]);
       uint64_t x[2][4], sums = 0;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -302,6 +347,7 @@ zl_status validate(const zl_qk_norm_rope_params* a) {
     for (int i = 0; i < a->n_freq; ++i)
       if (a->axes[i] >= a->n_axes) return ZL_ERR_INVALID_ARG;
   const int64_t T = int64_t(a->B) * a->q_len;
+  if (T > (1 << 30)) return ZL_ERR_UNSUPPORTED;  // (a terabyte of queries is more than fits)
   if (a->positions ? (a->n_axes > 1 && a->axis_stride < T) : !a->seq_lens && a->n_freq > 0)
     return ZL_ERR_INVALID_ARG;
   if (cached) {
