@@ -73,9 +73,13 @@ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 // us, with 4 44.9; verifying 4 tokens each, so 16 columns: 65.5 and 62.6; 32 heads on one
 // kv head: 27.2 and 25.2, without 36.)
 constexpr int unit_cost(int nt) { return nt == 1 ? 2 : 4; }
-// Units of at most this many tiles per slice get a CTA each where there are CTAs
-// enough: streaming them costs less than the merge of their parts.
-constexpr int kWholeTiles = 4;
+// Short units get a CTA each where there are CTAs enough: cut, each would take n tiles of
+// every slice times units / CTAs, and a merge, which costs as much as some 4 tiles. n is
+// the longest's, so 8 at most. (32 units of 8 tiles for 304 CTAs: 12.0 us cut, 14.6 whole; 128
+// of 5 13.1 and 12.3; with 16 columns 88 of 6 for 152 CTAs 18.1 and 15.2.)
+__host__ __device__ constexpr bool whole_units(int64_t units, int64_t ctas, int64_t n) {
+  return units <= ctas && n <= 8 && n * (ctas - units) <= 4 * ctas;
+}
 constexpr int kMaxDevices = 64;
 constexpr double kLog2e = 1.4426950408889634;
 // A row's softmax base moves when a score exceeds it by more than kMove, to kSlack
@@ -134,7 +138,7 @@ struct Cut {
   __device__ __forceinline__ Cut(const Q4Params& p, int64_t tiles, int longest) {
     W = tiles * p.units_per_seq;
     const int64_t units = int64_t(p.B) * p.units_per_seq;
-    whole = p.whole || (units <= p.ctas && longest <= kWholeTiles * p.S);
+    whole = p.whole || whole_units(units, p.ctas, (longest + p.S - 1) >> p.log_s);
     if (W < (INT64_C(1) << 31)) {  // (nearly always: 64-bit divisions are slow)
       const uint32_t w = uint32_t(W);
       G = min(uint32_t(p.ctas), max(w >> p.log_s, 1u));
@@ -1146,8 +1150,8 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
     pl->ctas = int(std::max<int64_t>(1, std::min<int64_t>(pl->ctas, most)));
   }
   const int64_t units = int64_t(a->B) * pl->units_per_seq;
-  pl->whole = a->max_seq_len > 0 && units <= pl->ctas &&
-              (int64_t(a->max_seq_len) + kTile - 1) / kTile <= kWholeTiles * pl->S;
+  const int64_t most = ((len + kTile - 1) / kTile + pl->S - 1) / pl->S;  // tiles of a slice
+  pl->whole = a->max_seq_len > 0 && whole_units(units, pl->ctas, most);
   if (pl->whole) pl->ctas = int(units);
   // a warp of the merge reads four parts at a time; more warps to a row where a unit
   // is cut into more
