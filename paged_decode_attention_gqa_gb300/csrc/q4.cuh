@@ -3,6 +3,7 @@
 #pragma once
 
 #include "../../include/zl_decode_attn.h"
+#include "ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,22 +48,23 @@ __device__ __forceinline__ Q4Scale q4_scale(uint32_t amax) {
   return q;
 }
 
-// x / s, one Newton step behind the product with r: a quotient that is halfway
-// between two codes comes out exact (with the bare product some ties fall off it).
-// The remainder is taken as y s - x so that a zero keeps x's sign.
-__device__ __forceinline__ float q4_quotient(float x, const Q4Scale& q) {
-  const float y = __fmul_rn(x, q.r);
-  return __fmaf_rn(-__fmaf_rn(y, q.s, -x), q.r, y);
-}
-
 // Codes of 8 bf16 elements (element 0 in the low half of x[0], nibble 0 of the
-// word). The conversion rounds to nearest, ties to even, and saturates at 6.
+// word): x / s by one Newton step behind the product with r, so that a quotient that is
+// halfway between two codes comes out exact (with the bare product some ties fall off it).
+// In terms of -x, two elements at a time; a zero keeps x's sign in every step. The
+// conversion rounds to nearest, ties to even, and saturates at 6.
 __device__ __forceinline__ uint32_t q4_codes(const uint32_t (&x)[4], const Q4Scale& q) {
+  const uint64_t s = pack_f32x2(q.s, q.s), r = pack_f32x2(-q.r, -q.r);
   float y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    y[2 * i] = q4_quotient(__uint_as_float(x[i] << 16), q);
-    y[2 * i + 1] = q4_quotient(__uint_as_float(x[i] & 0xFFFF0000u), q);
+    const uint32_t m = x[i] ^ 0x80008000u;
+    const uint64_t minus =
+        pack_f32x2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    const uint64_t first = mul_f32x2(minus, r);
+    const float2 v = unpack_f32x2(fma_f32x2(fma_f32x2(first, s, minus), r, first));
+    y[2 * i] = v.x;
+    y[2 * i + 1] = v.y;
   }
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
