@@ -110,18 +110,12 @@ struct Q4Params {
   int cost;              // places of a unit that hold no tile, a multiple of S
   int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
   int whole;             // 1: CTA c takes unit c and there is no merge (max_seq_len is short)
-  uint64_t page_inv;     // 2^36 / (halves of a page), rounded up
+  Divisor page;          // by page_size
   float scale_log2;
 };
 
 __device__ __forceinline__ void flag(uint32_t* f, uint32_t bits) {
   if (f) atomicOr(f, bits);
-}
-
-// The page of token t, a multiple of 16 below 2^31 (right as t / 16 times what page_inv is
-// too large by, below 64, stays below 2^36).
-__device__ __forceinline__ int page_of(const Q4Params& p, int t) {
-  return int((uint64_t(uint32_t(t) / kHalf) * p.page_inv) >> 36);
 }
 
 __device__ __forceinline__ int tiles_of(const Q4Params& p, int L) {
@@ -431,7 +425,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     if (k0 + (lane >> 1) < count) {
       int b = b_next, r = r_next;
       tile_behind(lane >> 1, b, r, unit, j);
-      const int t = j * kTile + (lane & 1) * kHalf, pg = page_of(p, t);
+      const int t = j * kTile + (lane & 1) * kHalf, pg = int(p.page.quotient(uint32_t(t)));
       // (a half behind the last token has no page; the table's row is not read there)
       if (!(lane & 1) || j + 1 + p.cost < prefix[b + 1] - prefix[b] ||
           (both[b / 32] >> (b % 32) & 1)) {
@@ -803,7 +797,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         if (any_bad) {
           const int at = tok0 + (lane & 1) * kHalf;
           int pg = 0;
-          if (at < L) pg = p.block_table[b * p.bt_stride + page_of(p, at)];
+          if (at < L) pg = p.block_table[b * p.bt_stride + p.page.quotient(uint32_t(at))];
           const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= p.num_pages) & 3u;
           whole = bad & 1u ? 0 : bad ? kHalf : kTile;
 #pragma unroll
@@ -1237,8 +1231,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.cost = unit_cost(pl.nt) * pl.S;
   p.box32 = a->page_size % kTile == 0;
   p.whole = pl.whole;
-  const uint64_t halves = uint64_t(a->page_size / kHalf);
-  p.page_inv = ((UINT64_C(1) << 36) + halves - 1) / halves;
+  p.page = Divisor(uint32_t(a->page_size));
   p.scale_log2 = float(double(a->scale) * kLog2e);
 
   cudaLaunchConfig_t cfg = {};

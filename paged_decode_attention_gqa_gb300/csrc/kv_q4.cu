@@ -5,9 +5,10 @@
 // other. A quarter-warp of 8 lanes takes a K or a V row, each lane one block of 16
 // elements (32 bytes of bf16, 8 of codes, a scale byte), so that no block is shared
 // between lanes and a row's 64 bytes of codes go out side by side. HBM bounds both: 8
-// chunks of 512 tokens of 8 heads appended and 2048-8192 tokens read back 44 us for 254 MB,
-// 5.7 TB/s where a copy reaches 6.8; 4 prompts of up to 16384 tokens written and read
-// 104 us, 5.9 TB/s. (Two rows at a time per thread: 115.)
+// chunks of 512 tokens of 8 heads appended and 2048-8192 tokens read back 43 us for 254 MB,
+// 5.9 TB/s where a copy reaches 6.8; 4 prompts of up to 16384 tokens written and read
+// 99 us, 6.2 TB/s. (Two rows at a time per thread took 115 where one took 105; divisions
+// that the device works out 104.)
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"
@@ -28,6 +29,7 @@ struct AppendQ4 {
   uint32_t* err_flags;
   int q_len, Hkv, page_size, num_pages;
   bool wide;  // rows on 32-byte boundaries
+  Divisor heads, page;
 };
 
 // Blocks (x, b): the rows (token, head) of sequence b, two to a warp.
@@ -49,9 +51,10 @@ __global__ void __launch_bounds__(256) append_q4_kernel(const __grid_constant__ 
   const int64_t stride = kv ? p.v_stride : p.k_stride;
   const uint32_t step = gridDim.x * (blockDim.x >> 4);
   for (uint32_t r = blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4); r < rows; r += step) {
-    const uint32_t i = r / uint32_t(p.Hkv), h = r - i * uint32_t(p.Hkv);
+    const uint32_t i = p.heads.quotient(r), h = r - i * uint32_t(p.Hkv);
     const int t = L - n + int(i);
-    const int page = p.block_table[b * p.bt_stride + t / p.page_size];
+    const uint32_t pg = p.page.quotient(uint32_t(t));
+    const int page = p.block_table[b * p.bt_stride + pg];
     const uint4* at = src + (int64_t(b) * p.q_len + i) * stride + int64_t(h) * 16 + 2 * j;
     uint32_t x[2][4];
     if (p.wide) {
@@ -69,7 +72,8 @@ __global__ void __launch_bounds__(256) append_q4_kernel(const __grid_constant__ 
     }
     const Q4Scale s = q4_scale(max(q4_amax8(x[0]), q4_amax8(x[1])));
     uint8_t* row = p.pool + int64_t(page) * p.page_stride +
-                   int64_t(t % p.page_size) * p.token_stride + int64_t(h) * p.head_stride;
+                   int64_t(t - int(pg) * p.page_size) * p.token_stride +
+                   int64_t(h) * p.head_stride;
     *reinterpret_cast<uint2*>(row + kv * kQ4VCodes + 8 * j) =
         make_uint2(q4_codes(x[0], s), q4_codes(x[1], s));
     row[kQ4KScales + 8 * kv + j] = uint8_t(s.byte);
@@ -86,6 +90,7 @@ struct ReadQ4 {
   __nv_bfloat16* v_out;
   uint32_t* err_flags;
   int tokens, Hkv, page_size, num_pages;
+  Divisor heads, page;
 };
 
 __global__ void __launch_bounds__(256) read_q4_kernel(const __grid_constant__ ReadQ4 p) {
@@ -103,15 +108,16 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const __grid_constant__ Re
   __nv_bfloat16* out = kv ? p.v_out : p.k_out;
   const uint32_t step = gridDim.x * (blockDim.x >> 4);
   for (uint32_t r = blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4); r < rows; r += step) {
-    const uint32_t t = r / uint32_t(p.Hkv), h = r - t * uint32_t(p.Hkv);
-    const int page = p.block_table[b * p.bt_stride + t / uint32_t(p.page_size)];
+    const uint32_t t = p.heads.quotient(r), h = r - t * uint32_t(p.Hkv);
+    const uint32_t pg = p.page.quotient(t);
+    const int page = p.block_table[b * p.bt_stride + pg];
     if (page < 0 || page >= p.num_pages) {
       if (h == 0 && (lane & 15) == 0 && p.err_flags) atomicOr(p.err_flags, ZL_DEVERR_BAD_PAGE);
       continue;
     }
     if (!out) continue;
     const uint8_t* row = p.pool + int64_t(page) * p.page_stride +
-                         int64_t(t % uint32_t(p.page_size)) * p.token_stride +
+                         int64_t(t - pg * uint32_t(p.page_size)) * p.token_stride +
                          int64_t(h) * p.head_stride;
     const uint2 w = *reinterpret_cast<const uint2*>(row + kv * kQ4VCodes + 8 * j);
     const uint32_t sb = row[kQ4KScales + 8 * kv + j];
@@ -175,6 +181,8 @@ extern "C" zl_status zl_kv_append_q4(const zl_kv_append_q4_params* a, zl_stream_
   p.Hkv = a->Hkv;
   p.page_size = a->page_size;
   p.num_pages = a->num_pages;
+  p.heads = Divisor(uint32_t(a->Hkv));
+  p.page = Divisor(uint32_t(a->page_size));
   p.wide = aligned_to(a->k_new, 32) && aligned_to(a->v_new, 32) && a->k_stride % 16 == 0 &&
            a->v_stride % 16 == 0;
   return launch_after(append_q4_kernel, row_grid(int64_t(a->q_len) * a->Hkv, a->B, sms), 256,
@@ -208,6 +216,8 @@ extern "C" zl_status zl_kv_read_q4(const zl_kv_read_q4_params* a, zl_stream_t st
   p.Hkv = a->Hkv;
   p.page_size = a->page_size;
   p.num_pages = a->num_pages;
+  p.heads = Divisor(uint32_t(a->Hkv));
+  p.page = Divisor(uint32_t(a->page_size));
   return launch_after(read_q4_kernel, row_grid(int64_t(a->tokens) * a->Hkv, a->B, sms), 256,
                       stream, p);
 }

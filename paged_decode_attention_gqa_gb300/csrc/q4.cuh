@@ -17,6 +17,21 @@ constexpr int kQ4KScales = 128;  // of K's scales
 constexpr int kQ4VScales = 136;  // of V's scales
 constexpr uint32_t kQ4BadScale = 255;
 
+// Quotients of numbers below 2^31 by a number d that the host knows: x mul >> shift, with
+// mul = 2^shift / d rounded up and 2^(shift - 31) the least power not below d, so that what
+// mul is too large by, less than d / d, adds less than 1 / d.
+struct Divisor {
+  uint32_t mul, shift;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) : shift(31) {
+    while ((UINT64_C(1) << (shift - 31)) < d) ++shift;
+    mul = uint32_t(((UINT64_C(1) << shift) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t x) const {
+    return uint32_t((uint64_t(x) * mul) >> shift);
+  }
+};
+
 // ------------------------------------------------------------------- writing
 // The scale of a block whose largest magnitude is the bf16 number of bits amax
 // (NaN and infinity: 0x7F80 and above).
