@@ -245,3 +245,59 @@ def test_rows_and_cache_of_other_sequences_stay():
             for h in range(2):
                 mine.add((int(m.bt[b, t // 16]), t % 16, h))
     assert {tuple(x) for x in changed} <= mine and len(changed) >= len(mine) - 1
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_that_follow_one_another_without_a_wait(graph):
+    """Each call reads what the one before it wrote: norm, attention, append of its output,
+    read-back, norm of that. The bits are those of calls that are waited for."""
+    B, Hq, Hkv, P, n = 3, 8, 4, 16, 2
+    m = Model(40, B, Hq, Hkv, P, 900)
+    lens = lengths([900, 77, 410])
+    k = torch.randn(B, 900, Hkv, 128, generator=m.g).to(torch.bfloat16).cuda()
+    zl.kv_append_q4(k, k, m.pool, m.bt, lens, page_size=P, new_lens=lens)
+    first, start = m.projection(n), m.pool.clone()
+    qkv, q = torch.empty_like(first), torch.empty(B, n, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    back = torch.zeros(2, B, 900, Hkv, 128, dtype=torch.bfloat16, device="cuda")
+    positions = torch.arange(n, dtype=torch.int32, device="cuda").repeat(B, 1)
+
+    def steps(after):
+        for _ in range(6):
+            m.norm(qkv, lens, q_out=q)
+            after()
+            m.attend(q, lens, out=out)
+            after()
+            zl.kv_append_q4(out[:, :, :Hkv], out[:, :, Hkv:], m.pool, m.bt, lens, page_size=P)
+            after()
+            zl.kv_read_q4(m.pool, m.bt, lens, k_out=back[0], v_out=back[1], page_size=P)
+            after()
+            # rows that were read (the newest of one sequence among them) go into the next step
+            zl.qk_norm_rope(back[0, :, 75:75 + n].contiguous(), back[1, :, 75:75 + n].contiguous(),
+                            rope=m.rope, positions=positions, q_out=qkv[:, :, Hq:Hq + Hkv],
+                            k_out=qkv[:, :, Hq + Hkv:])
+            after()
+
+    def run(after, g=None):
+        qkv.copy_(first)
+        m.pool.copy_(start)
+        back.zero_()
+        torch.cuda.synchronize()
+        g.replay() if g else steps(after)
+        torch.cuda.synchronize()
+        return [x.clone() for x in (qkv, q, out, back, m.pool)]
+
+    want = run(torch.cuda.synchronize)
+    g = None
+    if graph:
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            steps(lambda: None)
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            steps(lambda: None)
+    for _ in range(5):
+        for a, b in zip(want, run(lambda: None, g)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert int(m.err.item()) == 0 and bool(torch.isfinite(want[2]).all())
