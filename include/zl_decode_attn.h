@@ -628,7 +628,7 @@ zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* params, zl_stream_t 
 
 /* Workspace bytes zl_decode_attn_q4 needs, from the shapes, num_ctas and
    max_seq_len; 0 (and workspace NULL) where max_seq_len shows that every unit gets a CTA
-   of its own. */
+   or a few of its own. */
 zl_status zl_decode_attn_q4_workspace_size(const zl_decode_attn_q4_params* params, size_t* bytes);
 
 /*

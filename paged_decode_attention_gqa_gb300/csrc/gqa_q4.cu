@@ -28,7 +28,9 @@
 // slices of the tiles of each. The tiles of all (sequence, bundle, row group) units
 // are laid end to end and cut into equal ranges, one per CTA; slice s takes every
 // S-th tile. Slices are merged in shared memory at the end of each unit, units that
-// are cut between CTAs by a second, programmatically dependent launch, in CTA order.
+// are cut between CTAs by a second, programmatically dependent launch, in CTA order. Short
+// calls, as max_seq_len tells, have no cut and no second launch: a unit to a CTA, or to a
+// cluster of them that merges it out of its CTAs' shared memory.
 //
 // What an SM issues decides: an mma.sync holds the issue port for 8 cycles, every other
 // instruction for one, and nothing overlaps that (in registers alone, 16 conversions,
@@ -109,7 +111,8 @@ struct Q4Params {
   int ctas;              // CTAs of the attention kernel
   int cost;              // places of a unit that hold no tile, a multiple of S
   int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
-  int whole;             // 1: CTA c takes unit c and there is no merge (max_seq_len is short)
+  int whole;             // 1: no merge: CTA c takes unit c (max_seq_len is short), or
+  int log_c;             // 2^log_c CTAs, a cluster, share unit c >> log_c and merge it themselves
   Divisor page;          // by page_size
   float scale_log2;
 };
@@ -240,6 +243,21 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
+// From the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Merges n partials of a row, four columns per lane, in order.
 struct RowMerge {
   float m, den;
@@ -319,7 +337,9 @@ __device__ __forceinline__ void scan_tiles(const Q4Params& p, int32_t* prefix, i
   __syncthreads();
 }
 
-template <int NT>
+// CLUSTER: p.log_c > 0 (an instance of its own: the code that it adds costs short calls
+// 0.3 us).
+template <int NT, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kMaxWarps, ctas_per_sm(NT))
 q4_decode_kernel(const __grid_constant__ Q4Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -356,10 +376,18 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
   {
     const Cut cut(p, prefix[p.B], longest);
     if (cut.whole) {
-      if (c < int64_t(p.B) * M) {
-        b_c = c / M;
+      const int unit = CLUSTER ? c >> p.log_c : c;
+      if (unit < int64_t(p.B) * M) {
+        b_c = unit / M;
         len = prefix[b_c + 1] - prefix[b_c];
-        r_c = (c - b_c * M) * len;
+        r_c = (unit - b_c * M) * len;
+        if (CLUSTER && len > 0) {  // this CTA's share of each slice
+          const int n = len - p.cost, m = (n + S - 1) >> log_s;
+          const int k = c & ((1 << p.log_c) - 1);
+          const int j0 = (k * m >> p.log_c) << log_s;
+          len = min(((k + 1) * m >> p.log_c) << log_s, n) - j0;
+          r_c += j0;
+        }
       }
     } else if (c < int(cut.G) && cut.W > 0) {
       const int64_t s_c = cut.start(c);
@@ -894,12 +922,13 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
                                                        : lse2;
         }
       named_barrier(1 + hb, S * 32);
+      const int first = hb;  // warp of slice 0
       for (int r = sl; r < R; r += S) {
         // (the largest first: then nothing waits for the slice before)
         float top = -CUDART_INF_F, den = 0.f;
         bool bad = false;
         for (int s = 0; s < S; ++s) {
-          const float ls = merge_l[(s * HB + hb) * kRows + r];
+          const float ls = merge_l[(first + s * HB) * kRows + r];
           bad |= isnan(ls);
           top = fmaxf(top, ls);
         }
@@ -908,7 +937,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         if (!none) {
 #pragma unroll 4
           for (int s = 0; s < S; ++s) {
-            const int at = (s * HB + hb) * kRows + r;
+            const int at = (first + s * HB) * kRows + r;
             const float wgt = ex2_approx(merge_l[at] - top);
             const float4 os = reinterpret_cast<const float4*>(merge_o + at * 128)[lane];
             den += wgt;
@@ -921,7 +950,12 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
         }
         const float lse2 = none ? -CUDART_INF_F : top + lg2_approx(den);
-        if (cut_unit) {
+        if (CLUSTER) {  // (this warp alone reads or writes row r by now)
+          __syncwarp();
+          reinterpret_cast<float4*>(merge_o + (first * kRows + r) * 128)[lane] = v;
+          if (lane == 0)
+            merge_l[first * kRows + r] = bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
+        } else if (cut_unit) {
           const int64_t at = part0 + r;
           reinterpret_cast<float4*>(p.ws_o + at * 128)[lane] = v;
           if (lane == 0) p.ws_lse[at] = bad ? CUDART_NAN_F : isnan(lse2) ? CUDART_INF_F : lse2;
@@ -941,6 +975,42 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     for (int k = k_dead; k < min(count, k_dead + NS); ++k)
       mbar_wait(full + 8 * (k % NS), uint32_t(k / NS) & 1u, &never);
   }
+  if constexpr (!CLUSTER) return;
+
+  // ---- a cluster's unit: the rows of all its heads, spread over all its warps
+  if (len == 0)
+    for (int e = tid; e < HB * kRows; e += blockDim.x) merge_l[e] = -CUDART_INF_F;
+  __syncwarp();
+  cluster_sync();
+  const int unit = c >> p.log_c, b = unit / M;
+  if (b < p.B && prefix[b + 1] > prefix[b]) {
+    const int C = 1 << p.log_c, v = unit - b * M;
+    const int row0 = v % p.rgroups * p.rr, R = min(p.rr, p.rows - row0);
+    for (int id = (c & (C - 1)) * W + warp; id < HB * R; id += C * W) {
+      const int hh = id / R, r = id - hh * R;
+      const uint32_t l_at = smem_u32(merge_l + hh * kRows + r);
+      const uint32_t o_at = smem_u32(merge_o + (hh * kRows + r) * 128 + 4 * lane);
+      RowMerge m;
+      m.init();
+#pragma unroll 4
+      for (int k = 0; k < C; ++k) {
+        const float part = ld_cluster(mapa_shared(l_at, k));
+        float4 o4 = ld_cluster_v4(mapa_shared(o_at, k));
+        if (part != -CUDART_INF_F) m.add(part, o4);  // (nothing was written for none)
+      }
+      const bool none = m.bad || m.den == 0.f;
+      const float inv = none ? 0.f : rcp_approx(m.den);
+      const int64_t row = query_row(p, b, v / p.rgroups * HB + hh, row0 + r);
+      uint2 w = make_uint2(0u, 0u);
+      if (!none)
+        w = make_uint2(pack_bf16x2(m.o.x * inv, m.o.y * inv), pack_bf16x2(m.o.z * inv, m.o.w * inv));
+      reinterpret_cast<uint2*>(p.out + row * 128)[lane] = w;
+      if (p.lse && lane == 0)
+        p.lse[row] = none ? -CUDART_INF_F : (m.m + lg2_approx(m.den)) * 0.69314718055994531f;
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // (until then the others may read this CTA's rows)
 }
 
 // Rows of units that were cut: the parts in CTA order, PW warps to a row (each takes
@@ -1048,7 +1118,8 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
 struct Plan {
   int nt, g, rows, rgroups, rr, HB, S, stages, units_per_seq, ctas, merge_warps;
   int sms;
-  bool whole;  // known from max_seq_len: a CTA for every unit
+  bool whole;  // known from max_seq_len: a CTA for every unit, or
+  int log_c;   // a cluster of 2^log_c
   size_t smem, off_o, bytes;
 };
 
@@ -1089,10 +1160,12 @@ zl_status occupancy(size_t smem, int threads, int* n) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ZL_ERR_CUDA;
   std::atomic<int>& k = known[dev][threads / 32][smem / 1024];
   if ((*n = k.load(std::memory_order_relaxed)) > 0) return ZL_OK;
-  if (cudaFuncSetAttribute(q4_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           226 * 1024) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, q4_decode_kernel<NT>, threads, smem) !=
-          cudaSuccess ||
+  for (auto kernel : {q4_decode_kernel<NT, false>, q4_decode_kernel<NT, true>})
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024) !=
+        cudaSuccess)
+      return ZL_ERR_CUDA;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, q4_decode_kernel<NT, false>, threads,
+                                                    smem) != cudaSuccess ||
       *n < 1)
     return ZL_ERR_CUDA;
   k.store(*n, std::memory_order_relaxed);
@@ -1145,8 +1218,28 @@ zl_status make_plan(const zl_decode_attn_q4_params* a, Plan* pl) {
   }
   const int64_t units = int64_t(a->B) * pl->units_per_seq;
   const int64_t most = ((len + kTile - 1) / kTile + pl->S - 1) / pl->S;  // tiles of a slice
+  // Where they are short, one unit to a CTA, or a cluster of 2, 4 or 8 CTAs to a unit, which
+  // costs 2 tiles' time more (of 8: 4), where cut units and their merge cost 5 (with 16
+  // columns, whose tiles take longer, 4). (A cluster lies in one part of the device, where a
+  // few SMs may be left over: of 4 or 8, three quarters of the CTAs at most. 4 sequences of
+  // 1000-2000 tokens, 32 heads on 8: 11.9 us cut, 9.7 so; 3 of 807-1012, 5 query tokens, 12
+  // heads on 6, 12.2 whole and 10.4.)
+  pl->log_c = 0;
   pl->whole = a->max_seq_len > 0 && whole_units(units, pl->ctas, most);
-  if (pl->whole) pl->ctas = int(units);
+  if (a->max_seq_len > 0 && a->num_ctas == 0 && pl->S > 1) {
+    int64_t least = pl->whole ? most * pl->ctas
+                              : most * units + (pl->nt == 1 ? 5 : 4) * int64_t(pl->ctas);
+    for (int k = 1; k <= 3; ++k) {
+      const int64_t n = (most + (1 << k) - 1) >> k, cost = (n + (k < 3 ? 2 : 4)) * pl->ctas;
+      if ((units << k) * (k > 1 ? 4 : 3) > int64_t(pl->ctas) * 3 || n > 8 || 1 << k > most ||
+          cost >= least)
+        continue;
+      least = cost;
+      pl->log_c = k;
+      pl->whole = true;
+    }
+  }
+  if (pl->whole) pl->ctas = int(units << pl->log_c);
   // a warp of the merge reads four parts at a time; more warps to a row where a unit
   // is cut into more
   const int64_t parts = pl->ctas / units + 2;
@@ -1231,6 +1324,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.cost = unit_cost(pl.nt) * pl.S;
   p.box32 = a->page_size % kTile == 0;
   p.whole = pl.whole;
+  p.log_c = pl.log_c;
   p.page = Divisor(uint32_t(a->page_size));
   p.scale_log2 = float(double(a->scale) * kLog2e);
 
@@ -1239,13 +1333,21 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   cfg.blockDim = dim3(unsigned(pl.HB * pl.S) * 32);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1u << pl.log_c;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = pl.nt == 1 ? cudaLaunchKernelEx(&cfg, q4_decode_kernel<1>, p)
-                             : cudaLaunchKernelEx(&cfg, q4_decode_kernel<2>, p);
+  cfg.numAttrs = pl.log_c > 0 ? 2 : 1;
+  cudaError_t e;
+  if (pl.log_c > 0)
+    e = pl.nt == 1 ? cudaLaunchKernelEx(&cfg, q4_decode_kernel<1, true>, p)
+                   : cudaLaunchKernelEx(&cfg, q4_decode_kernel<2, true>, p);
+  else
+    e = pl.nt == 1 ? cudaLaunchKernelEx(&cfg, q4_decode_kernel<1, false>, p)
+                   : cudaLaunchKernelEx(&cfg, q4_decode_kernel<2, false>, p);
   if (e != cudaSuccess) return ZL_ERR_CUDA;
   if (pl.whole) return ZL_OK;  // no unit is cut
   const int64_t rows = int64_t(a->Hkv) * pl.rows;  // of a sequence

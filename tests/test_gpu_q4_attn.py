@@ -93,6 +93,41 @@ def test_many_short_sequences(B, hi, q_len, Hq, Hkv, bound):
     check(c, queries(c, q_len, Hq), max_seq_len=hi if bound else 0)
 
 
+CLUSTERS = [([700, 0, 33, 1999], 8, 2, 1, 16), ([2000, 1, 513, 257], 32, 8, 1, 48),
+            ([900], 2, 2, 1, 16), ([1500, 40], 5, 1, 3, 32), ([4000], 32, 1, 2, 64),
+            ([300, 600, 1200, 2400, 5], 16, 4, 1, 16), ([1000] * 19, 8, 1, 2, 16),
+            ([7000, 300], 8, 1, 1, 128)]
+
+
+@pytest.mark.parametrize("layout", ["NHD", "HND"])
+@pytest.mark.parametrize("lens,Hq,Hkv,q_len,P", CLUSTERS)
+def test_few_units_with_a_bound(lens, Hq, Hkv, q_len, P, layout):
+    """Several CTAs to a unit, which merge it themselves where the bound is short."""
+    c = Cache(34, [L if L == 0 else max(L, q_len) for L in lens], Hkv, P=P, layout=layout)
+    check(c, queries(c, q_len, Hq), max_seq_len=max(lens))
+
+
+def test_few_units_with_a_bound_and_bad_pages_numbers_and_lengths():
+    """A bad page, a NaN block and a bad length reach the rows that they reach without one."""
+    c = Cache(35, [1400, 900, 700, 64], 2)
+    q = queries(c, 2, 8)
+    q[1, 0, 3, 9] = float("nan")
+    c.bt[0, 50] = -1  # tokens 800 .. 815 of sequence 0
+    page, slot = c.place(2, 300)
+    c.pool[page, slot, 1, 136 + 2] = 255
+    c.lens[3] = 10 ** 6
+    a = run(c, q, num_ctas=5)
+    b = run(c, q, max_seq_len=1400)
+    assert a[2] == b[2] == zl.DEVERR_BAD_PAGE | zl.DEVERR_BAD_SEQ_LEN
+    for x, y in zip(a[:2], b[:2]):
+        assert np.array_equal(np.isnan(x), np.isnan(y)) and np.array_equal(np.isinf(x), np.isinf(y))
+        ok = np.isfinite(x)
+        # both are within a bf16 rounding and 2^-10 (P) of the same sums
+        assert np.allclose(x[ok], y[ok], rtol=2.0 ** -7, atol=2.0 ** -9)
+    assert not b[0][[0, 3]].any() and np.isnan(b[0][1, 0, 3]).all()
+    assert np.isnan(b[0][2, :, 4:, 32:48]).all() and np.isfinite(b[0][2, :, :4]).all()
+
+
 def test_remapped_pages_give_the_same_bits():
     c = Cache(21, [400, 90], 2)
     q = queries(c, 1, 8)
