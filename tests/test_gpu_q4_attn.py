@@ -107,6 +107,12 @@ def test_few_units_with_a_bound(lens, Hq, Hkv, q_len, P, layout):
     check(c, queries(c, q_len, Hq), max_seq_len=max(lens))
 
 
+def test_few_units_with_a_bound_that_does_not_hold():
+    c = Cache(36, [2500, 40, 1100], 2)
+    for bound in (1000, 700):
+        check(c, queries(c, 1, 8), max_seq_len=bound)
+
+
 def test_few_units_with_a_bound_and_bad_pages_numbers_and_lengths():
     """A bad page, a NaN block and a bad length reach the rows that they reach without one."""
     c = Cache(35, [1400, 900, 700, 64], 2)
