@@ -1251,9 +1251,20 @@ class Rope:
         for f in freq:
             num, den = f.as_integer_ratio()
             turns.append((2 * num * _INV_TWO_PI + (den << 192)) // (den << 193) % (1 << 64))
-        self._turns = (ctypes.c_uint64 * max(1, len(freq)))(*turns)
-        self._axes = (ctypes.c_uint8 * max(1, len(freq)))(*axes)
-        self.turns_at, self.axes_at = ctypes.addressof(self._turns), ctypes.addressof(self._axes)
+        self._lay_out(turns, axes)
+
+    def _lay_out(self, turns, axes):
+        self._turns = (ctypes.c_uint64 * max(1, len(turns)))(*turns)
+        self._axes = (ctypes.c_uint8 * max(1, len(axes)))(*axes)
+
+    # Copies and pickles carry the numbers and lay out arrays of their own (a call takes the
+    # arrays' addresses, so none is kept here that could outlive them).
+    def __getstate__(self):
+        return {**self.__dict__, "_turns": list(self._turns), "_axes": list(self._axes)}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._lay_out(state["_turns"], state["_axes"])
 
 
 # 2^256 / (2 pi), from pi to 80 digits
@@ -1364,8 +1375,8 @@ def qk_norm_rope(q, k, *, rope=None, positions=None, q_weight=None, k_weight=Non
                 ko_at, ko_st = k_out.data_ptr(), Hkv * 128
     status = (_raw.get("zl_qk_norm_rope") or _raw_fn("zl_qk_norm_rope", 1))(_pack(
         _NORM_ROPE, _NORM_ROPE.size, q_at, k_at, v_at, q_st, k_st, v_st, qo_at, ko_at, qo_st,
-        ko_st, qw, kw, eps, rope.scale, rope.turns_at, rope.axes_at, rope.n_freq, rope.n_axes,
-        rope.interleaved, cache, pos_at, axis_st, kp_at, vp_at, ps, ts, hs,
+        ko_st, qw, kw, eps, rope.scale, ctypes.addressof(rope._turns), ctypes.addressof(rope._axes),
+        rope.n_freq, rope.n_axes, rope.interleaved, cache, pos_at, axis_st, kp_at, vp_at, ps, ts, hs,
         bt_at, bt_stride, sl_at, B, q_len, Hq, Hkv, page_size, pages, err), on)
     if status != OK:
         _check(status, "zl_qk_norm_rope")

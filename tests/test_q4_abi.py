@@ -326,3 +326,53 @@ def test_the_plain_quantisation_on_known_blocks():
     assert k[0, :8].tolist() == [6, -6, 4, 2, 0, 1, -4, 1] and (v == -k).all()
     # a value of an exact grid comes back as it is
     assert (plain_q4.unpack(plain_q4.pack(k, v))[0] == k).all()
+
+
+# ------------------------------------------------------------ copies of a rotation
+def _handed_over(monkeypatch, rope):
+    """The parameters that a norm call with this rope hands to the library (a fake one)."""
+    import contextlib
+    got = []
+
+    def entry(packed, stream):
+        got.append(zl.NormRopeParams.from_buffer_copy(packed))
+        return zl.OK
+
+    monkeypatch.setattr(zl, "_on", lambda index, stream: (0, contextlib.nullcontext()))
+    monkeypatch.setitem(zl._raw, "zl_qk_norm_rope", entry)
+    d = _tensors()
+    zl.qk_norm_rope(d["q"], d["k"], rope=rope, positions=torch.zeros(4, 2, 3, dtype=torch.int32))
+    return got[0]
+
+
+@pytest.mark.parametrize("how", ["itself", "copy", "deepcopy", "pickle", "subclass"])
+def test_a_copied_rope_hands_over_its_own_arrays(monkeypatch, how):
+    """Whatever becomes of the original: its arrays are freed with it."""
+    import copy
+    import pickle
+
+    freq, axes = [0.5, 1.0, -2.0, 3.0] * 8, [0, 1, 2, 3] * 8
+    make = zl.Rope if how != "subclass" else type("Own", (zl.Rope,), {})
+    first = make(freq, axes=axes, interleaved=True, scale=1.5)
+    first.note = [1]
+    rope = {"itself": lambda: first, "copy": lambda: copy.copy(first),
+            "deepcopy": lambda: copy.deepcopy(first), "subclass": lambda: copy.deepcopy(first),
+            "pickle": lambda: pickle.loads(pickle.dumps(first))}[how]()
+    assert type(rope) is type(first) and rope.note == [1]
+    p = _handed_over(monkeypatch, rope)
+    assert p.freq_turns == ctypes.addressof(rope._turns) and p.axes == ctypes.addressof(rope._axes)
+    assert (p.n_freq, p.n_axes, p.interleaved, p.rope_scale) == (32, 4, 1, 1.5)
+    assert list(rope._turns) == list(first._turns) and list(rope._axes) == axes
+    if rope is not first:
+        assert p.freq_turns != ctypes.addressof(first._turns)
+
+
+def test_a_rope_inside_a_copied_model(monkeypatch):
+    import copy
+    model = {"layers": [zl.Rope(zl.rope_frequencies(64))]}
+    twin = copy.deepcopy(model)
+    want = list(model["layers"][0]._turns)
+    del model
+    rope = twin["layers"][0]
+    p = _handed_over(monkeypatch, rope)
+    assert p.freq_turns == ctypes.addressof(rope._turns) and list(rope._turns) == want
