@@ -524,7 +524,11 @@ zl_status zl_kv_commit(const zl_kv_commit_params* params, zl_stream_t stream);
  * roundings are exact: which side of a border a quotient lies on is decided without
  * error. A block that holds a NaN or an infinity gets scale byte 255 and codes 0:
  * all 16 read back as NaN. A value has at most 6 significant bits, so it is exact in
- * bf16 and, with the scales above, in fp16.
+ * bf16.
+ *
+ * A pool that others wrote may hold any scale up to byte 247 (61440): such blocks are
+ * read back and attended to as the values they stand for. Of 248 .. 255, no numbers, only
+ * 255 is specified.
  *
  * The pool is also a bf16 pool of 72 elements per row without V (v_pool NULL, D_k
  * 72, strides halved): zl_kv_commit and zl_kv_evict move its rows so.

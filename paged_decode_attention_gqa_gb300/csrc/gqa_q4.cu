@@ -9,9 +9,11 @@
 //   is the 16-row operand and query rows are columns, 8 to an instruction (NT = 1
 //   or 2 of them), so a token costs 8 + 8 instructions per 16, where queries as the
 //   16-row operand would take 16 + 16.
-// - Codes become fp16 pairs by one conversion each and take their scale in one
-//   fp16 product, exact (6 significant bits). fp16 rather than bf16: there is a
-//   conversion to it, and P keeps 11 bits. A query row is scaled by a power of two
+// - Codes become fp16 pairs by one conversion each and take an eighth of their scale
+//   (kUnit) in one fp16 product, exact: 6 significant bits, from 2^-21 to 46080. (The
+//   whole scale would leave fp16 where its byte is 0xE3 or more, which zl_kv_append_q4
+//   does not write, but others may.) fp16 rather than bf16: there is a conversion to
+//   it, and P keeps 11 bits. A query row is scaled by a power of two
 //   so that its largest element is in [2^14, 2^15): what falls below fp16's range is
 //   2^-39 of it, and the factor goes into the softmax scale.
 // - Which element, token or column sits where in a fragment is free as long as both
@@ -84,6 +86,11 @@ __host__ __device__ constexpr bool whole_units(int64_t units, int64_t ctas, int6
 }
 constexpr int kMaxDevices = 64;
 constexpr double kLog2e = 1.4426950408889634;
+// What an element counts in the products: 1 / kUnit of its value, put right in the
+// softmax factor and at the end of a piece.
+constexpr int kLogUnit = 3;
+constexpr float kUnit = 8.f;
+constexpr uint32_t kUnitF16x2 = 0x30003000u;  // 1 / kUnit twice, as fp16
 // A row's softmax base moves when a score exceeds it by more than kMove, to kSlack
 // below the largest: P stays below 2^15 (fp16), and starts at 2^7 so that only what
 // is 2^-21 of the largest leaves fp16's normal numbers.
@@ -588,7 +595,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         const float2 v = unpack_bf16x2(x[i]);
         qf[nt][i] = pack_f16x2(v.x * up, v.y * up);
       }
-      const float down = p.scale_log2 * __uint_as_float(uint32_t(127 - 14 + e) << 23);
+      const float down = p.scale_log2 * __uint_as_float(uint32_t(127 - 14 + kLogUnit + e) << 23);
       fac2[nt] = pack_f32x2(__shfl_sync(0xffffffffu, down, 8 * t4),
                             __shfl_sync(0xffffffffu, down, 8 * t4 + 4));
     }
@@ -629,10 +636,10 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           ca[hf] = *reinterpret_cast<const uint4*>(row + 16 * t4);
           cb[hf] = *reinterpret_cast<const uint4*>(row + kQ4Row + 16 * t4);
           const uint8_t* sc = row + kQ4KScales + 2 * t4;
-          fa[hf][0] = sc[0] * 0x00800080u;
-          fa[hf][1] = sc[1] * 0x00800080u;
-          fb[hf][0] = sc[kQ4Row] * 0x00800080u;
-          fb[hf][1] = sc[kQ4Row + 1] * 0x00800080u;
+          fa[hf][0] = mul_f16x2(sc[0] * 0x00800080u, kUnitF16x2);
+          fa[hf][1] = mul_f16x2(sc[1] * 0x00800080u, kUnitF16x2);
+          fb[hf][0] = mul_f16x2(sc[kQ4Row] * 0x00800080u, kUnitF16x2);
+          fb[hf][1] = mul_f16x2(sc[kQ4Row + 1] * 0x00800080u, kUnitF16x2);
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -763,7 +770,8 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           keep_apart(s2, tok_b);
           keep_apart(s3, tok_b + 1);
         }
-        const uint32_t f0 = s0 * 0x80u + s2 * 0x800000u, f1 = s1 * 0x80u + s3 * 0x800000u;
+        const uint32_t f0 = mul_f16x2(s0 * 0x80u + s2 * 0x800000u, kUnitF16x2);
+        const uint32_t f1 = mul_f16x2(s1 * 0x80u + s3 * 0x800000u, kUnitF16x2);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t wa0 = w ? a0.y : a0.x, wb0 = w ? b0.y : b0.x;
@@ -867,7 +875,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           const int r = 8 * nt + 2 * t4 + u;
           if (r >= R) continue;
           const bool none = bad_row[nt][u] || l[nt][u] == 0.f;
-          const float inv = none ? 0.f : rcp_approx(l[nt][u]);
+          const float inv = none ? 0.f : kUnit * rcp_approx(l[nt][u]);
           const float lse2 = none ? -CUDART_INF_F : lg2_approx(l[nt][u]) - base[nt][u];
           float v[16];
 #pragma unroll
@@ -907,7 +915,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
           const int r = 8 * nt + 2 * t4 + u;
           if (r >= R) continue;
           const bool none = bad_row[nt][u] || l[nt][u] == 0.f;
-          const float inv = none ? 0.f : rcp_approx(l[nt][u]);
+          const float inv = none ? 0.f : kUnit * rcp_approx(l[nt][u]);
           const float lse2 = none ? -CUDART_INF_F : lg2_approx(l[nt][u]) - base[nt][u];
           float* to = merge_o + (warp * kRows + r) * 128 + 16 * gid;
 #pragma unroll
