@@ -606,8 +606,9 @@ zl_status zl_kv_read_q4(const zl_kv_read_q4_params* params, zl_stream_t stream);
  *     block table reaches) below 2^31, and times Hkv below 2^40.
  *   - A query row that holds a NaN or an infinity and sees a token gives NaN (out
  *     and lse), and so does a row that sees a K or V block of scale 255 (K: the
- *     whole row; V: those 16 elements) or has a score beyond 32 bits. Rows
- *     that do not see such a token keep their results.
+ *     whole row; V: those 16 elements) or has a score above 32 bits' range. Rows
+ *     that do not see such a token keep their results. A score below that range
+ *     weighs 0; a row with no other scores is one that sees no token.
  */
 typedef struct {
   size_t struct_size; /* sizeof(zl_decode_attn_q4_params) */

@@ -96,6 +96,11 @@ constexpr uint32_t kUnitF16x2 = 0x30003000u;  // 1 / kUnit twice, as fp16
 // is 2^-21 of the largest leaves fp16's normal numbers.
 constexpr float kMove = 15.f;
 constexpr float kSlack = 7.f;
+// The base before there is one: the largest finite number, so that a score of -inf (below
+// 32 bits' range) weighs nothing with it, as with any other base, and every other score
+// moves it, but for those that are its own negative, whose P is 1. (With an infinity -inf
+// was NaN where a slice began with such scores, and weighed nothing elsewhere.)
+constexpr float kNoBase = 3.402823466e38f;
 
 struct Q4Params {
   CUtensorMap tmap;  // 4-D bytes {144, page_size, Hkv, num_pages}, box {144, 16 or 32, 1, 1}
@@ -606,7 +611,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     const int all_see = L - p.q_len + 1 + row0 / p.g;  // tokens that every row sees
 
     float o[NT][8][4];
-    float base[NT][2], l[NT][2];  // base: minus it is added to a score (+inf: none yet)
+    float base[NT][2], l[NT][2];  // base: it is added to a score (kNoBase: none yet)
     bool bad_row[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -614,7 +619,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
       for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        base[nt][u] = CUDART_INF_F;
+        base[nt][u] = kNoBase;
         l[nt][u] = 0.f;
         bad_row[nt][u] = false;
       }
@@ -711,8 +716,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
             // moves to kSlack below the largest where that is upwards
             const float nb = kSlack - mx;
             if (mx != -CUDART_INF_F && nb < base[nt][u]) {
-              const float alpha =
-                  base[nt][u] == CUDART_INF_F ? 0.f : ex2_approx(nb - base[nt][u]);
+              const float alpha = ex2_approx(nb - base[nt][u]);  // (0 from kNoBase)
               base[nt][u] = nb;
               l[nt][u] *= alpha;
 #pragma unroll
