@@ -186,7 +186,7 @@ typedef struct {
    ZL_DEVERR_TIMEOUT in *err_flags, and out / lse are left undefined. The
    context stays usable and the next call without the hook computes normally.
    This is how a stalled pipeline is reported, made to happen on purpose
-   without a fault. zl_decode_attn only. */
+   without a fault. zl_decode_attn; zl_decode_attn_q4, see there. */
 #define ZL_DECODE_TEST_STALL 0x80000000u
 
 /*
@@ -609,6 +609,10 @@ zl_status zl_kv_read_q4(const zl_kv_read_q4_params* params, zl_stream_t stream);
  *     whole row; V: those 16 elements) or has a score above 32 bits' range. Rows
  *     that do not see such a token keep their results. A score below that range
  *     weighs 0; a row with no other scores is one that sees no token.
+ *   - A wait that gives up (ZL_DEVERR_TIMEOUT) zeroes the rows that see a token
+ *     which was not read for it (out = 0, lse = -inf).
+ *   - flags: 0, or ZL_DECODE_TEST_STALL: one warp of every CTA takes that way, as
+ *     if its first tile never came.
  */
 typedef struct {
   size_t struct_size; /* sizeof(zl_decode_attn_q4_params) */
@@ -627,6 +631,7 @@ typedef struct {
   size_t workspace_bytes;
   uint32_t* err_flags; /* optional */
   int32_t num_ctas;
+  uint32_t flags;
 } zl_decode_attn_q4_params;
 
 zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* params, zl_stream_t stream);

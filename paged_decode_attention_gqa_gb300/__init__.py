@@ -278,6 +278,7 @@ class DecodeQ4Params(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t),
         ("err_flags", ctypes.c_void_p),
         ("num_ctas", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
     ]
 
 
@@ -539,7 +540,7 @@ _EVICT = struct.Struct("@N2P3qPqPq4P2qP2q10iPi0P")
 _COMMIT = struct.Struct("@N2P3qPq2PqPP8i2P2qi0P")
 _APPEND_Q4 = struct.Struct("@N2P2qP3qPq2P5iP0P")
 _READ_Q4 = struct.Struct("@NP3qPq3P5iP0P")
-_DECODE_Q4 = struct.Struct("@N2P3qPq3P7ifPNPi0P")
+_DECODE_Q4 = struct.Struct("@N2P3qPq3P7ifPNPiI0P")
 _NORM_ROPE = struct.Struct("@N3P3q2P2q2P2f2P4iPq2P3qPqP6iP0P")
 for _s, _c in ((_PARAMS, Params), (_SCORES, ScoreParams), (_EVICT, EvictParams),
                (_COMMIT, CommitParams), (_APPEND_Q4, AppendQ4Params), (_READ_Q4, ReadQ4Params),
@@ -1196,7 +1197,7 @@ def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None
             _check(_raw_fn("zl_decode_attn_q4_workspace_size", 1)(_pack(
                 _DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at,
                 lse_at, B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale, 0, 0, err,
-                num_ctas), ctypes.addressof(n)), "zl_decode_attn_q4_workspace_size")
+                num_ctas, 0), ctypes.addressof(n)), "zl_decode_attn_q4_workspace_size")
             if len(_sizes) >= 4096:
                 _sizes.clear()
             ws_bytes = _sizes[key] = n.value
@@ -1214,7 +1215,7 @@ def decode_attn_q4(q, pool, block_table, seq_lens, *, page_size, scale, out=None
     status = (_raw.get("zl_decode_attn_q4") or _raw_fn("zl_decode_attn_q4", 1))(_pack(
         _DECODE_Q4, _DECODE_Q4.size, q_at, at, ps, ts, hs, bt_at, bt_stride, sl_at, out_at, lse_at,
         B, q_len, Hq, Hkv, page_size, pages, max_seq_len, scale,
-        0 if workspace is None else workspace.data_ptr(), ws_bytes, err, num_ctas), on)
+        0 if workspace is None else workspace.data_ptr(), ws_bytes, err, num_ctas, 0), on)
     if status != OK:
         _check(status, "zl_decode_attn_q4")
     return out

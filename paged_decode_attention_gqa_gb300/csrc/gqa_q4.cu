@@ -85,6 +85,7 @@ __host__ __device__ constexpr bool whole_units(int64_t units, int64_t ctas, int6
   return units <= ctas && n <= 8 && n * (ctas - units) <= 4 * ctas;
 }
 constexpr int kMaxDevices = 64;
+constexpr uint64_t kTestStallNs = 50ull * 1000 * 1000;  // bound of the test hook's wait
 constexpr double kLog2e = 1.4426950408889634;
 // What an element counts in the products: 1 / kUnit of its value, put right in the
 // softmax factor and at the end of a piece.
@@ -123,6 +124,7 @@ struct Q4Params {
   int ctas;              // CTAs of the attention kernel
   int cost;              // places of a unit that hold no tile, a multiple of S
   int box32;             // 1: pages of a multiple of 32 tokens, copied 32 at a time
+  int test_stall;        // ZL_DECODE_TEST_STALL
   int whole;             // 1: no merge: CTA c takes unit c (max_seq_len is short), or
   int log_c;             // 2^log_c CTAs, a cluster, share unit c >> log_c and merge it themselves
   Divisor page;          // by page_size
@@ -553,6 +555,19 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     }
   };
   bool merged_before = false;
+  if (p.test_stall && warp == 0) {  // as where a wait of its first tile gives up
+    __shared__ int never_set;
+    if (lane == 0) {
+      never_set = 0;
+      if (!flag_wait(&never_set, kTestStallNs)) {
+        flag(p.err_flags, ZL_DEVERR_TIMEOUT);
+        *const_cast<volatile int*>(&abort_flag) = 1;
+      }
+    }
+    __syncwarp();
+    dead = true;
+    left_dead = left;
+  }
 
   int pos = 0;  // in this CTA's range
   while (pos < len) {
@@ -847,6 +862,11 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
         }
         // (a row that does not see the bad half still needs the good one)
         if (whole > 0) run_tile(std::true_type{}, tok0, min(L - tok0, whole));
+      } else {  // never read: its rows end as those that see a bad page
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) bad_row[nt][u] |= tok0 < limit(nt, u);
       }
       next();
       --todo;
@@ -1149,7 +1169,7 @@ zl_status validate(const zl_decode_attn_q4_params* a) {
   if (a->B < 1 || a->Hq < 1 || a->Hkv < 1 || a->q_len < 1 || a->page_size < 1 ||
       a->num_pages < 1 || a->block_table_stride < 1 || a->num_ctas < 0 || a->max_seq_len < 0)
     return ZL_ERR_INVALID_ARG;
-  if (a->Hq % a->Hkv != 0) return ZL_ERR_INVALID_ARG;
+  if (a->Hq % a->Hkv != 0 || a->flags & ~ZL_DECODE_TEST_STALL) return ZL_ERR_INVALID_ARG;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return ZL_ERR_INVALID_ARG;
   if (a->Hq / a->Hkv > 128 || a->q_len > 128 || a->B > kMaxBatch || a->Hkv > 65535 ||
       a->num_ctas > 65535)
@@ -1335,6 +1355,7 @@ extern "C" zl_status zl_decode_attn_q4(const zl_decode_attn_q4_params* a, zl_str
   p.ctas = pl.ctas;
   p.cost = unit_cost(pl.nt) * pl.S;
   p.box32 = a->page_size % kTile == 0;
+  p.test_stall = a->flags & ZL_DECODE_TEST_STALL ? 1 : 0;
   p.whole = pl.whole;
   p.log_c = pl.log_c;
   p.page = Divisor(uint32_t(a->page_size));

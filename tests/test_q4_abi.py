@@ -376,3 +376,10 @@ def test_a_rope_inside_a_copied_model(monkeypatch):
     rope = twin["layers"][0]
     p = _handed_over(monkeypatch, rope)
     assert p.freq_turns == ctypes.addressof(rope._turns) and list(rope._turns) == want
+
+
+@pytest.mark.parametrize("flags", [1, 0x40000000, 0x80000001])
+def test_decode_refuses_flags_that_are_none(flags):
+    assert status("zl_decode_attn_q4", _decode(flags=flags)) == zl.ERR_INVALID_ARG
+    if NO_GPU:
+        assert status("zl_decode_attn_q4", _decode(flags=zl.TEST_STALL)) == zl.ERR_CUDA
