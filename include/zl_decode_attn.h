@@ -603,7 +603,11 @@ zl_status zl_kv_read_q4(const zl_kv_read_q4_params* params, zl_stream_t stream);
  *     max_seq_len except within fp32 rounding.
  *   - Supported: Hq % Hkv == 0, Hq / Hkv <= 128, 1 <= q_len <= 128, page_size a
  *     multiple of 16 (<= 1024), 1 <= B <= 4096; B * (tiles of 16 tokens that the
- *     block table reaches) below 2^31, and times Hkv below 2^40.
+ *     block table reaches) below 2^31, and times Hkv below 2^40; and with N =
+ *     (tiles of 32 tokens that a row of the table reaches + 33) * Hkv *
+ *     ceil(Hq / Hkv * q_len / 16): N below 2^29 and B * N below num_ctas * 2^29
+ *     (num_ctas 0: below the device's SMs * 2^29). Beyond the last two some calls
+ *     are refused, those whose heads do not go side by side first.
  *   - A query row that holds a NaN or an infinity and sees a token gives NaN (out
  *     and lse), and so does a row that sees a K or V block of scale 255 (K: the
  *     whole row; V: those 16 elements) or has a score above 32 bits' range. Rows
