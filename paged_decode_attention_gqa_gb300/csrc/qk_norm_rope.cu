@@ -46,7 +46,7 @@ struct NormRope {
   uint32_t* err_flags;
   int64_t tokens;       // B * q_len
   int q_len, Hq, Hkv, page_size, num_pages;
-  int n_freq, interleaved;
+  int n_freq;
   int heads;            // Hq + Hkv (+ Hkv of v)
   int parts, part;      // parts of a token's heads, heads in each (a multiple of 4)
   uint64_t turns[kMaxFreq];
@@ -424,7 +424,6 @@ extern "C" zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* a, zl_stream_
   p.Hq = a->Hq;
   p.Hkv = a->Hkv;
   p.n_freq = a->n_freq;
-  p.interleaved = a->interleaved ? 1 : 0;
   for (int i = 0; i < a->n_freq; ++i) {
     p.turns[i] = a->freq_turns[i];
     p.axes[i] = a->axes ? a->axes[i] : 0;
@@ -440,7 +439,7 @@ extern "C" zl_status zl_qk_norm_rope(const zl_qk_norm_rope_params* a, zl_stream_
   const int64_t blocks = (p.tokens * p.parts + kWarps - 1) / kWarps;
   const unsigned grid = unsigned(std::min<int64_t>(blocks, 3 * sms));
   auto launch = [&](auto kernel) { return launch_after(kernel, dim3(grid), kThreads, stream, p); };
-  switch (a->cache * 2 + p.interleaved) {
+  switch (a->cache * 2 + (a->interleaved ? 1 : 0)) {
     case 0: return launch(qk_norm_rope_kernel<false, ZL_CACHE_NONE>);
     case 1: return launch(qk_norm_rope_kernel<true, ZL_CACHE_NONE>);
     case 2: return launch(qk_norm_rope_kernel<false, ZL_CACHE_BF16>);
