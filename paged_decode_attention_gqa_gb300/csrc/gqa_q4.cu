@@ -137,7 +137,7 @@ __device__ __forceinline__ void flag(uint32_t* f, uint32_t bits) {
 
 __device__ __forceinline__ int tiles_of(const Q4Params& p, int L) {
   if (L < 0 || int64_t(L) > p.bt_stride * p.page_size) return 0;
-  return (L + kTile - 1) / kTile;
+  return int((uint32_t(L) + kTile - 1) / kTile);  // (lengths go up to 2^31 - 1)
 }
 
 // How the line of W tiles is cut: G ranges, or (short units) one unit per CTA.
@@ -835,7 +835,7 @@ q4_decode_kernel(const __grid_constant__ Q4Params p) {
     const int stride = S * kTile;  // tokens from one to the next
     while (todo > 0) {
       int plain =
-          all_see >= tok0 + kTile ? min(todo, ((all_see - kTile - tok0) >> (log_s + 5)) + 1) : 0;
+          all_see - kTile >= tok0 ? min(todo, ((all_see - kTile - tok0) >> (log_s + 5)) + 1) : 0;
       for (; plain > 0 && !dead; --plain) {
         wait();
         if (dead || any_bad) break;

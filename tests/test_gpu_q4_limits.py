@@ -55,3 +55,32 @@ def test_what_the_header_promises_is_accepted(num_ctas, max_seq_len):
                                  block_table_stride=stride, num_ctas=num_ctas,
                                  max_seq_len=max_seq_len) == zl.OK, (B, q_len, g, Hkv, stride)
     assert seen > 100
+
+
+@pytest.mark.parametrize("L", [(1 << 31) - 32, (1 << 31) - 31, (1 << 31) - 1])
+def test_the_longest_sequences(L):
+    """Up to the last length that 32 bits hold, over four pages mapped again and again: K is
+    0, so the output is the mean of V over the tokens. A warp adds some 2^15 tiles in 32 bits,
+    two steps each, which may be off by 2^-23 of the sum so far: 2^-7 of the mean magnitude."""
+    import numpy as np
+    import torch
+    from plain_q4 import bf16, pack, random_rows, unpack
+
+    P, g = 1024, np.random.default_rng(9)
+    rows = np.stack([pack(np.zeros((P, 1, 128)), bf16(random_rows(g, P, 1))) for _ in range(4)])
+    v = unpack(rows)[1][:, :, 0]                      # [4, P, 128]
+    pool = torch.from_numpy(rows).cuda()
+    pages = torch.arange(1 << 21, dtype=torch.int32, device="cuda")[None] % 4
+    sl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    lse = torch.zeros(1, 2, 3, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, 3, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    out = zl.decode_attn_q4(q, pool, pages.contiguous(), sl, page_size=P, scale=0.1, lse=lse,
+                            err_flags=err)
+    assert int(err.item()) == 0
+    whole, rest = divmod(L, 4 * P)
+    every, some = v.reshape(4 * P, 128), v.reshape(4 * P, 128)[:rest]
+    want = (whole * every.sum(0) + some.sum(0)) / L
+    size = (whole * np.abs(every).sum(0) + np.abs(some).sum(0)) / L
+    assert (np.abs(bf16(out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -7 * size).all()
+    assert np.abs(bf16(lse) - np.log(L)).max() <= 2.0 ** -16
