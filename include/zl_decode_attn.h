@@ -608,6 +608,9 @@ zl_status zl_kv_read_q4(const zl_kv_read_q4_params* params, zl_stream_t stream);
  *     ceil(Hq / Hkv * q_len / 16): N below 2^29 and B * N below num_ctas * 2^29
  *     (num_ctas 0: below the device's SMs * 2^29). Beyond the last two some calls
  *     are refused, those whose heads do not go side by side first.
+ *   - A kv head's Hq / Hkv * q_len query rows go in groups of 16, each of which reads
+ *     and unpacks the cache. Above some 64 rows zl_kv_read_q4 and a call over its
+ *     bf16 rows take less time.
  *   - A query row that holds a NaN or an infinity and sees a token gives NaN (out
  *     and lse), and so does a row that sees a K or V block of scale 255 (K: the
  *     whole row; V: those 16 elements) or has a score above 32 bits' range. Rows

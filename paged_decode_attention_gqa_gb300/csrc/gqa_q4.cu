@@ -43,10 +43,11 @@
 // save (8 sequences of 32k-131k tokens: 126 us with them, 123 without).
 //
 // Measured, 32 query heads on 8 kv heads, from a graph: 8 sequences of 32k-131k tokens
-// 122 us, 6.0 TB/s of 6.8 that a copy reaches (HBM); 64 of 512-4096 tokens 42 us (7 until
+// 123 us, 5.9 TB/s of 6.8 that a copy reaches (HBM); 64 of 512-4096 tokens 42 us (7 until
 // the first tile is there, 28 of streaming, 7 of ends and merge), verifying 4 drafted
-// tokens each 58 us (matrix instructions: 64 a tile, from 8 warps); 32 of 1000-8000 tokens
-// with 32 heads on one kv head 23 us.
+// tokens each 58 us (matrix instructions: 64 a tile, from 8 warps), 16 tokens 194 us, 64 719:
+// every 16 rows of a kv head read, convert and scale its tiles again; 32 sequences of
+// 1000-8000 tokens with 32 heads on one kv head 23 us.
 #include "q4.cuh"
 #include "q4_host.h"
 #include "ptx.cuh"

@@ -10,8 +10,10 @@
 // sines and cosines stay in registers, and rows are loaded two rounds ahead, across
 // tokens, as the positions are. (16384 tokens of 40 heads: with blocks of 8 tokens that read
 // the angles from shared memory for every head, and with rows one round ahead, 66 us; ahead
-// within a token only, 61; so 59.7, 5.6 TB/s. Where a token has 6 heads, 62372 tokens, 79 and
-// 50.) Pairs of elements go through packed 32-bit operations.
+// within a token only, 61; so 60, 5.6 TB/s. Where a token has 6 heads, 62372 tokens, 79 and
+// 50.) Pairs of elements go through packed 32-bit operations. Into a 4-bit pool the rounding
+// to codes bounds it: 16384 tokens of 32 + 8 + 8 heads 82 us, 4.3 TB/s, an SM issuing in 71 %
+// of all cycles; into bf16 pools 79 us, 5.1 TB/s.
 //
 // The angle: positions times turns. freq_turns is a frequency in turns, 64 bits
 // behind the point, so the product's low 64 bits are the angle without its whole
