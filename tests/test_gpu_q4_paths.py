@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 
 
 class _Node(ctypes.Structure):
-    """CUDA_KERNEL_NODE_PARAMS of the driver's interface."""
+    """CUDA_KERNEL_NODE_PARAMS, as libcuda has it."""
     _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
                 ("smem", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
                 ("kernel", ctypes.c_void_p), ("context", ctypes.c_void_p)]
